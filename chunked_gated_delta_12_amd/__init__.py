@@ -13,6 +13,12 @@ has not been built, every call raises.
     o, S_T = kda_chunk_fwd_noalloc(q, k, v, theta, beta, S0=None, o=o, S_T=S_T)
     o      = kda_decode_step_gated(q, k, v, theta, beta, S, z)
     g, gc  = kda_gate(theta)
+
+Beside KDA, the gated delta rule with one decay a head, and the norms around a block:
+
+    o      = kda_gdr_step(q, k, v, g, beta, S, slots=slots)  # S updated in place
+    r, h   = kda_block_norm_fwd(y, x=x, z=z, w_post=w_post, s=s, w_pre=w_pre)
+    grads  = kda_block_norm_bwd(y, dr, dh, x=x, z=z, w_post=w_post, s=s, w_pre=w_pre)
 """
 from __future__ import annotations
 
@@ -27,6 +33,7 @@ LIB_PATH = os.path.join(_HERE, "libkda.so")
 HEADER_PATH = os.path.join(_HERE, "..", "include", "kda.h")
 
 KDA_BF16, KDA_F32 = 0, 1
+KDA_ACT_SIGMOID, KDA_ACT_SILU = 0, 1
 KDA_CHUNK = 16
 KDA_G_MIN = -5.0
 
@@ -77,6 +84,15 @@ def load_library(path: str = LIB_PATH):
     lib.kda_last_error.restype = ctypes.c_char_p
     lib.kda_abi_version.argtypes = []
     lib.kda_abi_version.restype = c_int
+    lib.kda_gdr_step.argtypes = [c_int] * 8 + [ctypes.c_float] + [vp] * 3 + [fp] * 3 + [vp, vp, vp, vp]
+    lib.kda_gdr_step.restype = c_int
+    lib.kda_block_norm_fwd.argtypes = [c_int, c_int, ctypes.c_longlong, c_int, ctypes.c_float] + [vp] * 9
+    lib.kda_block_norm_fwd.restype = c_int
+    lib.kda_block_norm_bwd.argtypes = ([c_int, c_int, ctypes.c_longlong, c_int, ctypes.c_float] + [vp] * 15
+                                       + [c_size, vp])
+    lib.kda_block_norm_bwd.restype = c_int
+    lib.kda_block_norm_bwd_workspace_size.argtypes = [ctypes.c_longlong, c_int, ctypes.POINTER(c_size)]
+    lib.kda_block_norm_bwd_workspace_size.restype = c_int
     _lib = lib
     return lib
 
@@ -318,7 +334,149 @@ def kda_gate(theta, *, g=True, g_cum=True, stream=None):
     return g, g_cum
 
 
-__all__ = ["kda_chunk_fwd", "kda_chunk_fwd_noalloc", "kda_chunk_fwd_gated", "kda_chunk_fwd_unbounded", "kda_chunk_bwd",
+# ----------------------------------------------------------------------------- one decay a head
+class _On:
+    """Makes the tensors' device and the work's stream current for one call: launches go to
+    the device, and what the call allocates belongs to the stream that uses it."""
+
+    def __init__(self, t, stream):
+        if not t.is_cuda:
+            raise ValueError("tensors must be on the GPU")
+        self.stream = torch.cuda.current_stream(t.device) if stream is None else stream
+        if self.stream.device != t.device:
+            raise ValueError(f"stream is on {self.stream.device}, tensors on {t.device}")
+        self.ctx = torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        self.ctx.__enter__()
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def __exit__(self, *exc):
+        return self.ctx.__exit__(*exc)
+
+
+def _dims(t, name, n):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != n:
+        raise ValueError(f"{name} has {t.dim()} dimensions, expected {n}")
+    return t.shape
+
+
+def _gdr_inputs(q, k, v, g, beta, scale):
+    """Checks what the calls of the rule share: (B, T, Hk, Hv, dk, dv, dtype code, scale)."""
+    B, T, Hk, dk = _dims(q, "q", 4)
+    Hv, dv = _dims(v, "v", 4)[2:]
+    dev, dt = q.device, q.dtype
+    code = _dtype_code(q)
+    _need(q, "q", dt, (B, T, Hk, dk), dev)
+    _need(k, "k", dt, (B, T, Hk, dk), dev)
+    _need(v, "v", dt, (B, T, Hv, dv), dev)
+    _need(g, "g", torch.float32, (B, T, Hv), dev)
+    _need(beta, "beta", torch.float32, (B, T, Hv), dev)
+    return B, T, Hk, Hv, dk, dv, code, float(dk ** -0.5 if scale is None else scale)
+
+
+def kda_gdr_step(q, k, v, g, beta, S, *, slots=None, ntok=None, scale=None, o=None, stream=None):
+    """T tokens of the gated delta rule (one decay a head) for each of B rows, the states in
+    a pool updated in place.  q, k [B,T,Hk,dk], v [B,T,Hv,dv] (bf16 or fp32), g, beta
+    [B,T,Hv] fp32, S [nslot,Hv,dk,dv] fp32; slots [B] int32 names each row's state (None:
+    row b has state b; outside the pool: a padded row), ntok [B] int32 how many of its
+    tokens are real (None: all).  scale defaults to dk ** -0.5.  Returns o [B,T,Hv,dv]; what
+    belongs to padded rows and tokens is left as it was (zero where o is made here)."""
+    lib = load_library()
+    B, T, Hk, Hv, dk, dv, code, scale = _gdr_inputs(q, k, v, g, beta, scale)
+    dev = q.device
+    nslot = _dims(S, "S", 4)[0]
+    _need(S, "S", torch.float32, (nslot, Hv, dk, dv), dev)
+    for name, t in (("slots", slots), ("ntok", ntok)):
+        if t is not None:
+            _need(t, name, torch.int32, (B,), dev)
+    with _On(q, stream) as st:
+        if o is None:
+            make = torch.empty if slots is None and ntok is None else torch.zeros
+            o = make((B, T, Hv, dv), dtype=q.dtype, device=dev)
+        _need(o, "o", q.dtype, (B, T, Hv, dv), dev)
+        _check("kda_gdr_step",
+               lib.kda_gdr_step(code, B, T, Hk, Hv, dk, dv, nslot, scale, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
+                                _ptr(S), _ptr(slots), _ptr(ntok), _ptr(o), st))
+    return o
+
+
+# ----------------------------------------------------------------------------- block norm
+_ACTS = {"sigmoid": KDA_ACT_SIGMOID, "silu": KDA_ACT_SILU}
+
+
+def _norm_inputs(y, x, z, w_post, s, w_pre, act):
+    if not isinstance(y, torch.Tensor) or y.dim() < 1:
+        raise TypeError("y must be a torch.Tensor with at least one dimension")
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    code = _dtype_code(y)
+    D = y.shape[-1]
+    for name, t in (("y", y), ("x", x), ("z", z)):
+        if t is not None:
+            _need(t, name, y.dtype, y.shape, y.device)
+    for name, t in (("w_post", w_post), ("s", s), ("w_pre", w_pre)):
+        if t is not None:
+            _need(t, name, torch.float32, (D,), y.device)
+    return code, _ACTS[act], y.numel() // max(1, D), D
+
+
+def kda_block_norm_fwd(y, *, x=None, z=None, w_post=None, s=None, w_pre=None, act="sigmoid", eps=1e-6, r=None, h=None,
+                       stream=None):
+    """The norms around a block with its gate and residual: with n = rmsnorm(y) w_post,
+    r = x + n act(z) s and h = rmsnorm(r) w_pre over the last dimension, every part but y
+    optional.  y, x, z [..., D] (bf16 or fp32), w_post, s, w_pre [D] fp32; act "sigmoid"
+    or "silu".  r may be x itself.  Returns (r, h); h is None without w_pre."""
+    lib = load_library()
+    code, a, rows, D = _norm_inputs(y, x, z, w_post, s, w_pre, act)
+    if h is not None and w_pre is None:
+        raise ValueError("h without w_pre")
+    with _On(y, stream) as st:
+        r = torch.empty_like(y) if r is None else r
+        _need(r, "r", y.dtype, y.shape, y.device)
+        if w_pre is not None:
+            h = torch.empty_like(y) if h is None else h
+            _need(h, "h", y.dtype, y.shape, y.device)
+        _check("kda_block_norm_fwd",
+               lib.kda_block_norm_fwd(code, a, rows, D, eps, _ptr(y), _ptr(x), _ptr(z), _ptr(w_post), _ptr(s), _ptr(w_pre),
+                                      _ptr(r), _ptr(h), st))
+    return r, h
+
+
+def kda_block_norm_bwd_workspace_size(rows, D) -> int:
+    n = ctypes.c_size_t(0)
+    _check("kda_block_norm_bwd_workspace_size",
+           load_library().kda_block_norm_bwd_workspace_size(rows, D, ctypes.byref(n)))
+    return int(n.value)
+
+
+def kda_block_norm_bwd(y, dr, dh=None, *, x=None, z=None, w_post=None, s=None, w_pre=None, act="sigmoid", eps=1e-6,
+                       workspace=None, stream=None):
+    """Backward of kda_block_norm_fwd for L = sum <dr, r> + <dh, h>, from its inputs alone
+    (dr may be None; dh goes with w_pre).  Returns a dict of dy, dx, dz (y's dtype) and
+    dw_post, ds, dw_pre (fp32); None for parts that were not given."""
+    lib = load_library()
+    code, a, rows, D = _norm_inputs(y, x, z, w_post, s, w_pre, act)
+    for name, t in (("dr", dr), ("dh", dh)):
+        if t is not None:
+            _need(t, name, y.dtype, y.shape, y.device)
+    with _On(y, stream) as st:
+        d = {name: None if t is None else torch.empty_like(t)
+             for name, t in (("dy", y), ("dx", x), ("dz", z), ("dw_post", w_post), ("ds", s), ("dw_pre", w_pre))}
+        if workspace is None and not (w_post is None and s is None and w_pre is None):
+            workspace = torch.empty(kda_block_norm_bwd_workspace_size(rows, D), dtype=torch.uint8, device=y.device)
+        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        _check("kda_block_norm_bwd",
+               lib.kda_block_norm_bwd(code, a, rows, D, eps, _ptr(y), _ptr(x), _ptr(z), _ptr(w_post), _ptr(s), _ptr(w_pre),
+                                      _ptr(dr), _ptr(dh), _ptr(d["dy"]), _ptr(d["dx"]), _ptr(d["dz"]), _ptr(d["dw_post"]),
+                                      _ptr(d["ds"]), _ptr(d["dw_pre"]), _ptr(workspace), ws_bytes, st))
+    return d
+
+
+__all__ = ["kda_gdr_step", "kda_block_norm_fwd", "kda_block_norm_bwd", "kda_block_norm_bwd_workspace_size",
+           "KDA_ACT_SIGMOID", "KDA_ACT_SILU", "kda_chunk_fwd", "kda_chunk_fwd_noalloc", "kda_chunk_fwd_gated", "kda_chunk_fwd_unbounded", "kda_chunk_bwd",
            "kda_chunk_bwd_workspace_size", "kda_decode_step",
            "kda_decode_step_gated", "kda_gate", "kda_chunk_fwd_workspace_size",
            "kda_chunk_fwd_auto_segments", "load_library", "header_functions", "KdaError",

@@ -23,6 +23,9 @@ LIB = os.path.join(HERE, "libkda.so")
 PEAKS_LIB = os.path.join(HERE, "libkda_peaks.so")
 PEAKS_SOURCES = ["kda_peaks.hip"]
 SOURCES = ["kda_api.cpp", "kda_gate.hip", "kda_decode.hip", "kda_chunk.hip", "kda_map.hip", "kda_out.hip", "kda_bwd.hip", "kda_bwd2.hip", "kda_gmap.hip"]
+# the operators beside KDA (the gated delta rule with one decay a head, the block norm),
+# linked into libkda.so with the sources above
+MORE_SOURCES = ["kda_gdr_step.hip", "kda_norm.hip"]
 ARCH = "gfx950"
 
 
@@ -61,10 +64,10 @@ def _link(objs, lib):
 
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
-    srcs = SOURCES + PEAKS_SOURCES
+    srcs = SOURCES + MORE_SOURCES + PEAKS_SOURCES
     with cf.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
         objs = dict(zip(srcs, ex.map(_compile, srcs)))
-    _link([objs[s] for s in SOURCES], LIB)
+    _link([objs[s] for s in SOURCES + MORE_SOURCES], LIB)
     _link([objs[s] for s in PEAKS_SOURCES], PEAKS_LIB)
     if verbose:
         print(f"built {LIB} and {PEAKS_LIB}")

@@ -89,6 +89,33 @@ int check_common(int dtype, int B, int H, int dk, int dv) {
     return KDA_OK;
 }
 
+// Alignment of every pointer that is not NULL, and no output over an input or another output.
+int check_ranges(const Range* in, int nin, const Range* out, int nout) {
+    for (int i = 0; i < nin + nout; ++i) {
+        const Range& r = i < nin ? in[i] : out[i - nin];
+        if (r.lo & 15u) return fail(KDA_ERR_ALIGN, "%s is not 16-byte aligned", r.name);
+    }
+    for (int o = 0; o < nout; ++o) {
+        for (int i = 0; i < nin; ++i)
+            if (overlap(out[o], in[i])) return fail(KDA_ERR_ALIAS, "%s overlaps %s", out[o].name, in[i].name);
+        for (int p = 0; p < o; ++p)
+            if (overlap(out[o], out[p])) return fail(KDA_ERR_ALIAS, "%s overlaps %s", out[o].name, out[p].name);
+    }
+    return KDA_OK;
+}
+
+// Sizes of the gated delta rule with one decay a head: `a` sequences or rows of T tokens.
+int check_gdr(int dtype, int a, int T, int Hk, int Hv, int dk, int dv, float scale) {
+    if (dtype != KDA_BF16 && dtype != KDA_F32) return fail(KDA_ERR_DTYPE, "unknown dtype %d", dtype);
+    if (a < 1 || T < 1 || Hk < 1) return fail(KDA_ERR_SHAPE, "sequences=%d T=%d Hk=%d must be >= 1", a, T, Hk);
+    if (Hv < Hk || Hv % Hk) return fail(KDA_ERR_SHAPE, "Hv=%d must be a multiple of Hk=%d", Hv, Hk);
+    if (dk != 32 && dk != 64 && dk != 128) return fail(KDA_ERR_SHAPE, "dk=%d not in {32, 64, 128}", dk);
+    if (dv < 32 || dv > 256 || dv % 32) return fail(KDA_ERR_SHAPE, "dv=%d must be a multiple of 32 from 32 to 256", dv);
+    if (!(scale - scale == 0.0f)) return fail(KDA_ERR_SHAPE, "scale must be finite");
+    if (!sizes_fit(a, T, Hv, 256)) return fail(KDA_ERR_SHAPE, "sequences*T*Hv too large");
+    return KDA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -373,6 +400,93 @@ int kda_gate(int B, int T, int H, int dk, const float* theta, float* g, float* g
     if (overlap(rg_, rc)) return fail(KDA_ERR_ALIAS, "g overlaps g_cum");
 
     hipError_t e = kda::launch_gate(B, T, H, dk, theta, g, g_cum, reinterpret_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(KDA_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
+// ---------------------------------------------------------------- one decay a head
+int kda_gdr_step(int dtype, int B, int T, int Hk, int Hv, int dk, int dv, int nslot, float scale, const void* q,
+                 const void* k, const void* v, const float* g, const float* beta, float* S, const int* slots,
+                 const int* ntok, void* o, void* stream) {
+    int st = check_gdr(dtype, B, T, Hk, Hv, dk, dv, scale);
+    if (st) return st;
+    if (nslot < 1 || (!slots && nslot < B))
+        return fail(KDA_ERR_SHAPE, "nslot=%d states for B=%d rows%s", nslot, B, slots ? "" : " without slots");
+    if (!sizes_fit(nslot, Hv, dk, dv) || (int64_t)B * Hv * (dv / 32) > 0x7fffffffLL)
+        return fail(KDA_ERR_SHAPE, "B*Hv or nslot*Hv too large");
+    if (!q || !k || !v || !g || !beta || !S || !o)
+        return fail(KDA_ERR_NULL, "q, k, v, g, beta, S and o must be non-NULL");
+    const size_t es = dtype == KDA_BF16 ? 2 : 4, tok = (size_t)B * T;
+    const Range in[] = {rng("q", q, tok * Hk * dk * es), rng("k", k, tok * Hk * dk * es), rng("v", v, tok * Hv * dv * es),
+                        rng("g", g, tok * Hv * 4), rng("beta", beta, tok * Hv * 4), rng("slots", slots, (size_t)B * 4),
+                        rng("ntok", ntok, (size_t)B * 4)};
+    const Range out[] = {rng("S", S, (size_t)nslot * Hv * dk * dv * 4), rng("o", o, tok * Hv * dv * es)};
+    if ((st = check_ranges(in, 7, out, 2))) return st;
+    hipError_t e = kda::launch_gdr_step(dtype == KDA_F32, B, T, Hk, Hv, dk, dv, nslot, scale, q, k, v, g, beta, S, slots,
+                                        ntok, o, reinterpret_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(KDA_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
+// ---------------------------------------------------------------- block norm
+static int check_norm(int dtype, int act, long long rows, int D, float eps) {
+    if (dtype != KDA_BF16 && dtype != KDA_F32) return fail(KDA_ERR_DTYPE, "unknown dtype %d", dtype);
+    if (act != KDA_ACT_SIGMOID && act != KDA_ACT_SILU) return fail(KDA_ERR_SHAPE, "unknown act %d", act);
+    if (rows < 1 || rows > (1LL << 40)) return fail(KDA_ERR_SHAPE, "rows=%lld outside [1, 2^40]", rows);
+    if (D < 8 || D > 8192 || D % 8) return fail(KDA_ERR_SHAPE, "D=%d must be a multiple of 8 from 8 to 8192", D);
+    if (!(eps >= 0.0f) || eps > 1.0f) return fail(KDA_ERR_SHAPE, "eps=%g outside [0, 1]", (double)eps);
+    return KDA_OK;
+}
+
+int kda_block_norm_fwd(int dtype, int act, long long rows, int D, float eps, const void* y, const void* x, const void* z,
+                       const float* w_post, const float* s, const float* w_pre, void* r, void* h, void* stream) {
+    int st = check_norm(dtype, act, rows, D, eps);
+    if (st) return st;
+    if (!y || !r) return fail(KDA_ERR_NULL, "y and r must be non-NULL");
+    if (!w_pre != !h) return fail(KDA_ERR_NULL, "h and w_pre go together: both or neither may be NULL");
+    const size_t n = (size_t)rows * D * (dtype == KDA_BF16 ? 2 : 4), w = (size_t)D * 4;
+    // r may be x itself: the residual stream updated in place
+    const Range in[] = {rng("y", y, n), rng("z", z, n), rng("w_post", w_post, w), rng("s", s, w), rng("w_pre", w_pre, w),
+                        rng("x", x == r ? nullptr : x, n)};
+    const Range out[] = {rng("r", r, n), rng("h", h, n)};
+    if ((st = check_ranges(in, 6, out, 2))) return st;
+    hipError_t e = kda::launch_norm_fwd(dtype == KDA_F32, rows, D, eps, act == KDA_ACT_SILU, y, x, z, w_post, s, w_pre, r,
+                                        h, reinterpret_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(KDA_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
+int kda_block_norm_bwd_workspace_size(long long rows, int D, size_t* bytes) {
+    if (!bytes) return fail(KDA_ERR_NULL, "bytes is NULL");
+    int st = check_norm(KDA_BF16, KDA_ACT_SIGMOID, rows, D, 0.0f);
+    if (st) return st;
+    *bytes = kda::norm_bwd_workspace_bytes(rows, D);
+    return ok();
+}
+
+int kda_block_norm_bwd(int dtype, int act, long long rows, int D, float eps, const void* y, const void* x, const void* z,
+                       const float* w_post, const float* s, const float* w_pre, const void* dr, const void* dh, void* dy,
+                       void* dx, void* dz, float* dw_post, float* ds, float* dw_pre, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+    int st = check_norm(dtype, act, rows, D, eps);
+    if (st) return st;
+    if (!y || !dy || (!dr && !dh)) return fail(KDA_ERR_NULL, "y, dy and one of dr and dh must be non-NULL");
+    if (!w_pre != !dh) return fail(KDA_ERR_NULL, "dh and w_pre go together: both or neither may be NULL");
+    if ((dx && !x) || (dz && !z) || (dw_post && !w_post) || (ds && !s) || (dw_pre && !w_pre))
+        return fail(KDA_ERR_NULL, "a gradient is asked for of an input that is NULL");
+    const size_t n = (size_t)rows * D * (dtype == KDA_BF16 ? 2 : 4), w = (size_t)D * 4;
+    const size_t need = dw_post || ds || dw_pre ? kda::norm_bwd_workspace_bytes(rows, D) : 0;
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(KDA_ERR_WORKSPACE, "workspace of %zu bytes needed, got %zu%s", need, workspace_bytes,
+                    workspace ? "" : " (NULL)");
+    const Range in[] = {rng("y", y, n), rng("x", x, n), rng("z", z, n), rng("w_post", w_post, w), rng("s", s, w),
+                        rng("w_pre", w_pre, w), rng("dr", dr, n), rng("dh", dh, n)};
+    const Range out[] = {rng("dy", dy, n), rng("dx", dx, n), rng("dz", dz, n), rng("dw_post", dw_post, w), rng("ds", ds, w),
+                         rng("dw_pre", dw_pre, w), rng("workspace", need ? workspace : nullptr, need)};
+    if ((st = check_ranges(in, 8, out, 7))) return st;
+    hipError_t e = kda::launch_norm_bwd(dtype == KDA_F32, rows, D, eps, act == KDA_ACT_SILU, y, x, z, w_post, s, w_pre, dr,
+                                        dh, dy, dx, dz, dw_post, ds, dw_pre, (float*)workspace,
+                                        reinterpret_cast<hipStream_t>(stream));
     if (e != hipSuccess) return fail(KDA_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
     return ok();
 }

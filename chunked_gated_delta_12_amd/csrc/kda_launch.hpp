@@ -113,4 +113,22 @@ hipError_t launch_chunk_bwd2(int B, int T, int H, int d, int nseg, int seg_len, 
 hipError_t launch_state_combine(int d, int BH, int nseg, const float* init, const float* ws_n, const void* ws_m,
                                 float* out, hipStream_t stream);
 
+// One call of the gated delta rule with one decay a head, token by token, on states
+// in a pool of nslot (slots NULL: row b has slot b; ntok NULL: T tokens a row).
+hipError_t launch_gdr_step(bool f32, int B, int T, int Hk, int Hv, int dk, int dv, int nslot, float scale,
+                           const void* q, const void* k, const void* v, const float* g, const float* beta, float* S,
+                           const int* slots, const int* ntok, void* o, hipStream_t stream);
+
+// The block norm and its backward (kda_norm.hip): x, z, w_post, s, w_pre, dr and dh may
+// be NULL (h and dh go with w_pre), and so may every gradient but dy.  part:
+// norm_bwd_workspace_bytes, or unused when no weight's gradient is asked for.
+hipError_t launch_norm_fwd(bool f32, int64_t rows, int D, float eps, bool silu, const void* y, const void* x,
+                           const void* z, const float* w_post, const float* s, const float* w_pre, void* r, void* h,
+                           hipStream_t stream);
+size_t norm_bwd_workspace_bytes(int64_t rows, int D);
+hipError_t launch_norm_bwd(bool f32, int64_t rows, int D, float eps, bool silu, const void* y, const void* x,
+                           const void* z, const float* w_post, const float* s, const float* w_pre, const void* dr,
+                           const void* dh, void* dy, void* dx, void* dz, float* dw_post, float* ds, float* dw_pre,
+                           float* part, hipStream_t stream);
+
 }  // namespace kda

@@ -275,6 +275,107 @@ int kda_decode_step_gated(int dtype, int B, int H, int dk, int dv,
 int kda_gate(int B, int T, int H, int dk, const float* theta, float* g, float* g_cum,
              void* stream);
 
+/* ===========================================================================
+ * The gated delta rule with one decay a head.
+ *
+ * The sibling of KDA whose forgetting is one factor a token and head instead of
+ * one a channel, given as a log-decay g_t <= 0 without a lower bound.  Per
+ * value head h, whose key head is h / (Hv / Hk), with a state S[dk][dv]:
+ *     S   <- exp(g_t) S
+ *     e_t  = v_t - S^T k_t
+ *     S   <- S + beta_t k_t e_t^T
+ *     o_t  = scale S^T q_t
+ * The entries below share the conventions above, and these:
+ *  - Hv is a multiple of Hk; dk is 32, 64 or 128; dv a multiple of 32 from 32
+ *    to 256, dk and dv independent of each other.
+ *  - g below -120 (minus infinity included) forgets the state entirely; beta is used
+ *    as given.  Positive g is used as it is (the state grows).
+ *  - KDA_BF16 means bf16 storage of q, k, v, o (and of do, dq, dk, dv).  The state,
+ *    g, beta and their gradients are fp32, and so is the arithmetic: products of
+ *    intermediate results run on the bf16 matrix cores as sums over their upper and
+ *    lower halves, which keeps 16 bits of each factor.  KDA_F32 keeps fp32
+ *    storage and fp32 products throughout.
+ * ------------------------------------------------------------------------- */
+
+/* ---------------------------------------------------------------------------
+ * kda_gdr_step: T tokens of the rule for each of B rows, from and to a state in a
+ * pool, in place (decode: T = 1; proposed tokens: T of a few).  The state is read
+ * and written once a call.
+ *
+ *   nslot        states in the pool
+ *   q, k         [B, T, Hk, dk]  dtype
+ *   v            [B, T, Hv, dv]  dtype
+ *   g, beta      [B, T, Hv]      fp32
+ *   S            [nslot, Hv, dk, dv]  fp32, the rows' states read and overwritten
+ *   slots        [B] int32, the state of each row, or NULL: row b has state b
+ *                (nslot >= B).  A slot outside [0, nslot) marks a padded row.  Of the
+ *                rows that name one slot the first has it and the others count as
+ *                padded.
+ *   ntok         [B] int32, how many of a row's T tokens are real (more than T counts
+ *                as T), or NULL: all.  With none the row is padded.
+ *   o            [B, T, Hv, dv]  dtype, written for the real tokens of rows that are not
+ *                padded and left as it was elsewhere; must not overlap any input
+ *   slots and ntok are read on the device, when the work runs.
+ * Returns a kda_status.
+ * ------------------------------------------------------------------------- */
+int kda_gdr_step(int dtype, int B, int T, int Hk, int Hv, int dk, int dv, int nslot, float scale,
+                 const void* q, const void* k, const void* v, const float* g, const float* beta,
+                 float* S, const int* slots, const int* ntok, void* o, void* stream);
+
+/* ===========================================================================
+ * The norms around a block, fused with its gate, residual scale and residual sum.
+ *
+ * Per row of D channels, every operand but y optional (NULL):
+ *     n = y / sqrt(mean(y^2) + eps) * w_post     norm after the block   (w_post NULL: n = y)
+ *     a = n * act(z) * s                         gate, residual scale   (z, s NULL: factor 1)
+ *     r = x + a                                  residual stream        (x NULL: r = a)
+ *     h = r / sqrt(mean(r^2) + eps) * w_pre      norm before the next block
+ * With rows = tokens x heads and D = dv, y and z alone it is the output norm and gate of
+ * a KDA or gated-delta-rule head; with rows = tokens it stands between two blocks.
+ * All arithmetic is fp32; h is formed from r before r is rounded.
+ *
+ *   dtype        storage of y, x, z, r, h and of their gradients
+ *   act          KDA_ACT_SIGMOID: act(z) = 1/(1+e^-z);  KDA_ACT_SILU: z/(1+e^-z)
+ *   rows, D      rows >= 1; D a multiple of 8 from 8 to 8192
+ *   eps          in [0, 1]
+ *   y, x, z      [rows, D]  dtype
+ *   w_post, s, w_pre   [D]  fp32
+ *   r            [rows, D]  dtype, written; may be x itself
+ *   h            [rows, D]  dtype, written; NULL exactly when w_pre is
+ * Returns a kda_status.
+ * ------------------------------------------------------------------------- */
+typedef enum kda_act { KDA_ACT_SIGMOID = 0, KDA_ACT_SILU = 1 } kda_act;
+
+int kda_block_norm_fwd(int dtype, int act, long long rows, int D, float eps,
+                       const void* y, const void* x, const void* z,
+                       const float* w_post, const float* s, const float* w_pre,
+                       void* r, void* h, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * kda_block_norm_bwd: gradients of L = sum <dr, r> + <dh, h>, from the inputs of the
+ * forward alone (nothing of it is saved).
+ *
+ *   dr           [rows, D]  dtype, or NULL (zero);  dh  [rows, D]  dtype, NULL exactly
+ *                when w_pre is; one of the two must be given
+ *   dy           [rows, D]  dtype, written
+ *   dx, dz       [rows, D]  dtype, written; or NULL to skip
+ *   dw_post, ds, dw_pre   [D]  fp32, written (sums over the rows, in a fixed order);
+ *                or NULL to skip
+ *   workspace    kda_block_norm_bwd_workspace_size bytes when a weight's gradient is
+ *                asked for; otherwise it may be NULL
+ *   No output may overlap an input, another output or the workspace.
+ * Returns a kda_status.
+ * ------------------------------------------------------------------------- */
+int kda_block_norm_bwd(int dtype, int act, long long rows, int D, float eps,
+                       const void* y, const void* x, const void* z,
+                       const float* w_post, const float* s, const float* w_pre,
+                       const void* dr, const void* dh,
+                       void* dy, void* dx, void* dz, float* dw_post, float* ds, float* dw_pre,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace kda_block_norm_bwd needs.  Writes *bytes; returns a kda_status. */
+int kda_block_norm_bwd_workspace_size(long long rows, int D, size_t* bytes);
+
 /* Static description of a status code (never NULL). */
 const char* kda_status_string(int status);
 
