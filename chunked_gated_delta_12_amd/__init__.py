@@ -16,6 +16,8 @@ has not been built, every call raises.
 
 Beside KDA, the gated delta rule with one decay a head, and the norms around a block:
 
+    o, S_T = kda_gdr_chunk_fwd(q, k, v, g, beta, S0, cu_seqlens=cu_seqlens)
+    grads  = kda_gdr_chunk_bwd(q, k, v, g, beta, do, S0, dS_T, cu_seqlens=cu_seqlens)
     o      = kda_gdr_step(q, k, v, g, beta, S, slots=slots)  # S updated in place
     r, h   = kda_block_norm_fwd(y, x=x, z=z, w_post=w_post, s=s, w_pre=w_pre)
     grads  = kda_block_norm_bwd(y, dr, dh, x=x, z=z, w_post=w_post, s=s, w_pre=w_pre)
@@ -84,6 +86,13 @@ def load_library(path: str = LIB_PATH):
     lib.kda_last_error.restype = ctypes.c_char_p
     lib.kda_abi_version.argtypes = []
     lib.kda_abi_version.restype = c_int
+    lib.kda_gdr_chunk_fwd.argtypes = [c_int] * 7 + [ctypes.c_float] + [vp] * 9 + [vp, c_size, vp]
+    lib.kda_gdr_chunk_fwd.restype = c_int
+    lib.kda_gdr_chunk_bwd.argtypes = [c_int] * 7 + [ctypes.c_float] + [vp] * 15 + [vp, c_size, vp]
+    lib.kda_gdr_chunk_bwd.restype = c_int
+    for fn in (lib.kda_gdr_chunk_fwd_workspace_size, lib.kda_gdr_chunk_bwd_workspace_size):
+        fn.argtypes = [c_int] * 6 + [ctypes.POINTER(c_size)]
+        fn.restype = c_int
     lib.kda_gdr_step.argtypes = [c_int] * 8 + [ctypes.c_float] + [vp] * 3 + [fp] * 3 + [vp, vp, vp, vp]
     lib.kda_gdr_step.restype = c_int
     lib.kda_block_norm_fwd.argtypes = [c_int, c_int, ctypes.c_longlong, c_int, ctypes.c_float] + [vp] * 9
@@ -377,6 +386,90 @@ def _gdr_inputs(q, k, v, g, beta, scale):
     return B, T, Hk, Hv, dk, dv, code, float(dk ** -0.5 if scale is None else scale)
 
 
+def _gdr_sequences(B, T, cu_seqlens, dev):
+    """(sequences, tokens of each or rows of all) and the shape of a state's leading axis."""
+    if cu_seqlens is None:
+        return B, T
+    if B != 1:
+        raise ValueError(f"packed sequences have a leading axis of 1, got {B}")
+    n = _dims(cu_seqlens, "cu_seqlens", 1)[0] - 1
+    _need(cu_seqlens, "cu_seqlens", torch.int32, (n + 1,), dev)
+    return n, T
+
+
+def kda_gdr_chunk_fwd_workspace_size(nseq, T, Hv, dk, dv, packed=False) -> int:
+    n = ctypes.c_size_t(0)
+    _check("kda_gdr_chunk_fwd_workspace_size",
+           load_library().kda_gdr_chunk_fwd_workspace_size(nseq, T, Hv, dk, dv, int(packed), ctypes.byref(n)))
+    return int(n.value)
+
+
+def kda_gdr_chunk_bwd_workspace_size(nseq, T, Hv, dk, dv, packed=False) -> int:
+    n = ctypes.c_size_t(0)
+    _check("kda_gdr_chunk_bwd_workspace_size",
+           load_library().kda_gdr_chunk_bwd_workspace_size(nseq, T, Hv, dk, dv, int(packed), ctypes.byref(n)))
+    return int(n.value)
+
+
+def kda_gdr_chunk_fwd(q, k, v, g, beta, S0=None, *, cu_seqlens=None, scale=None, o=None, S_T=None, want_state=True,
+                      workspace=None, stream=None):
+    """The gated delta rule with one decay a head over whole sequences.  q, k [B,T,Hk,dk],
+    v [B,T,Hv,dv] (bf16 or fp32), g (log-decay), beta [B,T,Hv] fp32, S0 [N,Hv,dk,dv] fp32 or
+    None; N = B, or with cu_seqlens [N+1] int32 (then B = 1) the packed sequences.  scale
+    defaults to dk ** -0.5.  Returns (o, S_T); S_T is None when want_state is False.  Rows of
+    no sequence are left as they were in o (zero where o is made here)."""
+    lib = load_library()
+    B, T, Hk, Hv, dk, dv, code, scale = _gdr_inputs(q, k, v, g, beta, scale)
+    dev = q.device
+    nseq, T = _gdr_sequences(B, T, cu_seqlens, dev)
+    if S0 is not None:
+        _need(S0, "S0", torch.float32, (nseq, Hv, dk, dv), dev)
+    nbytes = kda_gdr_chunk_fwd_workspace_size(nseq, T, Hv, dk, dv, cu_seqlens is not None)
+    with _On(q, stream) as st:
+        if o is None:
+            o = (torch.empty if cu_seqlens is None else torch.zeros)((B, T, Hv, dv), dtype=q.dtype, device=dev)
+        _need(o, "o", q.dtype, (B, T, Hv, dv), dev)
+        if S_T is None and want_state:
+            S_T = torch.empty((nseq, Hv, dk, dv), dtype=torch.float32, device=dev)
+        if S_T is not None:
+            _need(S_T, "S_T", torch.float32, (nseq, Hv, dk, dv), dev)
+        if workspace is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        _check("kda_gdr_chunk_fwd",
+               lib.kda_gdr_chunk_fwd(code, nseq, T, Hk, Hv, dk, dv, scale, _ptr(cu_seqlens), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
+                                     _ptr(beta), _ptr(S0), _ptr(o), _ptr(S_T), _ptr(workspace),
+                                     workspace.numel() * workspace.element_size(), st))
+    return o, S_T
+
+
+def kda_gdr_chunk_bwd(q, k, v, g, beta, do, S0=None, dS_T=None, *, cu_seqlens=None, scale=None, want_dS0=True,
+                      workspace=None, stream=None):
+    """Backward of kda_gdr_chunk_fwd for L = sum <do, o> + <dS_T, S_T>, from its inputs alone.
+    Returns a dict of dq, dk, dv (q's dtype), dg, dbeta and dS0 (fp32; dS0 None unless
+    want_dS0).  The gradients of rows of no sequence are zero."""
+    lib = load_library()
+    B, T, Hk, Hv, dk, dv, code, scale = _gdr_inputs(q, k, v, g, beta, scale)
+    dev = q.device
+    nseq, T = _gdr_sequences(B, T, cu_seqlens, dev)
+    _need(do, "do", q.dtype, (B, T, Hv, dv), dev)
+    for name, t in (("S0", S0), ("dS_T", dS_T)):
+        if t is not None:
+            _need(t, name, torch.float32, (nseq, Hv, dk, dv), dev)
+    nbytes = kda_gdr_chunk_bwd_workspace_size(nseq, T, Hv, dk, dv, cu_seqlens is not None)
+    with _On(q, stream) as st:
+        make = torch.empty_like if cu_seqlens is None else torch.zeros_like
+        d = {"dq": make(q), "dk": make(k), "dv": make(v), "dg": make(g), "dbeta": make(beta),
+             "dS0": torch.empty((nseq, Hv, dk, dv), dtype=torch.float32, device=dev) if want_dS0 else None}
+        if workspace is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        _check("kda_gdr_chunk_bwd",
+               lib.kda_gdr_chunk_bwd(code, nseq, T, Hk, Hv, dk, dv, scale, _ptr(cu_seqlens), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
+                                     _ptr(beta), _ptr(S0), _ptr(do), _ptr(dS_T), _ptr(d["dq"]), _ptr(d["dk"]), _ptr(d["dv"]),
+                                     _ptr(d["dg"]), _ptr(d["dbeta"]), _ptr(d["dS0"]), _ptr(workspace),
+                                     workspace.numel() * workspace.element_size(), st))
+    return d
+
+
 def kda_gdr_step(q, k, v, g, beta, S, *, slots=None, ntok=None, scale=None, o=None, stream=None):
     """T tokens of the gated delta rule (one decay a head) for each of B rows, the states in
     a pool updated in place.  q, k [B,T,Hk,dk], v [B,T,Hv,dv] (bf16 or fp32), g, beta
@@ -475,7 +568,8 @@ def kda_block_norm_bwd(y, dr, dh=None, *, x=None, z=None, w_post=None, s=None, w
     return d
 
 
-__all__ = ["kda_gdr_step", "kda_block_norm_fwd", "kda_block_norm_bwd", "kda_block_norm_bwd_workspace_size",
+__all__ = ["kda_gdr_chunk_fwd", "kda_gdr_chunk_bwd", "kda_gdr_chunk_fwd_workspace_size",
+           "kda_gdr_chunk_bwd_workspace_size", "kda_gdr_step", "kda_block_norm_fwd", "kda_block_norm_bwd", "kda_block_norm_bwd_workspace_size",
            "KDA_ACT_SIGMOID", "KDA_ACT_SILU", "kda_chunk_fwd", "kda_chunk_fwd_noalloc", "kda_chunk_fwd_gated", "kda_chunk_fwd_unbounded", "kda_chunk_bwd",
            "kda_chunk_bwd_workspace_size", "kda_decode_step",
            "kda_decode_step_gated", "kda_gate", "kda_chunk_fwd_workspace_size",

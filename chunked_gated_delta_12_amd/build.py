@@ -25,7 +25,8 @@ PEAKS_SOURCES = ["kda_peaks.hip"]
 SOURCES = ["kda_api.cpp", "kda_gate.hip", "kda_decode.hip", "kda_chunk.hip", "kda_map.hip", "kda_out.hip", "kda_bwd.hip", "kda_bwd2.hip", "kda_gmap.hip"]
 # the operators beside KDA (the gated delta rule with one decay a head, the block norm),
 # linked into libkda.so with the sources above
-MORE_SOURCES = ["kda_gdr_step.hip", "kda_norm.hip"]
+MORE_SOURCES = ["kda_gdr_step.hip", "kda_gdr_chunk.hip", "kda_gdr_prep.hip", "kda_gdr_chain.hip", "kda_gdr_grad.hip",
+                "kda_norm.hip"]
 ARCH = "gfx950"
 
 

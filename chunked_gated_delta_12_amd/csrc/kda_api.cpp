@@ -428,6 +428,83 @@ int kda_gdr_step(int dtype, int B, int T, int Hk, int Hv, int dk, int dv, int ns
     return ok();
 }
 
+static int check_gdr_chunk(int dtype, int nseq, int T, int Hk, int Hv, int dk, int dv, float scale, bool packed) {
+    int st = check_gdr(dtype, nseq, T, Hk, Hv, dk, dv, scale);
+    if (st) return st;
+    // chunk places times heads are workgroups of one launch
+    const int64_t slots = packed ? (int64_t)T / 64 + nseq : (int64_t)nseq * (((int64_t)T + 63) / 64);
+    if (slots > 0x7fffffffLL / Hv || (int64_t)nseq * Hv > 0x7fffffffLL / 8)
+        return fail(KDA_ERR_SHAPE, "sequences*chunks*Hv too large");
+    return KDA_OK;
+}
+
+static int gdr_workspace_size(bool bwd, int nseq, int T, int Hv, int dk, int dv, int packed, size_t* bytes) {
+    if (!bytes) return fail(KDA_ERR_NULL, "bytes is NULL");
+    int st = check_gdr_chunk(KDA_BF16, nseq, T, 1, Hv, dk, dv, 1.0f, packed != 0);
+    if (st) return st;
+    *bytes = bwd ? kda::gdr_bwd_workspace_bytes(nseq, T, Hv, dk, dv, packed != 0)
+                 : kda::gdr_fwd_workspace_bytes(nseq, T, Hv, dk, dv, packed != 0);
+    return ok();
+}
+
+int kda_gdr_chunk_fwd_workspace_size(int nseq, int T, int Hv, int dk, int dv, int packed, size_t* bytes) {
+    return gdr_workspace_size(false, nseq, T, Hv, dk, dv, packed, bytes);
+}
+
+int kda_gdr_chunk_bwd_workspace_size(int nseq, int T, int Hv, int dk, int dv, int packed, size_t* bytes) {
+    return gdr_workspace_size(true, nseq, T, Hv, dk, dv, packed, bytes);
+}
+
+int kda_gdr_chunk_fwd(int dtype, int nseq, int T, int Hk, int Hv, int dk, int dv, float scale, const int* cu_seqlens,
+                      const void* q, const void* k, const void* v, const float* g, const float* beta, const float* S0,
+                      void* o, float* S_T, void* workspace, size_t workspace_bytes, void* stream) {
+    int st = check_gdr_chunk(dtype, nseq, T, Hk, Hv, dk, dv, scale, cu_seqlens != nullptr);
+    if (st) return st;
+    if (!q || !k || !v || !g || !beta || !o) return fail(KDA_ERR_NULL, "q, k, v, g, beta and o must be non-NULL");
+    const size_t need = kda::gdr_fwd_workspace_bytes(nseq, T, Hv, dk, dv, cu_seqlens != nullptr);
+    if (!workspace || workspace_bytes < need)
+        return fail(KDA_ERR_WORKSPACE, "workspace of %zu bytes needed, got %zu%s", need, workspace_bytes,
+                    workspace ? "" : " (NULL)");
+    const size_t es = dtype == KDA_BF16 ? 2 : 4, tok = cu_seqlens ? (size_t)T : (size_t)nseq * T;
+    const size_t sb = (size_t)nseq * Hv * dk * dv * 4;
+    const Range in[] = {rng("q", q, tok * Hk * dk * es), rng("k", k, tok * Hk * dk * es), rng("v", v, tok * Hv * dv * es),
+                        rng("g", g, tok * Hv * 4), rng("beta", beta, tok * Hv * 4),
+                        rng("cu_seqlens", cu_seqlens, ((size_t)nseq + 1) * 4), rng("S0", S0 == S_T ? nullptr : S0, sb)};
+    const Range out[] = {rng("o", o, tok * Hv * dv * es), rng("S_T", S_T, sb), rng("workspace", workspace, need)};
+    if ((st = check_ranges(in, 7, out, 3))) return st;
+    const kda::GdrCall c{dtype == KDA_F32, nseq, T, Hk, Hv, dk, dv, cu_seqlens, scale, q, k, v, g, beta, S0};
+    hipError_t e = kda::launch_gdr_fwd(c, o, S_T, workspace, reinterpret_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(KDA_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
+int kda_gdr_chunk_bwd(int dtype, int nseq, int T, int Hk, int Hv, int dk, int dv, float scale, const int* cu_seqlens,
+                      const void* q, const void* k, const void* v, const float* g, const float* beta, const float* S0,
+                      const void* dout, const float* dS_T, void* dq, void* dkk, void* dvv, float* dg, float* dbeta,
+                      float* dS0, void* workspace, size_t workspace_bytes, void* stream) {
+    int st = check_gdr_chunk(dtype, nseq, T, Hk, Hv, dk, dv, scale, cu_seqlens != nullptr);
+    if (st) return st;
+    if (!q || !k || !v || !g || !beta || !dout || !dq || !dkk || !dvv || !dg || !dbeta)
+        return fail(KDA_ERR_NULL, "q, k, v, g, beta, do and every gradient but dS0 must be non-NULL");
+    const size_t need = kda::gdr_bwd_workspace_bytes(nseq, T, Hv, dk, dv, cu_seqlens != nullptr);
+    if (!workspace || workspace_bytes < need)
+        return fail(KDA_ERR_WORKSPACE, "workspace of %zu bytes needed, got %zu%s", need, workspace_bytes,
+                    workspace ? "" : " (NULL)");
+    const size_t es = dtype == KDA_BF16 ? 2 : 4, tok = cu_seqlens ? (size_t)T : (size_t)nseq * T;
+    const size_t sb = (size_t)nseq * Hv * dk * dv * 4, nq = tok * Hk * dk * es, nv = tok * Hv * dv * es, ng = tok * Hv * 4;
+    const Range in[] = {rng("q", q, nq), rng("k", k, nq), rng("v", v, nv), rng("g", g, ng), rng("beta", beta, ng),
+                        rng("cu_seqlens", cu_seqlens, ((size_t)nseq + 1) * 4), rng("S0", S0, sb), rng("do", dout, nv),
+                        rng("dS_T", dS_T, sb)};
+    const Range out[] = {rng("dq", dq, nq), rng("dk", dkk, nq), rng("dv", dvv, nv), rng("dg", dg, ng),
+                         rng("dbeta", dbeta, ng), rng("dS0", dS0, sb), rng("workspace", workspace, need)};
+    if ((st = check_ranges(in, 9, out, 7))) return st;
+    const kda::GdrCall c{dtype == KDA_F32, nseq, T, Hk, Hv, dk, dv, cu_seqlens, scale, q, k, v, g, beta, S0};
+    hipError_t e = kda::launch_gdr_bwd(c, dout, dS_T, dq, dkk, dvv, dg, dbeta, dS0, workspace,
+                                       reinterpret_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(KDA_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
 // ---------------------------------------------------------------- block norm
 static int check_norm(int dtype, int act, long long rows, int D, float eps) {
     if (dtype != KDA_BF16 && dtype != KDA_F32) return fail(KDA_ERR_DTYPE, "unknown dtype %d", dtype);

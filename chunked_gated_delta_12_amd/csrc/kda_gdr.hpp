@@ -1,0 +1,288 @@
+// kda_gdr.hpp -- building blocks of the chunked gated delta rule with one decay a head.
+//
+// A chunk is 64 tokens.  With S the state at its start, G_t the sum of g over its tokens
+// up to t, gam = e^G, om_t = e^(G_end - G_t) and D_ts = e^(G_t - G_s):
+//     N_ts = D_ts k_t.k_s (s < t),   X = (I + N diag(beta))^-1,   e = X (V - gam (K S))
+//     P_ts = scale D_ts q_t.k_s (s <= t),   O = scale gam (Q S) + P (beta e)
+//     S'   = gam_end S + K^T (om beta e)
+// and backwards, dS' being the gradient at the chunk's end:
+//     dU = P^T dO + om (K dS'),   Z = X^T (beta dU) = dV
+//     dS = gam_end dS' + scale Q^T (gam dO) - K^T (gam Z)
+// No factor exceeds one for g <= 0, so the decay needs no bound.
+//
+// Precision: q, k, v and do enter the bf16 matrix cores as they are.  Every other
+// operand (X, P, S, e, Z, ...) is an fp32 value split into an upper and a lower bf16
+// half, x = hi + lo up to 2^-18 |x|, and a product is the sum of the halves' products
+// without lo*lo: two matrix instructions against an exact operand, three against a
+// split one.  One rounding to bf16 instead (2^-9) would leave o within its own
+// rounding but the fp32 state and the fp32 gradients of g and beta at 3e-3.
+// In fp32 storage all of it runs on the fp32 matrix cores.
+//
+// Operands live in LDS and in the workspace as fragment blocks of 16 rows by 32 columns
+// of the contraction: lane (g, r) = 16 g + r holds row r and its eight slots of group g
+// contiguously, so reads are 16 bytes a lane without bank conflicts.  Two slot maps:
+//   natural:      slot s of group g is column 8 g + s           (rows of q, k: channels)
+//   accumulator:  slot s < 4 is column 4 g + s, s >= 4 is 16 + 4 g + (s - 4), which is what
+//                 two accumulator tiles hold in place           (tokens, and dv columns)
+// A state's accumulator tile t = 2 b + h holds in row 4 g + i channel 32 b + 8 g + 4 h + i:
+// with that, pairs of its tiles are B operands of the natural map.
+#pragma once
+
+#include "kda_device.hpp"
+
+namespace kda {
+namespace gdr {
+
+constexpr int C = 64;                   // tokens a chunk
+constexpr int MT = 4;                   // 16-token tiles a chunk
+constexpr int SPB = 2048;               // bytes of a fragment block of fp32 values, split or not
+constexpr int TRI = 6;                  // blocks of a triangular 64 x 64 operand that are not zero
+constexpr int TRI_BYTES = TRI * SPB;
+
+typedef short s16x4 __attribute__((__vector_size__(8)));
+typedef uint32_t u32x4 __attribute__((__vector_size__(16)));
+
+// Blocks (m, kb) of a lower triangular operand: kb <= m / 2; of an upper one: kb >= m / 2.
+__host__ __device__ constexpr int lower_block(int m, int kb) { return m < 2 ? m : 2 + 2 * (m - 2) + kb; }
+__host__ __device__ constexpr int upper_block(int m, int kb) { return m < 2 ? 2 * m + kb : 4 + (m - 2); }
+
+// What a call works on.  Sequences either all have T tokens (cu NULL; rows are [nseq][T])
+// or are packed into T rows, sequence n from cu[n] to cu[n + 1].
+struct Args {
+    int nseq, T, Hk, Hv, dv;
+    const int* cu;
+    float scale;
+};
+
+// A sequence's rows; its chunks' places in the workspace start at `slot`.  Offsets are
+// held to [0, T] and to their order, so that none reads or writes past the tensors.
+struct Seq {
+    int64_t row0;
+    int len, slot;
+};
+
+__device__ __forceinline__ Seq seq_of(const Args& a, int n) {
+    if (!a.cu) return Seq{(int64_t)n * a.T, a.T, (int)((int64_t)n * ((a.T + (int64_t)C - 1) / C))};
+    int lo = a.cu[n], hi = a.cu[n + 1];
+    lo = lo < 0 ? 0 : lo > a.T ? a.T : lo;
+    hi = hi < lo ? lo : hi > a.T ? a.T : hi;
+    return Seq{lo, hi - lo, lo / C + n};
+}
+
+// The workspace's chunk places of a call: ceil(len / 64) of each sequence at most.
+inline int64_t slots_of(int nseq, int T, bool packed) {
+    return packed ? (int64_t)T / C + nseq : (int64_t)nseq * (((int64_t)T + C - 1) / C);
+}
+
+// The chunk at a place of the workspace; n < 0: none is there.
+struct Chunk {
+    int n, c, valid;
+    int64_t row0;
+};
+
+__device__ __forceinline__ Chunk chunk_at(const Args& a, int slot, int lane) {
+    int n;
+    if (!a.cu) {
+        n = (int)(slot / (int)((a.T + (int64_t)C - 1) / C));
+    } else {   // places rise with the sequence: count those that start at or before this one
+        int cnt = 0;
+        for (int n0 = 0; n0 < a.nseq; n0 += 64) {
+            bool le = false;
+            if (n0 + lane < a.nseq) le = seq_of(a, n0 + lane).slot <= slot;
+            const int k = __popcll(__ballot(le));
+            cnt += k;
+            if (k < 64) break;
+        }
+        n = cnt - 1;
+    }
+    if (n < 0) return Chunk{-1, 0, 0, 0};
+    const Seq s = seq_of(a, n);
+    const int c = slot - s.slot;
+    if (c < 0 || (int64_t)c * C >= s.len) return Chunk{-1, 0, 0, 0};
+    const int left = s.len - c * C;
+    return Chunk{n, c, left < C ? left : C, s.row0 + (int64_t)c * C};
+}
+
+// ---------------------------------------------------------------- operands
+template <typename E> struct Arith;
+
+template <> struct Arith<bf16> {
+    typedef bf16x8 Ex;                        // an operand that is exact in bf16
+    struct Sp { bf16x8 hi, lo; };             // an fp32 operand in two halves
+    static constexpr int EXB = 1024;          // bytes of an exact block
+    static __device__ __forceinline__ Sp split(f32x4 a, f32x4 b) {
+        Sp s;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s.hi[i] = (bf16)a[i];
+            s.hi[4 + i] = (bf16)b[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s.lo[i] = (bf16)(a[i] - (float)s.hi[i]);
+            s.lo[4 + i] = (bf16)(b[i] - (float)s.hi[4 + i]);
+        }
+        return s;
+    }
+    static __device__ __forceinline__ f32x4 mma(Ex a, Ex b, f32x4 c) { return mfma_k32(a, b, c); }
+    static __device__ __forceinline__ f32x4 mma(Ex a, const Sp& b, f32x4 c) { return mfma_k32(a, b.hi, mfma_k32(a, b.lo, c)); }
+    static __device__ __forceinline__ f32x4 mma(const Sp& a, Ex b, f32x4 c) { return mfma_k32(a.hi, b, mfma_k32(a.lo, b, c)); }
+    static __device__ __forceinline__ f32x4 mma(const Sp& a, const Sp& b, f32x4 c) {
+        return mfma_k32(a.hi, b.hi, mfma_k32(a.hi, b.lo, mfma_k32(a.lo, b.hi, c)));
+    }
+    static __device__ __forceinline__ Ex ld_ex(const char* base, int blk, int lane) {
+        return *reinterpret_cast<const bf16x8*>(base + blk * EXB + lane * 16);
+    }
+    static __device__ __forceinline__ Sp ld_sp(const char* base, int blk, int lane) {
+        const char* p = base + blk * SPB + lane * 16;
+        return Sp{*reinterpret_cast<const bf16x8*>(p), *reinterpret_cast<const bf16x8*>(p + 1024)};
+    }
+    static __device__ __forceinline__ void st_sp(char* base, int blk, int lane, const Sp& s) {
+        char* p = base + blk * SPB + lane * 16;
+        *reinterpret_cast<bf16x8*>(p) = s.hi;
+        *reinterpret_cast<bf16x8*>(p + 1024) = s.lo;
+    }
+    // Eight natural slots of a row in global memory.
+    static __device__ __forceinline__ Ex ld_row(const bf16* p) { return *reinterpret_cast<const bf16x8*>(p); }
+    // Eight accumulator slots of a row: columns 4g.. and 16 + 4g.. from p = row + 4 g.
+    static __device__ __forceinline__ Ex ld_row_acc(const bf16* p) { return cat8(ld_b4(p), ld_b4(p + 16)); }
+    // Four rows by 16 columns read transposed: lane r of a group of 16 gives the address of
+    // row r >> 2, columns 4 (r & 3).., and receives column r of the four rows.
+    static __device__ __forceinline__ bf16x4 ld_tr(const char* p) {
+        typedef __attribute__((address_space(3))) s16x4* L;
+        return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((L)(__attribute__((address_space(3))) void*)p));
+    }
+    // Rows of a natural-map block set [token tile][kb], transposed: channel tile 2 kb + h as
+    // rows, the 32 tokens of block tb as accumulator slots.
+    template <int KB>
+    static __device__ __forceinline__ Ex ld_ex_t(const char* base, int kb, int h, int tb, int g, int r) {
+        const int at = ((r & 3) * 16 + 4 * g + (r >> 2)) * 16 + h * 8;
+        return cat8(ld_tr(base + ((2 * tb) * KB + kb) * EXB + at), ld_tr(base + ((2 * tb + 1) * KB + kb) * EXB + at));
+    }
+    // Tokens 16 m + 4 g + i of column col + r of a row-major tile with `ld` columns.
+    static __device__ __forceinline__ f32x4 ld_col(const char* base, int ld, int m, int col, int g, int r) {
+        const bf16x4 x = ld_tr(base + ((16 * m + 4 * g + (r >> 2)) * ld + col + 4 * (r & 3)) * 2);
+        return f32x4{(float)x[0], (float)x[1], (float)x[2], (float)x[3]};
+    }
+    static __device__ __forceinline__ Ex cols(f32x4 a, f32x4 b) {
+        return Ex{(bf16)a[0], (bf16)a[1], (bf16)a[2], (bf16)a[3], (bf16)b[0], (bf16)b[1], (bf16)b[2], (bf16)b[3]};
+    }
+    // Column n = r of the 32 x 16 matrix that picks slot `s` of group `grp`.
+    static __device__ __forceinline__ Ex pick(int s, bool here) {
+        Ex x;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = (bf16)(here && i == s ? 1.0f : 0.0f);
+        return x;
+    }
+    // a's rows, transposed through the product with a picking matrix (exact), as half a
+    // block of accumulator slots; returns the values.
+    static __device__ __forceinline__ f32x4 put_t(char* blk, int lane, int half, const Sp& a, Ex j) {
+        const f32x4 z = {0, 0, 0, 0};
+        const f32x4 hi = mfma_k32(a.hi, j, z), lo = mfma_k32(a.lo, j, z);
+        char* p = blk + lane * 16 + half * 8;
+        *reinterpret_cast<bf16x4*>(p) = bf16x4{(bf16)hi[0], (bf16)hi[1], (bf16)hi[2], (bf16)hi[3]};
+        *reinterpret_cast<bf16x4*>(p + 1024) = bf16x4{(bf16)lo[0], (bf16)lo[1], (bf16)lo[2], (bf16)lo[3]};
+        return f32x4{hi[0] + lo[0], hi[1] + lo[1], hi[2] + lo[2], hi[3] + lo[3]};
+    }
+    static __device__ __forceinline__ float at(Ex x, int i) { return (float)x[i]; }
+    static __device__ __forceinline__ float dot(const Sp& x, const Sp& y) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += ((float)x.hi[i] + (float)x.lo[i]) * ((float)y.hi[i] + (float)y.lo[i]);
+        return s;
+    }
+    static __device__ __forceinline__ void st4(bf16* p, f32x4 x) {
+        *reinterpret_cast<bf16x4*>(p) = bf16x4{(bf16)x[0], (bf16)x[1], (bf16)x[2], (bf16)x[3]};
+    }
+};
+
+template <> struct Arith<float> {
+    struct Ex { f32x4 a, b; };
+    typedef Ex Sp;
+    static constexpr int EXB = SPB;
+    static __device__ __forceinline__ Sp split(f32x4 a, f32x4 b) { return Sp{a, b}; }
+    static __device__ __forceinline__ f32x4 mma(const Ex& x, const Ex& y, f32x4 c) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c = mfma_k4(x.a[i], y.a[i], c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c = mfma_k4(x.b[i], y.b[i], c);
+        return c;
+    }
+    // a block is two planes of 16 bytes a lane: slots 0..3 and 4..7
+    static __device__ __forceinline__ Ex ld_ex(const char* base, int blk, int lane) {
+        const char* p = base + blk * SPB + lane * 16;
+        return Ex{*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 1024)};
+    }
+    static __device__ __forceinline__ Sp ld_sp(const char* base, int blk, int lane) { return ld_ex(base, blk, lane); }
+    static __device__ __forceinline__ void st_sp(char* base, int blk, int lane, const Sp& s) {
+        char* p = base + blk * SPB + lane * 16;
+        *reinterpret_cast<f32x4*>(p) = s.a;
+        *reinterpret_cast<f32x4*>(p + 1024) = s.b;
+    }
+    static __device__ __forceinline__ Ex ld_row(const float* p) {
+        return Ex{*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 4)};
+    }
+    static __device__ __forceinline__ Ex ld_row_acc(const float* p) {
+        return Ex{*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 16)};
+    }
+    template <int KB>
+    static __device__ __forceinline__ Ex ld_ex_t(const char* base, int kb, int h, int tb, int g, int r) {
+        Ex x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = h * 1024 + ((r >> 2) * 16 + 4 * g + i) * 16 + (r & 3) * 4;
+            x.a[i] = *reinterpret_cast<const float*>(base + ((2 * tb) * KB + kb) * SPB + at);
+            x.b[i] = *reinterpret_cast<const float*>(base + ((2 * tb + 1) * KB + kb) * SPB + at);
+        }
+        return x;
+    }
+    static __device__ __forceinline__ f32x4 ld_col(const char* base, int ld, int m, int col, int g, int r) {
+        const float* p = reinterpret_cast<const float*>(base) + (16 * m + 4 * g) * ld + col + r;
+        return f32x4{p[0], p[ld], p[2 * ld], p[3 * ld]};
+    }
+    static __device__ __forceinline__ Ex cols(f32x4 a, f32x4 b) { return Ex{a, b}; }
+    static __device__ __forceinline__ Ex pick(int s, bool here) {
+        Ex x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x.a[i] = here && i == s ? 1.0f : 0.0f;
+            x.b[i] = here && 4 + i == s ? 1.0f : 0.0f;
+        }
+        return x;
+    }
+    static __device__ __forceinline__ f32x4 put_t(char* blk, int lane, int half, const Sp& a, const Ex& j) {
+        const f32x4 x = mma(a, j, f32x4{0, 0, 0, 0});
+        *reinterpret_cast<f32x4*>(blk + half * 1024 + lane * 16) = x;
+        return x;
+    }
+    static __device__ __forceinline__ float at(const Ex& x, int i) { return i < 4 ? x.a[i & 3] : x.b[i & 3]; }
+    static __device__ __forceinline__ float dot(const Sp& x, const Sp& y) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s += x.a[i] * y.a[i] + x.b[i] * y.b[i];
+        return s;
+    }
+    static __device__ __forceinline__ void st4(float* p, f32x4 x) { *reinterpret_cast<f32x4*>(p) = x; }
+};
+
+// The picking matrix of put_t for half h of a block: slot 4 h + (r & 3) of group r >> 2.  In
+// an accumulator-map block of tokens that is token 16 h + r; in a natural-map block of
+// channels it is the channel that row r of accumulator tile h holds.
+template <typename E>
+__device__ __forceinline__ typename Arith<E>::Ex pick_half(int h, int g, int r) {
+    return Arith<E>::pick(4 * h + (r & 3), (r >> 2) == g);
+}
+
+// ---------------------------------------------------------------- workspace
+// A chunk of one head: X and P (and for the backward pass their transposes) as split
+// blocks, then for the backward pass G in 64 bits, then gam and om.
+__host__ __device__ constexpr int64_t prep_bytes(bool bwd) {
+    return (bwd ? 4 * (int64_t)TRI_BYTES + C * 8 : 2 * (int64_t)TRI_BYTES) + 2 * C * 4;
+}
+// The backward pass's records of a chunk of one head: a state (dk / 16 by dv / 32 blocks,
+// rows channels in the order of the accumulator tiles) and a 64 x dv operand (4 by dv / 32 blocks, rows tokens).
+__host__ __device__ constexpr int64_t state_bytes(int dk, int dv) { return (int64_t)(dk / 16) * (dv / 32) * SPB; }
+__host__ __device__ constexpr int64_t rows_bytes(int dv) { return (int64_t)MT * (dv / 32) * SPB; }
+
+}  // namespace gdr
+}  // namespace kda

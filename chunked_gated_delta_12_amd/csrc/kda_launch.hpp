@@ -119,6 +119,22 @@ hipError_t launch_gdr_step(bool f32, int B, int T, int Hk, int Hv, int dk, int d
                            const void* q, const void* k, const void* v, const float* g, const float* beta, float* S,
                            const int* slots, const int* ntok, void* o, hipStream_t stream);
 
+// The chunked gated delta rule with one decay a head (kda_gdr_chunk.hip).  Sequences of T
+// tokens each (cu NULL) or packed into T rows.
+struct GdrCall {
+    bool f32;
+    int nseq, T, Hk, Hv, dk, dv;
+    const int* cu;
+    float scale;
+    const void *q, *k, *v;
+    const float *g, *beta, *S0;
+};
+size_t gdr_fwd_workspace_bytes(int nseq, int T, int Hv, int dk, int dv, bool packed);
+size_t gdr_bwd_workspace_bytes(int nseq, int T, int Hv, int dk, int dv, bool packed);
+hipError_t launch_gdr_fwd(const GdrCall& c, void* o, float* S_T, void* workspace, hipStream_t stream);
+hipError_t launch_gdr_bwd(const GdrCall& c, const void* dout, const float* dS_T, void* dq, void* dk, void* dv, float* dg,
+                          float* dbeta, float* dS0, void* workspace, hipStream_t stream);
+
 // The block norm and its backward (kda_norm.hip): x, z, w_post, s, w_pre, dr and dh may
 // be NULL (h and dh go with w_pre), and so may every gradient but dy.  part:
 // norm_bwd_workspace_bytes, or unused when no weight's gradient is asked for.

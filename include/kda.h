@@ -298,6 +298,58 @@ int kda_gate(int B, int T, int H, int dk, const float* theta, float* g, float* g
  * ------------------------------------------------------------------------- */
 
 /* ---------------------------------------------------------------------------
+ * kda_gdr_chunk_fwd: the rule over whole sequences in chunks of 64 tokens (prefill,
+ * training), from a start state to a last state.
+ *
+ *   nseq, T      cu_seqlens NULL: nseq sequences of T tokens each, tensors [nseq, T, ...].
+ *                Otherwise the sequences are packed into T rows, tensors [T, ...].
+ *   cu_seqlens   [nseq + 1] int32, read on the device: sequence n has the rows from
+ *                cu_seqlens[n] up to cu_seqlens[n + 1].  Offsets rise from at least 0
+ *                to at most T; equal ones are a sequence of no tokens, whose S_T is its
+ *                S0.  Rows of no sequence are neither read nor written.  Offsets out of order
+ *                or range are held to both, so nothing outside the tensors is touched; the
+ *                results are then unspecified.
+ *   q, k         [.., Hk, dk]  dtype
+ *   v            [.., Hv, dv]  dtype
+ *   g, beta      [.., Hv]      fp32
+ *   S0           [nseq, Hv, dk, dv]  fp32, or NULL for zero
+ *   o            [.., Hv, dv]  dtype, written
+ *   S_T          [nseq, Hv, dk, dv]  fp32, written; or NULL to skip.  May be S0 itself.
+ *   workspace    kda_gdr_chunk_fwd_workspace_size bytes; contents on entry do not matter
+ *   Any other overlap of an output with an input, an output or the workspace is rejected.
+ * Returns a kda_status.
+ * ------------------------------------------------------------------------- */
+int kda_gdr_chunk_fwd(int dtype, int nseq, int T, int Hk, int Hv, int dk, int dv, float scale,
+                      const int* cu_seqlens, const void* q, const void* k, const void* v,
+                      const float* g, const float* beta, const float* S0, void* o, float* S_T,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * kda_gdr_chunk_bwd: gradients of L = sum <do, o> + <dS_T, S_T> with respect to q, k, v,
+ * g, beta and S0, from the forward's inputs (nothing of it is saved).
+ *
+ *   do           as o;  dS_T  as S_T, or NULL for zero
+ *   dq, dk       as q, summed over the value heads of a key head; dv as v: dtype, written
+ *   dg, dbeta    as g, fp32, written
+ *   dS0          as S0, fp32, written; or NULL to skip
+ *   workspace    kda_gdr_chunk_bwd_workspace_size bytes (at dk = dv = 128 240 KB a chunk
+ *                of 64 tokens and value head)
+ *   Every other argument is that of kda_gdr_chunk_fwd; no output may overlap anything.
+ * Returns a kda_status.
+ * ------------------------------------------------------------------------- */
+int kda_gdr_chunk_bwd(int dtype, int nseq, int T, int Hk, int Hv, int dk, int dv, float scale,
+                      const int* cu_seqlens, const void* q, const void* k, const void* v,
+                      const float* g, const float* beta, const float* S0,
+                      const void* do_, const float* dS_T,
+                      void* dq, void* dk_, void* dv_, float* dg, float* dbeta, float* dS0,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of the two calls; packed: whether cu_seqlens is given.  Writes *bytes;
+ * returns a kda_status. */
+int kda_gdr_chunk_fwd_workspace_size(int nseq, int T, int Hv, int dk, int dv, int packed, size_t* bytes);
+int kda_gdr_chunk_bwd_workspace_size(int nseq, int T, int Hv, int dk, int dv, int packed, size_t* bytes);
+
+/* ---------------------------------------------------------------------------
  * kda_gdr_step: T tokens of the rule for each of B rows, from and to a state in a
  * pool, in place (decode: T = 1; proposed tokens: T of a few).  The state is read
  * and written once a call.
