@@ -435,6 +435,10 @@ static int check_gdr_chunk(int dtype, int nseq, int T, int Hk, int Hv, int dk, i
     const int64_t slots = packed ? (int64_t)T / 64 + nseq : (int64_t)nseq * (((int64_t)T + 63) / 64);
     if (slots > 0x7fffffffLL / Hv || (int64_t)nseq * Hv > 0x7fffffffLL / 8)
         return fail(KDA_ERR_SHAPE, "sequences*chunks*Hv too large");
+    // a chunk of one tensor, 64*H*d*4 bytes at most, is addressed with 32-bit offsets
+    if ((int64_t)Hk * dk >= (1LL << 23) || (int64_t)Hv * dv >= (1LL << 23))
+        return fail(KDA_ERR_SHAPE, "Hk*dk=%lld or Hv*dv=%lld too large (256*H*d must stay below 2^31)", (long long)Hk * dk,
+                    (long long)Hv * dv);
     return KDA_OK;
 }
 

@@ -54,53 +54,95 @@ struct Args {
     float scale;
 };
 
-// A sequence's rows; its chunks' places in the workspace start at `slot`.  Offsets are
-// held to [0, T] and to their order, so that none reads or writes past the tensors.
+// Units of `unit` tokens have places in the workspace: those of sequence n from place_of(n) on.
+// Packed, floor(first row / unit) + n leaves room for a part unit a sequence.
+__device__ __forceinline__ int place_of(const Args& a, int n, int64_t unit) {
+    if (!a.cu) return (int)((int64_t)n * ((a.T + unit - 1) / unit));
+    int lo = a.cu[n];
+    lo = lo < 0 ? 0 : lo > a.T ? a.T : lo;
+    return (int)(lo / unit) + n;
+}
+__host__ __device__ inline int64_t places_of(int nseq, int T, bool packed, int64_t unit) {
+    return packed ? (int64_t)T / unit + nseq : (int64_t)nseq * (((int64_t)T + unit - 1) / unit);
+}
+
+// A sequence's rows (n the same for the wavefront).  Offsets are held to [0, T] and to their
+// order, so that none reads or writes past the tensors.
 struct Seq {
     int64_t row0;
-    int len, slot;
+    int len;
 };
-
 __device__ __forceinline__ Seq seq_of(const Args& a, int n) {
-    if (!a.cu) return Seq{(int64_t)n * a.T, a.T, (int)((int64_t)n * ((a.T + (int64_t)C - 1) / C))};
-    int lo = a.cu[n], hi = a.cu[n + 1];
+    if (!a.cu) return Seq{(int64_t)n * a.T, a.T};
+    int lo = __builtin_amdgcn_readfirstlane(a.cu[n]), hi = __builtin_amdgcn_readfirstlane(a.cu[n + 1]);
     lo = lo < 0 ? 0 : lo > a.T ? a.T : lo;
     hi = hi < lo ? lo : hi > a.T ? a.T : hi;
-    return Seq{lo, hi - lo, lo / C + n};
+    return Seq{lo, hi - lo};
 }
 
-// The workspace's chunk places of a call: ceil(len / 64) of each sequence at most.
-inline int64_t slots_of(int nseq, int T, bool packed) {
-    return packed ? (int64_t)T / C + nseq : (int64_t)nseq * (((int64_t)T + C - 1) / C);
-}
-
-// The chunk at a place of the workspace; n < 0: none is there.
-struct Chunk {
-    int n, c, valid;
-    int64_t row0;
+// The sequence whose places hold `place`, and which of its units it is; n < 0: none.
+struct Unit {
+    int n, i;
 };
-
-__device__ __forceinline__ Chunk chunk_at(const Args& a, int slot, int lane) {
+__device__ __forceinline__ Unit unit_at(const Args& a, int place, int64_t unit, int lane) {
     int n;
     if (!a.cu) {
-        n = (int)(slot / (int)((a.T + (int64_t)C - 1) / C));
+        n = (int)(place / ((a.T + unit - 1) / unit));
     } else {   // places rise with the sequence: count those that start at or before this one
         int cnt = 0;
         for (int n0 = 0; n0 < a.nseq; n0 += 64) {
-            bool le = false;
-            if (n0 + lane < a.nseq) le = seq_of(a, n0 + lane).slot <= slot;
+            const bool le = n0 + lane < a.nseq && place_of(a, n0 + lane, unit) <= place;
             const int k = __popcll(__ballot(le));
             cnt += k;
             if (k < 64) break;
         }
         n = cnt - 1;
     }
-    if (n < 0) return Chunk{-1, 0, 0, 0};
-    const Seq s = seq_of(a, n);
-    const int c = slot - s.slot;
-    if (c < 0 || (int64_t)c * C >= s.len) return Chunk{-1, 0, 0, 0};
-    const int left = s.len - c * C;
-    return Chunk{n, c, left < C ? left : C, s.row0 + (int64_t)c * C};
+    if (n < 0) return Unit{-1, 0};
+    return Unit{n, place - __builtin_amdgcn_readfirstlane(place_of(a, n, unit))};
+}
+
+// The chunk at a place of 64-token units; n < 0: none is there.
+struct Chunk {
+    int n, c, valid;
+    int64_t row0;
+};
+__device__ __forceinline__ Chunk chunk_at(const Args& a, int place, int lane) {
+    const Unit u = unit_at(a, place, C, lane);
+    if (u.n < 0 || u.i < 0) return Chunk{-1, 0, 0, 0};
+    const Seq s = seq_of(a, u.n);
+    if ((int64_t)u.i * C >= s.len) return Chunk{-1, 0, 0, 0};
+    const int left = s.len - u.i * C;
+    return Chunk{u.n, u.i, left < C ? left : C, s.row0 + (int64_t)u.i * C};
+}
+
+// Segments: a sequence of more than `over` chunks is walked in pieces of `seg` chunks, joined
+// by their affine maps; others in one piece.  seg = 0: none is cut.
+struct Segs {
+    int seg, over;
+};
+__host__ __device__ inline int64_t seg_unit(const Segs& g) { return g.seg ? (int64_t)g.seg * C : (int64_t)1 << 40; }
+
+// The piece at a place of seg_unit tokens: chunks [c0, c1) of sequence n, piece i of cnt.
+struct Piece {
+    int n, i, cnt, c0, c1;
+    int slot;       // the sequence's first place among the chunks
+    Seq s;
+};
+__device__ __forceinline__ Piece piece_at(const Args& a, const Segs& sg, int place, int lane) {
+    const Unit u = unit_at(a, place, seg_unit(sg), lane);
+    Piece p{-1, 0, 0, 0, 0, 0, Seq{0, 0}};
+    if (u.n < 0 || u.i < 0) return p;
+    p.s = seq_of(a, u.n);
+    const int nch = (int)(((int64_t)p.s.len + C - 1) / C);
+    p.cnt = sg.seg && nch > sg.over ? (nch + sg.seg - 1) / sg.seg : 1;
+    if (u.i >= p.cnt) return p;
+    p.n = u.n;
+    p.i = u.i;
+    p.c0 = p.cnt > 1 ? u.i * sg.seg : 0;
+    p.c1 = p.cnt > 1 && u.i + 1 < p.cnt ? p.c0 + sg.seg : nch;
+    p.slot = __builtin_amdgcn_readfirstlane(place_of(a, u.n, C));
+    return p;
 }
 
 // ---------------------------------------------------------------- operands
@@ -175,14 +217,14 @@ template <> struct Arith<bf16> {
         return x;
     }
     // a's rows, transposed through the product with a picking matrix (exact), as half a
-    // block of accumulator slots; returns the values.
-    static __device__ __forceinline__ f32x4 put_t(char* blk, int lane, int half, const Sp& a, Ex j) {
+    // block of accumulator slots at byte `blk` of the record; returns the values.
+    static __device__ __forceinline__ uint32_t half_at(int lane, int half) { return (uint32_t)(lane * 16 + half * 8); }
+    static __device__ __forceinline__ f32x4 put_t(Rsrc rec, uint32_t blk, const Sp& a, Ex j) {
         const f32x4 z = {0, 0, 0, 0};
         const f32x4 hi = mfma_k32(a.hi, j, z), lo = mfma_k32(a.lo, j, z);
-        char* p = blk + lane * 16 + half * 8;
-        *reinterpret_cast<bf16x4*>(p) = bf16x4{(bf16)hi[0], (bf16)hi[1], (bf16)hi[2], (bf16)hi[3]};
-        *reinterpret_cast<bf16x4*>(p + 1024) = bf16x4{(bf16)lo[0], (bf16)lo[1], (bf16)lo[2], (bf16)lo[3]};
-        return f32x4{hi[0] + lo[0], hi[1] + lo[1], hi[2] + lo[2], hi[3] + lo[3]};
+        buf_st_quad(q4(hi), rec, blk);
+        buf_st_quad(q4(lo), rec, blk + 1024);
+        return hi + lo;
     }
     static __device__ __forceinline__ float at(Ex x, int i) { return (float)x[i]; }
     static __device__ __forceinline__ float dot(const Sp& x, const Sp& y) {
@@ -190,6 +232,15 @@ template <> struct Arith<bf16> {
 #pragma unroll
         for (int i = 0; i < 8; ++i) s += ((float)x.hi[i] + (float)x.lo[i]) * ((float)y.hi[i] + (float)y.lo[i]);
         return s;
+    }
+    typedef bf16x4 Q4;
+    static __device__ __forceinline__ Q4 q4(f32x4 x) { return Q4{(bf16)x[0], (bf16)x[1], (bf16)x[2], (bf16)x[3]}; }
+    // One accumulator tile as half a split block.
+    static __device__ __forceinline__ void put_half(char* base, int blk, int lane, int half, f32x4 x) {
+        char* p = base + blk * SPB + lane * 16 + half * 8;
+        const bf16x4 hi = q4(x);
+        *reinterpret_cast<bf16x4*>(p) = hi;
+        *reinterpret_cast<bf16x4*>(p + 1024) = q4(f32x4{x[0] - (float)hi[0], x[1] - (float)hi[1], x[2] - (float)hi[2], x[3] - (float)hi[3]});
     }
     static __device__ __forceinline__ void st4(bf16* p, f32x4 x) {
         *reinterpret_cast<bf16x4*>(p) = bf16x4{(bf16)x[0], (bf16)x[1], (bf16)x[2], (bf16)x[3]};
@@ -250,9 +301,10 @@ template <> struct Arith<float> {
         }
         return x;
     }
-    static __device__ __forceinline__ f32x4 put_t(char* blk, int lane, int half, const Sp& a, const Ex& j) {
+    static __device__ __forceinline__ uint32_t half_at(int lane, int half) { return (uint32_t)(half * 1024 + lane * 16); }
+    static __device__ __forceinline__ f32x4 put_t(Rsrc rec, uint32_t blk, const Sp& a, const Ex& j) {
         const f32x4 x = mma(a, j, f32x4{0, 0, 0, 0});
-        *reinterpret_cast<f32x4*>(blk + half * 1024 + lane * 16) = x;
+        buf_st_quad(x, rec, blk);
         return x;
     }
     static __device__ __forceinline__ float at(const Ex& x, int i) { return i < 4 ? x.a[i & 3] : x.b[i & 3]; }
@@ -261,6 +313,11 @@ template <> struct Arith<float> {
 #pragma unroll
         for (int i = 0; i < 4; ++i) s += x.a[i] * y.a[i] + x.b[i] * y.b[i];
         return s;
+    }
+    typedef f32x4 Q4;
+    static __device__ __forceinline__ Q4 q4(f32x4 x) { return x; }
+    static __device__ __forceinline__ void put_half(char* base, int blk, int lane, int half, f32x4 x) {
+        *reinterpret_cast<f32x4*>(base + blk * SPB + half * 1024 + lane * 16) = x;
     }
     static __device__ __forceinline__ void st4(float* p, f32x4 x) { *reinterpret_cast<f32x4*>(p) = x; }
 };
@@ -274,11 +331,14 @@ __device__ __forceinline__ typename Arith<E>::Ex pick_half(int h, int g, int r) 
 }
 
 // ---------------------------------------------------------------- workspace
-// A chunk of one head: X and P (and for the backward pass their transposes) as split
-// blocks, then for the backward pass G in 64 bits, then gam and om.
+// A chunk of one head.  Forward: X and P diag(beta) as split blocks, then gam and om beta.
+// Backward: X, X^T and diag(beta) P^T, then gam, om beta and om, and G log2(e) in 64 bits.
 __host__ __device__ constexpr int64_t prep_bytes(bool bwd) {
-    return (bwd ? 4 * (int64_t)TRI_BYTES + C * 8 : 2 * (int64_t)TRI_BYTES) + 2 * C * 4;
+    return bwd ? 3 * (int64_t)TRI_BYTES + 3 * C * 4 + C * 8 : 2 * (int64_t)TRI_BYTES + 2 * C * 4;
 }
+__host__ __device__ constexpr int64_t prep_factors(bool bwd) { return (bwd ? 3 : 2) * (int64_t)TRI_BYTES; }
+// The map of a piece of one head, [dk][dv + dk] fp32: N, then M.
+__host__ __device__ constexpr int64_t map_bytes(int dk, int dv) { return (int64_t)dk * (dv + dk) * 4; }
 // The backward pass's records of a chunk of one head: a state (dk / 16 by dv / 32 blocks,
 // rows channels in the order of the accumulator tiles) and a 64 x dv operand (4 by dv / 32 blocks, rows tokens).
 __host__ __device__ constexpr int64_t state_bytes(int dk, int dv) { return (int64_t)(dk / 16) * (dv / 32) * SPB; }

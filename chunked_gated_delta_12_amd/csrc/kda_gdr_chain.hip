@@ -1,19 +1,23 @@
 // kda_gdr_chain.hip -- the chunked gated delta rule's walk over a sequence's chunks: the
-// states forwards (with the outputs, or saving each chunk's start state for the backward
-// pass), and the states' gradients backwards.  Mathematics, precision and layouts: kda_gdr.hpp.
+// states forwards (with the outputs, saving each chunk's start state for the backward
+// pass, or forming a piece's affine map), and the states' gradients backwards.
+// Mathematics, precision and layouts: kda_gdr.hpp.
 //
-// Columns of the state (dv) are independent.  A workgroup of four wavefronts has one head
-// of one sequence and 64 NTL columns, a wavefront 16 NTL of them: its slice of the state
+// Columns of the state (dv) are independent.  A workgroup of NW wavefronts has one head of
+// one piece of a sequence and 16 NW columns, a wavefront 16 of them: its slice of the state
 // stays in fp32 accumulators for the whole walk, and every product of a chunk takes its
 // result straight from the one before it (an accumulator tile is a B operand; read as an A
 // operand it is its transpose), so the wavefronts share nothing but the chunk's operands.
 // Those lie in LDS as fragment blocks: bf16 double-buffered, the next chunk's loads in
-// flight in registers under this chunk's products, one barrier a chunk.
-//   forwards:   Y = V - gam (K S);  e = X Y;  O^T = scale gam (S^T Q^T) + U^T P^T, U = beta e;
-//               S <- gam_end S + K^T (om U)
-//   backwards:  dU = om (K dS) + P^T dO;  Z = X^T (beta dU);
+// flight in registers under this chunk's products, one barrier a chunk.  Loads go through
+// buffer resources that end with the chunk's last token, so a part chunk reads zeros.
+//   forwards:   e = X (V - gam (K S));  S <- gam_end S + K^T (om beta e)
+//               O^T = scale gam (S^T Q^T) + e^T (P diag(beta))^T
+//   backwards:  Z = X^T (om beta (K dS) + (diag(beta) P^T) dO)
 //               dS <- gam_end dS + Q^T (scale gam dO) - K^T (gam Z)
-// K^T and Q^T are read from the same blocks as K and Q with the transposing LDS read.
+// K^T and Q^T are read from the same blocks as K and Q with the transposing LDS read.  A
+// chunk's outputs are stored at the start of the next one: behind the loads they would be
+// waited for at the loop's end.
 #include "kda_gdr.hpp"
 #include "kda_launch.hpp"
 
@@ -22,493 +26,302 @@ namespace gdr {
 
 namespace {
 
-constexpr int NW = 4;                 // wavefronts a workgroup
-constexpr int NTHR = 64 * NW;
+enum Mode { FWD, SAVE, MAP, BACK, BMAP };
 
-enum Mode { FWD, SAVE, BACK };
-
-// LDS of one buffer, and the 16-byte pieces a thread loads of each part.
-template <typename E, int DK, int NTL, int MODE>
+// LDS of one buffer: K, Q, X (or X^T), P (or P^T), the value rows and the factors.
+template <typename E, int DK, int NW, int MODE>
 struct Lay {
-    static constexpr int KB = DK / 32;
-    static constexpr int SLAB = 16 * NTL * NW;
-    static constexpr int QK = MT * KB * Arith<E>::EXB;         // K or Q
-    static constexpr bool HAS_Q = MODE != SAVE, HAS_P = MODE != SAVE;
-    static constexpr int Q_AT = QK, X_AT = Q_AT + (HAS_Q ? QK : 0), P_AT = X_AT + TRI_BYTES,
-                         V_AT = P_AT + (HAS_P ? TRI_BYTES : 0), VB = C * SLAB * (int)sizeof(E), F_AT = V_AT + VB,
-                         BYTES = F_AT + 3 * C * 4;
+    static constexpr int KB = DK / 32, NTHR = 64 * NW, SLAB = 16 * NW;
+    static constexpr bool BWD = MODE >= BACK;                      // rows of dO and P^T instead of V and P
+    static constexpr bool HAS_Q = MODE == FWD || BWD, HAS_P = HAS_Q;
+    static constexpr int QK = MT * KB * Arith<E>::EXB;
+    static constexpr int XP = (HAS_P ? 2 : 1) * TRI_BYTES;
+    // a row of values: 32 bytes more than its columns, so that the rows of a transposing read
+    // spread over the banks
+    static constexpr int VLD = SLAB + 32 / (int)sizeof(E), VROW = SLAB * (int)sizeof(E) / 16, VB = C * VLD * (int)sizeof(E);
+    static constexpr int Q_AT = QK, X_AT = Q_AT + (HAS_Q ? QK : 0), P_AT = X_AT + TRI_BYTES, V_AT = X_AT + XP, F_AT = V_AT + VB,
+                         BYTES = F_AT + 2 * C * 4;
     static constexpr int BUFS = 2 * BYTES <= 160 * 1024 ? 2 : 1;
-    static constexpr int NQK = QK / (16 * NTHR) ? QK / (16 * NTHR) : 1, NTRI = TRI_BYTES / (16 * NTHR),
-                         NV = VB / (16 * NTHR) ? VB / (16 * NTHR) : 1;
+    // 16-byte pieces, and how many of them a thread moves
+    static constexpr int PQK = QK / 16, PXP = XP / 16, PV = C * VROW;
+    static constexpr int NQK = (PQK + NTHR - 1) / NTHR, NXP = (PXP + NTHR - 1) / NTHR, NV = (PV + NTHR - 1) / NTHR;
 };
 
+__device__ __forceinline__ u32x4 buf_ld128(Rsrc s, uint32_t off) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(s, (int)off, 0, 0));
+}
+__device__ __forceinline__ f32x4 ld4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+
 // One chunk's operands on their way from global memory to LDS.
-template <typename E, int DK, int NTL, int MODE>
+template <typename E, int DK, int NW, int MODE>
 struct Stage {
-    typedef Lay<E, DK, NTL, MODE> L;
-    u32x4 k[L::NQK], q[L::NQK], x[L::NTRI], p[L::NTRI], v[L::NV];
+    typedef Lay<E, DK, NW, MODE> L;
+    u32x4 k[L::NQK], q[L::NQK], x[L::NXP], v[L::NV];
     float f;
+    uint32_t kq_off[L::NQK], v_off[L::NV];   // byte offsets in a chunk's rows, the same for every chunk
 
-    // piece u of a K or Q block set: row and channel it starts at
-    static __device__ __forceinline__ void place(int u, int& row, int& ch) {
-        const int lane = u & 63, g = lane >> 4, r = lane & 15;
-        int blk, half = 0;
-        if constexpr (sizeof(E) == 2) {
-            blk = u >> 6;
-        } else {
-            blk = u >> 7;
-            half = (u >> 6) & 1;
-        }
-        row = 16 * (blk / L::KB) + r;
-        ch = 32 * (blk % L::KB) + 8 * g + 4 * half;
-    }
-
-    // kq: rows of the key head; vv: rows of the value head from the slab's first column, ncol
-    // of them; pre: the chunk's X (or its transpose); preP: P (or its transpose); gm: gam, om
-    __device__ __forceinline__ void load(const E* kk, const E* qq, int64_t ldk, const E* vv, int64_t ldv, int ncol,
-                                         const float* bt, int ldb, const char* pre, const char* preP, const float* gm,
-                                         int valid) {
+    __device__ __forceinline__ void init(int64_t ldk, int64_t ldv, int ncol) {
         const int tid = threadIdx.x;
 #pragma unroll
         for (int j = 0; j < L::NQK; ++j) {
-            int row, ch;
-            place((tid + j * NTHR) % (L::QK / 16), row, ch);
-            row = row < valid ? row : valid - 1;
-            k[j] = *reinterpret_cast<const u32x4*>(kk + row * ldk + ch);
-            if constexpr (L::HAS_Q) q[j] = *reinterpret_cast<const u32x4*>(qq + row * ldk + ch);
+            const int u = tid + j * L::NTHR, l = u & 63;
+            const int blk = sizeof(E) == 2 ? u >> 6 : u >> 7, half = sizeof(E) == 2 ? 0 : (u >> 6) & 1;
+            const int row = 16 * (blk / L::KB) + (l & 15), ch = 32 * (blk % L::KB) + 8 * (l >> 4) + 4 * half;
+            kq_off[j] = u < L::PQK ? (uint32_t)(row * ldk + ch) * (uint32_t)sizeof(E) : 0xffffffffu;
         }
-#pragma unroll
-        for (int j = 0; j < L::NTRI; ++j) {
-            x[j] = *reinterpret_cast<const u32x4*>(pre + (tid + j * NTHR) * 16);
-            if constexpr (L::HAS_P) p[j] = *reinterpret_cast<const u32x4*>(preP + (tid + j * NTHR) * 16);
-        }
-        constexpr int EPP = 16 / (int)sizeof(E), PPR = L::SLAB / EPP;   // elements a piece, pieces a row
+        constexpr int EPP = 16 / (int)sizeof(E);
 #pragma unroll
         for (int j = 0; j < L::NV; ++j) {
-            const int u = (tid + j * NTHR) % (C * PPR);
-            int row = u / PPR, col = (u % PPR) * EPP;
-            col = col < ncol ? col : 0;   // columns past the head's end are not used
-            const bool in = row < valid;
-            row = in ? row : valid - 1;
-            v[j] = *reinterpret_cast<const u32x4*>(vv + row * ldv + col);
-            if (MODE == BACK && !in) v[j] = u32x4{0, 0, 0, 0};   // no gradient past the end
+            const int u = tid + j * L::NTHR, row = u / L::VROW, col = (u % L::VROW) * EPP;
+            v_off[j] = u < L::PV && col < ncol ? (uint32_t)(row * ldv + col) * (uint32_t)sizeof(E) : 0xffffffffu;
         }
-        f = 0.0f;
-        if (tid < 2 * C) f = gm[tid];
-        else if (tid < 3 * C && tid - 2 * C < valid) f = bt[(int64_t)(tid - 2 * C) * ldb];
+    }
+
+    __device__ __forceinline__ void load(Rsrc kr, Rsrc qr, Rsrc vr, const char* x0, const char* p0, const float* fac) {
+        const int tid = threadIdx.x;
+#pragma unroll
+        for (int j = 0; j < L::NQK; ++j) {
+            k[j] = buf_ld128(kr, kq_off[j]);
+            if constexpr (L::HAS_Q) q[j] = buf_ld128(qr, kq_off[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < L::NXP; ++j) {
+            const int u = tid + j * L::NTHR;
+            const char* p = u < TRI_BYTES / 16 ? x0 + u * 16 : p0 + (u - TRI_BYTES / 16) * 16;
+            if (L::PXP % L::NTHR == 0 || u < L::PXP) x[j] = *reinterpret_cast<const u32x4*>(p);
+        }
+#pragma unroll
+        for (int j = 0; j < L::NV; ++j) v[j] = buf_ld128(vr, v_off[j]);
+        if (L::NTHR == 2 * C || tid < 2 * C) f = fac[tid];
     }
 
     __device__ __forceinline__ void store(char* buf) const {
         const int tid = threadIdx.x;
 #pragma unroll
         for (int j = 0; j < L::NQK; ++j) {
-            const int u = tid + j * NTHR;
-            if (L::QK / 16 >= NTHR || u < L::QK / 16) {
+            const int u = tid + j * L::NTHR;
+            if (L::PQK % L::NTHR == 0 || u < L::PQK) {
                 *reinterpret_cast<u32x4*>(buf + u * 16) = k[j];
                 if constexpr (L::HAS_Q) *reinterpret_cast<u32x4*>(buf + L::Q_AT + u * 16) = q[j];
             }
         }
 #pragma unroll
-        for (int j = 0; j < L::NTRI; ++j) {
-            *reinterpret_cast<u32x4*>(buf + L::X_AT + (tid + j * NTHR) * 16) = x[j];
-            if constexpr (L::HAS_P) *reinterpret_cast<u32x4*>(buf + L::P_AT + (tid + j * NTHR) * 16) = p[j];
+        for (int j = 0; j < L::NXP; ++j) {
+            const int u = tid + j * L::NTHR;
+            if (L::PXP % L::NTHR == 0 || u < L::PXP) *reinterpret_cast<u32x4*>(buf + L::X_AT + u * 16) = x[j];
         }
 #pragma unroll
-        for (int j = 0; j < L::NV; ++j) *reinterpret_cast<u32x4*>(buf + L::V_AT + (tid + j * NTHR) * 16) = v[j];
-        if (tid < 3 * C) reinterpret_cast<float*>(buf + L::F_AT)[tid] = f;
+        for (int j = 0; j < L::NV; ++j) {
+            const int u = tid + j * L::NTHR;
+            if (L::PV % L::NTHR == 0 || u < L::PV)
+                *reinterpret_cast<u32x4*>(buf + L::V_AT + (u / L::VROW) * L::VLD * (int)sizeof(E) + (u % L::VROW) * 16) = v[j];
+        }
+        if (L::NTHR == 2 * C || tid < 2 * C) reinterpret_cast<float*>(buf + L::F_AT)[tid] = f;
     }
 };
 
-__device__ __forceinline__ f32x4 ld4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+struct Ptrs {
+    const void *q, *k, *v;      // v: do where the walk is backwards
+    const float* init;          // [nseq] states (or their gradients) or NULL
+    const float* starts;        // those of the pieces of cut sequences, [piece place][Hv][dk][dv]
+    const char* prep;
+    int64_t prep_stride;
+    void* out;                  // o; dv where the walk is backwards
+    float* last;                // S_T or dS0, or NULL
+    char *ws_s, *ws_e;          // SAVE, BACK: the chunks' states and rows
+    float* maps;                // MAP: [piece place][Hv][dk][dv + dk]; BMAP: [..][dk][dv]
+    bool all;
+};
 
-// Forwards.  SAVE writes no output but, per chunk, the start state and e as the gradient
-// kernel's operands.  S0 and S_T may be NULL.
-template <typename E, int DK, int NTL, int MODE>
-__global__ void __launch_bounds__(NTHR, 1)
-chain_kernel(Args a, const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ v,
-             const float* __restrict__ beta, const float* S0, const char* __restrict__ prep, int64_t prep_stride,
-             E* __restrict__ o, float* S_T, char* __restrict__ ws_s, char* __restrict__ ws_e) {
+template <typename E, int DK, int NW, int MODE>
+__global__ void __launch_bounds__(64 * NW, NW / 4 > 0 ? NW / 4 : 1)
+chain_kernel(Args a, Segs sg, Ptrs io) {
     typedef Arith<E> A;
-    typedef Lay<E, DK, NTL, MODE> L;
+    typedef Lay<E, DK, NW, MODE> L;
     constexpr int KB = L::KB, ST = DK / 16;
+    constexpr bool BWD = L::BWD;
     __shared__ alignas(16) char lds[L::BUFS * L::BYTES];
     const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int nslab = (a.dv + L::SLAB - 1) / L::SLAB;
+    const int ncols = MODE == MAP ? a.dv + DK : a.dv;
+    const int nslab = (ncols + L::SLAB - 1) / L::SLAB;
     const int slab = (int)(blockIdx.x % (unsigned)nslab);
     const int h = (int)(blockIdx.x / (unsigned)nslab % (unsigned)a.Hv);
-    const int n = (int)(blockIdx.x / (unsigned)nslab / (unsigned)a.Hv);
-    const Seq sq = seq_of(a, n);
-    const int nch = (sq.len + C - 1) / C;
+    const int place = (int)(blockIdx.x / (unsigned)nslab / (unsigned)a.Hv);
+    const Piece pc = piece_at(a, sg, place, lane);
+    if (pc.n < 0) return;
+    // maps: forwards of every piece but the last one (all where both directions are joined),
+    // backwards of every one but the first
+    if (MODE == MAP && (pc.cnt < 2 || (!io.all && pc.i + 1 == pc.cnt))) return;
+    if (MODE == BMAP && pc.i == 0) return;
+    const int nch = pc.c1 - pc.c0;
     const int hk = h / (a.Hv / a.Hk);
     const int64_t ldk = (int64_t)a.Hk * DK, ldv = (int64_t)a.Hv * a.dv;
-    const int c0 = slab * L::SLAB, col0 = c0 + w * 16 * NTL;   // the slab's and the wavefront's first column
-    const bool act = col0 < a.dv;
-    const E* kp = k + sq.row0 * ldk + (int64_t)hk * DK;
-    const E* qp = q + sq.row0 * ldk + (int64_t)hk * DK;
-    const E* vp = v + sq.row0 * ldv + (int64_t)h * a.dv + c0;
-    const float* bp = beta + sq.row0 * a.Hv + h;
-    const int64_t sbase = ((int64_t)n * a.Hv + h) * DK * a.dv;
+    const int c0 = slab * L::SLAB, col0 = c0 + w * 16;   // the slab's and the wavefront's first column
+    const bool act = col0 < ncols;
+    const bool isM = MODE == MAP && col0 >= a.dv;        // a column of the map's linear part: no values
+    const E* kp = (const E*)io.k + pc.s.row0 * ldk + (int64_t)hk * DK;
+    const E* qp = (const E*)io.q + pc.s.row0 * ldk + (int64_t)hk * DK;
+    const E* vp = (const E*)io.v + pc.s.row0 * ldv + (int64_t)h * a.dv + c0;
 
-    f32x4 S[NTL][ST];
-#pragma unroll
-    for (int t = 0; t < ST; ++t)
-#pragma unroll
-        for (int j = 0; j < NTL; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                S[j][t][i] = S0 && act ? S0[sbase + (int64_t)(32 * (t / 2) + 8 * g + 4 * (t & 1) + i) * a.dv + col0 + 16 * j + r] : 0.0f;
-
-    Stage<E, DK, NTL, MODE> st;
-    auto load = [&](int c) {
-        const int left = sq.len - c * C;
-        const char* pre = prep + (((int64_t)sq.slot + c) * a.Hv + h) * prep_stride;
-        st.load(kp + (int64_t)c * C * ldk, qp + (int64_t)c * C * ldk, ldk, vp + (int64_t)c * C * ldv, ldv, a.dv - c0,
-                bp + (int64_t)c * C * a.Hv, a.Hv, pre, pre + TRI_BYTES,
-                reinterpret_cast<const float*>(pre + prep_stride - 2 * C * 4), left < C ? left : C);
-    };
-    if (nch > 0) {
-        load(0);
-        st.store(lds);
-    }
-    lds_barrier();
-    for (int c = 0; c < nch; ++c) {
-        const char* buf = lds + (L::BUFS == 2 ? (c & 1) * L::BYTES : 0);
-        load(c + 1 < nch ? c + 1 : c);   // the last chunk again rather than a branch
-        if (act) {
-            const float* gam = reinterpret_cast<const float*>(buf + L::F_AT);
-            const float *om = gam + C, *bt = gam + 2 * C;
-            const f32x4 zero = {0, 0, 0, 0};
-            typename A::Sp sb[NTL][KB];
-#pragma unroll
-            for (int j = 0; j < NTL; ++j)
-#pragma unroll
-                for (int b = 0; b < KB; ++b) sb[j][b] = A::split(S[j][2 * b], S[j][2 * b + 1]);
-            if constexpr (MODE == SAVE) {
-                char* to = ws_s + (((int64_t)sq.slot + c) * a.Hv + h) * state_bytes(DK, a.dv);
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const typename A::Ex pk = pick_half<E>(hh, g, r);
-#pragma unroll
-                    for (int b = 0; b < KB; ++b)
-#pragma unroll
-                        for (int j = 0; j < NTL; ++j) {
-                            const int ct = col0 / 16 + j;
-                            A::put_t(to + ((int64_t)(2 * b + hh) * (a.dv / 32) + ct / 2) * SPB, lane, ct & 1, sb[j][b], pk);
-                        }
-                }
-            }
-            // Y = V - gam (K S)
-            f32x4 y[NTL][MT];
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-#pragma unroll
-                for (int j = 0; j < NTL; ++j) y[j][m] = zero;
-#pragma unroll
-                for (int b = 0; b < KB; ++b) {
-                    const typename A::Ex kf = A::ld_ex(buf, m * KB + b, lane);
-#pragma unroll
-                    for (int j = 0; j < NTL; ++j) y[j][m] = A::mma(kf, sb[j][b], y[j][m]);
-                }
-                const f32x4 gm = ld4(gam + 16 * m + 4 * g);
-#pragma unroll
-                for (int j = 0; j < NTL; ++j) {
-                    const f32x4 vv = A::ld_col(buf + L::V_AT, L::SLAB, m, w * 16 * NTL + 16 * j, g, r);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) y[j][m][i] = vv[i] - gm[i] * y[j][m][i];
-                }
-            }
-            // e = X Y; U = beta e, and om U for the state
-            typename A::Sp yb[NTL][2], ub[NTL][2], wb[NTL][2];
-#pragma unroll
-            for (int j = 0; j < NTL; ++j)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) yb[j][b] = A::split(y[j][2 * b], y[j][2 * b + 1]);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-#pragma unroll
-                for (int j = 0; j < NTL; ++j) y[j][m] = zero;
-#pragma unroll
-                for (int b = 0; b <= m / 2; ++b) {
-                    const typename A::Sp xf = A::ld_sp(buf + L::X_AT, lower_block(m, b), lane);
-#pragma unroll
-                    for (int j = 0; j < NTL; ++j) y[j][m] = A::mma(xf, yb[j][b], y[j][m]);
-                }
-            }
-            if constexpr (MODE == SAVE) {
-                char* to = ws_e + (((int64_t)sq.slot + c) * a.Hv + h) * rows_bytes(a.dv);
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const typename A::Ex pk = pick_half<E>(hh, g, r);
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-#pragma unroll
-                        for (int j = 0; j < NTL; ++j) {
-                            const int ct = col0 / 16 + j;
-                            A::put_t(to + ((int64_t)(2 * b + hh) * (a.dv / 32) + ct / 2) * SPB, lane, ct & 1,
-                                     A::split(y[j][2 * b], y[j][2 * b + 1]), pk);
-                        }
-                }
-            }
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const f32x4 b4 = ld4(bt + 16 * m + 4 * g);
-#pragma unroll
-                for (int j = 0; j < NTL; ++j) y[j][m] *= b4;
-            }
-            if constexpr (MODE == FWD) {
-#pragma unroll
-                for (int j = 0; j < NTL; ++j)
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) ub[j][b] = A::split(y[j][2 * b], y[j][2 * b + 1]);
-            }
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const f32x4 o4 = ld4(om + 16 * m + 4 * g);
-#pragma unroll
-                for (int j = 0; j < NTL; ++j) y[j][m] *= o4;
-            }
-#pragma unroll
-            for (int j = 0; j < NTL; ++j)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) wb[j][b] = A::split(y[j][2 * b], y[j][2 * b + 1]);
-            // S <- gam_end S + K^T (om U)
-            const float ge = gam[C - 1];
-#pragma unroll
-            for (int t = 0; t < ST; ++t) {
-#pragma unroll
-                for (int j = 0; j < NTL; ++j) S[j][t] *= ge;
-#pragma unroll
-                for (int tb = 0; tb < 2; ++tb) {
-                    const typename A::Ex kt = A::template ld_ex_t<KB>(buf, t / 2, t & 1, tb, g, r);
-#pragma unroll
-                    for (int j = 0; j < NTL; ++j) S[j][t] = A::mma(kt, wb[j][tb], S[j][t]);
-                }
-            }
-            if constexpr (MODE == FWD) {
-                // O^T = scale gam (S^T Q^T) + U^T P^T: lane (g, r) has columns 4 g.. of token r
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    f32x4 ot[NTL];
-#pragma unroll
-                    for (int j = 0; j < NTL; ++j) ot[j] = zero;
-#pragma unroll
-                    for (int b = 0; b < KB; ++b) {
-                        const typename A::Ex qf = A::ld_ex(buf + L::Q_AT, m * KB + b, lane);
-#pragma unroll
-                        for (int j = 0; j < NTL; ++j) ot[j] = A::mma(sb[j][b], qf, ot[j]);
-                    }
-                    const float gs = a.scale * gam[16 * m + r];
-#pragma unroll
-                    for (int j = 0; j < NTL; ++j) ot[j] *= gs;
-#pragma unroll
-                    for (int b = 0; b <= m / 2; ++b) {
-                        const typename A::Sp pf = A::ld_sp(buf + L::P_AT, lower_block(m, b), lane);
-#pragma unroll
-                        for (int j = 0; j < NTL; ++j) ot[j] = A::mma(ub[j][b], pf, ot[j]);
-                    }
-                    const int64_t tok = (int64_t)c * C + 16 * m + r;
-                    if (tok < sq.len)
-#pragma unroll
-                        for (int j = 0; j < NTL; ++j)
-                            A::st4(o + (sq.row0 + tok) * ldv + (int64_t)h * a.dv + col0 + 16 * j + 4 * g, ot[j]);
-                }
-            }
+    // the state at the piece's start (backwards: the gradient at its end)
+    f32x4 S[ST];
+    {
+        const float* from = nullptr;
+        if (MODE != MAP && MODE != BMAP) {
+            if (pc.cnt > 1) from = io.starts + ((int64_t)place * a.Hv + h) * DK * a.dv;
+            else if (io.init) from = io.init + ((int64_t)pc.n * a.Hv + h) * DK * a.dv;
         }
-        if constexpr (L::BUFS == 1) lds_barrier();
-        st.store(lds + (L::BUFS == 2 ? ((c + 1) & 1) * L::BYTES : 0));
-        lds_barrier();
-    }
-    if (S_T && act)
 #pragma unroll
         for (int t = 0; t < ST; ++t)
 #pragma unroll
-            for (int j = 0; j < NTL; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    S_T[sbase + (int64_t)(32 * (t / 2) + 8 * g + 4 * (t & 1) + i) * a.dv + col0 + 16 * j + r] = S[j][t][i];
-}
+            for (int i = 0; i < 4; ++i) {
+                const int row = 32 * (t / 2) + 8 * g + 4 * (t & 1) + i;
+                S[t][i] = from && act ? from[(int64_t)row * a.dv + col0 + r] : isM && col0 + r == a.dv + row ? 1.0f : 0.0f;
+            }
+    }
 
-// Backwards: per chunk, the states' gradient at its end and Z, as the gradient kernel's
-// operands, and dV = Z; after the first chunk dS0.  dS_T and dS0 may be NULL.
-template <typename E, int DK, int NTL>
-__global__ void __launch_bounds__(NTHR, 1)
-back_kernel(Args a, const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ dout,
-            const float* __restrict__ beta, const float* dS_T, const char* __restrict__ prep, int64_t prep_stride,
-            E* __restrict__ dv, float* dS0, char* __restrict__ ws_d, char* __restrict__ ws_z) {
-    typedef Arith<E> A;
-    typedef Lay<E, DK, NTL, BACK> L;
-    constexpr int KB = L::KB, ST = DK / 16;
-    __shared__ alignas(16) char lds[L::BUFS * L::BYTES];
-    const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int nslab = (a.dv + L::SLAB - 1) / L::SLAB;
-    const int slab = (int)(blockIdx.x % (unsigned)nslab);
-    const int h = (int)(blockIdx.x / (unsigned)nslab % (unsigned)a.Hv);
-    const int n = (int)(blockIdx.x / (unsigned)nslab / (unsigned)a.Hv);
-    const Seq sq = seq_of(a, n);
-    const int nch = (sq.len + C - 1) / C;
-    const int hk = h / (a.Hv / a.Hk);
-    const int64_t ldk = (int64_t)a.Hk * DK, ldv = (int64_t)a.Hv * a.dv;
-    const int c0 = slab * L::SLAB, col0 = c0 + w * 16 * NTL;
-    const bool act = col0 < a.dv;
-    const E* kp = k + sq.row0 * ldk + (int64_t)hk * DK;
-    const E* qp = q + sq.row0 * ldk + (int64_t)hk * DK;
-    const E* dp = dout + sq.row0 * ldv + (int64_t)h * a.dv + c0;
-    const float* bp = beta + sq.row0 * a.Hv + h;
-    const int64_t sbase = ((int64_t)n * a.Hv + h) * DK * a.dv;
-
-    f32x4 S[NTL][ST];
-#pragma unroll
-    for (int t = 0; t < ST; ++t)
-#pragma unroll
-        for (int j = 0; j < NTL; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                S[j][t][i] = dS_T && act ? dS_T[sbase + (int64_t)(32 * (t / 2) + 8 * g + 4 * (t & 1) + i) * a.dv + col0 + 16 * j + r] : 0.0f;
-
-    Stage<E, DK, NTL, BACK> st;
+    Stage<E, DK, NW, MODE> st;
+    st.init(ldk, ldv, a.dv - c0);
     auto load = [&](int c) {
-        const int left = sq.len - c * C;
-        const char* pre = prep + (((int64_t)sq.slot + c) * a.Hv + h) * prep_stride;
-        st.load(kp + (int64_t)c * C * ldk, qp + (int64_t)c * C * ldk, ldk, dp + (int64_t)c * C * ldv, ldv, a.dv - c0,
-                bp + (int64_t)c * C * a.Hv, a.Hv, pre + 2 * TRI_BYTES, pre + 3 * TRI_BYTES,
-                reinterpret_cast<const float*>(pre + prep_stride - 2 * C * 4), left < C ? left : C);
+        const int left = pc.s.len - c * C;
+        const int valid = left < C ? left : C;
+        const int64_t row = (int64_t)c * C;
+        // rows past the chunk's last token read as zero; the head's offset is in the base
+        const Rsrc kr = make_rsrc(kp + row * ldk, (uint32_t)((valid - 1) * ldk + DK) * (uint32_t)sizeof(E));
+        const Rsrc qr = make_rsrc(qp + row * ldk, (uint32_t)((valid - 1) * ldk + DK) * (uint32_t)sizeof(E));
+        const int vc = a.dv - c0 < L::SLAB ? a.dv - c0 : L::SLAB;   // none in a slab of the linear part alone
+        const Rsrc vr = make_rsrc(vp + row * ldv, vc > 0 ? (uint32_t)((valid - 1) * ldv + vc) * (uint32_t)sizeof(E) : 0u);
+        const char* pre = io.prep + (((int64_t)pc.slot + c) * a.Hv + h) * io.prep_stride;
+        st.load(kr, qr, vr, BWD ? pre + TRI_BYTES : pre, BWD ? pre + 2 * TRI_BYTES : pre + TRI_BYTES,
+                reinterpret_cast<const float*>(pre + prep_factors(MODE != FWD && io.prep_stride == prep_bytes(true))));
+    };
+    auto chunk_of = [&](int it) { return BWD ? pc.c1 - 1 - it : pc.c0 + it; };
+    // a chunk's finished rows, stored one chunk later
+    typename A::Q4 fin[MT];
+    auto flush = [&](int c) {
+        const int left = pc.s.len - c * C, valid = left < C ? left : C;
+        const Rsrc orr = make_rsrc((E*)io.out + (pc.s.row0 + (int64_t)c * C) * ldv, (uint32_t)(valid * ldv) * (uint32_t)sizeof(E));
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+            buf_st_quad(fin[m], orr, act ? (uint32_t)((16 * m + r) * ldv + (int64_t)h * a.dv + col0 + 4 * g) * (uint32_t)sizeof(E) : 0xffffffffu);
     };
     if (nch > 0) {
-        load(nch - 1);
+        load(chunk_of(0));
         st.store(lds);
     }
     lds_barrier();
+    // where this wavefront's columns are in a record; past its end where it has none
+    const uint32_t w_off = act ? (uint32_t)(col0 / 32 * SPB) + A::half_at(lane, (col0 >> 4) & 1) : 0x80000000u;
+    const typename A::Ex pk0 = pick_half<E>(0, g, r), pk1 = pick_half<E>(1, g, r);
     for (int it = 0; it < nch; ++it) {
-        const int c = nch - 1 - it;
         const char* buf = lds + (L::BUFS == 2 ? (it & 1) * L::BYTES : 0);
-        load(c > 0 ? c - 1 : 0);
-        if (act) {
-            const float* gam = reinterpret_cast<const float*>(buf + L::F_AT);
-            const float *om = gam + C, *bt = gam + 2 * C;
+        const int c = chunk_of(it);
+        if ((MODE == FWD || MODE == BACK) && it > 0) flush(chunk_of(it - 1));
+        load(chunk_of(it + 1 < nch ? it + 1 : it));   // the last chunk again rather than a branch
+        {
+            const float *gam = reinterpret_cast<const float*>(buf + L::F_AT), *ob = gam + C;
             const f32x4 zero = {0, 0, 0, 0};
-            typename A::Sp sb[NTL][KB];
+            const char* vl = buf + L::V_AT;
+            typename A::Sp sb[KB];
 #pragma unroll
-            for (int j = 0; j < NTL; ++j)
+            for (int b = 0; b < KB; ++b) sb[b] = A::split(S[2 * b], S[2 * b + 1]);
+            const int64_t rec = ((int64_t)pc.slot + c) * a.Hv + h;
+            if constexpr (MODE == SAVE || MODE == BACK) {
+                const Rsrc to = make_rsrc(io.ws_s + rec * state_bytes(DK, a.dv), (uint32_t)state_bytes(DK, a.dv));
 #pragma unroll
-                for (int b = 0; b < KB; ++b) sb[j][b] = A::split(S[j][2 * b], S[j][2 * b + 1]);
-            {
-                char* to = ws_d + (((int64_t)sq.slot + c) * a.Hv + h) * state_bytes(DK, a.dv);
+                for (int b = 0; b < KB; ++b)
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const typename A::Ex pk = pick_half<E>(hh, g, r);
-#pragma unroll
-                    for (int b = 0; b < KB; ++b)
-#pragma unroll
-                        for (int j = 0; j < NTL; ++j) {
-                            const int ct = col0 / 16 + j;
-                            A::put_t(to + ((int64_t)(2 * b + hh) * (a.dv / 32) + ct / 2) * SPB, lane, ct & 1, sb[j][b], pk);
-                        }
-                }
+                    for (int hh = 0; hh < 2; ++hh) A::put_t(to, w_off + (uint32_t)((2 * b + hh) * (a.dv / 32) * SPB), sb[b], hh ? pk1 : pk0);
             }
-            // dO of this wavefront's columns
-            f32x4 dov[NTL][MT];
-            typename A::Ex dob[NTL][2];
+            f32x4 y[MT], dov[MT];
+            typename A::Ex dob[2];
+            if constexpr (BWD) {
 #pragma unroll
-            for (int j = 0; j < NTL; ++j) {
+                for (int m = 0; m < MT; ++m) dov[m] = A::ld_col(vl, L::VLD, m, w * 16, g, r);
 #pragma unroll
-                for (int m = 0; m < MT; ++m) dov[j][m] = A::ld_col(buf + L::V_AT, L::SLAB, m, w * 16 * NTL + 16 * j, g, r);
-#pragma unroll
-                for (int b = 0; b < 2; ++b) dob[j][b] = A::cols(dov[j][2 * b], dov[j][2 * b + 1]);
+                for (int b = 0; b < 2; ++b) dob[b] = A::cols(dov[2 * b], dov[2 * b + 1]);
             }
-            // beta dU = beta (om (K dS) + P^T dO)
-            f32x4 y[NTL][MT];
+            // V - gam (K S), or om beta (K dS) + (diag(beta) P^T) dO
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
+                y[m] = zero;
 #pragma unroll
-                for (int j = 0; j < NTL; ++j) y[j][m] = zero;
+                for (int b = 0; b < KB; ++b) y[m] = A::mma(A::ld_ex(buf, m * KB + b, lane), sb[b], y[m]);
+                if constexpr (BWD) {
+                    y[m] *= ld4(ob + 16 * m + 4 * g);
 #pragma unroll
-                for (int b = 0; b < KB; ++b) {
-                    const typename A::Ex kf = A::ld_ex(buf, m * KB + b, lane);
-#pragma unroll
-                    for (int j = 0; j < NTL; ++j) y[j][m] = A::mma(kf, sb[j][b], y[j][m]);
+                    for (int b = m / 2; b < 2; ++b) y[m] = A::mma(A::ld_sp(buf + L::P_AT, upper_block(m, b), lane), dob[b], y[m]);
+                } else {
+                    const f32x4 gm = ld4(gam + 16 * m + 4 * g);
+                    f32x4 vv = A::ld_col(vl, L::VLD, m, w * 16, g, r);
+                    if (isM) vv = zero;
+                    y[m] = vv - gm * y[m];
                 }
-                const f32x4 o4 = ld4(om + 16 * m + 4 * g), b4 = ld4(bt + 16 * m + 4 * g);
-#pragma unroll
-                for (int j = 0; j < NTL; ++j) y[j][m] *= o4;
-#pragma unroll
-                for (int b = m / 2; b < 2; ++b) {
-                    const typename A::Sp pf = A::ld_sp(buf + L::P_AT, upper_block(m, b), lane);
-#pragma unroll
-                    for (int j = 0; j < NTL; ++j) y[j][m] = A::mma(pf, dob[j][b], y[j][m]);
-                }
-#pragma unroll
-                for (int j = 0; j < NTL; ++j) y[j][m] *= b4;
             }
-            // Z = X^T (beta dU)
-            typename A::Sp yb[NTL][2];
+            // e = X y, or Z = X^T y
+            typename A::Sp yb[2];
 #pragma unroll
-            for (int j = 0; j < NTL; ++j)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) yb[j][b] = A::split(y[j][2 * b], y[j][2 * b + 1]);
+            for (int b = 0; b < 2; ++b) yb[b] = A::split(y[2 * b], y[2 * b + 1]);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
+                y[m] = zero;
 #pragma unroll
-                for (int j = 0; j < NTL; ++j) y[j][m] = zero;
-#pragma unroll
-                for (int b = m / 2; b < 2; ++b) {
-                    const typename A::Sp xf = A::ld_sp(buf + L::X_AT, upper_block(m, b), lane);
-#pragma unroll
-                    for (int j = 0; j < NTL; ++j) y[j][m] = A::mma(xf, yb[j][b], y[j][m]);
-                }
+                for (int b = BWD ? m / 2 : 0; b <= (BWD ? 1 : m / 2); ++b)
+                    y[m] = A::mma(A::ld_sp(buf + L::X_AT, BWD ? upper_block(m, b) : lower_block(m, b), lane), yb[b], y[m]);
             }
-            {
-                char* to = ws_z + (((int64_t)sq.slot + c) * a.Hv + h) * rows_bytes(a.dv);
+            typename A::Sp eb[2], wb[2], db[2];
+            if constexpr (MODE != MAP && MODE != BMAP) {
 #pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const typename A::Ex pk = pick_half<E>(hh, g, r);
-#pragma unroll
-                    for (int b = 0; b < 2; ++b)
-#pragma unroll
-                        for (int j = 0; j < NTL; ++j) {
-                            const int ct = col0 / 16 + j;
-                            const f32x4 z = A::put_t(to + ((int64_t)(2 * b + hh) * (a.dv / 32) + ct / 2) * SPB, lane, ct & 1,
-                                                     A::split(y[j][2 * b], y[j][2 * b + 1]), pk);
-                            const int64_t tok = (int64_t)c * C + 32 * b + 16 * hh + r;
-                            if (tok < sq.len) A::st4(dv + (sq.row0 + tok) * ldv + (int64_t)h * a.dv + 16 * ct + 4 * g, z);
-                        }
-                }
+                for (int b = 0; b < 2; ++b) eb[b] = A::split(y[2 * b], y[2 * b + 1]);
             }
-            // dS <- gam_end dS + Q^T (scale gam dO) - K^T (gam Z)
-            typename A::Sp zb[NTL][2], db[NTL][2];
+            if constexpr (MODE == SAVE || MODE == BACK) {
+                const Rsrc to = make_rsrc(io.ws_e + rec * rows_bytes(a.dv), (uint32_t)rows_bytes(a.dv));
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const f32x4 gm = ld4(gam + 16 * m + 4 * g);
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int j = 0; j < NTL; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        y[j][m][i] *= -gm[i];
-                        dov[j][m][i] *= a.scale * gm[i];
+                    for (int hh = 0; hh < 2; ++hh) {
+                        const f32x4 z = A::put_t(to, w_off + (uint32_t)((2 * b + hh) * (a.dv / 32) * SPB), eb[b], hh ? pk1 : pk0);
+                        if constexpr (MODE == BACK) fin[2 * b + hh] = A::q4(z);
                     }
             }
+            // om beta e, or -gam Z and scale gam dO, for the state
 #pragma unroll
-            for (int j = 0; j < NTL; ++j)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    zb[j][b] = A::split(y[j][2 * b], y[j][2 * b + 1]);
-                    db[j][b] = A::split(dov[j][2 * b], dov[j][2 * b + 1]);
+            for (int m = 0; m < MT; ++m) {
+                const f32x4 f4 = ld4((BWD ? gam : ob) + 16 * m + 4 * g);
+                if constexpr (BWD) {
+                    y[m] *= -f4;
+                    dov[m] *= f4 * a.scale;
+                } else {
+                    y[m] *= f4;
                 }
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                wb[b] = A::split(y[2 * b], y[2 * b + 1]);
+                if constexpr (BWD) db[b] = A::split(dov[2 * b], dov[2 * b + 1]);
+            }
             const float ge = gam[C - 1];
 #pragma unroll
             for (int t = 0; t < ST; ++t) {
-#pragma unroll
-                for (int j = 0; j < NTL; ++j) S[j][t] *= ge;
+                S[t] *= ge;
 #pragma unroll
                 for (int tb = 0; tb < 2; ++tb) {
-                    const typename A::Ex kt = A::template ld_ex_t<KB>(buf, t / 2, t & 1, tb, g, r);
-                    const typename A::Ex qt = A::template ld_ex_t<KB>(buf + L::Q_AT, t / 2, t & 1, tb, g, r);
+                    if constexpr (BWD) S[t] = A::mma(A::template ld_ex_t<KB>(buf + L::Q_AT, t / 2, t & 1, tb, g, r), db[tb], S[t]);
+                    S[t] = A::mma(A::template ld_ex_t<KB>(buf, t / 2, t & 1, tb, g, r), wb[tb], S[t]);
+                }
+            }
+            if constexpr (MODE == FWD) {
+                // O^T: lane (g, r) has columns 4 g.. of token r
 #pragma unroll
-                    for (int j = 0; j < NTL; ++j) {
-                        S[j][t] = A::mma(qt, db[j][tb], S[j][t]);
-                        S[j][t] = A::mma(kt, zb[j][tb], S[j][t]);
-                    }
+                for (int m = 0; m < MT; ++m) {
+                    f32x4 ot = zero;
+#pragma unroll
+                    for (int b = 0; b < KB; ++b) ot = A::mma(sb[b], A::ld_ex(buf + L::Q_AT, m * KB + b, lane), ot);
+                    ot *= a.scale * gam[16 * m + r];
+#pragma unroll
+                    for (int b = 0; b <= m / 2; ++b) ot = A::mma(eb[b], A::ld_sp(buf + L::P_AT, lower_block(m, b), lane), ot);
+                    fin[m] = A::q4(ot);
                 }
             }
         }
@@ -516,101 +329,179 @@ back_kernel(Args a, const E* __restrict__ q, const E* __restrict__ k, const E* _
         st.store(lds + (L::BUFS == 2 ? ((it + 1) & 1) * L::BYTES : 0));
         lds_barrier();
     }
-    if (dS0 && act)
+    if ((MODE == FWD || MODE == BACK) && nch > 0) flush(chunk_of(nch - 1));
+    // the state behind the piece
+    float* to = nullptr;
+    int64_t ld = a.dv;
+    if (MODE == MAP || MODE == BMAP) {
+        ld = ncols;
+        to = io.maps + ((int64_t)place * a.Hv + h) * DK * ld;
+    } else if (io.last && (BWD ? pc.i == 0 : pc.i + 1 == pc.cnt)) {
+        to = io.last + ((int64_t)pc.n * a.Hv + h) * DK * ld;
+    }
+    if (to && act)
 #pragma unroll
         for (int t = 0; t < ST; ++t)
 #pragma unroll
-            for (int j = 0; j < NTL; ++j)
+            for (int i = 0; i < 4; ++i) to[(32 * (t / 2) + 8 * g + 4 * (t & 1) + i) * ld + col0 + r] = S[t][i];
+}
+
+// Joins the maps of a cut sequence's pieces: forwards X_0 = S0, X_{i+1} = M_i X_i + N_i, backwards
+// X_last = dS_T, X_{i-1} = M_i^T X_i + N'_i, every X_i written to `starts`.  A workgroup has one
+// head and 32 columns, a wavefront 16 of them and a quarter of the rows; X goes from
+// step to step through LDS as split fragments.  Two column tiles share what is read of M.
+template <typename E, int DK, bool BWD>
+__global__ void __launch_bounds__(512)
+join_kernel(Args a, Segs sg, const float* __restrict__ init, const float* __restrict__ maps, const float* __restrict__ nmaps,
+            float* __restrict__ starts) {
+    typedef Arith<E> A;
+    constexpr int KB = DK / 32, ST = DK / 16, RT = ST >= 4 ? ST / 4 : 1;   // row tiles a wavefront
+    __shared__ alignas(16) char lds[2][2 * KB * SPB];
+    const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), ct = w & 1, rq = w >> 1;
+    const int nslab = a.dv / 32;
+    const int slab = (int)(blockIdx.x % (unsigned)nslab), h = (int)(blockIdx.x / (unsigned)nslab % (unsigned)a.Hv);
+    const int n = (int)(blockIdx.x / (unsigned)nslab / (unsigned)a.Hv);
+    const int p0 = __builtin_amdgcn_readfirstlane(place_of(a, n, seg_unit(sg)));
+    const Piece pc = piece_at(a, sg, p0, lane);
+    if (pc.n != n || pc.cnt < 2) return;
+    const int col = 32 * slab + 16 * ct + r;
+    const bool on = rq * RT < ST;
+    const int64_t mld = a.dv + DK, nld = BWD ? a.dv : mld;
+    f32x4 X[RT];
+    auto rowof = [&](int t) { return 32 * (t / 2) + 8 * g + 4 * (t & 1); };   // this lane's first row of accumulator tile t
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    dS0[sbase + (int64_t)(32 * (t / 2) + 8 * g + 4 * (t & 1) + i) * a.dv + col0 + 16 * j + r] = S[j][t][i];
+    for (int j = 0; j < RT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            X[j][i] = init && on ? init[(((int64_t)n * a.Hv + h) * DK + rowof(rq * RT + j) + i) * a.dv + col] : 0.0f;
+    for (int s = 0; s < pc.cnt; ++s) {
+        const int at = p0 + (BWD ? pc.cnt - 1 - s : s);
+        float* to = starts + ((int64_t)at * a.Hv + h) * DK * a.dv + col;
+        char* buf = lds[s & 1];
+        if (on) {
+#pragma unroll
+            for (int j = 0; j < RT; ++j) {
+                const int t = rq * RT + j;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) to[(int64_t)(rowof(t) + i) * a.dv] = X[j][i];
+                A::put_half(buf, ct * KB + t / 2, lane, t & 1, X[j]);
+            }
+        }
+        if (s + 1 == pc.cnt) break;
+        lds_barrier();
+        if (on) {
+            const float* M = maps + ((int64_t)at * a.Hv + h) * DK * mld + a.dv;
+            const float* N = nmaps + ((int64_t)at * a.Hv + h) * DK * nld;
+            typename A::Sp xb[KB];
+#pragma unroll
+            for (int b = 0; b < KB; ++b) xb[b] = A::ld_sp(buf, ct * KB + b, lane);
+#pragma unroll
+            for (int j = 0; j < RT; ++j) {
+                const int t = rq * RT + j, row = 32 * (t / 2) + 8 * (r >> 2) + 4 * (t & 1) + (r & 3);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) X[j][i] = N[(int64_t)(rowof(t) + i) * nld + col];
+#pragma unroll
+                for (int b = 0; b < KB; ++b) {
+                    f32x4 lo, hi;
+                    if constexpr (BWD) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            lo[i] = M[(int64_t)(32 * b + 8 * g + i) * mld + row];
+                            hi[i] = M[(int64_t)(32 * b + 8 * g + 4 + i) * mld + row];
+                        }
+                    } else {
+                        lo = ld4(M + row * mld + 32 * b + 8 * g);
+                        hi = ld4(M + row * mld + 32 * b + 8 * g + 4);
+                    }
+                    X[j] = A::mma(A::split(lo, hi), xb[b], X[j]);
+                }
+            }
+        }
+    }
 }
 
-template <int NTL>
-unsigned chain_grid(const Args& a) {
-    const int slab = 16 * NTL * NW;
-    return (unsigned)((int64_t)a.nseq * a.Hv * ((a.dv + slab - 1) / slab));
-}
-
-// Two column tiles a wavefront share each operand fragment's LDS read, one leaves twice the
-// workgroups: two where the workgroups then still fill the chip.
-bool wide(bool f32, const Args& a) { return !f32 && (int64_t)a.nseq * a.Hv * ((a.dv + 127) / 128) >= 256 && a.dv % 128 == 0; }
-
-template <typename E, int DK, int NTL>
-hipError_t fwd_t(bool save, const Args& a, const void* q, const void* k, const void* v, const float* beta, const float* S0,
-                 const char* prep, int64_t stride, void* o, float* S_T, char* ws_s, char* ws_e, hipStream_t stream) {
-    const dim3 grid(chain_grid<NTL>(a));
-    if (save)
-        hipLaunchKernelGGL((chain_kernel<E, DK, NTL, SAVE>), grid, dim3(NTHR), 0, stream, a, (const E*)q, (const E*)k,
-                           (const E*)v, beta, S0, prep, stride, (E*)o, S_T, ws_s, ws_e);
-    else
-        hipLaunchKernelGGL((chain_kernel<E, DK, NTL, FWD>), grid, dim3(NTHR), 0, stream, a, (const E*)q, (const E*)k,
-                           (const E*)v, beta, S0, prep, stride, (E*)o, S_T, ws_s, ws_e);
+template <typename E, int DK, int NW>
+hipError_t chain_t(int mode, const Args& a, const Segs& sg, const Ptrs& io, hipStream_t stream) {
+    const int slab = 16 * NW, cols = mode == MAP ? a.dv + DK : a.dv;
+    const int64_t n = places_of(a.nseq, a.T, a.cu != nullptr, seg_unit(sg)) * a.Hv * ((cols + slab - 1) / slab);
+    const dim3 grid((unsigned)n), block(64 * NW);
+    switch (mode) {
+        case FWD: hipLaunchKernelGGL((chain_kernel<E, DK, NW, FWD>), grid, block, 0, stream, a, sg, io); break;
+        case SAVE: hipLaunchKernelGGL((chain_kernel<E, DK, NW, SAVE>), grid, block, 0, stream, a, sg, io); break;
+        case MAP: hipLaunchKernelGGL((chain_kernel<E, DK, NW, MAP>), grid, block, 0, stream, a, sg, io); break;
+        case BACK: hipLaunchKernelGGL((chain_kernel<E, DK, NW, BACK>), grid, block, 0, stream, a, sg, io); break;
+        case BMAP: hipLaunchKernelGGL((chain_kernel<E, DK, NW, BMAP>), grid, block, 0, stream, a, sg, io); break;
+    }
     return hipGetLastError();
 }
 
-template <typename E, int DK, int NTL>
-hipError_t back_t(const Args& a, const void* q, const void* k, const void* dout, const float* beta, const float* dS_T,
-                  const char* prep, int64_t stride, void* dv, float* dS0, char* ws_d, char* ws_z, hipStream_t stream) {
-    hipLaunchKernelGGL((back_kernel<E, DK, NTL>), dim3(chain_grid<NTL>(a)), dim3(NTHR), 0, stream, a, (const E*)q, (const E*)k,
-                       (const E*)dout, beta, dS_T, prep, stride, (E*)dv, dS0, ws_d, ws_z);
+// Wavefronts a workgroup: eight share one set of operands over 128 columns; four where a
+// head has no more columns, or where workgroups of eight would leave half the chip empty.
+template <typename E, int DK>
+hipError_t chain_d(int mode, const Args& a, const Segs& sg, const Ptrs& io, hipStream_t stream) {
+    const int cols = mode == MAP ? a.dv + DK : a.dv;
+    const int64_t heads = places_of(a.nseq, a.T, a.cu != nullptr, seg_unit(sg)) * a.Hv;
+    if (sizeof(E) == 4 || cols <= 64 || heads * ((cols + 63) / 64) <= 256) return chain_t<E, DK, 4>(mode, a, sg, io, stream);
+    if constexpr (sizeof(E) == 2) return chain_t<E, DK, 8>(mode, a, sg, io, stream);
+    return hipErrorInvalidValue;
+}
+
+template <typename E, int DK>
+hipError_t join_d(bool bwd, const Args& a, const Segs& sg, const float* init, const float* maps, const float* nmaps,
+                  float* starts, hipStream_t stream) {
+    const dim3 grid((unsigned)((int64_t)a.nseq * a.Hv * (a.dv / 32)));
+    if (bwd) hipLaunchKernelGGL((join_kernel<E, DK, true>), grid, dim3(512), 0, stream, a, sg, init, maps, nmaps, starts);
+    else hipLaunchKernelGGL((join_kernel<E, DK, false>), grid, dim3(512), 0, stream, a, sg, init, maps, nmaps, starts);
     return hipGetLastError();
 }
+
+#define KDA_GDR_TYPES(F, ...)                                \
+    if (f32) {                                               \
+        switch (dk) {                                        \
+            case 32: return F<float, 32>(__VA_ARGS__);       \
+            case 64: return F<float, 64>(__VA_ARGS__);       \
+            case 128: return F<float, 128>(__VA_ARGS__);     \
+        }                                                    \
+    } else {                                                 \
+        switch (dk) {                                        \
+            case 32: return F<bf16, 32>(__VA_ARGS__);        \
+            case 64: return F<bf16, 64>(__VA_ARGS__);        \
+            case 128: return F<bf16, 128>(__VA_ARGS__);      \
+        }                                                    \
+    }                                                        \
+    return hipErrorInvalidValue
 
 }  // namespace
 
-hipError_t launch_chain(bool f32, int dk, bool save, const Args& a, const void* q, const void* k, const void* v,
-                        const float* beta, const float* S0, const char* prep, int64_t stride, void* o, float* S_T,
-                        char* ws_s, char* ws_e, hipStream_t stream) {
-#define KDA_GC(E, D, N) return fwd_t<E, D, N>(save, a, q, k, v, beta, S0, prep, stride, o, S_T, ws_s, ws_e, stream)
-    if (f32) {
-        switch (dk) {
-            case 32: KDA_GC(float, 32, 1);
-            case 64: KDA_GC(float, 64, 1);
-            case 128: KDA_GC(float, 128, 1);
-        }
-    } else if (wide(f32, a)) {
-        switch (dk) {
-            case 32: KDA_GC(bf16, 32, 2);
-            case 64: KDA_GC(bf16, 64, 2);
-            case 128: KDA_GC(bf16, 128, 2);
-        }
-    } else {
-        switch (dk) {
-            case 32: KDA_GC(bf16, 32, 1);
-            case 64: KDA_GC(bf16, 64, 1);
-            case 128: KDA_GC(bf16, 128, 1);
-        }
-    }
-#undef KDA_GC
-    return hipErrorInvalidValue;
+hipError_t launch_fwd_chain(bool f32, int dk, const Args& a, const Segs& sg, const void* q, const void* k, const void* v,
+                            const float* S0, const float* starts, const char* prep, void* o, float* S_T, hipStream_t stream) {
+    const Ptrs io{q, k, v, S0, starts, prep, prep_bytes(false), o, S_T, nullptr, nullptr, nullptr, false};
+    KDA_GDR_TYPES(chain_d, FWD, a, sg, io, stream);
 }
 
-hipError_t launch_back(bool f32, int dk, const Args& a, const void* q, const void* k, const void* dout, const float* beta,
-                       const float* dS_T, const char* prep, int64_t stride, void* dv, float* dS0, char* ws_d, char* ws_z,
-                       hipStream_t stream) {
-#define KDA_GB(E, D, N) return back_t<E, D, N>(a, q, k, dout, beta, dS_T, prep, stride, dv, dS0, ws_d, ws_z, stream)
-    if (f32) {
-        switch (dk) {
-            case 32: KDA_GB(float, 32, 1);
-            case 64: KDA_GB(float, 64, 1);
-            case 128: KDA_GB(float, 128, 1);
-        }
-    } else if (wide(f32, a)) {
-        switch (dk) {
-            case 32: KDA_GB(bf16, 32, 2);
-            case 64: KDA_GB(bf16, 64, 2);
-            case 128: KDA_GB(bf16, 128, 2);
-        }
-    } else {
-        switch (dk) {
-            case 32: KDA_GB(bf16, 32, 1);
-            case 64: KDA_GB(bf16, 64, 1);
-            case 128: KDA_GB(bf16, 128, 1);
-        }
-    }
-#undef KDA_GB
-    return hipErrorInvalidValue;
+hipError_t launch_save_chain(bool f32, int dk, const Args& a, const Segs& sg, const void* k, const void* v, const float* S0,
+                             const float* starts, const char* prep, char* ws_s, char* ws_e, hipStream_t stream) {
+    const Ptrs io{k, k, v, S0, starts, prep, prep_bytes(true), nullptr, nullptr, ws_s, ws_e, nullptr, false};
+    KDA_GDR_TYPES(chain_d, SAVE, a, sg, io, stream);
+}
+
+hipError_t launch_map_chain(bool f32, int dk, bool bwd, const Args& a, const Segs& sg, const void* k, const void* v,
+                            const char* prep, float* maps, hipStream_t stream) {
+    const Ptrs io{k, k, v, nullptr, nullptr, prep, prep_bytes(bwd), nullptr, nullptr, nullptr, nullptr, maps, bwd};
+    KDA_GDR_TYPES(chain_d, MAP, a, sg, io, stream);
+}
+
+hipError_t launch_back_chain(bool f32, int dk, bool map, const Args& a, const Segs& sg, const void* q, const void* k,
+                             const void* dout, const float* dS_T, const float* starts, const char* prep, void* dv, float* dS0,
+                             char* ws_d, char* ws_z, float* maps, hipStream_t stream) {
+    const Ptrs io{q, k, dout, dS_T, starts, prep, prep_bytes(true), dv, dS0, ws_d, ws_z, maps, false};
+    KDA_GDR_TYPES(chain_d, map ? BMAP : BACK, a, sg, io, stream);
+}
+
+hipError_t launch_join(bool f32, int dk, bool bwd, const Args& a, const Segs& sg, const float* init, const float* maps,
+                       const float* nmaps, float* starts, hipStream_t stream) {
+    KDA_GDR_TYPES(join_d, bwd, a, sg, init, maps, nmaps, starts, stream);
 }
 
 }  // namespace gdr

@@ -1,7 +1,9 @@
 // kda_gdr_chunk.hip -- the launches of the chunked gated delta rule with one decay a head and
 // the layout of its workspace.
-//   forward:   prep (X, P of every chunk) -> chain (states, outputs)
-//   backward:  prep (with transposes) -> chain (states saved) -> chain backwards -> grad
+//   forward:   prep (X, P of every chunk) -> [maps -> join] -> chain (states, outputs)
+//   backward:  prep -> [maps, backward maps -> joins] -> chain saving the states ->
+//              chain backwards -> grad
+// The steps in brackets run where sequences are cut into pieces that are walked side by side.
 #include "kda_gdr.hpp"
 #include "kda_launch.hpp"
 
@@ -10,57 +12,120 @@ namespace gdr {
 
 hipError_t launch_prep(bool f32, int dk, bool bwd, const Args& a, const void* q, const void* k, const float* g,
                        const float* beta, char* ws, hipStream_t stream);
-hipError_t launch_chain(bool f32, int dk, bool save, const Args& a, const void* q, const void* k, const void* v,
-                        const float* beta, const float* S0, const char* prep, int64_t stride, void* o, float* S_T,
-                        char* ws_s, char* ws_e, hipStream_t stream);
-hipError_t launch_back(bool f32, int dk, const Args& a, const void* q, const void* k, const void* dout, const float* beta,
-                       const float* dS_T, const char* prep, int64_t stride, void* dv, float* dS0, char* ws_d, char* ws_z,
-                       hipStream_t stream);
+hipError_t launch_fwd_chain(bool f32, int dk, const Args& a, const Segs& sg, const void* q, const void* k, const void* v,
+                            const float* S0, const float* starts, const char* prep, void* o, float* S_T, hipStream_t stream);
+hipError_t launch_save_chain(bool f32, int dk, const Args& a, const Segs& sg, const void* k, const void* v, const float* S0,
+                             const float* starts, const char* prep, char* ws_s, char* ws_e, hipStream_t stream);
+hipError_t launch_map_chain(bool f32, int dk, bool bwd, const Args& a, const Segs& sg, const void* k, const void* v,
+                            const char* prep, float* maps, hipStream_t stream);
+hipError_t launch_back_chain(bool f32, int dk, bool map, const Args& a, const Segs& sg, const void* q, const void* k,
+                             const void* dout, const float* dS_T, const float* starts, const char* prep, void* dv, float* dS0,
+                             char* ws_d, char* ws_z, float* maps, hipStream_t stream);
+hipError_t launch_join(bool f32, int dk, bool bwd, const Args& a, const Segs& sg, const float* init, const float* maps,
+                       const float* nmaps, float* starts, hipStream_t stream);
 hipError_t launch_grad(bool f32, int dk_, const Args& a, const void* q, const void* k, const float* beta, const void* dout,
                        const char* prep, const char* ws_s, const char* ws_e, const char* ws_d, const char* ws_z, void* dq,
                        void* dk, float* dg, float* dbeta, hipStream_t stream);
 
+namespace {
+
+// Cutting a sequence costs a second walk of it (the maps, over dv + dk columns), so it pays
+// where one workgroup's walk would outlast the whole call's work spread over the 256
+// compute units by more than about that: `seg` is the even share in chunks, and sequences
+// of more than 9/4 of it are cut.  Pieces of fewer than eight chunks are not worth their join.
+Segs segs_of(int nseq, int T, int Hv, int dv, bool packed) {
+    const int64_t work = places_of(nseq, T, packed, C) * Hv * ((dv + 127) / 128);
+    int64_t seg = (work + 255) / 256;
+    if (seg < 8) seg = 8;
+    const int64_t over = seg * 9 / 4;
+    if (((int64_t)T + C - 1) / C <= over) return Segs{0, 0};   // none can be longer
+    return Segs{(int)seg, (int)over};
+}
+
+// The parts of a workspace, in order; each a multiple of 16 bytes.
+struct Plan {
+    Segs sg;
+    int64_t prep, s, d, e, z, maps, nmaps, starts, dstarts, bytes;
+};
+Plan plan_of(bool bwd, int nseq, int T, int Hv, int dk, int dv, bool packed) {
+    Plan p{};
+    p.sg = segs_of(nseq, T, Hv, dv, packed);
+    const int64_t n = places_of(nseq, T, packed, C) * Hv;
+    const int64_t m = p.sg.seg ? places_of(nseq, T, packed, seg_unit(p.sg)) * Hv : 0;
+    int64_t at = 0;
+    auto take = [&](int64_t& x, int64_t bytes) {
+        x = at;
+        at += bytes;
+    };
+    take(p.prep, n * prep_bytes(bwd));
+    if (bwd) {
+        take(p.s, n * state_bytes(dk, dv));
+        take(p.d, n * state_bytes(dk, dv));
+        take(p.e, n * rows_bytes(dv));
+        take(p.z, n * rows_bytes(dv));
+    }
+    take(p.maps, m * map_bytes(dk, dv));
+    take(p.starts, m * dk * dv * 4);
+    if (bwd) {
+        take(p.nmaps, m * dk * dv * 4);
+        take(p.dstarts, m * dk * dv * 4);
+    }
+    p.bytes = at;
+    return p;
+}
+
+Args args_of(const GdrCall& c) { return Args{c.nseq, c.T, c.Hk, c.Hv, c.dv, c.cu, c.scale}; }
+
+}  // namespace
 }  // namespace gdr
 
 size_t gdr_fwd_workspace_bytes(int nseq, int T, int Hv, int dk, int dv, bool packed) {
-    (void)dk;
-    (void)dv;
-    return (size_t)(gdr::slots_of(nseq, T, packed) * Hv * gdr::prep_bytes(false));
+    return (size_t)gdr::plan_of(false, nseq, T, Hv, dk, dv, packed).bytes;
 }
 
 size_t gdr_bwd_workspace_bytes(int nseq, int T, int Hv, int dk, int dv, bool packed) {
-    return (size_t)(gdr::slots_of(nseq, T, packed) * Hv *
-                    (gdr::prep_bytes(true) + 2 * gdr::state_bytes(dk, dv) + 2 * gdr::rows_bytes(dv)));
+    return (size_t)gdr::plan_of(true, nseq, T, Hv, dk, dv, packed).bytes;
 }
 
-static gdr::Args args_of(const GdrCall& c) { return gdr::Args{c.nseq, c.T, c.Hk, c.Hv, c.dv, c.cu, c.scale}; }
+#define KDA_DO(CALL)                         \
+    do {                                     \
+        const hipError_t e_ = (CALL);        \
+        if (e_ != hipSuccess) return e_;     \
+    } while (0)
 
 hipError_t launch_gdr_fwd(const GdrCall& c, void* o, float* S_T, void* workspace, hipStream_t stream) {
-    const gdr::Args a = args_of(c);
+    const gdr::Args a = gdr::args_of(c);
+    const gdr::Plan p = gdr::plan_of(false, c.nseq, c.T, c.Hv, c.dk, c.dv, c.cu != nullptr);
     char* ws = (char*)workspace;
-    hipError_t e = gdr::launch_prep(c.f32, c.dk, false, a, c.q, c.k, c.g, c.beta, ws, stream);
-    if (e != hipSuccess) return e;
-    return gdr::launch_chain(c.f32, c.dk, false, a, c.q, c.k, c.v, c.beta, c.S0, ws, gdr::prep_bytes(false), o, S_T, nullptr,
-                             nullptr, stream);
+    float *maps = (float*)(ws + p.maps), *starts = (float*)(ws + p.starts);
+    KDA_DO(gdr::launch_prep(c.f32, c.dk, false, a, c.q, c.k, c.g, c.beta, ws + p.prep, stream));
+    if (p.sg.seg) {
+        KDA_DO(gdr::launch_map_chain(c.f32, c.dk, false, a, p.sg, c.k, c.v, ws + p.prep, maps, stream));
+        KDA_DO(gdr::launch_join(c.f32, c.dk, false, a, p.sg, c.S0, maps, maps, starts, stream));
+    }
+    return gdr::launch_fwd_chain(c.f32, c.dk, a, p.sg, c.q, c.k, c.v, c.S0, starts, ws + p.prep, o, S_T, stream);
 }
 
 hipError_t launch_gdr_bwd(const GdrCall& c, const void* dout, const float* dS_T, void* dq, void* dk, void* dv, float* dg,
                           float* dbeta, float* dS0, void* workspace, hipStream_t stream) {
-    const gdr::Args a = args_of(c);
-    const int64_t n = gdr::slots_of(c.nseq, c.T, c.cu != nullptr) * c.Hv;
-    const int64_t pb = gdr::prep_bytes(true);
-    char* prep = (char*)workspace;
-    char* ws_s = prep + n * pb;
-    char* ws_d = ws_s + n * gdr::state_bytes(c.dk, c.dv);
-    char* ws_e = ws_d + n * gdr::state_bytes(c.dk, c.dv);
-    char* ws_z = ws_e + n * gdr::rows_bytes(c.dv);
-    hipError_t e = gdr::launch_prep(c.f32, c.dk, true, a, c.q, c.k, c.g, c.beta, prep, stream);
-    if (e != hipSuccess) return e;
-    e = gdr::launch_chain(c.f32, c.dk, true, a, c.q, c.k, c.v, c.beta, c.S0, prep, pb, nullptr, nullptr, ws_s, ws_e, stream);
-    if (e != hipSuccess) return e;
-    e = gdr::launch_back(c.f32, c.dk, a, c.q, c.k, dout, c.beta, dS_T, prep, pb, dv, dS0, ws_d, ws_z, stream);
-    if (e != hipSuccess) return e;
-    return gdr::launch_grad(c.f32, c.dk, a, c.q, c.k, c.beta, dout, prep, ws_s, ws_e, ws_d, ws_z, dq, dk, dg, dbeta, stream);
+    const gdr::Args a = gdr::args_of(c);
+    const gdr::Plan p = gdr::plan_of(true, c.nseq, c.T, c.Hv, c.dk, c.dv, c.cu != nullptr);
+    char* ws = (char*)workspace;
+    float *maps = (float*)(ws + p.maps), *nmaps = (float*)(ws + p.nmaps);
+    float *starts = (float*)(ws + p.starts), *dstarts = (float*)(ws + p.dstarts);
+    KDA_DO(gdr::launch_prep(c.f32, c.dk, true, a, c.q, c.k, c.g, c.beta, ws + p.prep, stream));
+    if (p.sg.seg) {
+        KDA_DO(gdr::launch_map_chain(c.f32, c.dk, true, a, p.sg, c.k, c.v, ws + p.prep, maps, stream));
+        KDA_DO(gdr::launch_back_chain(c.f32, c.dk, true, a, p.sg, c.q, c.k, dout, nullptr, nullptr, ws + p.prep, nullptr,
+                                      nullptr, nullptr, nullptr, nmaps, stream));
+        KDA_DO(gdr::launch_join(c.f32, c.dk, false, a, p.sg, c.S0, maps, maps, starts, stream));
+        KDA_DO(gdr::launch_join(c.f32, c.dk, true, a, p.sg, dS_T, maps, nmaps, dstarts, stream));
+    }
+    KDA_DO(gdr::launch_save_chain(c.f32, c.dk, a, p.sg, c.k, c.v, c.S0, starts, ws + p.prep, ws + p.s, ws + p.e, stream));
+    KDA_DO(gdr::launch_back_chain(c.f32, c.dk, false, a, p.sg, c.q, c.k, dout, dS_T, dstarts, ws + p.prep, dv, dS0, ws + p.d,
+                                  ws + p.z, nullptr, stream));
+    return gdr::launch_grad(c.f32, c.dk, a, c.q, c.k, c.beta, dout, ws + p.prep, ws + p.s, ws + p.e, ws + p.d, ws + p.z, dq,
+                            dk, dg, dbeta, stream);
 }
 
 }  // namespace kda

@@ -142,11 +142,10 @@ grad_kernel(Args a, const E* __restrict__ q, const E* __restrict__ k, const floa
         const int64_t rec = (int64_t)slot * a.Hv + hk * rep + vh;
         const int h = hk * rep + vh;
         if (tid < C) {
-            const char* p = prep + rec * prep_bytes(true);
-            Gs[tid] = reinterpret_cast<const double*>(p + 4 * TRI_BYTES)[tid];
-            const float* f = reinterpret_cast<const float*>(p + prep_bytes(true) - 2 * C * 4);
+            const float* f = reinterpret_cast<const float*>(prep + rec * prep_bytes(true) + prep_factors(true));
             gam[tid] = f[tid];
-            om[tid] = f[C + tid];
+            om[tid] = f[2 * C + tid];
+            Gs[tid] = reinterpret_cast<const double*>(f + 3 * C)[tid];
             bts[tid] = tid < ch.valid ? beta[(ch.row0 + tid) * a.Hv + h] : 0.0f;
         }
         f32x4 dos[ST], zs[ST], eds[ST], xl[MT], wl[MT], xu[MT], wu[MT];
@@ -219,14 +218,14 @@ grad_kernel(Args a, const E* __restrict__ q, const E* __restrict__ k, const floa
                 const int o = 16 * n + 4 * g + i;
                 if (n <= w) {   // [s = o][t = tok]
                     const bool in = o <= tok;
-                    const float d = in ? expf((float)(Gt - Gs[o])) * bts[o] : 0.0f;
+                    const float d = in ? __builtin_amdgcn_exp2f((float)(Gt - Gs[o])) * bts[o] : 0.0f;
                     x[i] = in ? a.scale * d * xl[n][i] : 0.0f;
                     m[i] = o < tok ? -d * wl[n][i] : 0.0f;
                     dGp += x[i] * qkl[i] + m[i] * kkl[i];
                 }
                 if (n >= w) {   // [t = o][s = tok]
                     const bool in = tok <= o;
-                    const float d = in ? expf((float)(Gs[o] - Gt)) : 0.0f;
+                    const float d = in ? __builtin_amdgcn_exp2f((float)(Gs[o] - Gt)) : 0.0f;
                     x2[i] = in ? a.scale * d * xu[n][i] : 0.0f;
                     m2[i] = tok < o ? -d * wu[n][i] : 0.0f;
                     dGm += x2[i] * qku[i] + m2[i] * kku[i];
@@ -321,7 +320,7 @@ template <typename E, int DK>
 hipError_t grad_t(const Args& a, const void* q, const void* k, const float* beta, const void* dout, const char* prep,
                   const char* ws_s, const char* ws_e, const char* ws_d, const char* ws_z, void* dq, void* dk, float* dg,
                   float* dbeta, hipStream_t stream) {
-    const int64_t slots = slots_of(a.nseq, a.T, a.cu != nullptr);
+    const int64_t slots = places_of(a.nseq, a.T, a.cu != nullptr, C);
     hipLaunchKernelGGL((grad_kernel<E, DK>), dim3((unsigned)(slots * a.Hk)), dim3(256), 0, stream, a, (const E*)q, (const E*)k,
                        beta, (const E*)dout, prep, ws_s, ws_e, ws_d, ws_z, (E*)dq, (E*)dk, dg, dbeta);
     return hipGetLastError();

@@ -6,7 +6,7 @@
 // cores (exact bf16 inputs), P as K Q^T so that its result sits in the lanes as the
 // fragment that the chain reads.  Decays come from differences of the prefix sums in 64
 // bits: a strong decay early in the chunk would otherwise take digits from the weak ones
-// behind it.  X: the four diagonal 16 x 16 blocks by forward substitution in registers,
+// behind it (as powers of two, which is what the hardware exponential takes).  X: the four diagonal 16 x 16 blocks by forward substitution in registers,
 // one a wavefront, then X_mn = -X_mm sum_j M_mj X_jn block by block in fp32 on the fp32
 // matrix cores, m = 1, 2, 3, the blocks of one m on different wavefronts.
 #include "kda_gdr.hpp"
@@ -39,7 +39,11 @@ __device__ __forceinline__ void solve_rows(f32x4& x, const f32x4& m, int lane, i
     }
 }
 
-constexpr int LD = 68;   // row length of the fp32 tiles in LDS
+// 16 x 16 fp32 tiles in LDS: M's below the diagonal, X's on and below it.
+constexpr int LD = 20;
+constexpr int TILE = 16 * LD;
+__device__ __forceinline__ int m_tile(int m, int n) { return (m * (m - 1) / 2 + n) * TILE; }
+__device__ __forceinline__ int x_tile(int m, int n) { return (6 + m * (m + 1) / 2 + n) * TILE; }
 
 template <typename E, int DK, bool BWD>
 __global__ void __launch_bounds__(256)
@@ -47,10 +51,9 @@ prep_kernel(Args a, const E* __restrict__ q, const E* __restrict__ k, const floa
             const float* __restrict__ beta, char* __restrict__ ws) {
     typedef Arith<E> A;
     constexpr int KB = DK / 32;
-    __shared__ alignas(16) float Ms[C * LD];
-    __shared__ alignas(16) float Xs[C * LD];
-    __shared__ double Gs[C];
-    __shared__ float Bs[C];
+    __shared__ alignas(16) float tiles[16 * TILE];
+    __shared__ alignas(16) double Gs[C];   // prefix sums, in powers of two
+    __shared__ alignas(16) float Bs[C];
     const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int slot = (int)(blockIdx.x / (unsigned)a.Hv), h = (int)(blockIdx.x % (unsigned)a.Hv);
@@ -61,85 +64,100 @@ prep_kernel(Args a, const E* __restrict__ q, const E* __restrict__ k, const floa
     const E* kc = k + ch.row0 * ld + hk * DK + 8 * g;
     const E* qc = q + ch.row0 * ld + hk * DK + 8 * g;
     char* out = ws + (int64_t)blockIdx.x * prep_bytes(BWD);
+    const f32x4 zero = {0, 0, 0, 0};
 
-    if (w == 0) {   // prefix sums; past the chunk's end g = 0 and beta = 0: tokens that change nothing
-        const int64_t at = (ch.row0 + (lane < ch.valid ? lane : 0)) * a.Hv + h;
-        float gt = gate[at];
-        const float bt = beta[at];
-        gt = gt < -120.0f ? -120.0f : gt;   // e^-120 is zero in fp32 already; keeps -inf out of the differences
-        double G = lane < ch.valid ? (double)gt : 0.0;
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) {
-            const double up = __shfl_up(G, m);
-            if (lane >= m) G += up;
-        }
-        Gs[lane] = G;
-        Bs[lane] = lane < ch.valid ? bt : 0.0f;
-        const double end = __shfl(G, 63);
-        float* gm = reinterpret_cast<float*>(out + prep_bytes(BWD) - 2 * C * 4);
-        if (BWD) reinterpret_cast<double*>(out + 4 * TRI_BYTES)[lane] = G;
-        gm[lane] = expf((float)G);
-        gm[C + lane] = expf((float)(end - G));
-    }
+    const int64_t at = (ch.row0 + (lane < ch.valid ? lane : 0)) * a.Hv + h;
+    const float gt0 = gate[at], bt0 = beta[at];
     auto row = [&](int m) { return (int64_t)(16 * m + r < ch.valid ? 16 * m + r : ch.valid - 1) * ld; };
     typename A::Ex kw[KB], qw[KB];
 #pragma unroll
     for (int b = 0; b < KB; ++b) {
         kw[b] = A::ld_row(kc + row(w) + 32 * b);
-        qw[b] = A::ld_row(qc + row(w) + 32 * b);
+        if (!BWD) qw[b] = A::ld_row(qc + row(w) + 32 * b);
     }
-    const f32x4 zero = {0, 0, 0, 0};
-    f32x4 nn[MT], pp[MT], pt[MT];
+    if (w == 0) {   // past the chunk's end g = 0 and beta = 0: tokens that change nothing
+        const float gt = gt0 < -120.0f ? -120.0f : gt0;   // e^-120 is zero in fp32 already; keeps -inf out of the differences
+        double G = lane < ch.valid ? (double)gt * 1.4426950408889634074 : 0.0;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            const double up = __shfl_up(G, m);
+            if (lane >= m) G += up;
+        }
+        const float bt = lane < ch.valid ? bt0 : 0.0f;
+        Gs[lane] = G;
+        Bs[lane] = bt;
+        const double end = __shfl(G, 63);
+        const float om = __builtin_amdgcn_exp2f((float)(end - G));
+        float* f = reinterpret_cast<float*>(out + prep_factors(BWD));
+        f[lane] = __builtin_amdgcn_exp2f((float)G);
+        f[C + lane] = om * bt;
+        if (BWD) {
+            f[2 * C + lane] = om;
+            reinterpret_cast<double*>(f + 3 * C)[lane] = G;
+        }
+    }
+    f32x4 nn[MT], pp[MT];   // K K^T: rows tokens of w, columns of n; P transposed (see below)
 #pragma unroll
     for (int n = 0; n < MT; ++n) {
-        nn[n] = pp[n] = pt[n] = zero;
+        nn[n] = pp[n] = zero;
         if (n <= w) {
 #pragma unroll
             for (int b = 0; b < KB; ++b) {
                 const typename A::Ex kn = A::ld_row(kc + row(n) + 32 * b);
-                nn[n] = A::mma(kw[b], kn, nn[n]);   // rows tokens of w, columns tokens of n
-                pp[n] = A::mma(kn, qw[b], pp[n]);   // rows keys of n, columns queries of w
+                nn[n] = A::mma(kw[b], kn, nn[n]);
+                if (!BWD) pp[n] = A::mma(kn, qw[b], pp[n]);   // rows keys of n, columns queries of w
             }
         }
         if (BWD && n >= w) {
 #pragma unroll
             for (int b = 0; b < KB; ++b)
-                pt[n] = A::mma(A::ld_row(qc + row(n) + 32 * b), kw[b], pt[n]);   // rows queries of n, columns keys of w
+                pp[n] = A::mma(A::ld_row(qc + row(n) + 32 * b), kw[b], pp[n]);   // rows queries of n, columns keys of w
         }
     }
     __syncthreads();
     f32x4 md = zero;
+    const double Gr = Gs[16 * w + r];
+    double Gw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) Gw[i] = Gs[16 * w + 4 * g + i];
 #pragma unroll
     for (int n = 0; n < MT; ++n) {
+        const double Gn = Gs[16 * n + r];
         if (n <= w) {
+            f32x4 m4;
+            const float bs = Bs[16 * n + r];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = 16 * w + 4 * g + i, s = 16 * n + r;
-                const bool in = s < t;
-                const float d = expf(in ? (float)(Gs[t] - Gs[s]) : 0.0f);
-                const float m = in ? d * nn[n][i] * Bs[s] : 0.0f;
-                Ms[t * LD + s] = m;
-                if (n == w) md[i] = m;
-                const int t2 = 16 * w + r, s2 = 16 * n + 4 * g + i;
-                const bool in2 = s2 <= t2;
-                const float d2 = expf(in2 ? (float)(Gs[t2] - Gs[s2]) : 0.0f);
-                pp[n][i] = in2 && t2 < ch.valid ? a.scale * d2 * pp[n][i] : 0.0f;
+            for (int i = 0; i < 4; ++i) {   // M of token 16 w + 4 g + i on token 16 n + r
+                const bool in = 16 * n + r < 16 * w + 4 * g + i;
+                const float d = __builtin_amdgcn_exp2f(in ? (float)(Gw[i] - Gn) : 0.0f);
+                m4[i] = in ? d * nn[n][i] * bs : 0.0f;
+            }
+            if (n == w) {
+                md = m4;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tiles[m_tile(w, n) + (4 * g + i) * LD + r] = m4[i];
             }
         }
-        if (BWD && n >= w) {
+        if (BWD ? n >= w : n <= w) {
+            const f32x4 b4 = *reinterpret_cast<const f32x4*>(&Bs[16 * n + 4 * g]);
+            const float br = Bs[16 * w + r];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int t = 16 * n + 4 * g + i, s = 16 * w + r;
-                const bool in = s <= t;
-                const float d = expf(in ? (float)(Gs[t] - Gs[s]) : 0.0f);
-                pt[n][i] = in && t < ch.valid ? a.scale * d * pt[n][i] : 0.0f;
+                // the lane's token, 16 w + r, against token o: the query (forward) or the key
+                const int o = 16 * n + 4 * g + i, t = 16 * w + r;
+                const bool in = BWD ? t <= o : o <= t;
+                const double df = BWD ? Gs[o] - Gr : Gr - Gs[o];
+                const float d = __builtin_amdgcn_exp2f(in ? (float)df : 0.0f);
+                const float x = a.scale * d * pp[n][i] * (BWD ? br : b4[i]);
+                pp[n][i] = in && (BWD ? o : t) < ch.valid ? x : 0.0f;
             }
         }
     }
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-        if (b <= w / 2) A::st_sp(out + TRI_BYTES, lower_block(w, b), lane, A::split(pp[2 * b], pp[2 * b + 1]));
-        if (BWD && b >= w / 2) A::st_sp(out + 3 * TRI_BYTES, upper_block(w, b), lane, A::split(pt[2 * b], pt[2 * b + 1]));
+        if (!BWD && b <= w / 2) A::st_sp(out + TRI_BYTES, lower_block(w, b), lane, A::split(pp[2 * b], pp[2 * b + 1]));
+        if (BWD && b >= w / 2) A::st_sp(out + 2 * TRI_BYTES, upper_block(w, b), lane, A::split(pp[2 * b], pp[2 * b + 1]));
     }
     // the diagonal block of X
     f32x4 x;
@@ -150,42 +168,41 @@ prep_kernel(Args a, const E* __restrict__ q, const E* __restrict__ k, const floa
     solve_rows<2>(x, md, lane, g);
     solve_rows<3>(x, md, lane, g);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) Xs[(16 * w + 4 * g + i) * LD + 16 * w + r] = x[i];
-    __syncthreads();
+    for (int i = 0; i < 4; ++i) tiles[x_tile(w, w) + (4 * g + i) * LD + r] = x[i];
+    lds_barrier();
     // the blocks below it, row of blocks by row of blocks
     for (int m = 1; m < MT; ++m) {
         if (w < m) {
             f32x4 y = zero;
             for (int j = w; j < m; ++j) {
-                const f32x4 mm = *reinterpret_cast<const f32x4*>(&Ms[(16 * m + r) * LD + 16 * j + 4 * g]);
+                const f32x4 mm = *reinterpret_cast<const f32x4*>(&tiles[m_tile(m, j) + r * LD + 4 * g]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y = mfma_k4(mm[i], Xs[(16 * j + 4 * g + i) * LD + 16 * w + r], y);
+                for (int i = 0; i < 4; ++i) y = mfma_k4(mm[i], tiles[x_tile(j, w) + (4 * g + i) * LD + r], y);
             }
-            const f32x4 xm = *reinterpret_cast<const f32x4*>(&Xs[(16 * m + r) * LD + 16 * m + 4 * g]);
+            const f32x4 xm = *reinterpret_cast<const f32x4*>(&tiles[x_tile(m, m) + r * LD + 4 * g]);
             f32x4 z = zero;
 #pragma unroll
             for (int i = 0; i < 4; ++i) z = mfma_k4(xm[i], y[i], z);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) Xs[(16 * m + 4 * g + i) * LD + 16 * w + r] = -z[i];
+            for (int i = 0; i < 4; ++i) tiles[x_tile(m, w) + (4 * g + i) * LD + r] = -z[i];
         }
-        __syncthreads();
+        lds_barrier();
     }
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
         if (b <= w / 2) {
-            const float* p = &Xs[(16 * w + r) * LD + 32 * b + 4 * g];
-            const f32x4 lo = *reinterpret_cast<const f32x4*>(p);
-            const f32x4 hi = 2 * b + 1 <= w ? *reinterpret_cast<const f32x4*>(p + 16) : zero;
+            const f32x4 lo = *reinterpret_cast<const f32x4*>(&tiles[x_tile(w, 2 * b) + r * LD + 4 * g]);
+            const f32x4 hi = 2 * b + 1 <= w ? *reinterpret_cast<const f32x4*>(&tiles[x_tile(w, 2 * b + 1) + r * LD + 4 * g]) : zero;
             A::st_sp(out, lower_block(w, b), lane, A::split(lo, hi));
         }
         if (BWD && b >= w / 2) {
             f32x4 lo = zero, hi;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if (2 * b >= w) lo[i] = Xs[(32 * b + 4 * g + i) * LD + 16 * w + r];
-                hi[i] = Xs[(32 * b + 16 + 4 * g + i) * LD + 16 * w + r];
+                if (2 * b >= w) lo[i] = tiles[x_tile(2 * b, w) + (4 * g + i) * LD + r];
+                hi[i] = tiles[x_tile(2 * b + 1, w) + (4 * g + i) * LD + r];
             }
-            A::st_sp(out + 2 * TRI_BYTES, upper_block(w, b), lane, A::split(lo, hi));
+            A::st_sp(out + TRI_BYTES, upper_block(w, b), lane, A::split(lo, hi));
         }
     }
 }
@@ -205,7 +222,7 @@ hipError_t prep_t(bool bwd, const Args& a, int64_t slots, const void* q, const v
 
 hipError_t launch_prep(bool f32, int dk, bool bwd, const Args& a, const void* q, const void* k, const float* g,
                        const float* beta, char* ws, hipStream_t stream) {
-    const int64_t slots = slots_of(a.nseq, a.T, a.cu != nullptr);
+    const int64_t slots = places_of(a.nseq, a.T, a.cu != nullptr, C);
 #define KDA_GP(E, D) return prep_t<E, D>(bwd, a, slots, q, k, g, beta, ws, stream)
     if (f32) {
         switch (dk) {

@@ -205,6 +205,29 @@ def test_many_workgroups(dk, dv):
 
 @pytest.mark.gpu
 @both
+@pytest.mark.parametrize("lens,Hk,Hv,dk,dv", [
+    ([1500], 1, 2, 64, 64), ([1217], 1, 1, 128, 128), ([30, 1300, 0, 1153, 64], 1, 2, 32, 96), ([1200, 1160], 2, 2, 64, 160)])
+def test_cut_sequences(lens, Hk, Hv, dk, dv, dtype):
+    """Few heads over sequences of more than 18 chunks: walked in pieces of eight chunks joined
+    by their maps, beside sequences that are not cut."""
+    x, cu = make(lens, Hk, Hv, dk, dv, dtype, sum(lens), head=5, tail=2, gmu=-5.0)
+    check(x, cu, dk ** -0.5, dtype)
+
+
+@pytest.mark.gpu
+def test_cut_sequence_in_place():
+    """The last piece writes S_T while the first has yet to read S0: one buffer for both."""
+    x, cu = make([1400], 1, 2, 64, 64, torch.bfloat16, 31, gmu=-6.0)
+    o, S = run_fwd(x, cu, 1.0)
+    d = to(x)
+    for _ in range(3):
+        S2 = d["S0"].clone()
+        o2, _ = kda.kda_gdr_chunk_fwd(*(d[k] for k in ("q", "k", "v", "g", "beta")), S2, S_T=S2, scale=1.0)
+        assert torch.equal(o, o2) and torch.equal(S, S2)
+
+
+@pytest.mark.gpu
+@both
 def test_state_in_place_and_resumed(dtype):
     """A sequence in two calls, the second from the first's state written over its start state."""
     x, cu = make([200], 1, 2, 64, 64, dtype, 16)
@@ -433,6 +456,7 @@ def test_refusals(lib, which):
     need = size(2, 100, 2, 64, 64, True)
     assert call(ws_bytes=need - 1) == 5 and call(ws=None) == 5
     assert call(cu=None, ws_bytes=size(2, 100, 2, 64, 64, False) - 1) == 5
+    assert call(Hk=1 << 18, Hv=1 << 18) == 2            # a chunk's rows past 32-bit offsets
     assert call(q=a["q"] + 8) == 4 and call(cu=a["cu"] + 4) == 4
     if which == "fwd":
         assert call(o=a["v"]) == 6 and call(o=a["S_T"]) == 6 and call(S_T=a["S0"] + 16) == 6 and call(ws=a["cu"]) == 6
@@ -447,9 +471,13 @@ def test_workspace_sizes(lib):
     assert f(3, 64, 2, 64, 64) == f(3, 1, 2, 64, 64) == f(1, 192, 2, 64, 64)
     assert f(3, 65, 2, 64, 64) == 2 * f(3, 64, 2, 64, 64)
     assert f(4, 128, 2, 64, 64, True) == f(6, 64, 2, 64, 64)
+    # long sequences of few heads are cut: pieces of 64 chunks here, each with its map and start state
+    one = f(1, 64, 1, 128, 128)
+    assert f(1, 65536, 16, 128, 128) == 16 * (1024 * one + 16 * (128 * 256 + 128 * 128) * 4)
+    assert f(64, 4096, 16, 128, 128) == 64 * 64 * 16 * one
     b = kda.kda_gdr_chunk_bwd_workspace_size
-    # X, P and their transposes, two states and two token operands, 4 bytes a value
-    assert b(1, 64, 1, 128, 128) == 4 * 6 * 2048 + 512 + 512 + 2 * 4 * 128 * 128 + 2 * 4 * 64 * 128
+    # X, its transpose and P's, the tokens' factors, two states and two token operands
+    assert b(1, 64, 1, 128, 128) == 3 * 6 * 2048 + 3 * 256 + 512 + 2 * 4 * 128 * 128 + 2 * 4 * 64 * 128
     with pytest.raises(kda.KdaError):
         f(0, 64, 2, 64, 64)
     with pytest.raises(kda.KdaError):
