@@ -412,7 +412,7 @@ int kda_gdr_step(int dtype, int B, int T, int Hk, int Hv, int dk, int dv, int ns
     if (st) return st;
     if (nslot < 1 || (!slots && nslot < B))
         return fail(KDA_ERR_SHAPE, "nslot=%d states for B=%d rows%s", nslot, B, slots ? "" : " without slots");
-    if (!sizes_fit(nslot, Hv, dk, dv) || (int64_t)B * Hv * (dv / 32) > 0x7fffffffLL)
+    if (!sizes_fit(nslot, Hv, dk, dv) || (int64_t)B * Hv * (dv / 32) >= 1LL << 26)   // workgroups of 64 threads
         return fail(KDA_ERR_SHAPE, "B*Hv or nslot*Hv too large");
     if (!q || !k || !v || !g || !beta || !S || !o)
         return fail(KDA_ERR_NULL, "q, k, v, g, beta, S and o must be non-NULL");
@@ -431,9 +431,10 @@ int kda_gdr_step(int dtype, int B, int T, int Hk, int Hv, int dk, int dv, int ns
 static int check_gdr_chunk(int dtype, int nseq, int T, int Hk, int Hv, int dk, int dv, float scale, bool packed) {
     int st = check_gdr(dtype, nseq, T, Hk, Hv, dk, dv, scale);
     if (st) return st;
-    // chunk places times heads are workgroups of one launch
+    // a launch has at most 2^32 threads: one workgroup of 256 a chunk and head, up to eight of
+    // 512 a sequence and head
     const int64_t slots = packed ? (int64_t)T / 64 + nseq : (int64_t)nseq * (((int64_t)T + 63) / 64);
-    if (slots > 0x7fffffffLL / Hv || (int64_t)nseq * Hv > 0x7fffffffLL / 8)
+    if (slots >= (1LL << 24) / Hv || (int64_t)nseq * Hv >= 1LL << 20)
         return fail(KDA_ERR_SHAPE, "sequences*chunks*Hv too large");
     // a chunk of one tensor, 64*H*d*4 bytes at most, is addressed with 32-bit offsets
     if ((int64_t)Hk * dk >= (1LL << 23) || (int64_t)Hv * dv >= (1LL << 23))

@@ -3,10 +3,10 @@
 // A chunk is 64 tokens.  With S the state at its start, G_t the sum of g over its tokens
 // up to t, gam = e^G, om_t = e^(G_end - G_t) and D_ts = e^(G_t - G_s):
 //     N_ts = D_ts k_t.k_s (s < t),   X = (I + N diag(beta))^-1,   e = X (V - gam (K S))
-//     P_ts = scale D_ts q_t.k_s (s <= t),   O = scale gam (Q S) + P (beta e)
+//     P_ts = scale D_ts q_t.k_s beta_s (s <= t),   O = scale gam (Q S) + P e
 //     S'   = gam_end S + K^T (om beta e)
 // and backwards, dS' being the gradient at the chunk's end:
-//     dU = P^T dO + om (K dS'),   Z = X^T (beta dU) = dV
+//     Z = X^T (P^T dO + om beta (K dS')) = dV
 //     dS = gam_end dS' + scale Q^T (gam dO) - K^T (gam Z)
 // No factor exceeds one for g <= 0, so the decay needs no bound.
 //
@@ -146,25 +146,32 @@ __device__ __forceinline__ Piece piece_at(const Args& a, const Segs& sg, int pla
 }
 
 // ---------------------------------------------------------------- operands
+// Where lane (g, r)'s 16 bytes of a natural block of q or k lie in LDS: row r of group g at
+// r ^ 4 g, so that the transposed reads, which take a row of every group, spread over the banks.
+__device__ __forceinline__ int swz(int lane) { return lane ^ ((lane >> 4) << 2); }
+
 template <typename E> struct Arith;
 
 template <> struct Arith<bf16> {
     typedef bf16x8 Ex;                        // an operand that is exact in bf16
     struct Sp { bf16x8 hi, lo; };             // an fp32 operand in two halves
     static constexpr int EXB = 1024;          // bytes of an exact block
+    // Two values as the halves of their split: (upper pair, lower pair).  Six instructions: two
+    // packed conversions, the upper halves back as floats, two differences.
+    static __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+        hi = __builtin_bit_cast(uint32_t, bf16x2{(bf16)a, (bf16)b});
+        asm("" : "+v"(hi));   // one conversion for both values, not another one for the upper half of each
+        const float ha = __builtin_bit_cast(float, hi << 16), hb = __builtin_bit_cast(float, hi & 0xffff0000u);
+        lo = __builtin_bit_cast(uint32_t, bf16x2{(bf16)(a - ha), (bf16)(b - hb)});
+    }
     static __device__ __forceinline__ Sp split(f32x4 a, f32x4 b) {
-        Sp s;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            s.hi[i] = (bf16)a[i];
-            s.hi[4 + i] = (bf16)b[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            s.lo[i] = (bf16)(a[i] - (float)s.hi[i]);
-            s.lo[4 + i] = (bf16)(b[i] - (float)s.hi[4 + i]);
-        }
-        return s;
+        u32x4 h, l;
+        uint32_t x, y;
+        split2(a[0], a[1], x, y); h[0] = x; l[0] = y;
+        split2(a[2], a[3], x, y); h[1] = x; l[1] = y;
+        split2(b[0], b[1], x, y); h[2] = x; l[2] = y;
+        split2(b[2], b[3], x, y); h[3] = x; l[3] = y;
+        return Sp{__builtin_bit_cast(bf16x8, h), __builtin_bit_cast(bf16x8, l)};
     }
     static __device__ __forceinline__ f32x4 mma(Ex a, Ex b, f32x4 c) { return mfma_k32(a, b, c); }
     static __device__ __forceinline__ f32x4 mma(Ex a, const Sp& b, f32x4 c) { return mfma_k32(a, b.hi, mfma_k32(a, b.lo, c)); }
@@ -172,8 +179,24 @@ template <> struct Arith<bf16> {
     static __device__ __forceinline__ f32x4 mma(const Sp& a, const Sp& b, f32x4 c) {
         return mfma_k32(a.hi, b.hi, mfma_k32(a.hi, b.lo, mfma_k32(a.lo, b.hi, c)));
     }
+    // The same for N accumulators: one half's product of each before the next, so that no
+    // instruction waits for the one before it.
+    template <int N>
+    static __device__ __forceinline__ void mma_n(const Ex (&a)[N], const Sp& b, f32x4 (&c)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) c[i] = mfma_k32(a[i], b.lo, c[i]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) c[i] = mfma_k32(a[i], b.hi, c[i]);
+    }
+    template <int N>
+    static __device__ __forceinline__ void mma_n(const Sp& a, const Ex (&b)[N], f32x4 (&c)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) c[i] = mfma_k32(a.lo, b[i], c[i]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) c[i] = mfma_k32(a.hi, b[i], c[i]);
+    }
     static __device__ __forceinline__ Ex ld_ex(const char* base, int blk, int lane) {
-        return *reinterpret_cast<const bf16x8*>(base + blk * EXB + lane * 16);
+        return *reinterpret_cast<const bf16x8*>(base + blk * EXB + swz(lane) * 16);
     }
     static __device__ __forceinline__ Sp ld_sp(const char* base, int blk, int lane) {
         const char* p = base + blk * SPB + lane * 16;
@@ -198,8 +221,14 @@ template <> struct Arith<bf16> {
     // rows, the 32 tokens of block tb as accumulator slots.
     template <int KB>
     static __device__ __forceinline__ Ex ld_ex_t(const char* base, int kb, int h, int tb, int g, int r) {
-        const int at = ((r & 3) * 16 + 4 * g + (r >> 2)) * 16 + h * 8;
+        const int at = swz((r & 3) * 16 + 4 * g + (r >> 2)) * 16 + h * 8;
         return cat8(ld_tr(base + ((2 * tb) * KB + kb) * EXB + at), ld_tr(base + ((2 * tb + 1) * KB + kb) * EXB + at));
+    }
+    // Row tile n of the transpose of a lower triangular split operand, columns of block tb.
+    static __device__ __forceinline__ Sp ld_tri_t(const char* base, int n, int tb, int g, int r) {
+        const int at = ((r & 3) * 16 + 4 * g + (r >> 2)) * 16 + (n & 1) * 8;
+        const char *a = base + lower_block(2 * tb, n / 2) * SPB + at, *b = base + lower_block(2 * tb + 1, n / 2) * SPB + at;
+        return Sp{cat8(ld_tr(a), ld_tr(b)), cat8(ld_tr(a + 1024), ld_tr(b + 1024))};
     }
     // Tokens 16 m + 4 g + i of column col + r of a row-major tile with `ld` columns.
     static __device__ __forceinline__ f32x4 ld_col(const char* base, int ld, int m, int col, int g, int r) {
@@ -259,12 +288,22 @@ template <> struct Arith<float> {
         for (int i = 0; i < 4; ++i) c = mfma_k4(x.b[i], y.b[i], c);
         return c;
     }
+    template <int N>
+    static __device__ __forceinline__ void mma_n(const Ex (&a)[N], const Ex& b, f32x4 (&c)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) c[i] = mma(a[i], b, c[i]);
+    }
+    template <int N>
+    static __device__ __forceinline__ void mma_n(const Ex& a, const Ex (&b)[N], f32x4 (&c)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) c[i] = mma(a, b[i], c[i]);
+    }
     // a block is two planes of 16 bytes a lane: slots 0..3 and 4..7
-    static __device__ __forceinline__ Ex ld_ex(const char* base, int blk, int lane) {
+    static __device__ __forceinline__ Ex ld_ex(const char* base, int blk, int lane) { return ld_sp(base, blk, swz(lane)); }
+    static __device__ __forceinline__ Sp ld_sp(const char* base, int blk, int lane) {
         const char* p = base + blk * SPB + lane * 16;
         return Ex{*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 1024)};
     }
-    static __device__ __forceinline__ Sp ld_sp(const char* base, int blk, int lane) { return ld_ex(base, blk, lane); }
     static __device__ __forceinline__ void st_sp(char* base, int blk, int lane, const Sp& s) {
         char* p = base + blk * SPB + lane * 16;
         *reinterpret_cast<f32x4*>(p) = s.a;
@@ -281,9 +320,19 @@ template <> struct Arith<float> {
         Ex x;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int at = h * 1024 + ((r >> 2) * 16 + 4 * g + i) * 16 + (r & 3) * 4;
+            const int at = h * 1024 + swz((r >> 2) * 16 + 4 * g + i) * 16 + (r & 3) * 4;
             x.a[i] = *reinterpret_cast<const float*>(base + ((2 * tb) * KB + kb) * SPB + at);
             x.b[i] = *reinterpret_cast<const float*>(base + ((2 * tb + 1) * KB + kb) * SPB + at);
+        }
+        return x;
+    }
+    static __device__ __forceinline__ Sp ld_tri_t(const char* base, int n, int tb, int g, int r) {
+        Sp x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = (n & 1) * 1024 + ((r >> 2) * 16 + 4 * g + i) * 16 + (r & 3) * 4;
+            x.a[i] = *reinterpret_cast<const float*>(base + lower_block(2 * tb, n / 2) * SPB + at);
+            x.b[i] = *reinterpret_cast<const float*>(base + lower_block(2 * tb + 1, n / 2) * SPB + at);
         }
         return x;
     }
@@ -331,12 +380,9 @@ __device__ __forceinline__ typename Arith<E>::Ex pick_half(int h, int g, int r) 
 }
 
 // ---------------------------------------------------------------- workspace
-// A chunk of one head.  Forward: X and P diag(beta) as split blocks, then gam and om beta.
-// Backward: X, X^T and diag(beta) P^T, then gam, om beta and om, and G log2(e) in 64 bits.
-__host__ __device__ constexpr int64_t prep_bytes(bool bwd) {
-    return bwd ? 3 * (int64_t)TRI_BYTES + 3 * C * 4 + C * 8 : 2 * (int64_t)TRI_BYTES + 2 * C * 4;
-}
-__host__ __device__ constexpr int64_t prep_factors(bool bwd) { return (bwd ? 3 : 2) * (int64_t)TRI_BYTES; }
+// A chunk of one head: X as split blocks, then per token gam, om beta, om, beta, and
+// G log2(e) in 64 bits.
+constexpr int PREP_BYTES = TRI_BYTES + 4 * C * 4 + C * 8;
 // The map of a piece of one head, [dk][dv + dk] fp32: N, then M.
 __host__ __device__ constexpr int64_t map_bytes(int dk, int dv) { return (int64_t)dk * (dv + dk) * 4; }
 // The backward pass's records of a chunk of one head: a state (dk / 16 by dv / 32 blocks,

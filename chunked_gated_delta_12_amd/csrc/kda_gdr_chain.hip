@@ -12,12 +12,13 @@
 // flight in registers under this chunk's products, one barrier a chunk.  Loads go through
 // buffer resources that end with the chunk's last token, so a part chunk reads zeros.
 //   forwards:   e = X (V - gam (K S));  S <- gam_end S + K^T (om beta e)
-//               O^T = scale gam (S^T Q^T) + e^T (P diag(beta))^T
-//   backwards:  Z = X^T (om beta (K dS) + (diag(beta) P^T) dO)
+//               O^T = scale gam (S^T Q^T) + e^T P^T
+//   backwards:  Z = X^T (om beta (K dS) + P^T dO)
 //               dS <- gam_end dS + Q^T (scale gam dO) - K^T (gam Z)
-// K^T and Q^T are read from the same blocks as K and Q with the transposing LDS read.  A
-// chunk's outputs are stored at the start of the next one: behind the loads they would be
-// waited for at the loop's end.
+// K^T, Q^T and X^T are read from the same blocks as K, Q and X with the transposing LDS read.
+// P is formed here, its tiles spread over the wavefronts: read from memory it would be a fifth
+// of the chunk's bytes.  A chunk's outputs are stored at the start of the next one: behind the
+// loads they would be waited for at the loop's end.
 #include "kda_gdr.hpp"
 #include "kda_launch.hpp"
 
@@ -28,23 +29,24 @@ namespace {
 
 enum Mode { FWD, SAVE, MAP, BACK, BMAP };
 
-// LDS of one buffer: K, Q, X (or X^T), P (or P^T), the value rows and the factors.
+// LDS of one buffer: K, Q, the chunk's record (X and the factors) and the value rows; P once.
 template <typename E, int DK, int NW, int MODE>
 struct Lay {
     static constexpr int KB = DK / 32, NTHR = 64 * NW, SLAB = 16 * NW;
-    static constexpr bool BWD = MODE >= BACK;                      // rows of dO and P^T instead of V and P
+    static constexpr bool BWD = MODE >= BACK;                      // rows of dO instead of V
     static constexpr bool HAS_Q = MODE == FWD || BWD, HAS_P = HAS_Q;
     static constexpr int QK = MT * KB * Arith<E>::EXB;
-    static constexpr int XP = (HAS_P ? 2 : 1) * TRI_BYTES;
     // a row of values: 32 bytes more than its columns, so that the rows of a transposing read
     // spread over the banks
     static constexpr int VLD = SLAB + 32 / (int)sizeof(E), VROW = SLAB * (int)sizeof(E) / 16, VB = C * VLD * (int)sizeof(E);
-    static constexpr int Q_AT = QK, X_AT = Q_AT + (HAS_Q ? QK : 0), P_AT = X_AT + TRI_BYTES, V_AT = X_AT + XP, F_AT = V_AT + VB,
-                         BYTES = F_AT + 2 * C * 4;
-    static constexpr int BUFS = 2 * BYTES <= 160 * 1024 ? 2 : 1;
+    static constexpr int Q_AT = QK, X_AT = Q_AT + (HAS_Q ? QK : 0), F_AT = X_AT + TRI_BYTES, V_AT = X_AT + PREP_BYTES,
+                         BYTES = V_AT + VB, PB = HAS_P ? TRI_BYTES : 0;
+    static constexpr int BUFS = 2 * BYTES + PB <= 160 * 1024 ? 2 : 1;
     // 16-byte pieces, and how many of them a thread moves
-    static constexpr int PQK = QK / 16, PXP = XP / 16, PV = C * VROW;
+    static constexpr int PQK = QK / 16, PXP = PREP_BYTES / 16, PV = C * VROW;
     static constexpr int NQK = (PQK + NTHR - 1) / NTHR, NXP = (PXP + NTHR - 1) / NTHR, NV = (PV + NTHR - 1) / NTHR;
+    // bf16 rows leave through LDS, in the buffer that the chunk is done with
+    static constexpr bool ROWS = (MODE == FWD || MODE == BACK) && sizeof(E) == 2 && BUFS == 2;
 };
 
 __device__ __forceinline__ u32x4 buf_ld128(Rsrc s, uint32_t off) {
@@ -57,7 +59,6 @@ template <typename E, int DK, int NW, int MODE>
 struct Stage {
     typedef Lay<E, DK, NW, MODE> L;
     u32x4 k[L::NQK], q[L::NQK], x[L::NXP], v[L::NV];
-    float f;
     uint32_t kq_off[L::NQK], v_off[L::NV];   // byte offsets in a chunk's rows, the same for every chunk
 
     __device__ __forceinline__ void init(int64_t ldk, int64_t ldv, int ncol) {
@@ -77,22 +78,16 @@ struct Stage {
         }
     }
 
-    __device__ __forceinline__ void load(Rsrc kr, Rsrc qr, Rsrc vr, const char* x0, const char* p0, const float* fac) {
-        const int tid = threadIdx.x;
+    __device__ __forceinline__ void load(Rsrc kr, Rsrc qr, Rsrc vr, Rsrc xr) {
 #pragma unroll
         for (int j = 0; j < L::NQK; ++j) {
             k[j] = buf_ld128(kr, kq_off[j]);
             if constexpr (L::HAS_Q) q[j] = buf_ld128(qr, kq_off[j]);
         }
 #pragma unroll
-        for (int j = 0; j < L::NXP; ++j) {
-            const int u = tid + j * L::NTHR;
-            const char* p = u < TRI_BYTES / 16 ? x0 + u * 16 : p0 + (u - TRI_BYTES / 16) * 16;
-            if (L::PXP % L::NTHR == 0 || u < L::PXP) x[j] = *reinterpret_cast<const u32x4*>(p);
-        }
+        for (int j = 0; j < L::NXP; ++j) x[j] = buf_ld128(xr, (uint32_t)(threadIdx.x + j * L::NTHR) * 16);
 #pragma unroll
         for (int j = 0; j < L::NV; ++j) v[j] = buf_ld128(vr, v_off[j]);
-        if (L::NTHR == 2 * C || tid < 2 * C) f = fac[tid];
     }
 
     __device__ __forceinline__ void store(char* buf) const {
@@ -101,8 +96,9 @@ struct Stage {
         for (int j = 0; j < L::NQK; ++j) {
             const int u = tid + j * L::NTHR;
             if (L::PQK % L::NTHR == 0 || u < L::PQK) {
-                *reinterpret_cast<u32x4*>(buf + u * 16) = k[j];
-                if constexpr (L::HAS_Q) *reinterpret_cast<u32x4*>(buf + L::Q_AT + u * 16) = q[j];
+                const int at = ((u & ~63) + swz(u & 63)) * 16;
+                *reinterpret_cast<u32x4*>(buf + at) = k[j];
+                if constexpr (L::HAS_Q) *reinterpret_cast<u32x4*>(buf + L::Q_AT + at) = q[j];
             }
         }
 #pragma unroll
@@ -116,7 +112,6 @@ struct Stage {
             if (L::PV % L::NTHR == 0 || u < L::PV)
                 *reinterpret_cast<u32x4*>(buf + L::V_AT + (u / L::VROW) * L::VLD * (int)sizeof(E) + (u % L::VROW) * 16) = v[j];
         }
-        if (L::NTHR == 2 * C || tid < 2 * C) reinterpret_cast<float*>(buf + L::F_AT)[tid] = f;
     }
 };
 
@@ -125,12 +120,12 @@ struct Ptrs {
     const float* init;          // [nseq] states (or their gradients) or NULL
     const float* starts;        // those of the pieces of cut sequences, [piece place][Hv][dk][dv]
     const char* prep;
-    int64_t prep_stride;
     void* out;                  // o; dv where the walk is backwards
     float* last;                // S_T or dS0, or NULL
     char *ws_s, *ws_e;          // SAVE, BACK: the chunks' states and rows
     float* maps;                // MAP: [piece place][Hv][dk][dv + dk]; BMAP: [..][dk][dv]
     bool all;
+    int places;
 };
 
 template <typename E, int DK, int NW, int MODE>
@@ -140,14 +135,19 @@ chain_kernel(Args a, Segs sg, Ptrs io) {
     typedef Lay<E, DK, NW, MODE> L;
     constexpr int KB = L::KB, ST = DK / 16;
     constexpr bool BWD = L::BWD;
-    __shared__ alignas(16) char lds[L::BUFS * L::BYTES];
+    __shared__ alignas(16) char lds[L::BUFS * L::BYTES + L::PB];
+    char* const pl = lds + L::BUFS * L::BYTES;   // P
     const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int ncols = MODE == MAP ? a.dv + DK : a.dv;
     const int nslab = (ncols + L::SLAB - 1) / L::SLAB;
-    const int slab = (int)(blockIdx.x % (unsigned)nslab);
-    const int h = (int)(blockIdx.x / (unsigned)nslab % (unsigned)a.Hv);
-    const int place = (int)(blockIdx.x / (unsigned)nslab / (unsigned)a.Hv);
+    // Workgroups go to the eight XCDs in turn: those of one key head's value heads and slabs,
+    // which read the same K and Q, are eight apart and share one XCD's L2.
+    const unsigned inner = (unsigned)(a.Hv / a.Hk * nslab), grp = blockIdx.x / (8 * inner), in8 = blockIdx.x % (8 * inner);
+    const unsigned outer = grp * 8 + in8 % 8, sub = in8 / 8;
+    const int place = (int)(outer / (unsigned)a.Hk), hk = (int)(outer % (unsigned)a.Hk);
+    const int h = hk * (a.Hv / a.Hk) + (int)(sub / (unsigned)nslab), slab = (int)(sub % (unsigned)nslab);
+    if (place >= io.places) return;
     const Piece pc = piece_at(a, sg, place, lane);
     if (pc.n < 0) return;
     // maps: forwards of every piece but the last one (all where both directions are joined),
@@ -155,7 +155,6 @@ chain_kernel(Args a, Segs sg, Ptrs io) {
     if (MODE == MAP && (pc.cnt < 2 || (!io.all && pc.i + 1 == pc.cnt))) return;
     if (MODE == BMAP && pc.i == 0) return;
     const int nch = pc.c1 - pc.c0;
-    const int hk = h / (a.Hv / a.Hk);
     const int64_t ldk = (int64_t)a.Hk * DK, ldv = (int64_t)a.Hv * a.dv;
     const int c0 = slab * L::SLAB, col0 = c0 + w * 16;   // the slab's and the wavefront's first column
     const bool act = col0 < ncols;
@@ -181,6 +180,10 @@ chain_kernel(Args a, Segs sg, Ptrs io) {
             }
     }
 
+    // The start state has arrived before the loop: otherwise the loop would wait for its loads
+    // anew in every iteration, and so for the chunk that it has just asked for.
+#pragma unroll
+    for (int t = 0; t < ST; ++t) asm volatile("" : "+v"(S[t]));
     Stage<E, DK, NW, MODE> st;
     st.init(ldk, ldv, a.dv - c0);
     auto load = [&](int c) {
@@ -192,20 +195,41 @@ chain_kernel(Args a, Segs sg, Ptrs io) {
         const Rsrc qr = make_rsrc(qp + row * ldk, (uint32_t)((valid - 1) * ldk + DK) * (uint32_t)sizeof(E));
         const int vc = a.dv - c0 < L::SLAB ? a.dv - c0 : L::SLAB;   // none in a slab of the linear part alone
         const Rsrc vr = make_rsrc(vp + row * ldv, vc > 0 ? (uint32_t)((valid - 1) * ldv + vc) * (uint32_t)sizeof(E) : 0u);
-        const char* pre = io.prep + (((int64_t)pc.slot + c) * a.Hv + h) * io.prep_stride;
-        st.load(kr, qr, vr, BWD ? pre + TRI_BYTES : pre, BWD ? pre + 2 * TRI_BYTES : pre + TRI_BYTES,
-                reinterpret_cast<const float*>(pre + prep_factors(MODE != FWD && io.prep_stride == prep_bytes(true))));
+        st.load(kr, qr, vr, make_rsrc(io.prep + (((int64_t)pc.slot + c) * a.Hv + h) * PREP_BYTES, PREP_BYTES));
     };
     auto chunk_of = [&](int it) { return BWD ? pc.c1 - 1 - it : pc.c0 + it; };
-    // a chunk's finished rows, stored one chunk later
+    // A chunk's finished rows are stored one chunk later: from LDS, 16 bytes a thread in whole
+    // rows of the slab (`from`: that chunk's buffer), or from the registers.
     typename A::Q4 fin[MT];
-    auto flush = [&](int c) {
+    auto flush = [&](int c, const char* from) {
         const int left = pc.s.len - c * C, valid = left < C ? left : C;
         const Rsrc orr = make_rsrc((E*)io.out + (pc.s.row0 + (int64_t)c * C) * ldv, (uint32_t)(valid * ldv) * (uint32_t)sizeof(E));
+        if constexpr (L::ROWS) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-            buf_st_quad(fin[m], orr, act ? (uint32_t)((16 * m + r) * ldv + (int64_t)h * a.dv + col0 + 4 * g) * (uint32_t)sizeof(E) : 0xffffffffu);
+            for (int j = 0; j < L::NV; ++j) {
+                const int u = (int)threadIdx.x + j * L::NTHR, row = u / L::VROW, col = c0 + (u % L::VROW) * 8;
+                const u32x4 x = *reinterpret_cast<const u32x4*>(from + L::V_AT + row * L::VLD * 2 + (u % L::VROW) * 16);
+                __builtin_amdgcn_raw_buffer_store_b128(
+                    x, orr, col < a.dv ? (int)((row * ldv + (int64_t)h * a.dv + col) * 2) : (int)0x80000000u, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                buf_st_quad(fin[m], orr, act ? (uint32_t)((16 * m + r) * ldv + (int64_t)h * a.dv + col0 + 4 * g) * (uint32_t)sizeof(E) : 0x80000000u);
+        }
     };
+    // the row of a finished token: 4 g .. of this wavefront's columns of token 16 m + r
+    auto done = [&](const char* buf, int m, f32x4 x) {
+        if constexpr (L::ROWS)
+            *reinterpret_cast<typename A::Q4*>(const_cast<char*>(buf) + L::V_AT + ((16 * m + r) * L::VLD + w * 16 + 4 * g) * 2) = A::q4(x);
+        else
+            fin[m] = A::q4(x);
+    };
+    if (L::HAS_P) {   // the halves of P's blocks above the diagonal, which stay zero
+        const f32x4 none = {0, 0, 0, 0};
+        if (w == 0) A::put_half(pl, BWD ? upper_block(1, 0) : lower_block(0, 0), lane, BWD ? 0 : 1, none);
+        if (w == 1) A::put_half(pl, BWD ? upper_block(3, 1) : lower_block(2, 1), lane, BWD ? 0 : 1, none);
+    }
     if (nch > 0) {
         load(chunk_of(0));
         st.store(lds);
@@ -217,12 +241,35 @@ chain_kernel(Args a, Segs sg, Ptrs io) {
     for (int it = 0; it < nch; ++it) {
         const char* buf = lds + (L::BUFS == 2 ? (it & 1) * L::BYTES : 0);
         const int c = chunk_of(it);
-        if ((MODE == FWD || MODE == BACK) && it > 0) flush(chunk_of(it - 1));
+        if ((MODE == FWD || MODE == BACK) && it > 0) flush(chunk_of(it - 1), lds + (L::BUFS == 2 ? ((it - 1) & 1) * L::BYTES : 0));
         load(chunk_of(it + 1 < nch ? it + 1 : it));   // the last chunk again rather than a branch
         {
             const float *gam = reinterpret_cast<const float*>(buf + L::F_AT), *ob = gam + C;
             const f32x4 zero = {0, 0, 0, 0};
             const char* vl = buf + L::V_AT;
+            if constexpr (L::HAS_P) {
+                // P's ten tiles on the wavefronts in turn: of queries m and keys n, [s][t] (backwards
+                // [t][s]), so that a lane has a quarter fragment
+                const float* bt = gam + 3 * C;
+                const double* G = reinterpret_cast<const double*>(gam + 4 * C);
+                for (int i = w; i < 10; i += NW) {
+                    const int m = i >= 6 ? 3 : i >= 3 ? 2 : i >= 1 ? 1 : 0, n = i - m * (m + 1) / 2;
+                    f32x4 p = zero;
+#pragma unroll
+                    for (int b = 0; b < KB; ++b) {
+                        const typename A::Ex kf = A::ld_ex(buf, n * KB + b, lane), qf = A::ld_ex(buf + L::Q_AT, m * KB + b, lane);
+                        p = BWD ? A::mma(qf, kf, p) : A::mma(kf, qf, p);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int t = BWD ? 16 * m + 4 * g + j : 16 * m + r, s = BWD ? 16 * n + r : 16 * n + 4 * g + j;
+                        const float d = __builtin_amdgcn_exp2f(s <= t ? (float)(G[t] - G[s]) : 0.0f);
+                        p[j] = s <= t ? a.scale * d * bt[s] * p[j] : 0.0f;
+                    }
+                    A::put_half(pl, BWD ? upper_block(n, m >> 1) : lower_block(m, n >> 1), lane, BWD ? m & 1 : n & 1, p);
+                }
+                if (BWD) lds_barrier();
+            }
             typename A::Sp sb[KB];
 #pragma unroll
             for (int b = 0; b < KB; ++b) sb[b] = A::split(S[2 * b], S[2 * b + 1]);
@@ -242,34 +289,43 @@ chain_kernel(Args a, Segs sg, Ptrs io) {
 #pragma unroll
                 for (int b = 0; b < 2; ++b) dob[b] = A::cols(dov[2 * b], dov[2 * b + 1]);
             }
-            // V - gam (K S), or om beta (K dS) + (diag(beta) P^T) dO
+            // V - gam (K S), or om beta (K dS) + P^T dO
+#pragma unroll
+            for (int m = 0; m < MT; ++m) y[m] = zero;
+#pragma unroll
+            for (int b = 0; b < KB; ++b) {
+                typename A::Ex kf[MT];
+#pragma unroll
+                for (int m = 0; m < MT; ++m) kf[m] = A::ld_ex(buf, m * KB + b, lane);
+                A::mma_n(kf, sb[b], y);
+            }
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                y[m] = zero;
-#pragma unroll
-                for (int b = 0; b < KB; ++b) y[m] = A::mma(A::ld_ex(buf, m * KB + b, lane), sb[b], y[m]);
                 if constexpr (BWD) {
                     y[m] *= ld4(ob + 16 * m + 4 * g);
-#pragma unroll
-                    for (int b = m / 2; b < 2; ++b) y[m] = A::mma(A::ld_sp(buf + L::P_AT, upper_block(m, b), lane), dob[b], y[m]);
                 } else {
-                    const f32x4 gm = ld4(gam + 16 * m + 4 * g);
                     f32x4 vv = A::ld_col(vl, L::VLD, m, w * 16, g, r);
                     if (isM) vv = zero;
-                    y[m] = vv - gm * y[m];
+                    y[m] = vv - ld4(gam + 16 * m + 4 * g) * y[m];
                 }
+            }
+            if constexpr (BWD) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int m = 0; m <= 2 * b + 1; ++m) y[m] = A::mma(A::ld_sp(pl, upper_block(m, b), lane), dob[b], y[m]);
             }
             // e = X y, or Z = X^T y
             typename A::Sp yb[2];
 #pragma unroll
             for (int b = 0; b < 2; ++b) yb[b] = A::split(y[2 * b], y[2 * b + 1]);
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                y[m] = zero;
+            for (int m = 0; m < MT; ++m) y[m] = zero;
 #pragma unroll
-                for (int b = BWD ? m / 2 : 0; b <= (BWD ? 1 : m / 2); ++b)
-                    y[m] = A::mma(A::ld_sp(buf + L::X_AT, BWD ? upper_block(m, b) : lower_block(m, b), lane), yb[b], y[m]);
-            }
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int m = BWD ? 0 : 2 * b; m < (BWD ? 2 * b + 2 : MT); ++m)
+                    y[m] = A::mma(BWD ? A::ld_tri_t(buf + L::X_AT, m, b, g, r) : A::ld_sp(buf + L::X_AT, lower_block(m, b), lane), yb[b], y[m]);
             typename A::Sp eb[2], wb[2], db[2];
             if constexpr (MODE != MAP && MODE != BMAP) {
 #pragma unroll
@@ -282,7 +338,7 @@ chain_kernel(Args a, Segs sg, Ptrs io) {
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
                         const f32x4 z = A::put_t(to, w_off + (uint32_t)((2 * b + hh) * (a.dv / 32) * SPB), eb[b], hh ? pk1 : pk0);
-                        if constexpr (MODE == BACK) fin[2 * b + hh] = A::q4(z);
+                        if constexpr (MODE == BACK) done(buf, 2 * b + hh, z);
                     }
             }
             // om beta e, or -gam Z and scale gam dO, for the state
@@ -303,33 +359,47 @@ chain_kernel(Args a, Segs sg, Ptrs io) {
             }
             const float ge = gam[C - 1];
 #pragma unroll
-            for (int t = 0; t < ST; ++t) {
-                S[t] *= ge;
+            for (int t = 0; t < ST; ++t) S[t] *= ge;
 #pragma unroll
-                for (int tb = 0; tb < 2; ++tb) {
-                    if constexpr (BWD) S[t] = A::mma(A::template ld_ex_t<KB>(buf + L::Q_AT, t / 2, t & 1, tb, g, r), db[tb], S[t]);
-                    S[t] = A::mma(A::template ld_ex_t<KB>(buf, t / 2, t & 1, tb, g, r), wb[tb], S[t]);
+            for (int tb = 0; tb < 2; ++tb) {
+                typename A::Ex kt[ST];
+                if constexpr (BWD) {
+#pragma unroll
+                    for (int t = 0; t < ST; ++t) kt[t] = A::template ld_ex_t<KB>(buf + L::Q_AT, t / 2, t & 1, tb, g, r);
+                    A::mma_n(kt, db[tb], S);
                 }
+#pragma unroll
+                for (int t = 0; t < ST; ++t) kt[t] = A::template ld_ex_t<KB>(buf, t / 2, t & 1, tb, g, r);
+                A::mma_n(kt, wb[tb], S);
             }
             if constexpr (MODE == FWD) {
                 // O^T: lane (g, r) has columns 4 g.. of token r
+                f32x4 ot[MT];
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    f32x4 ot = zero;
+                for (int m = 0; m < MT; ++m) ot[m] = zero;
 #pragma unroll
-                    for (int b = 0; b < KB; ++b) ot = A::mma(sb[b], A::ld_ex(buf + L::Q_AT, m * KB + b, lane), ot);
-                    ot *= a.scale * gam[16 * m + r];
+                for (int b = 0; b < KB; ++b) {
+                    typename A::Ex qf[MT];
 #pragma unroll
-                    for (int b = 0; b <= m / 2; ++b) ot = A::mma(eb[b], A::ld_sp(buf + L::P_AT, lower_block(m, b), lane), ot);
-                    fin[m] = A::q4(ot);
+                    for (int m = 0; m < MT; ++m) qf[m] = A::ld_ex(buf + L::Q_AT, m * KB + b, lane);
+                    A::mma_n(sb[b], qf, ot);
                 }
+#pragma unroll
+                for (int m = 0; m < MT; ++m) ot[m] *= a.scale * gam[16 * m + r];
+                lds_barrier();   // every tile of P is there
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int m = 2 * b; m < MT; ++m) ot[m] = A::mma(eb[b], A::ld_sp(pl, lower_block(m, b), lane), ot[m]);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) done(buf, m, ot[m]);
             }
         }
         if constexpr (L::BUFS == 1) lds_barrier();
         st.store(lds + (L::BUFS == 2 ? ((it + 1) & 1) * L::BYTES : 0));
         lds_barrier();
     }
-    if ((MODE == FWD || MODE == BACK) && nch > 0) flush(chunk_of(nch - 1));
+    if ((MODE == FWD || MODE == BACK) && nch > 0) flush(chunk_of(nch - 1), lds + (L::BUFS == 2 ? ((nch - 1) & 1) * L::BYTES : 0));
     // the state behind the piece
     float* to = nullptr;
     int64_t ld = a.dv;
@@ -422,10 +492,12 @@ join_kernel(Args a, Segs sg, const float* __restrict__ init, const float* __rest
 }
 
 template <typename E, int DK, int NW>
-hipError_t chain_t(int mode, const Args& a, const Segs& sg, const Ptrs& io, hipStream_t stream) {
+hipError_t chain_t(int mode, const Args& a, const Segs& sg, const Ptrs& io0, hipStream_t stream) {
     const int slab = 16 * NW, cols = mode == MAP ? a.dv + DK : a.dv;
-    const int64_t n = places_of(a.nseq, a.T, a.cu != nullptr, seg_unit(sg)) * a.Hv * ((cols + slab - 1) / slab);
-    const dim3 grid((unsigned)n), block(64 * NW);
+    Ptrs io = io0;
+    io.places = (int)places_of(a.nseq, a.T, a.cu != nullptr, seg_unit(sg));
+    const int64_t outer = ((int64_t)io.places * a.Hk + 7) / 8 * 8;
+    const dim3 grid((unsigned)(outer * (a.Hv / a.Hk) * ((cols + slab - 1) / slab))), block(64 * NW);
     switch (mode) {
         case FWD: hipLaunchKernelGGL((chain_kernel<E, DK, NW, FWD>), grid, block, 0, stream, a, sg, io); break;
         case SAVE: hipLaunchKernelGGL((chain_kernel<E, DK, NW, SAVE>), grid, block, 0, stream, a, sg, io); break;
@@ -476,26 +548,26 @@ hipError_t join_d(bool bwd, const Args& a, const Segs& sg, const float* init, co
 
 hipError_t launch_fwd_chain(bool f32, int dk, const Args& a, const Segs& sg, const void* q, const void* k, const void* v,
                             const float* S0, const float* starts, const char* prep, void* o, float* S_T, hipStream_t stream) {
-    const Ptrs io{q, k, v, S0, starts, prep, prep_bytes(false), o, S_T, nullptr, nullptr, nullptr, false};
+    const Ptrs io{q, k, v, S0, starts, prep, o, S_T, nullptr, nullptr, nullptr, false, 0};
     KDA_GDR_TYPES(chain_d, FWD, a, sg, io, stream);
 }
 
 hipError_t launch_save_chain(bool f32, int dk, const Args& a, const Segs& sg, const void* k, const void* v, const float* S0,
                              const float* starts, const char* prep, char* ws_s, char* ws_e, hipStream_t stream) {
-    const Ptrs io{k, k, v, S0, starts, prep, prep_bytes(true), nullptr, nullptr, ws_s, ws_e, nullptr, false};
+    const Ptrs io{k, k, v, S0, starts, prep, nullptr, nullptr, ws_s, ws_e, nullptr, false, 0};
     KDA_GDR_TYPES(chain_d, SAVE, a, sg, io, stream);
 }
 
 hipError_t launch_map_chain(bool f32, int dk, bool bwd, const Args& a, const Segs& sg, const void* k, const void* v,
                             const char* prep, float* maps, hipStream_t stream) {
-    const Ptrs io{k, k, v, nullptr, nullptr, prep, prep_bytes(bwd), nullptr, nullptr, nullptr, nullptr, maps, bwd};
+    const Ptrs io{k, k, v, nullptr, nullptr, prep, nullptr, nullptr, nullptr, nullptr, maps, bwd, 0};
     KDA_GDR_TYPES(chain_d, MAP, a, sg, io, stream);
 }
 
 hipError_t launch_back_chain(bool f32, int dk, bool map, const Args& a, const Segs& sg, const void* q, const void* k,
                              const void* dout, const float* dS_T, const float* starts, const char* prep, void* dv, float* dS0,
                              char* ws_d, char* ws_z, float* maps, hipStream_t stream) {
-    const Ptrs io{q, k, dout, dS_T, starts, prep, prep_bytes(true), dv, dS0, ws_d, ws_z, maps, false};
+    const Ptrs io{q, k, dout, dS_T, starts, prep, dv, dS0, ws_d, ws_z, maps, false, 0};
     KDA_GDR_TYPES(chain_d, map ? BMAP : BACK, a, sg, io, stream);
 }
 

@@ -1,6 +1,6 @@
 // kda_gdr_chunk.hip -- the launches of the chunked gated delta rule with one decay a head and
 // the layout of its workspace.
-//   forward:   prep (X, P of every chunk) -> [maps -> join] -> chain (states, outputs)
+//   forward:   prep (X and the decays of every chunk) -> [maps -> join] -> chain (states, outputs)
 //   backward:  prep -> [maps, backward maps -> joins] -> chain saving the states ->
 //              chain backwards -> grad
 // The steps in brackets run where sequences are cut into pieces that are walked side by side.
@@ -10,8 +10,8 @@
 namespace kda {
 namespace gdr {
 
-hipError_t launch_prep(bool f32, int dk, bool bwd, const Args& a, const void* q, const void* k, const float* g,
-                       const float* beta, char* ws, hipStream_t stream);
+hipError_t launch_prep(bool f32, int dk, const Args& a, const void* k, const float* g, const float* beta, char* ws,
+                       hipStream_t stream);
 hipError_t launch_fwd_chain(bool f32, int dk, const Args& a, const Segs& sg, const void* q, const void* k, const void* v,
                             const float* S0, const float* starts, const char* prep, void* o, float* S_T, hipStream_t stream);
 hipError_t launch_save_chain(bool f32, int dk, const Args& a, const Segs& sg, const void* k, const void* v, const float* S0,
@@ -23,7 +23,7 @@ hipError_t launch_back_chain(bool f32, int dk, bool map, const Args& a, const Se
                              char* ws_d, char* ws_z, float* maps, hipStream_t stream);
 hipError_t launch_join(bool f32, int dk, bool bwd, const Args& a, const Segs& sg, const float* init, const float* maps,
                        const float* nmaps, float* starts, hipStream_t stream);
-hipError_t launch_grad(bool f32, int dk_, const Args& a, const void* q, const void* k, const float* beta, const void* dout,
+hipError_t launch_grad(bool f32, int dk_, const Args& a, const void* q, const void* k, const void* dout,
                        const char* prep, const char* ws_s, const char* ws_e, const char* ws_d, const char* ws_z, void* dq,
                        void* dk, float* dg, float* dbeta, hipStream_t stream);
 
@@ -57,7 +57,7 @@ Plan plan_of(bool bwd, int nseq, int T, int Hv, int dk, int dv, bool packed) {
         x = at;
         at += bytes;
     };
-    take(p.prep, n * prep_bytes(bwd));
+    take(p.prep, n * (int64_t)PREP_BYTES);
     if (bwd) {
         take(p.s, n * state_bytes(dk, dv));
         take(p.d, n * state_bytes(dk, dv));
@@ -98,7 +98,7 @@ hipError_t launch_gdr_fwd(const GdrCall& c, void* o, float* S_T, void* workspace
     const gdr::Plan p = gdr::plan_of(false, c.nseq, c.T, c.Hv, c.dk, c.dv, c.cu != nullptr);
     char* ws = (char*)workspace;
     float *maps = (float*)(ws + p.maps), *starts = (float*)(ws + p.starts);
-    KDA_DO(gdr::launch_prep(c.f32, c.dk, false, a, c.q, c.k, c.g, c.beta, ws + p.prep, stream));
+    KDA_DO(gdr::launch_prep(c.f32, c.dk, a, c.k, c.g, c.beta, ws + p.prep, stream));
     if (p.sg.seg) {
         KDA_DO(gdr::launch_map_chain(c.f32, c.dk, false, a, p.sg, c.k, c.v, ws + p.prep, maps, stream));
         KDA_DO(gdr::launch_join(c.f32, c.dk, false, a, p.sg, c.S0, maps, maps, starts, stream));
@@ -113,7 +113,7 @@ hipError_t launch_gdr_bwd(const GdrCall& c, const void* dout, const float* dS_T,
     char* ws = (char*)workspace;
     float *maps = (float*)(ws + p.maps), *nmaps = (float*)(ws + p.nmaps);
     float *starts = (float*)(ws + p.starts), *dstarts = (float*)(ws + p.dstarts);
-    KDA_DO(gdr::launch_prep(c.f32, c.dk, true, a, c.q, c.k, c.g, c.beta, ws + p.prep, stream));
+    KDA_DO(gdr::launch_prep(c.f32, c.dk, a, c.k, c.g, c.beta, ws + p.prep, stream));
     if (p.sg.seg) {
         KDA_DO(gdr::launch_map_chain(c.f32, c.dk, true, a, p.sg, c.k, c.v, ws + p.prep, maps, stream));
         KDA_DO(gdr::launch_back_chain(c.f32, c.dk, true, a, p.sg, c.q, c.k, dout, nullptr, nullptr, ws + p.prep, nullptr,
@@ -124,7 +124,7 @@ hipError_t launch_gdr_bwd(const GdrCall& c, const void* dout, const float* dS_T,
     KDA_DO(gdr::launch_save_chain(c.f32, c.dk, a, p.sg, c.k, c.v, c.S0, starts, ws + p.prep, ws + p.s, ws + p.e, stream));
     KDA_DO(gdr::launch_back_chain(c.f32, c.dk, false, a, p.sg, c.q, c.k, dout, dS_T, dstarts, ws + p.prep, dv, dS0, ws + p.d,
                                   ws + p.z, nullptr, stream));
-    return gdr::launch_grad(c.f32, c.dk, a, c.q, c.k, c.beta, dout, ws + p.prep, ws + p.s, ws + p.e, ws + p.d, ws + p.z, dq,
+    return gdr::launch_grad(c.f32, c.dk, a, c.q, c.k, dout, ws + p.prep, ws + p.s, ws + p.e, ws + p.d, ws + p.z, dq,
                             dk, dg, dbeta, stream);
 }
 

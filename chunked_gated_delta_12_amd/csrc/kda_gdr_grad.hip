@@ -44,8 +44,8 @@ __device__ __forceinline__ float over_groups(float x) {
 
 template <typename E, int DK>
 __global__ void __launch_bounds__(256, 1)
-grad_kernel(Args a, const E* __restrict__ q, const E* __restrict__ k, const float* __restrict__ beta,
-            const E* __restrict__ dout, const char* __restrict__ prep, const char* __restrict__ ws_s,
+grad_kernel(Args a, const E* __restrict__ q, const E* __restrict__ k, const E* __restrict__ dout,
+            const char* __restrict__ prep, const char* __restrict__ ws_s,
             const char* __restrict__ ws_e, const char* __restrict__ ws_d, const char* __restrict__ ws_z,
             E* __restrict__ dq, E* __restrict__ dk, float* __restrict__ dg, float* __restrict__ dbeta) {
     typedef Arith<E> A;
@@ -78,8 +78,9 @@ grad_kernel(Args a, const E* __restrict__ q, const E* __restrict__ k, const floa
         int row = 16 * (blk / KB) + (l & 15);
         row = row < ch.valid ? row : ch.valid - 1;
         const int64_t at = row * ldk + 32 * (blk % KB) + 8 * (l >> 4) + 4 * half;
-        *reinterpret_cast<u32x4*>(kl + u * 16) = *reinterpret_cast<const u32x4*>(kc + at);
-        *reinterpret_cast<u32x4*>(ql + u * 16) = *reinterpret_cast<const u32x4*>(qc + at);
+        const int to = ((u & ~63) + swz(l)) * 16;
+        *reinterpret_cast<u32x4*>(kl + to) = *reinterpret_cast<const u32x4*>(kc + at);
+        *reinterpret_cast<u32x4*>(ql + to) = *reinterpret_cast<const u32x4*>(qc + at);
     }
 
     // one 32-column block of one value head's operands
@@ -142,11 +143,11 @@ grad_kernel(Args a, const E* __restrict__ q, const E* __restrict__ k, const floa
         const int64_t rec = (int64_t)slot * a.Hv + hk * rep + vh;
         const int h = hk * rep + vh;
         if (tid < C) {
-            const float* f = reinterpret_cast<const float*>(prep + rec * prep_bytes(true) + prep_factors(true));
+            const float* f = reinterpret_cast<const float*>(prep + rec * PREP_BYTES + TRI_BYTES);
             gam[tid] = f[tid];
             om[tid] = f[2 * C + tid];
-            Gs[tid] = reinterpret_cast<const double*>(f + 3 * C)[tid];
-            bts[tid] = tid < ch.valid ? beta[(ch.row0 + tid) * a.Hv + h] : 0.0f;
+            bts[tid] = f[3 * C + tid];
+            Gs[tid] = reinterpret_cast<const double*>(f + 4 * C)[tid];
         }
         f32x4 dos[ST], zs[ST], eds[ST], xl[MT], wl[MT], xu[MT], wu[MT];
         float dot = 0.0f;   // <S, dS>
@@ -160,7 +161,7 @@ grad_kernel(Args a, const E* __restrict__ q, const E* __restrict__ k, const floa
                 const int nv = b + 1 < nb ? vh : vh + 1 < rep ? vh + 1 : vh;
                 load(nv, b + 1 < nb ? b + 1 : vh + 1 < rep ? 0 : b);
             }
-            const Ex ow = A::ld_ex(buf + L::O_AT, w, lane);
+            const Ex ow = A::ld_ex(buf + L::O_AT, w, swz(lane));
             const Sp zw = A::ld_sp(buf + L::Z_AT, w, lane), ew = A::ld_sp(buf + L::E_AT, w, lane);
 #pragma unroll
             for (int t = 0; t < ST; ++t) {
@@ -178,7 +179,7 @@ grad_kernel(Args a, const E* __restrict__ q, const E* __restrict__ k, const floa
                     wl[n] = A::mma(en, zw, wl[n]);
                 }
                 if (n >= w) {
-                    xu[n] = A::mma(A::ld_ex(buf + L::O_AT, n, lane), ew, xu[n]);
+                    xu[n] = A::mma(A::ld_ex(buf + L::O_AT, n, swz(lane)), ew, xu[n]);
                     wu[n] = A::mma(A::ld_sp(buf + L::Z_AT, n, lane), ew, wu[n]);
                 }
             }
@@ -317,21 +318,21 @@ grad_kernel(Args a, const E* __restrict__ q, const E* __restrict__ k, const floa
 }
 
 template <typename E, int DK>
-hipError_t grad_t(const Args& a, const void* q, const void* k, const float* beta, const void* dout, const char* prep,
+hipError_t grad_t(const Args& a, const void* q, const void* k, const void* dout, const char* prep,
                   const char* ws_s, const char* ws_e, const char* ws_d, const char* ws_z, void* dq, void* dk, float* dg,
                   float* dbeta, hipStream_t stream) {
     const int64_t slots = places_of(a.nseq, a.T, a.cu != nullptr, C);
     hipLaunchKernelGGL((grad_kernel<E, DK>), dim3((unsigned)(slots * a.Hk)), dim3(256), 0, stream, a, (const E*)q, (const E*)k,
-                       beta, (const E*)dout, prep, ws_s, ws_e, ws_d, ws_z, (E*)dq, (E*)dk, dg, dbeta);
+                       (const E*)dout, prep, ws_s, ws_e, ws_d, ws_z, (E*)dq, (E*)dk, dg, dbeta);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_grad(bool f32, int dk_, const Args& a, const void* q, const void* k, const float* beta, const void* dout,
+hipError_t launch_grad(bool f32, int dk_, const Args& a, const void* q, const void* k, const void* dout,
                        const char* prep, const char* ws_s, const char* ws_e, const char* ws_d, const char* ws_z, void* dq,
                        void* dk, float* dg, float* dbeta, hipStream_t stream) {
-#define KDA_GG(E, D) return grad_t<E, D>(a, q, k, beta, dout, prep, ws_s, ws_e, ws_d, ws_z, dq, dk, dg, dbeta, stream)
+#define KDA_GG(E, D) return grad_t<E, D>(a, q, k, dout, prep, ws_s, ws_e, ws_d, ws_z, dq, dk, dg, dbeta, stream)
     if (f32) {
         switch (dk_) {
             case 32: KDA_GG(float, 32);

@@ -1,10 +1,8 @@
 // kda_gdr_prep.hip -- what the chunked gated delta rule needs of a chunk before any state
-// is known: X = (I + N diag(beta))^-1 and P (kda_gdr.hpp), all chunks at once.
+// is known: X = (I + N diag(beta))^-1 and the tokens' decays (kda_gdr.hpp), all chunks at once.
 //
-// One workgroup has one chunk of one value head, wavefront w its token tile w.  Operands
-// of the two products Q K^T and K K^T go from global memory straight into the matrix
-// cores (exact bf16 inputs), P as K Q^T so that its result sits in the lanes as the
-// fragment that the chain reads.  Decays come from differences of the prefix sums in 64
+// One workgroup has one chunk of one value head, wavefront w its token tile w.  K K^T goes
+// from global memory straight into the matrix cores (exact bf16 inputs).  Decays come from differences of the prefix sums in 64
 // bits: a strong decay early in the chunk would otherwise take digits from the weak ones
 // behind it (as powers of two, which is what the hardware exponential takes).  X: the four diagonal 16 x 16 blocks by forward substitution in registers,
 // one a wavefront, then X_mn = -X_mm sum_j M_mj X_jn block by block in fp32 on the fp32
@@ -45,10 +43,10 @@ constexpr int TILE = 16 * LD;
 __device__ __forceinline__ int m_tile(int m, int n) { return (m * (m - 1) / 2 + n) * TILE; }
 __device__ __forceinline__ int x_tile(int m, int n) { return (6 + m * (m + 1) / 2 + n) * TILE; }
 
-template <typename E, int DK, bool BWD>
+template <typename E, int DK>
 __global__ void __launch_bounds__(256)
-prep_kernel(Args a, const E* __restrict__ q, const E* __restrict__ k, const float* __restrict__ gate,
-            const float* __restrict__ beta, char* __restrict__ ws) {
+prep_kernel(Args a, const E* __restrict__ k, const float* __restrict__ gate, const float* __restrict__ beta,
+            char* __restrict__ ws) {
     typedef Arith<E> A;
     constexpr int KB = DK / 32;
     __shared__ alignas(16) float tiles[16 * TILE];
@@ -62,19 +60,15 @@ prep_kernel(Args a, const E* __restrict__ q, const E* __restrict__ k, const floa
     const int hk = h / (a.Hv / a.Hk);
     const int64_t ld = (int64_t)a.Hk * DK;
     const E* kc = k + ch.row0 * ld + hk * DK + 8 * g;
-    const E* qc = q + ch.row0 * ld + hk * DK + 8 * g;
-    char* out = ws + (int64_t)blockIdx.x * prep_bytes(BWD);
+    char* out = ws + (int64_t)blockIdx.x * PREP_BYTES;
     const f32x4 zero = {0, 0, 0, 0};
 
     const int64_t at = (ch.row0 + (lane < ch.valid ? lane : 0)) * a.Hv + h;
     const float gt0 = gate[at], bt0 = beta[at];
     auto row = [&](int m) { return (int64_t)(16 * m + r < ch.valid ? 16 * m + r : ch.valid - 1) * ld; };
-    typename A::Ex kw[KB], qw[KB];
+    typename A::Ex kw[KB];
 #pragma unroll
-    for (int b = 0; b < KB; ++b) {
-        kw[b] = A::ld_row(kc + row(w) + 32 * b);
-        if (!BWD) qw[b] = A::ld_row(qc + row(w) + 32 * b);
-    }
+    for (int b = 0; b < KB; ++b) kw[b] = A::ld_row(kc + row(w) + 32 * b);
     if (w == 0) {   // past the chunk's end g = 0 and beta = 0: tokens that change nothing
         const float gt = gt0 < -120.0f ? -120.0f : gt0;   // e^-120 is zero in fp32 already; keeps -inf out of the differences
         double G = lane < ch.valid ? (double)gt * 1.4426950408889634074 : 0.0;
@@ -88,42 +82,31 @@ prep_kernel(Args a, const E* __restrict__ q, const E* __restrict__ k, const floa
         Bs[lane] = bt;
         const double end = __shfl(G, 63);
         const float om = __builtin_amdgcn_exp2f((float)(end - G));
-        float* f = reinterpret_cast<float*>(out + prep_factors(BWD));
+        float* f = reinterpret_cast<float*>(out + TRI_BYTES);
         f[lane] = __builtin_amdgcn_exp2f((float)G);
         f[C + lane] = om * bt;
-        if (BWD) {
-            f[2 * C + lane] = om;
-            reinterpret_cast<double*>(f + 3 * C)[lane] = G;
-        }
+        f[2 * C + lane] = om;
+        f[3 * C + lane] = bt;
+        reinterpret_cast<double*>(f + 4 * C)[lane] = G;
     }
-    f32x4 nn[MT], pp[MT];   // K K^T: rows tokens of w, columns of n; P transposed (see below)
+    f32x4 nn[MT];   // K K^T: rows tokens of w, columns of n
 #pragma unroll
     for (int n = 0; n < MT; ++n) {
-        nn[n] = pp[n] = zero;
+        nn[n] = zero;
         if (n <= w) {
 #pragma unroll
-            for (int b = 0; b < KB; ++b) {
-                const typename A::Ex kn = A::ld_row(kc + row(n) + 32 * b);
-                nn[n] = A::mma(kw[b], kn, nn[n]);
-                if (!BWD) pp[n] = A::mma(kn, qw[b], pp[n]);   // rows keys of n, columns queries of w
-            }
-        }
-        if (BWD && n >= w) {
-#pragma unroll
-            for (int b = 0; b < KB; ++b)
-                pp[n] = A::mma(A::ld_row(qc + row(n) + 32 * b), kw[b], pp[n]);   // rows queries of n, columns keys of w
+            for (int b = 0; b < KB; ++b) nn[n] = A::mma(kw[b], A::ld_row(kc + row(n) + 32 * b), nn[n]);
         }
     }
     __syncthreads();
     f32x4 md = zero;
-    const double Gr = Gs[16 * w + r];
     double Gw[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) Gw[i] = Gs[16 * w + 4 * g + i];
 #pragma unroll
     for (int n = 0; n < MT; ++n) {
-        const double Gn = Gs[16 * n + r];
         if (n <= w) {
+            const double Gn = Gs[16 * n + r];
             f32x4 m4;
             const float bs = Bs[16 * n + r];
 #pragma unroll
@@ -139,25 +122,6 @@ prep_kernel(Args a, const E* __restrict__ q, const E* __restrict__ k, const floa
                 for (int i = 0; i < 4; ++i) tiles[m_tile(w, n) + (4 * g + i) * LD + r] = m4[i];
             }
         }
-        if (BWD ? n >= w : n <= w) {
-            const f32x4 b4 = *reinterpret_cast<const f32x4*>(&Bs[16 * n + 4 * g]);
-            const float br = Bs[16 * w + r];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                // the lane's token, 16 w + r, against token o: the query (forward) or the key
-                const int o = 16 * n + 4 * g + i, t = 16 * w + r;
-                const bool in = BWD ? t <= o : o <= t;
-                const double df = BWD ? Gs[o] - Gr : Gr - Gs[o];
-                const float d = __builtin_amdgcn_exp2f(in ? (float)df : 0.0f);
-                const float x = a.scale * d * pp[n][i] * (BWD ? br : b4[i]);
-                pp[n][i] = in && (BWD ? o : t) < ch.valid ? x : 0.0f;
-            }
-        }
-    }
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-        if (!BWD && b <= w / 2) A::st_sp(out + TRI_BYTES, lower_block(w, b), lane, A::split(pp[2 * b], pp[2 * b + 1]));
-        if (BWD && b >= w / 2) A::st_sp(out + 2 * TRI_BYTES, upper_block(w, b), lane, A::split(pp[2 * b], pp[2 * b + 1]));
     }
     // the diagonal block of X
     f32x4 x;
@@ -195,35 +159,21 @@ prep_kernel(Args a, const E* __restrict__ q, const E* __restrict__ k, const floa
             const f32x4 hi = 2 * b + 1 <= w ? *reinterpret_cast<const f32x4*>(&tiles[x_tile(w, 2 * b + 1) + r * LD + 4 * g]) : zero;
             A::st_sp(out, lower_block(w, b), lane, A::split(lo, hi));
         }
-        if (BWD && b >= w / 2) {
-            f32x4 lo = zero, hi;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (2 * b >= w) lo[i] = tiles[x_tile(2 * b, w) + (4 * g + i) * LD + r];
-                hi[i] = tiles[x_tile(2 * b + 1, w) + (4 * g + i) * LD + r];
-            }
-            A::st_sp(out + TRI_BYTES, upper_block(w, b), lane, A::split(lo, hi));
-        }
     }
 }
 
 template <typename E, int DK>
-hipError_t prep_t(bool bwd, const Args& a, int64_t slots, const void* q, const void* k, const float* g, const float* beta,
-                  char* ws, hipStream_t stream) {
-    const dim3 grid((unsigned)(slots * a.Hv));
-    if (bwd)
-        hipLaunchKernelGGL((prep_kernel<E, DK, true>), grid, dim3(256), 0, stream, a, (const E*)q, (const E*)k, g, beta, ws);
-    else
-        hipLaunchKernelGGL((prep_kernel<E, DK, false>), grid, dim3(256), 0, stream, a, (const E*)q, (const E*)k, g, beta, ws);
+hipError_t prep_t(const Args& a, const void* k, const float* g, const float* beta, char* ws, hipStream_t stream) {
+    const dim3 grid((unsigned)(places_of(a.nseq, a.T, a.cu != nullptr, C) * a.Hv));
+    hipLaunchKernelGGL((prep_kernel<E, DK>), grid, dim3(256), 0, stream, a, (const E*)k, g, beta, ws);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_prep(bool f32, int dk, bool bwd, const Args& a, const void* q, const void* k, const float* g,
-                       const float* beta, char* ws, hipStream_t stream) {
-    const int64_t slots = places_of(a.nseq, a.T, a.cu != nullptr, C);
-#define KDA_GP(E, D) return prep_t<E, D>(bwd, a, slots, q, k, g, beta, ws, stream)
+hipError_t launch_prep(bool f32, int dk, const Args& a, const void* k, const float* g, const float* beta, char* ws,
+                       hipStream_t stream) {
+#define KDA_GP(E, D) return prep_t<E, D>(a, k, g, beta, ws, stream)
     if (f32) {
         switch (dk) {
             case 32: KDA_GP(float, 32);

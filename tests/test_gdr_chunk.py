@@ -476,8 +476,8 @@ def test_workspace_sizes(lib):
     assert f(1, 65536, 16, 128, 128) == 16 * (1024 * one + 16 * (128 * 256 + 128 * 128) * 4)
     assert f(64, 4096, 16, 128, 128) == 64 * 64 * 16 * one
     b = kda.kda_gdr_chunk_bwd_workspace_size
-    # X, its transpose and P's, the tokens' factors, two states and two token operands
-    assert b(1, 64, 1, 128, 128) == 3 * 6 * 2048 + 3 * 256 + 512 + 2 * 4 * 128 * 128 + 2 * 4 * 64 * 128
+    # X, the tokens' factors, two states and two token operands
+    assert b(1, 64, 1, 128, 128) == 6 * 2048 + 4 * 256 + 512 + 2 * 4 * 128 * 128 + 2 * 4 * 64 * 128
     with pytest.raises(kda.KdaError):
         f(0, 64, 2, 64, 64)
     with pytest.raises(kda.KdaError):
