@@ -247,7 +247,13 @@ template <> struct Arith<bf16> {
     }
     // a's rows, transposed through the product with a picking matrix (exact), as half a
     // block of accumulator slots at byte `blk` of the record; returns the values.
-    static __device__ __forceinline__ uint32_t half_at(int lane, int half) { return (uint32_t)(lane * 16 + half * 8); }
+    static __device__ __forceinline__ uint32_t half_at(int lane, int half) { return (uint32_t)(half * 512 + lane * 8); }
+    // A block of such a record: each half of the slots contiguous, as the column tile that wrote it.
+    static __device__ __forceinline__ Sp ld_rec(const char* base, int blk, int lane) {
+        const char* p = base + blk * SPB + lane * 8;
+        return Sp{cat8(ld_b4((const bf16*)p), ld_b4((const bf16*)(p + 512))),
+                  cat8(ld_b4((const bf16*)(p + 1024)), ld_b4((const bf16*)(p + 1536)))};
+    }
     static __device__ __forceinline__ f32x4 put_t(Rsrc rec, uint32_t blk, const Sp& a, Ex j) {
         const f32x4 z = {0, 0, 0, 0};
         const f32x4 hi = mfma_k32(a.hi, j, z), lo = mfma_k32(a.lo, j, z);
@@ -351,6 +357,7 @@ template <> struct Arith<float> {
         return x;
     }
     static __device__ __forceinline__ uint32_t half_at(int lane, int half) { return (uint32_t)(half * 1024 + lane * 16); }
+    static __device__ __forceinline__ Sp ld_rec(const char* base, int blk, int lane) { return ld_sp(base, blk, lane); }
     static __device__ __forceinline__ f32x4 put_t(Rsrc rec, uint32_t blk, const Sp& a, const Ex& j) {
         const f32x4 x = mma(a, j, f32x4{0, 0, 0, 0});
         buf_st_quad(x, rec, blk);

@@ -78,14 +78,20 @@ struct Stage {
         }
     }
 
-    __device__ __forceinline__ void load(Rsrc kr, Rsrc qr, Rsrc vr, Rsrc xr) {
+    __device__ __forceinline__ void load_k(Rsrc kr) {
 #pragma unroll
-        for (int j = 0; j < L::NQK; ++j) {
-            k[j] = buf_ld128(kr, kq_off[j]);
-            if constexpr (L::HAS_Q) q[j] = buf_ld128(qr, kq_off[j]);
-        }
+        for (int j = 0; j < L::NQK; ++j) k[j] = buf_ld128(kr, kq_off[j]);
+    }
+    __device__ __forceinline__ void load_q(Rsrc qr) {
+        if constexpr (L::HAS_Q)
+#pragma unroll
+            for (int j = 0; j < L::NQK; ++j) q[j] = buf_ld128(qr, kq_off[j]);
+    }
+    __device__ __forceinline__ void load_x(Rsrc xr) {
 #pragma unroll
         for (int j = 0; j < L::NXP; ++j) x[j] = buf_ld128(xr, (uint32_t)(threadIdx.x + j * L::NTHR) * 16);
+    }
+    __device__ __forceinline__ void load_v(Rsrc vr) {
 #pragma unroll
         for (int j = 0; j < L::NV; ++j) v[j] = buf_ld128(vr, v_off[j]);
     }
@@ -186,16 +192,17 @@ chain_kernel(Args a, Segs sg, Ptrs io) {
     for (int t = 0; t < ST; ++t) asm volatile("" : "+v"(S[t]));
     Stage<E, DK, NW, MODE> st;
     st.init(ldk, ldv, a.dv - c0);
-    auto load = [&](int c) {
+    struct Res { Rsrc k, q, v, x; };
+    auto res_of = [&](int c) {
         const int left = pc.s.len - c * C;
         const int valid = left < C ? left : C;
         const int64_t row = (int64_t)c * C;
         // rows past the chunk's last token read as zero; the head's offset is in the base
-        const Rsrc kr = make_rsrc(kp + row * ldk, (uint32_t)((valid - 1) * ldk + DK) * (uint32_t)sizeof(E));
-        const Rsrc qr = make_rsrc(qp + row * ldk, (uint32_t)((valid - 1) * ldk + DK) * (uint32_t)sizeof(E));
         const int vc = a.dv - c0 < L::SLAB ? a.dv - c0 : L::SLAB;   // none in a slab of the linear part alone
-        const Rsrc vr = make_rsrc(vp + row * ldv, vc > 0 ? (uint32_t)((valid - 1) * ldv + vc) * (uint32_t)sizeof(E) : 0u);
-        st.load(kr, qr, vr, make_rsrc(io.prep + (((int64_t)pc.slot + c) * a.Hv + h) * PREP_BYTES, PREP_BYTES));
+        return Res{make_rsrc(kp + row * ldk, (uint32_t)((valid - 1) * ldk + DK) * (uint32_t)sizeof(E)),
+                   make_rsrc(qp + row * ldk, (uint32_t)((valid - 1) * ldk + DK) * (uint32_t)sizeof(E)),
+                   make_rsrc(vp + row * ldv, vc > 0 ? (uint32_t)((valid - 1) * ldv + vc) * (uint32_t)sizeof(E) : 0u),
+                   make_rsrc(io.prep + (((int64_t)pc.slot + c) * a.Hv + h) * PREP_BYTES, PREP_BYTES)};
     };
     auto chunk_of = [&](int it) { return BWD ? pc.c1 - 1 - it : pc.c0 + it; };
     // A chunk's finished rows are stored one chunk later: from LDS, 16 bytes a thread in whole
@@ -231,7 +238,11 @@ chain_kernel(Args a, Segs sg, Ptrs io) {
         if (w == 1) A::put_half(pl, BWD ? upper_block(3, 1) : lower_block(2, 1), lane, BWD ? 0 : 1, none);
     }
     if (nch > 0) {
-        load(chunk_of(0));
+        const Res rs = res_of(chunk_of(0));
+        st.load_k(rs.k);
+        st.load_q(rs.q);
+        st.load_x(rs.x);
+        st.load_v(rs.v);
         st.store(lds);
     }
     lds_barrier();
@@ -242,7 +253,8 @@ chain_kernel(Args a, Segs sg, Ptrs io) {
         const char* buf = lds + (L::BUFS == 2 ? (it & 1) * L::BYTES : 0);
         const int c = chunk_of(it);
         if ((MODE == FWD || MODE == BACK) && it > 0) flush(chunk_of(it - 1), lds + (L::BUFS == 2 ? ((it - 1) & 1) * L::BYTES : 0));
-        load(chunk_of(it + 1 < nch ? it + 1 : it));   // the last chunk again rather than a branch
+        const Res rs = res_of(chunk_of(it + 1 < nch ? it + 1 : it));   // the last chunk again rather than a branch
+        st.load_k(rs.k);
         {
             const float *gam = reinterpret_cast<const float*>(buf + L::F_AT), *ob = gam + C;
             const f32x4 zero = {0, 0, 0, 0};
@@ -289,6 +301,8 @@ chain_kernel(Args a, Segs sg, Ptrs io) {
 #pragma unroll
                 for (int b = 0; b < 2; ++b) dob[b] = A::cols(dov[2 * b], dov[2 * b + 1]);
             }
+            st.load_q(rs.q);
+            __builtin_amdgcn_sched_barrier(0x1 | 0x2 | 0x4 | 0x8 | 0x100 | 0x200);
             // V - gam (K S), or om beta (K dS) + P^T dO
 #pragma unroll
             for (int m = 0; m < MT; ++m) y[m] = zero;
@@ -315,6 +329,8 @@ chain_kernel(Args a, Segs sg, Ptrs io) {
 #pragma unroll
                     for (int m = 0; m <= 2 * b + 1; ++m) y[m] = A::mma(A::ld_sp(pl, upper_block(m, b), lane), dob[b], y[m]);
             }
+            st.load_v(rs.v);
+            __builtin_amdgcn_sched_barrier(0x1 | 0x2 | 0x4 | 0x8 | 0x100 | 0x200);
             // e = X y, or Z = X^T y
             typename A::Sp yb[2];
 #pragma unroll
@@ -357,6 +373,8 @@ chain_kernel(Args a, Segs sg, Ptrs io) {
                 wb[b] = A::split(y[2 * b], y[2 * b + 1]);
                 if constexpr (BWD) db[b] = A::split(dov[2 * b], dov[2 * b + 1]);
             }
+            st.load_x(rs.x);
+            __builtin_amdgcn_sched_barrier(0x1 | 0x2 | 0x4 | 0x8 | 0x100 | 0x200);
             const float ge = gam[C - 1];
 #pragma unroll
             for (int t = 0; t < ST; ++t) S[t] *= ge;
@@ -419,7 +437,7 @@ chain_kernel(Args a, Segs sg, Ptrs io) {
 // Joins the maps of a cut sequence's pieces: forwards X_0 = S0, X_{i+1} = M_i X_i + N_i, backwards
 // X_last = dS_T, X_{i-1} = M_i^T X_i + N'_i, every X_i written to `starts`.  A workgroup has one
 // head and 32 columns, a wavefront 16 of them and a quarter of the rows; X goes from
-// step to step through LDS as split fragments.  Two column tiles share what is read of M.
+// step to step through LDS as split fragments, the next step's M and N are in flight meanwhile.
 template <typename E, int DK, bool BWD>
 __global__ void __launch_bounds__(512)
 join_kernel(Args a, Segs sg, const float* __restrict__ init, const float* __restrict__ maps, const float* __restrict__ nmaps,
@@ -437,56 +455,63 @@ join_kernel(Args a, Segs sg, const float* __restrict__ init, const float* __rest
     if (pc.n != n || pc.cnt < 2) return;
     const int col = 32 * slab + 16 * ct + r;
     const bool on = rq * RT < ST;
+    const int t0 = on ? rq * RT : 0;   // wavefronts past the rows work on the first ones and store nothing
     const int64_t mld = a.dv + DK, nld = BWD ? a.dv : mld;
-    f32x4 X[RT];
+    f32x4 X[RT], N[RT], M[RT][KB][2];
     auto rowof = [&](int t) { return 32 * (t / 2) + 8 * g + 4 * (t & 1); };   // this lane's first row of accumulator tile t
+    auto place = [&](int s) { return p0 + (BWD ? pc.cnt - 1 - s : s); };
+    auto fetch = [&](int s) {
+        const float* m = maps + ((int64_t)place(s) * a.Hv + h) * DK * mld + a.dv;
+        const float* nn = nmaps + ((int64_t)place(s) * a.Hv + h) * DK * nld;
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+            const int t = t0 + j, row = 32 * (t / 2) + 8 * (r >> 2) + 4 * (t & 1) + (r & 3);
+#pragma unroll
+            for (int b = 0; b < KB; ++b)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    if constexpr (BWD) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) M[j][b][q][i] = m[(int64_t)(32 * b + 8 * g + 4 * q + i) * mld + row];
+                    } else {
+                        M[j][b][q] = ld4(m + row * mld + 32 * b + 8 * g + 4 * q);
+                    }
+                }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) N[j][i] = nn[(int64_t)(rowof(t) + i) * nld + col];
+        }
+    };
+    fetch(0);
 #pragma unroll
     for (int j = 0; j < RT; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            X[j][i] = init && on ? init[(((int64_t)n * a.Hv + h) * DK + rowof(rq * RT + j) + i) * a.dv + col] : 0.0f;
+        for (int i = 0; i < 4; ++i) X[j][i] = init ? init[(((int64_t)n * a.Hv + h) * DK + rowof(t0 + j) + i) * a.dv + col] : 0.0f;
     for (int s = 0; s < pc.cnt; ++s) {
-        const int at = p0 + (BWD ? pc.cnt - 1 - s : s);
-        float* to = starts + ((int64_t)at * a.Hv + h) * DK * a.dv + col;
+        float* to = starts + ((int64_t)place(s) * a.Hv + h) * DK * a.dv + col;
         char* buf = lds[s & 1];
         if (on) {
 #pragma unroll
             for (int j = 0; j < RT; ++j) {
-                const int t = rq * RT + j;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) to[(int64_t)(rowof(t) + i) * a.dv] = X[j][i];
-                A::put_half(buf, ct * KB + t / 2, lane, t & 1, X[j]);
+                for (int i = 0; i < 4; ++i) to[(int64_t)(rowof(t0 + j) + i) * a.dv] = X[j][i];
+                A::put_half(buf, ct * KB + (t0 + j) / 2, lane, (t0 + j) & 1, X[j]);
             }
         }
         if (s + 1 == pc.cnt) break;
+        typename A::Sp mf[RT][KB];
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+            X[j] = N[j];
+#pragma unroll
+            for (int b = 0; b < KB; ++b) mf[j][b] = A::split(M[j][b][0], M[j][b][1]);
+        }
+        fetch(s + 2 < pc.cnt ? s + 1 : s);
         lds_barrier();
-        if (on) {
-            const float* M = maps + ((int64_t)at * a.Hv + h) * DK * mld + a.dv;
-            const float* N = nmaps + ((int64_t)at * a.Hv + h) * DK * nld;
-            typename A::Sp xb[KB];
 #pragma unroll
-            for (int b = 0; b < KB; ++b) xb[b] = A::ld_sp(buf, ct * KB + b, lane);
+        for (int b = 0; b < KB; ++b) {
+            const typename A::Sp xb = A::ld_sp(buf, ct * KB + b, lane);
 #pragma unroll
-            for (int j = 0; j < RT; ++j) {
-                const int t = rq * RT + j, row = 32 * (t / 2) + 8 * (r >> 2) + 4 * (t & 1) + (r & 3);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) X[j][i] = N[(int64_t)(rowof(t) + i) * nld + col];
-#pragma unroll
-                for (int b = 0; b < KB; ++b) {
-                    f32x4 lo, hi;
-                    if constexpr (BWD) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            lo[i] = M[(int64_t)(32 * b + 8 * g + i) * mld + row];
-                            hi[i] = M[(int64_t)(32 * b + 8 * g + 4 + i) * mld + row];
-                        }
-                    } else {
-                        lo = ld4(M + row * mld + 32 * b + 8 * g);
-                        hi = ld4(M + row * mld + 32 * b + 8 * g + 4);
-                    }
-                    X[j] = A::mma(A::split(lo, hi), xb[b], X[j]);
-                }
-            }
+            for (int j = 0; j < RT; ++j) X[j] = A::mma(mf[j][b], xb, X[j]);
         }
     }
 }
@@ -513,7 +538,9 @@ hipError_t chain_t(int mode, const Args& a, const Segs& sg, const Ptrs& io0, hip
 template <typename E, int DK>
 hipError_t chain_d(int mode, const Args& a, const Segs& sg, const Ptrs& io, hipStream_t stream) {
     const int cols = mode == MAP ? a.dv + DK : a.dv;
-    const int64_t heads = places_of(a.nseq, a.T, a.cu != nullptr, seg_unit(sg)) * a.Hv;
+    // Pieces to expect.  The lengths of packed sequences are not known here: as if all were equal.
+    const int64_t chunks = places_of(a.nseq, a.T, a.cu != nullptr, C), places = places_of(a.nseq, a.T, a.cu != nullptr, seg_unit(sg));
+    const int64_t heads = (sg.seg && chunks / a.nseq > sg.over ? places : a.nseq) * a.Hv;
     if (sizeof(E) == 4 || cols <= 64 || heads * ((cols + 63) / 64) <= 256) return chain_t<E, DK, 4>(mode, a, sg, io, stream);
     if constexpr (sizeof(E) == 2) return chain_t<E, DK, 8>(mode, a, sg, io, stream);
     return hipErrorInvalidValue;

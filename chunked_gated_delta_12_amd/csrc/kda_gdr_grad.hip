@@ -162,10 +162,10 @@ grad_kernel(Args a, const E* __restrict__ q, const E* __restrict__ k, const E* _
                 load(nv, b + 1 < nb ? b + 1 : vh + 1 < rep ? 0 : b);
             }
             const Ex ow = A::ld_ex(buf + L::O_AT, w, swz(lane));
-            const Sp zw = A::ld_sp(buf + L::Z_AT, w, lane), ew = A::ld_sp(buf + L::E_AT, w, lane);
+            const Sp zw = A::ld_rec(buf + L::Z_AT, w, lane), ew = A::ld_rec(buf + L::E_AT, w, lane);
 #pragma unroll
             for (int t = 0; t < ST; ++t) {
-                const Sp sf = A::ld_sp(buf + L::S_AT, t, lane), df = A::ld_sp(buf + L::D_AT, t, lane);
+                const Sp sf = A::ld_rec(buf + L::S_AT, t, lane), df = A::ld_rec(buf + L::D_AT, t, lane);
                 dos[t] = A::mma(sf, ow, dos[t]);
                 zs[t] = A::mma(sf, zw, zs[t]);
                 eds[t] = A::mma(df, ew, eds[t]);
@@ -173,14 +173,14 @@ grad_kernel(Args a, const E* __restrict__ q, const E* __restrict__ k, const E* _
             }
 #pragma unroll
             for (int n = 0; n < MT; ++n) {
-                const Sp en = A::ld_sp(buf + L::E_AT, n, lane);
+                const Sp en = A::ld_rec(buf + L::E_AT, n, lane);
                 if (n <= w) {
                     xl[n] = A::mma(en, ow, xl[n]);
                     wl[n] = A::mma(en, zw, wl[n]);
                 }
                 if (n >= w) {
                     xu[n] = A::mma(A::ld_ex(buf + L::O_AT, n, swz(lane)), ew, xu[n]);
-                    wu[n] = A::mma(A::ld_sp(buf + L::Z_AT, n, lane), ew, wu[n]);
+                    wu[n] = A::mma(A::ld_rec(buf + L::Z_AT, n, lane), ew, wu[n]);
                 }
             }
             if constexpr (L::BUFS == 1) lds_barrier();
