@@ -148,6 +148,10 @@ __device__ __forceinline__ Piece piece_at(const Args& a, const Segs& sg, int pla
 // ---------------------------------------------------------------- operands
 // Where lane (g, r)'s 16 bytes of a natural block of q or k lie in LDS: row r of group g at
 // r ^ 4 g, so that the transposed reads, which take a row of every group, spread over the banks.
+__device__ __forceinline__ u32x4 buf_ld128(Rsrc s, uint32_t off) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(s, (int)off, 0, 0));
+}
+
 __device__ __forceinline__ int swz(int lane) { return lane ^ ((lane >> 4) << 2); }
 
 template <typename E> struct Arith;
@@ -247,19 +251,23 @@ template <> struct Arith<bf16> {
     }
     // a's rows, transposed through the product with a picking matrix (exact), as half a
     // block of accumulator slots at byte `blk` of the record; returns the values.
-    static __device__ __forceinline__ uint32_t half_at(int lane, int half) { return (uint32_t)(half * 512 + lane * 8); }
-    // A block of such a record: each half of the slots contiguous, as the column tile that wrote it.
-    static __device__ __forceinline__ Sp ld_rec(const char* base, int blk, int lane) {
-        const char* p = base + blk * SPB + lane * 8;
-        return Sp{cat8(ld_b4((const bf16*)p), ld_b4((const bf16*)(p + 512))),
-                  cat8(ld_b4((const bf16*)(p + 1024)), ld_b4((const bf16*)(p + 1536)))};
-    }
     static __device__ __forceinline__ f32x4 put_t(Rsrc rec, uint32_t blk, const Sp& a, Ex j) {
         const f32x4 z = {0, 0, 0, 0};
         const f32x4 hi = mfma_k32(a.hi, j, z), lo = mfma_k32(a.lo, j, z);
         buf_st_quad(q4(hi), rec, blk);
         buf_st_quad(q4(lo), rec, blk + 1024);
         return hi + lo;
+    }
+    // A block of such a record: an upper and a lower plane, each half of the slots contiguous.
+    static __device__ __forceinline__ uint32_t rec_at(int lane, int half) { return (uint32_t)(half * 512 + lane * 8); }
+    static __device__ __forceinline__ Sp ld_rec(const char* base, int blk, int lane) {
+        const char* p = base + blk * SPB + lane * 8;
+        return Sp{cat8(ld_b4((const bf16*)p), ld_b4((const bf16*)(p + 512))),
+                  cat8(ld_b4((const bf16*)(p + 1024)), ld_b4((const bf16*)(p + 1536)))};
+    }
+    static __device__ __forceinline__ Sp ld_rec(Rsrc rec, uint32_t at) {
+        typedef BufQuad<bf16> Q;
+        return Sp{cat8(Q::ld(rec, at, 0), Q::ld(rec, at + 512, 0)), cat8(Q::ld(rec, at + 1024, 0), Q::ld(rec, at + 1536, 0))};
     }
     static __device__ __forceinline__ float at(Ex x, int i) { return (float)x[i]; }
     static __device__ __forceinline__ float dot(const Sp& x, const Sp& y) {
@@ -356,8 +364,12 @@ template <> struct Arith<float> {
         }
         return x;
     }
-    static __device__ __forceinline__ uint32_t half_at(int lane, int half) { return (uint32_t)(half * 1024 + lane * 16); }
     static __device__ __forceinline__ Sp ld_rec(const char* base, int blk, int lane) { return ld_sp(base, blk, lane); }
+    static __device__ __forceinline__ uint32_t rec_at(int lane, int half) { return (uint32_t)(half * 1024 + lane * 16); }
+    static __device__ __forceinline__ Sp ld_rec(Rsrc rec, uint32_t at) {
+        typedef BufQuad<float> Q;
+        return Sp{Q::ld(rec, at, 0), Q::ld(rec, at + 1024, 0)};
+    }
     static __device__ __forceinline__ f32x4 put_t(Rsrc rec, uint32_t blk, const Sp& a, const Ex& j) {
         const f32x4 x = mma(a, j, f32x4{0, 0, 0, 0});
         buf_st_quad(x, rec, blk);
@@ -396,6 +408,8 @@ __host__ __device__ constexpr int64_t map_bytes(int dk, int dv) { return (int64_
 // rows channels in the order of the accumulator tiles) and a 64 x dv operand (4 by dv / 32 blocks, rows tokens).
 __host__ __device__ constexpr int64_t state_bytes(int dk, int dv) { return (int64_t)(dk / 16) * (dv / 32) * SPB; }
 __host__ __device__ constexpr int64_t rows_bytes(int dv) { return (int64_t)MT * (dv / 32) * SPB; }
+// One behind the other: the start state, the end's gradient, e, Z.
+__host__ __device__ constexpr int64_t rec_bytes(int dk, int dv) { return 2 * (state_bytes(dk, dv) + rows_bytes(dv)); }
 
 }  // namespace gdr
 }  // namespace kda

@@ -49,9 +49,6 @@ struct Lay {
     static constexpr bool ROWS = (MODE == FWD || MODE == BACK) && sizeof(E) == 2 && BUFS == 2;
 };
 
-__device__ __forceinline__ u32x4 buf_ld128(Rsrc s, uint32_t off) {
-    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(s, (int)off, 0, 0));
-}
 __device__ __forceinline__ f32x4 ld4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
 
 // One chunk's operands on their way from global memory to LDS.
@@ -128,7 +125,7 @@ struct Ptrs {
     const char* prep;
     void* out;                  // o; dv where the walk is backwards
     float* last;                // S_T or dS0, or NULL
-    char *ws_s, *ws_e;          // SAVE, BACK: the chunks' states and rows
+    char* recs;                 // SAVE, BACK: the chunks' records
     float* maps;                // MAP: [piece place][Hv][dk][dv + dk]; BMAP: [..][dk][dv]
     bool all;
     int places;
@@ -247,7 +244,7 @@ chain_kernel(Args a, Segs sg, Ptrs io) {
     }
     lds_barrier();
     // where this wavefront's columns are in a record; past its end where it has none
-    const uint32_t w_off = act ? (uint32_t)(col0 / 32 * SPB) + A::half_at(lane, (col0 >> 4) & 1) : 0x80000000u;
+    const uint32_t w_off = act ? (uint32_t)(col0 / 32 * SPB) + A::rec_at(lane, (col0 >> 4) & 1) : 0x80000000u;
     const typename A::Ex pk0 = pick_half<E>(0, g, r), pk1 = pick_half<E>(1, g, r);
     for (int it = 0; it < nch; ++it) {
         const char* buf = lds + (L::BUFS == 2 ? (it & 1) * L::BYTES : 0);
@@ -287,7 +284,7 @@ chain_kernel(Args a, Segs sg, Ptrs io) {
             for (int b = 0; b < KB; ++b) sb[b] = A::split(S[2 * b], S[2 * b + 1]);
             const int64_t rec = ((int64_t)pc.slot + c) * a.Hv + h;
             if constexpr (MODE == SAVE || MODE == BACK) {
-                const Rsrc to = make_rsrc(io.ws_s + rec * state_bytes(DK, a.dv), (uint32_t)state_bytes(DK, a.dv));
+                const Rsrc to = make_rsrc(io.recs + rec * rec_bytes(DK, a.dv) + (BWD ? state_bytes(DK, a.dv) : 0), (uint32_t)state_bytes(DK, a.dv));
 #pragma unroll
                 for (int b = 0; b < KB; ++b)
 #pragma unroll
@@ -348,7 +345,8 @@ chain_kernel(Args a, Segs sg, Ptrs io) {
                 for (int b = 0; b < 2; ++b) eb[b] = A::split(y[2 * b], y[2 * b + 1]);
             }
             if constexpr (MODE == SAVE || MODE == BACK) {
-                const Rsrc to = make_rsrc(io.ws_e + rec * rows_bytes(a.dv), (uint32_t)rows_bytes(a.dv));
+                const Rsrc to = make_rsrc(io.recs + rec * rec_bytes(DK, a.dv) + 2 * state_bytes(DK, a.dv) + (BWD ? rows_bytes(a.dv) : 0),
+                                          (uint32_t)rows_bytes(a.dv));
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -575,26 +573,26 @@ hipError_t join_d(bool bwd, const Args& a, const Segs& sg, const float* init, co
 
 hipError_t launch_fwd_chain(bool f32, int dk, const Args& a, const Segs& sg, const void* q, const void* k, const void* v,
                             const float* S0, const float* starts, const char* prep, void* o, float* S_T, hipStream_t stream) {
-    const Ptrs io{q, k, v, S0, starts, prep, o, S_T, nullptr, nullptr, nullptr, false, 0};
+    const Ptrs io{q, k, v, S0, starts, prep, o, S_T, nullptr, nullptr, false, 0};
     KDA_GDR_TYPES(chain_d, FWD, a, sg, io, stream);
 }
 
 hipError_t launch_save_chain(bool f32, int dk, const Args& a, const Segs& sg, const void* k, const void* v, const float* S0,
-                             const float* starts, const char* prep, char* ws_s, char* ws_e, hipStream_t stream) {
-    const Ptrs io{k, k, v, S0, starts, prep, nullptr, nullptr, ws_s, ws_e, nullptr, false, 0};
+                             const float* starts, const char* prep, char* recs, hipStream_t stream) {
+    const Ptrs io{k, k, v, S0, starts, prep, nullptr, nullptr, recs, nullptr, false, 0};
     KDA_GDR_TYPES(chain_d, SAVE, a, sg, io, stream);
 }
 
 hipError_t launch_map_chain(bool f32, int dk, bool bwd, const Args& a, const Segs& sg, const void* k, const void* v,
                             const char* prep, float* maps, hipStream_t stream) {
-    const Ptrs io{k, k, v, nullptr, nullptr, prep, nullptr, nullptr, nullptr, nullptr, maps, bwd, 0};
+    const Ptrs io{k, k, v, nullptr, nullptr, prep, nullptr, nullptr, nullptr, maps, bwd, 0};
     KDA_GDR_TYPES(chain_d, MAP, a, sg, io, stream);
 }
 
 hipError_t launch_back_chain(bool f32, int dk, bool map, const Args& a, const Segs& sg, const void* q, const void* k,
                              const void* dout, const float* dS_T, const float* starts, const char* prep, void* dv, float* dS0,
-                             char* ws_d, char* ws_z, float* maps, hipStream_t stream) {
-    const Ptrs io{q, k, dout, dS_T, starts, prep, dv, dS0, ws_d, ws_z, maps, false, 0};
+                             char* recs, float* maps, hipStream_t stream) {
+    const Ptrs io{q, k, dout, dS_T, starts, prep, dv, dS0, recs, maps, false, 0};
     KDA_GDR_TYPES(chain_d, map ? BMAP : BACK, a, sg, io, stream);
 }
 

@@ -15,29 +15,33 @@ hipError_t launch_prep(bool f32, int dk, const Args& a, const void* k, const flo
 hipError_t launch_fwd_chain(bool f32, int dk, const Args& a, const Segs& sg, const void* q, const void* k, const void* v,
                             const float* S0, const float* starts, const char* prep, void* o, float* S_T, hipStream_t stream);
 hipError_t launch_save_chain(bool f32, int dk, const Args& a, const Segs& sg, const void* k, const void* v, const float* S0,
-                             const float* starts, const char* prep, char* ws_s, char* ws_e, hipStream_t stream);
+                             const float* starts, const char* prep, char* recs, hipStream_t stream);
 hipError_t launch_map_chain(bool f32, int dk, bool bwd, const Args& a, const Segs& sg, const void* k, const void* v,
                             const char* prep, float* maps, hipStream_t stream);
 hipError_t launch_back_chain(bool f32, int dk, bool map, const Args& a, const Segs& sg, const void* q, const void* k,
                              const void* dout, const float* dS_T, const float* starts, const char* prep, void* dv, float* dS0,
-                             char* ws_d, char* ws_z, float* maps, hipStream_t stream);
+                             char* recs, float* maps, hipStream_t stream);
 hipError_t launch_join(bool f32, int dk, bool bwd, const Args& a, const Segs& sg, const float* init, const float* maps,
                        const float* nmaps, float* starts, hipStream_t stream);
 hipError_t launch_grad(bool f32, int dk_, const Args& a, const void* q, const void* k, const void* dout,
-                       const char* prep, const char* ws_s, const char* ws_e, const char* ws_d, const char* ws_z, void* dq,
-                       void* dk, float* dg, float* dbeta, hipStream_t stream);
+                       const char* prep, const char* recs, void* dq, void* dk, float* dg, float* dbeta, hipStream_t stream);
 
 namespace {
 
 // Cutting a sequence costs a second walk of it (the maps, over dv + dk columns), so it pays
 // where one workgroup's walk would outlast the whole call's work spread over the 256
-// compute units by more than about that: `seg` is the even share in chunks, and sequences
-// of more than 9/4 of it are cut.  Pieces of fewer than eight chunks are not worth their join.
+// compute units by more than about that.  `seg` chunks are the even share, with half a
+// workgroup set aside for the part piece that each sequence ends with; sequences of more than
+// one and a half of it are cut.  Measured: one sequence of 1,024 chunks and 16 heads 5.25 ms
+// whole, 1.0 ms in pieces of 66, 1.1 ms in 32 or 86; eight of 64 chunks 8% slower when cut in
+// two.  Pieces of fewer than eight chunks are not worth their join.
 Segs segs_of(int nseq, int T, int Hv, int dv, bool packed) {
-    const int64_t work = places_of(nseq, T, packed, C) * Hv * ((dv + 127) / 128);
-    int64_t seg = (work + 255) / 256;
+    const int64_t heads = (int64_t)Hv * ((dv + 127) / 128), work = places_of(nseq, T, packed, C) * heads;
+    int64_t share = 256 - nseq * heads / 2;
+    if (share < 64) share = 64;
+    int64_t seg = (work + share - 1) / share;
     if (seg < 8) seg = 8;
-    const int64_t over = seg * 9 / 4;
+    const int64_t over = seg * 3 / 2;
     if (((int64_t)T + C - 1) / C <= over) return Segs{0, 0};   // none can be longer
     return Segs{(int)seg, (int)over};
 }
@@ -45,7 +49,7 @@ Segs segs_of(int nseq, int T, int Hv, int dv, bool packed) {
 // The parts of a workspace, in order; each a multiple of 16 bytes.
 struct Plan {
     Segs sg;
-    int64_t prep, s, d, e, z, maps, nmaps, starts, dstarts, bytes;
+    int64_t prep, recs, maps, nmaps, starts, dstarts, bytes;
 };
 Plan plan_of(bool bwd, int nseq, int T, int Hv, int dk, int dv, bool packed) {
     Plan p{};
@@ -58,12 +62,7 @@ Plan plan_of(bool bwd, int nseq, int T, int Hv, int dk, int dv, bool packed) {
         at += bytes;
     };
     take(p.prep, n * (int64_t)PREP_BYTES);
-    if (bwd) {
-        take(p.s, n * state_bytes(dk, dv));
-        take(p.d, n * state_bytes(dk, dv));
-        take(p.e, n * rows_bytes(dv));
-        take(p.z, n * rows_bytes(dv));
-    }
+    if (bwd) take(p.recs, n * rec_bytes(dk, dv));
     take(p.maps, m * map_bytes(dk, dv));
     take(p.starts, m * dk * dv * 4);
     if (bwd) {
@@ -117,15 +116,14 @@ hipError_t launch_gdr_bwd(const GdrCall& c, const void* dout, const float* dS_T,
     if (p.sg.seg) {
         KDA_DO(gdr::launch_map_chain(c.f32, c.dk, true, a, p.sg, c.k, c.v, ws + p.prep, maps, stream));
         KDA_DO(gdr::launch_back_chain(c.f32, c.dk, true, a, p.sg, c.q, c.k, dout, nullptr, nullptr, ws + p.prep, nullptr,
-                                      nullptr, nullptr, nullptr, nmaps, stream));
+                                      nullptr, nullptr, nmaps, stream));
         KDA_DO(gdr::launch_join(c.f32, c.dk, false, a, p.sg, c.S0, maps, maps, starts, stream));
         KDA_DO(gdr::launch_join(c.f32, c.dk, true, a, p.sg, dS_T, maps, nmaps, dstarts, stream));
     }
-    KDA_DO(gdr::launch_save_chain(c.f32, c.dk, a, p.sg, c.k, c.v, c.S0, starts, ws + p.prep, ws + p.s, ws + p.e, stream));
-    KDA_DO(gdr::launch_back_chain(c.f32, c.dk, false, a, p.sg, c.q, c.k, dout, dS_T, dstarts, ws + p.prep, dv, dS0, ws + p.d,
-                                  ws + p.z, nullptr, stream));
-    return gdr::launch_grad(c.f32, c.dk, a, c.q, c.k, dout, ws + p.prep, ws + p.s, ws + p.e, ws + p.d, ws + p.z, dq,
-                            dk, dg, dbeta, stream);
+    KDA_DO(gdr::launch_save_chain(c.f32, c.dk, a, p.sg, c.k, c.v, c.S0, starts, ws + p.prep, ws + p.recs, stream));
+    KDA_DO(gdr::launch_back_chain(c.f32, c.dk, false, a, p.sg, c.q, c.k, dout, dS_T, dstarts, ws + p.prep, dv, dS0, ws + p.recs,
+                                  nullptr, stream));
+    return gdr::launch_grad(c.f32, c.dk, a, c.q, c.k, dout, ws + p.prep, ws + p.recs, dq, dk, dg, dbeta, stream);
 }
 
 }  // namespace kda
