@@ -434,83 +434,68 @@ chain_kernel(Args a, Segs sg, Ptrs io) {
 
 // Joins the maps of a cut sequence's pieces: forwards X_0 = S0, X_{i+1} = M_i X_i + N_i, backwards
 // X_last = dS_T, X_{i-1} = M_i^T X_i + N'_i, every X_i written to `starts`.  A workgroup has one
-// head and 32 columns, a wavefront 16 of them and a quarter of the rows; X goes from
+// head and 16 columns, a wavefront one tile of rows; X goes from
 // step to step through LDS as split fragments, the next step's M and N are in flight meanwhile.
 template <typename E, int DK, bool BWD>
 __global__ void __launch_bounds__(512)
 join_kernel(Args a, Segs sg, const float* __restrict__ init, const float* __restrict__ maps, const float* __restrict__ nmaps,
             float* __restrict__ starts) {
     typedef Arith<E> A;
-    constexpr int KB = DK / 32, ST = DK / 16, RT = ST >= 4 ? ST / 4 : 1;   // row tiles a wavefront
-    __shared__ alignas(16) char lds[2][2 * KB * SPB];
+    constexpr int KB = DK / 32, ST = DK / 16;
+    __shared__ alignas(16) char lds[2][KB * SPB];
     const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), ct = w & 1, rq = w >> 1;
-    const int nslab = a.dv / 32;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int nslab = a.dv / 16;
     const int slab = (int)(blockIdx.x % (unsigned)nslab), h = (int)(blockIdx.x / (unsigned)nslab % (unsigned)a.Hv);
     const int n = (int)(blockIdx.x / (unsigned)nslab / (unsigned)a.Hv);
     const int p0 = __builtin_amdgcn_readfirstlane(place_of(a, n, seg_unit(sg)));
     const Piece pc = piece_at(a, sg, p0, lane);
     if (pc.n != n || pc.cnt < 2) return;
-    const int col = 32 * slab + 16 * ct + r;
-    const bool on = rq * RT < ST;
-    const int t0 = on ? rq * RT : 0;   // wavefronts past the rows work on the first ones and store nothing
+    const int col = 16 * slab + r;
+    const bool on = w < ST;
+    const int t = on ? w : 0;   // wavefronts past the rows work on the first tile and store nothing
     const int64_t mld = a.dv + DK, nld = BWD ? a.dv : mld;
-    f32x4 X[RT], N[RT], M[RT][KB][2];
-    auto rowof = [&](int t) { return 32 * (t / 2) + 8 * g + 4 * (t & 1); };   // this lane's first row of accumulator tile t
+    f32x4 X, N, M[KB][2];
+    const int row0 = 32 * (t / 2) + 8 * g + 4 * (t & 1);                          // this lane's first row as a result
+    const int rowa = 32 * (t / 2) + 8 * (r >> 2) + 4 * (t & 1) + (r & 3);         // and its row as an operand
     auto place = [&](int s) { return p0 + (BWD ? pc.cnt - 1 - s : s); };
     auto fetch = [&](int s) {
         const float* m = maps + ((int64_t)place(s) * a.Hv + h) * DK * mld + a.dv;
         const float* nn = nmaps + ((int64_t)place(s) * a.Hv + h) * DK * nld;
 #pragma unroll
-        for (int j = 0; j < RT; ++j) {
-            const int t = t0 + j, row = 32 * (t / 2) + 8 * (r >> 2) + 4 * (t & 1) + (r & 3);
+        for (int b = 0; b < KB; ++b)
 #pragma unroll
-            for (int b = 0; b < KB; ++b)
+            for (int q = 0; q < 2; ++q) {
+                if constexpr (BWD) {
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    if constexpr (BWD) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) M[j][b][q][i] = m[(int64_t)(32 * b + 8 * g + 4 * q + i) * mld + row];
-                    } else {
-                        M[j][b][q] = ld4(m + row * mld + 32 * b + 8 * g + 4 * q);
-                    }
+                    for (int i = 0; i < 4; ++i) M[b][q][i] = m[(int64_t)(32 * b + 8 * g + 4 * q + i) * mld + rowa];
+                } else {
+                    M[b][q] = ld4(m + rowa * mld + 32 * b + 8 * g + 4 * q);
                 }
+            }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) N[j][i] = nn[(int64_t)(rowof(t) + i) * nld + col];
-        }
+        for (int i = 0; i < 4; ++i) N[i] = nn[(int64_t)(row0 + i) * nld + col];
     };
     fetch(0);
 #pragma unroll
-    for (int j = 0; j < RT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) X[j][i] = init ? init[(((int64_t)n * a.Hv + h) * DK + rowof(t0 + j) + i) * a.dv + col] : 0.0f;
+    for (int i = 0; i < 4; ++i) X[i] = init ? init[(((int64_t)n * a.Hv + h) * DK + row0 + i) * a.dv + col] : 0.0f;
     for (int s = 0; s < pc.cnt; ++s) {
         float* to = starts + ((int64_t)place(s) * a.Hv + h) * DK * a.dv + col;
         char* buf = lds[s & 1];
         if (on) {
 #pragma unroll
-            for (int j = 0; j < RT; ++j) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) to[(int64_t)(rowof(t0 + j) + i) * a.dv] = X[j][i];
-                A::put_half(buf, ct * KB + (t0 + j) / 2, lane, (t0 + j) & 1, X[j]);
-            }
+            for (int i = 0; i < 4; ++i) to[(int64_t)(row0 + i) * a.dv] = X[i];
+            A::put_half(buf, t / 2, lane, t & 1, X);
         }
         if (s + 1 == pc.cnt) break;
-        typename A::Sp mf[RT][KB];
+        typename A::Sp mf[KB];
+        X = N;
 #pragma unroll
-        for (int j = 0; j < RT; ++j) {
-            X[j] = N[j];
-#pragma unroll
-            for (int b = 0; b < KB; ++b) mf[j][b] = A::split(M[j][b][0], M[j][b][1]);
-        }
+        for (int b = 0; b < KB; ++b) mf[b] = A::split(M[b][0], M[b][1]);
         fetch(s + 2 < pc.cnt ? s + 1 : s);
         lds_barrier();
 #pragma unroll
-        for (int b = 0; b < KB; ++b) {
-            const typename A::Sp xb = A::ld_sp(buf, ct * KB + b, lane);
-#pragma unroll
-            for (int j = 0; j < RT; ++j) X[j] = A::mma(mf[j][b], xb, X[j]);
-        }
+        for (int b = 0; b < KB; ++b) X = A::mma(mf[b], A::ld_sp(buf, b, lane), X);
     }
 }
 
@@ -547,7 +532,7 @@ hipError_t chain_d(int mode, const Args& a, const Segs& sg, const Ptrs& io, hipS
 template <typename E, int DK>
 hipError_t join_d(bool bwd, const Args& a, const Segs& sg, const float* init, const float* maps, const float* nmaps,
                   float* starts, hipStream_t stream) {
-    const dim3 grid((unsigned)((int64_t)a.nseq * a.Hv * (a.dv / 32)));
+    const dim3 grid((unsigned)((int64_t)a.nseq * a.Hv * (a.dv / 16)));
     if (bwd) hipLaunchKernelGGL((join_kernel<E, DK, true>), grid, dim3(512), 0, stream, a, sg, init, maps, nmaps, starts);
     else hipLaunchKernelGGL((join_kernel<E, DK, false>), grid, dim3(512), 0, stream, a, sg, init, maps, nmaps, starts);
     return hipGetLastError();

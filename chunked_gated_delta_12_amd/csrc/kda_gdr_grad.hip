@@ -37,7 +37,7 @@ template <typename E, int DK>
 struct GradLay {
     static constexpr int KB = DK / 32, ST = DK / 16, EXB = Arith<E>::EXB;
     static constexpr int SPLIT = 8 / ST, TT = MT / SPLIT;     // wavefronts a channel tile, token tiles of each
-    static constexpr int GB = sizeof(E) == 2 ? 4 : 2;         // 32-column blocks of a unit in LDS at once
+    static constexpr int GB = sizeof(E) == 2 ? 4 : 1;         // 32-column blocks of a unit in LDS at once
     static constexpr int QK = MT * KB * EXB;
     static constexpr int E_AT = 0, Z_AT = MT * SPB, O_AT = 2 * MT * SPB, BLK = O_AT + MT * EXB;   // one column block
     static constexpr int BUF = GB * BLK;
