@@ -144,7 +144,7 @@ def _need(t, name, dtype, shape, device):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -346,22 +346,35 @@ def kda_gate(theta, *, g=True, g_cum=True, stream=None):
 # ----------------------------------------------------------------------------- one decay a head
 class _On:
     """Makes the tensors' device and the work's stream current for one call: launches go to
-    the device, and what the call allocates belongs to the stream that uses it."""
+    the device, and what the call allocates belongs to the stream that uses it.  Where both
+    are current already there is nothing to do (a decode step's call is mostly host time)."""
+
+    __slots__ = ("raw", "ctx")
 
     def __init__(self, t, stream):
         if not t.is_cuda:
             raise ValueError("tensors must be on the GPU")
-        self.stream = torch.cuda.current_stream(t.device) if stream is None else stream
-        if self.stream.device != t.device:
-            raise ValueError(f"stream is on {self.stream.device}, tensors on {t.device}")
-        self.ctx = torch.cuda.stream(self.stream)
+        if stream is None:
+            if t.device.index == torch.cuda.current_device():
+                self.raw, self.ctx = torch._C._cuda_getCurrentRawStream(t.device.index), None
+                return
+            stream = torch.cuda.current_stream(t.device)
+        if stream.device != t.device:
+            raise ValueError(f"stream is on {stream.device}, tensors on {t.device}")
+        self.raw, self.ctx = stream.cuda_stream, torch.cuda.stream(stream)
 
     def __enter__(self):
-        self.ctx.__enter__()
-        return ctypes.c_void_p(self.stream.cuda_stream)
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.raw
 
     def __exit__(self, *exc):
-        return self.ctx.__exit__(*exc)
+        if self.ctx is not None:
+            return self.ctx.__exit__(*exc)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _dims(t, name, n):
@@ -436,8 +449,8 @@ def kda_gdr_chunk_fwd(q, k, v, g, beta, S0=None, *, cu_seqlens=None, scale=None,
         if workspace is None:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         _check("kda_gdr_chunk_fwd",
-               lib.kda_gdr_chunk_fwd(code, nseq, T, Hk, Hv, dk, dv, scale, _ptr(cu_seqlens), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
-                                     _ptr(beta), _ptr(S0), _ptr(o), _ptr(S_T), _ptr(workspace),
+               lib.kda_gdr_chunk_fwd(code, nseq, T, Hk, Hv, dk, dv, scale, _at(cu_seqlens), _at(q), _at(k), _at(v), _at(g),
+                                     _at(beta), _at(S0), _at(o), _at(S_T), _at(workspace),
                                      workspace.numel() * workspace.element_size(), st))
     return o, S_T
 
@@ -463,9 +476,9 @@ def kda_gdr_chunk_bwd(q, k, v, g, beta, do, S0=None, dS_T=None, *, cu_seqlens=No
         if workspace is None:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         _check("kda_gdr_chunk_bwd",
-               lib.kda_gdr_chunk_bwd(code, nseq, T, Hk, Hv, dk, dv, scale, _ptr(cu_seqlens), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
-                                     _ptr(beta), _ptr(S0), _ptr(do), _ptr(dS_T), _ptr(d["dq"]), _ptr(d["dk"]), _ptr(d["dv"]),
-                                     _ptr(d["dg"]), _ptr(d["dbeta"]), _ptr(d["dS0"]), _ptr(workspace),
+               lib.kda_gdr_chunk_bwd(code, nseq, T, Hk, Hv, dk, dv, scale, _at(cu_seqlens), _at(q), _at(k), _at(v), _at(g),
+                                     _at(beta), _at(S0), _at(do), _at(dS_T), _at(d["dq"]), _at(d["dk"]), _at(d["dv"]),
+                                     _at(d["dg"]), _at(d["dbeta"]), _at(d["dS0"]), _at(workspace),
                                      workspace.numel() * workspace.element_size(), st))
     return d
 
@@ -491,8 +504,8 @@ def kda_gdr_step(q, k, v, g, beta, S, *, slots=None, ntok=None, scale=None, o=No
             o = make((B, T, Hv, dv), dtype=q.dtype, device=dev)
         _need(o, "o", q.dtype, (B, T, Hv, dv), dev)
         _check("kda_gdr_step",
-               lib.kda_gdr_step(code, B, T, Hk, Hv, dk, dv, nslot, scale, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
-                                _ptr(S), _ptr(slots), _ptr(ntok), _ptr(o), st))
+               lib.kda_gdr_step(code, B, T, Hk, Hv, dk, dv, nslot, scale, _at(q), _at(k), _at(v), _at(g), _at(beta),
+                                _at(S), _at(slots), _at(ntok), _at(o), st))
     return o
 
 
@@ -533,8 +546,8 @@ def kda_block_norm_fwd(y, *, x=None, z=None, w_post=None, s=None, w_pre=None, ac
             h = torch.empty_like(y) if h is None else h
             _need(h, "h", y.dtype, y.shape, y.device)
         _check("kda_block_norm_fwd",
-               lib.kda_block_norm_fwd(code, a, rows, D, eps, _ptr(y), _ptr(x), _ptr(z), _ptr(w_post), _ptr(s), _ptr(w_pre),
-                                      _ptr(r), _ptr(h), st))
+               lib.kda_block_norm_fwd(code, a, rows, D, eps, _at(y), _at(x), _at(z), _at(w_post), _at(s), _at(w_pre),
+                                      _at(r), _at(h), st))
     return r, h
 
 
@@ -562,9 +575,9 @@ def kda_block_norm_bwd(y, dr, dh=None, *, x=None, z=None, w_post=None, s=None, w
             workspace = torch.empty(kda_block_norm_bwd_workspace_size(rows, D), dtype=torch.uint8, device=y.device)
         ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
         _check("kda_block_norm_bwd",
-               lib.kda_block_norm_bwd(code, a, rows, D, eps, _ptr(y), _ptr(x), _ptr(z), _ptr(w_post), _ptr(s), _ptr(w_pre),
-                                      _ptr(dr), _ptr(dh), _ptr(d["dy"]), _ptr(d["dx"]), _ptr(d["dz"]), _ptr(d["dw_post"]),
-                                      _ptr(d["ds"]), _ptr(d["dw_pre"]), _ptr(workspace), ws_bytes, st))
+               lib.kda_block_norm_bwd(code, a, rows, D, eps, _at(y), _at(x), _at(z), _at(w_post), _at(s), _at(w_pre),
+                                      _at(dr), _at(dh), _at(d["dy"]), _at(d["dx"]), _at(d["dz"]), _at(d["dw_post"]),
+                                      _at(d["ds"]), _at(d["dw_pre"]), _at(workspace), ws_bytes, st))
     return d
 
 
