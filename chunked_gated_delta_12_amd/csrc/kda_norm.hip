@@ -206,6 +206,10 @@ norm_bwd_kernel(int64_t rows, int D, float eps, bool silu, const E* __restrict__
     __shared__ float lds[64];
     constexpr int G = block_of(L) / L;
     __shared__ float acc_lds[G > 1 ? block_of(L) * NV * 8 : 1];
+    // 1,024 lanes a row leave 128 registers a lane, too few for three weights' sums beside a row:
+    // the sums of w_pre are in LDS there, every lane at entries of its own
+    constexpr bool PRE_LDS = L == 1024;
+    __shared__ float pre_lds[PRE_LDS ? L * NV * 8 : 1];
     const int lane = threadIdx.x % L, grp = threadIdx.x / L;
     const int nvec = D / 8;
     const float inv = 1.0f / (float)D;
@@ -217,6 +221,9 @@ norm_bwd_kernel(int64_t rows, int D, float eps, bool silu, const E* __restrict__
         const int j = lane + i * L;
         on[i] = j < nvec;
         a_post[i] = a_s[i] = a_pre[i] = V8{};
+        if constexpr (PRE_LDS)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) pre_lds[(i * 8 + e) * L + lane] = 0.0f;
         if (on[i]) {
             if (w_post) wp[i] = ld8(w_post + 8 * j);
             if (s) sc[i] = ld8(s + 8 * j);
@@ -293,7 +300,8 @@ norm_bwd_kernel(int64_t rows, int D, float eps, bool silu, const E* __restrict__
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     vd[i].f[e] += rr * vh[i].f[e] * wn[i].f[e] - vx[i].f[e] * k;
-                    a_pre[i].f[e] += vh[i].f[e] * (vx[i].f[e] * rr);
+                    if constexpr (PRE_LDS) pre_lds[(i * 8 + e) * L + lane] += vh[i].f[e] * (vx[i].f[e] * rr);
+                    else a_pre[i].f[e] += vh[i].f[e] * (vx[i].f[e] * rr);
                 }
         }
         if (dx)
@@ -349,6 +357,11 @@ norm_bwd_kernel(int64_t rows, int D, float eps, bool silu, const E* __restrict__
     if (!part) return;
     // the workgroup's rows: groups of lanes summed in order through LDS
     float* out = part + (int64_t)blockIdx.x * 3 * D;
+    if constexpr (PRE_LDS)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) a_pre[i].f[e] = pre_lds[(i * 8 + e) * L + lane];
     for (int k = 0; k < 3; ++k) {
         if (!(k == 0 ? w_post : k == 1 ? s : w_pre)) continue;
         V8 a[NV];
