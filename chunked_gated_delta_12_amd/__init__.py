@@ -377,6 +377,17 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
+def _check_workspace(t, device):
+    if t is None:
+        return
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"workspace is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
 def _dims(t, name, n):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -437,6 +448,7 @@ def kda_gdr_chunk_fwd(q, k, v, g, beta, S0=None, *, cu_seqlens=None, scale=None,
     nseq, T = _gdr_sequences(B, T, cu_seqlens, dev)
     if S0 is not None:
         _need(S0, "S0", torch.float32, (nseq, Hv, dk, dv), dev)
+    _check_workspace(workspace, dev)
     nbytes = kda_gdr_chunk_fwd_workspace_size(nseq, T, Hv, dk, dv, cu_seqlens is not None)
     with _On(q, stream) as st:
         if o is None:
@@ -468,6 +480,7 @@ def kda_gdr_chunk_bwd(q, k, v, g, beta, do, S0=None, dS_T=None, *, cu_seqlens=No
     for name, t in (("S0", S0), ("dS_T", dS_T)):
         if t is not None:
             _need(t, name, torch.float32, (nseq, Hv, dk, dv), dev)
+    _check_workspace(workspace, dev)
     nbytes = kda_gdr_chunk_bwd_workspace_size(nseq, T, Hv, dk, dv, cu_seqlens is not None)
     with _On(q, stream) as st:
         make = torch.empty_like if cu_seqlens is None else torch.zeros_like
@@ -568,6 +581,7 @@ def kda_block_norm_bwd(y, dr, dh=None, *, x=None, z=None, w_post=None, s=None, w
     for name, t in (("dr", dr), ("dh", dh)):
         if t is not None:
             _need(t, name, y.dtype, y.shape, y.device)
+    _check_workspace(workspace, y.device)
     with _On(y, stream) as st:
         d = {name: None if t is None else torch.empty_like(t)
              for name, t in (("dy", y), ("dx", x), ("dz", z), ("dw_post", w_post), ("ds", s), ("dw_pre", w_pre))}

@@ -299,7 +299,9 @@ int kda_gate(int B, int T, int H, int dk, const float* theta, float* g, float* g
 
 /* ---------------------------------------------------------------------------
  * kda_gdr_chunk_fwd: the rule over whole sequences in chunks of 64 tokens (prefill,
- * training), from a start state to a last state.
+ * training), from a start state to a last state.  A value that is not finite may reach every
+ * row of its chunk and head, the ones before it among them, and everything behind it in its
+ * sequence; other sequences and heads never see it.
  *
  *   nseq, T      cu_seqlens NULL: nseq sequences of T tokens each, tensors [nseq, T, ...].
  *                Otherwise the sequences are packed into T rows, tensors [T, ...].
@@ -332,7 +334,7 @@ int kda_gdr_chunk_fwd(int dtype, int nseq, int T, int Hk, int Hv, int dk, int dv
  *   dq, dk       as q, summed over the value heads of a key head; dv as v: dtype, written
  *   dg, dbeta    as g, fp32, written
  *   dS0          as S0, fp32, written; or NULL to skip
- *   workspace    kda_gdr_chunk_bwd_workspace_size bytes (at dk = dv = 128 240 KB a chunk
+ *   workspace    kda_gdr_chunk_bwd_workspace_size bytes (at dk = dv = 128 206 KiB a chunk
  *                of 64 tokens and value head)
  *   Every other argument is that of kda_gdr_chunk_fwd; no output may overlap anything.
  * Returns a kda_status.

@@ -330,3 +330,32 @@ def test_binding_refusals(lib):
         kda.kda_block_norm_fwd(torch.zeros(64, 4).t())   # not contiguous
     with pytest.raises(ValueError):
         kda.kda_block_norm_fwd(y)                        # not on the GPU
+
+
+def test_workspace_of_the_caller_is_checked(lib):
+    y, w = torch.zeros(4, 64), torch.ones(64)
+    with pytest.raises(ValueError, match="workspace is on"):
+        kda.kda_block_norm_bwd(y, y, w_post=w, workspace=torch.empty(1 << 20, dtype=torch.uint8, device="meta"))
+    with pytest.raises(TypeError, match="workspace"):
+        kda.kda_block_norm_bwd(y, y, w_post=w, workspace=b"")
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once():
+    """Two streams, each call with a workspace of its own: what each gives alone, bit for bit."""
+    ds = [gpu(make((3000,), 1000, torch.bfloat16, 60 + i, {"x", "z", "w_post", "s", "w_pre"})) for i in range(2)]
+
+    def call(d, stream):
+        opt = {k: d[k] for k in NAMES if k != "y"}
+        g = kda.kda_block_norm_bwd(d["y"], d["dr"], d["dh"], stream=stream, **opt)
+        return [*kda.kda_block_norm_fwd(d["y"], stream=stream, **opt)] + [g[k] for k in sorted(g)]
+
+    want = []
+    for d in ds:
+        want.append(call(d, None))
+        torch.cuda.synchronize()
+    got = [call(d, s) for d, s in zip(ds, [torch.cuda.Stream() for _ in ds])]
+    torch.cuda.synchronize()
+    for p, q in zip(want, got):
+        for j, (u, v) in enumerate(zip(p, q)):
+            assert torch.equal(u, v), j

@@ -502,3 +502,76 @@ def test_binding_refusals(lib):
         kda.kda_gdr_chunk_bwd(*a, x["do"][:, :5], cu_seqlens=c)
     with pytest.raises(ValueError):
         kda.kda_gdr_chunk_fwd(a[0], a[1], a[2], a[3][0], a[4], cu_seqlens=c)
+
+
+@pytest.mark.parametrize("which", ["fwd", "bwd"])
+def test_workspace_of_the_caller_is_checked(lib, which):
+    """What the kernels would write through is refused on the host: another device, a view with gaps, no tensor."""
+    x, cu = make([10, 20], 1, 2, 32, 32, torch.float32, 1)
+    a = [x[k] for k in ("q", "k", "v", "g", "beta")] + ([x["do"]] if which == "bwd" else [])
+    call = kda.kda_gdr_chunk_fwd if which == "fwd" else kda.kda_gdr_chunk_bwd
+    with pytest.raises(ValueError, match="workspace is on"):
+        call(*a, workspace=torch.empty(1 << 20, dtype=torch.uint8, device="meta"))
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        call(*a, workspace=torch.empty(1 << 20, dtype=torch.uint8)[::2])
+    with pytest.raises(TypeError, match="workspace"):
+        call(*a, workspace=1 << 20)
+
+
+@pytest.mark.gpu
+@both
+def test_two_calls_at_once(dtype):
+    """Two streams, each with a workspace of its own, cut sequences among them: what each gives alone."""
+    xs = [make([4500, 64], 1, 2, 64, 64, dtype, 40 + i) for i in range(2)]
+    ds = [to(x) for x, _ in xs]
+    c = torch.tensor(xs[0][1], dtype=torch.int32, device=DEV)
+
+    def both_passes(d, stream):
+        a = [d[k] for k in ("q", "k", "v", "g", "beta")]
+        o, S = kda.kda_gdr_chunk_fwd(*a, d["S0"], cu_seqlens=c, scale=1.0, stream=stream)
+        g = kda.kda_gdr_chunk_bwd(*a, d["do"], d["S0"], d["dS_T"], cu_seqlens=c, scale=1.0, stream=stream)
+        return [o, S] + [g[k] for k in sorted(g)]
+
+    want = []
+    for d in ds:
+        want.append(both_passes(d, None))
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ds]
+    got = [both_passes(d, s) for d, s in zip(ds, streams)]
+    torch.cuda.synchronize()
+    for p, q in zip(want, got):
+        for j, (u, v) in enumerate(zip(p, q)):
+            assert torch.equal(u, v), j
+
+
+@pytest.mark.gpu
+def test_two_graphs_share_a_workspace():
+    """Two captured calls of different sizes on one workspace, replayed in turn on one stream; the
+    workspace holds NaN before the first, and one byte too few is refused."""
+    xs = [make([4500], 1, 2, 64, 64, torch.bfloat16, 50), make([70, 9], 1, 2, 64, 64, torch.bfloat16, 51)]
+    ds = [(to(x), torch.tensor(cu, dtype=torch.int32, device=DEV)) for x, cu in xs]
+    need = max(kda.kda_gdr_chunk_bwd_workspace_size(len(cu) - 1, cu[-1], 2, 64, 64, True) for _, cu in xs)
+    ws = torch.full((need // 4,), float("nan"), device=DEV)
+
+    def call(d, c, w):
+        a = [d[k] for k in ("q", "k", "v", "g", "beta")]
+        o, S = kda.kda_gdr_chunk_fwd(*a, d["S0"], cu_seqlens=c, scale=1.0, workspace=w)
+        g = kda.kda_gdr_chunk_bwd(*a, d["do"], d["S0"], d["dS_T"], cu_seqlens=c, scale=1.0, workspace=w)
+        return [o, S] + [g[k] for k in sorted(g)]
+
+    with pytest.raises(kda.KdaError):
+        call(*ds[0], ws.view(torch.uint8)[:-1])
+    want = [call(d, c, None) for d, c in ds]
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for d, c in ds:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            got.append(call(d, c, ws))
+        graphs.append(gr)
+    for turn in range(3):
+        for i, gr in enumerate(graphs):
+            gr.replay()
+            torch.cuda.synchronize()
+            for j, (u, v) in enumerate(zip(want[i], got[i])):
+                assert torch.equal(u, v), (turn, i, j)
