@@ -41,7 +41,7 @@ struct Lay {
     static constexpr int VLD = SLAB + 32 / (int)sizeof(E), VROW = SLAB * (int)sizeof(E) / 16, VB = C * VLD * (int)sizeof(E);
     static constexpr int Q_AT = QK, X_AT = Q_AT + (HAS_Q ? QK : 0), F_AT = X_AT + TRI_BYTES, V_AT = X_AT + PREP_BYTES,
                          BYTES = V_AT + VB, PB = HAS_P ? TRI_BYTES : 0;
-    static constexpr int BUFS = 2 * BYTES + PB <= 160 * 1024 ? 2 : 1;
+    static constexpr int BUFS = 2 * BYTES + PB <= 160 * 1024 ? 2 : 1, ALL = BUFS * BYTES + PB;
     // 16-byte pieces, and how many of them a thread moves
     static constexpr int PQK = QK / 16, PXP = PREP_BYTES / 16, PV = C * VROW;
     static constexpr int NQK = (PQK + NTHR - 1) / NTHR, NXP = (PXP + NTHR - 1) / NTHR, NV = (PV + NTHR - 1) / NTHR;
@@ -131,22 +131,21 @@ struct Ptrs {
     int places;
 };
 
+// One walk by workgroup `block` of those that the walk has.
 template <typename E, int DK, int NW, int MODE>
-__global__ void __launch_bounds__(64 * NW, NW / 4 > 0 ? NW / 4 : 1)
-chain_kernel(Args a, Segs sg, Ptrs io) {
+__device__ __forceinline__ void walk(const Args& a, const Segs& sg, const Ptrs& io, unsigned block, char* lds) {
     typedef Arith<E> A;
     typedef Lay<E, DK, NW, MODE> L;
     constexpr int KB = L::KB, ST = DK / 16;
     constexpr bool BWD = L::BWD;
-    __shared__ alignas(16) char lds[L::BUFS * L::BYTES + L::PB];
     char* const pl = lds + L::BUFS * L::BYTES;   // P
     const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int ncols = MODE == MAP ? a.dv + DK : a.dv;
     const int nslab = (ncols + L::SLAB - 1) / L::SLAB;
-    // Workgroups go to the eight XCDs in turn: those of one key head's value heads and slabs,
+    // Workgroups (the first of a walk at a multiple of eight) go to the eight XCDs in turn: those of one key head's value heads and slabs,
     // which read the same K and Q, are eight apart and share one XCD's L2.
-    const unsigned inner = (unsigned)(a.Hv / a.Hk * nslab), grp = blockIdx.x / (8 * inner), in8 = blockIdx.x % (8 * inner);
+    const unsigned inner = (unsigned)(a.Hv / a.Hk * nslab), grp = block / (8 * inner), in8 = block % (8 * inner);
     const unsigned outer = grp * 8 + in8 % 8, sub = in8 / 8;
     const int place = (int)(outer / (unsigned)a.Hk), hk = (int)(outer % (unsigned)a.Hk);
     const int h = hk * (a.Hv / a.Hk) + (int)(sub / (unsigned)nslab), slab = (int)(sub % (unsigned)nslab);
@@ -432,6 +431,26 @@ chain_kernel(Args a, Segs sg, Ptrs io) {
             for (int i = 0; i < 4; ++i) to[(32 * (t / 2) + 8 * g + 4 * (t & 1) + i) * ld + col0 + r] = S[t][i];
 }
 
+template <typename E, int DK, int NW, int MODE>
+__global__ void __launch_bounds__(64 * NW, NW / 4)
+chain_kernel(Args a, Segs sg, Ptrs io) {
+    __shared__ alignas(16) char lds[Lay<E, DK, NW, MODE>::ALL];
+    walk<E, DK, NW, MODE>(a, sg, io, blockIdx.x, lds);
+}
+
+// Two walks in one launch, the longer one's workgroups first: the backward pass walks each way
+// once, neither needs the other, and each alone leaves compute units idle where there are
+// fewer than 256 workgroups (8 sequences of 4,096 tokens, 16 heads of 128 x 128 in bf16: 400 and
+// 470 us one after the other in workgroups of four wavefronts, 728 together in eight).
+template <typename E, int DK, int NW, int BACKWARDS, int FORWARDS>
+__global__ void __launch_bounds__(64 * NW, NW / 4)
+pair_kernel(Args a, Segs sg, Ptrs back, Ptrs forth, unsigned nback) {
+    constexpr int B = Lay<E, DK, NW, BACKWARDS>::ALL, F = Lay<E, DK, NW, FORWARDS>::ALL;
+    __shared__ alignas(16) char lds[B > F ? B : F];
+    if (blockIdx.x < nback) walk<E, DK, NW, BACKWARDS>(a, sg, back, blockIdx.x, lds);
+    else walk<E, DK, NW, FORWARDS>(a, sg, forth, blockIdx.x - nback, lds);
+}
+
 // Joins the maps of a cut sequence's pieces: forwards X_0 = S0, X_{i+1} = M_i X_i + N_i, backwards
 // X_last = dS_T, X_{i-1} = M_i^T X_i + N'_i, every X_i written to `starts`.  A workgroup has one
 // head and 16 columns, a wavefront one tile of rows; X goes from
@@ -499,34 +518,66 @@ join_kernel(Args a, Segs sg, const float* __restrict__ init, const float* __rest
     }
 }
 
-template <typename E, int DK, int NW>
-hipError_t chain_t(int mode, const Args& a, const Segs& sg, const Ptrs& io0, hipStream_t stream) {
-    const int slab = 16 * NW, cols = mode == MAP ? a.dv + DK : a.dv;
-    Ptrs io = io0;
-    io.places = (int)places_of(a.nseq, a.T, a.cu != nullptr, seg_unit(sg));
-    const int64_t outer = ((int64_t)io.places * a.Hk + 7) / 8 * 8;
-    const dim3 grid((unsigned)(outer * (a.Hv / a.Hk) * ((cols + slab - 1) / slab))), block(64 * NW);
-    switch (mode) {
-        case FWD: hipLaunchKernelGGL((chain_kernel<E, DK, NW, FWD>), grid, block, 0, stream, a, sg, io); break;
-        case SAVE: hipLaunchKernelGGL((chain_kernel<E, DK, NW, SAVE>), grid, block, 0, stream, a, sg, io); break;
-        case MAP: hipLaunchKernelGGL((chain_kernel<E, DK, NW, MAP>), grid, block, 0, stream, a, sg, io); break;
-        case BACK: hipLaunchKernelGGL((chain_kernel<E, DK, NW, BACK>), grid, block, 0, stream, a, sg, io); break;
-        case BMAP: hipLaunchKernelGGL((chain_kernel<E, DK, NW, BMAP>), grid, block, 0, stream, a, sg, io); break;
-    }
-    return hipGetLastError();
+// Workgroups of a walk over `cols` columns: a multiple of eight.
+int64_t groups_of(const Args& a, int places, int cols, int slab) {
+    return ((int64_t)places * a.Hk + 7) / 8 * 8 * (a.Hv / a.Hk) * ((cols + slab - 1) / slab);
 }
 
 // Wavefronts a workgroup: eight share one set of operands over 128 columns; four where a
 // head has no more columns, or where workgroups of eight would leave half the chip empty.
-template <typename E, int DK>
-hipError_t chain_d(int mode, const Args& a, const Segs& sg, const Ptrs& io, hipStream_t stream) {
-    const int cols = mode == MAP ? a.dv + DK : a.dv;
+// `slabs` of 64 columns a head.
+bool wide(const Args& a, const Segs& sg, int slabs) {
     // Pieces to expect.  The lengths of packed sequences are not known here: as if all were equal.
     const int64_t chunks = places_of(a.nseq, a.T, a.cu != nullptr, C), places = places_of(a.nseq, a.T, a.cu != nullptr, seg_unit(sg));
     const int64_t heads = (sg.seg && chunks / a.nseq > sg.over ? places : a.nseq) * a.Hv;
-    if (sizeof(E) == 4 || cols <= 64 || heads * ((cols + 63) / 64) <= 256) return chain_t<E, DK, 4>(mode, a, sg, io, stream);
-    if constexpr (sizeof(E) == 2) return chain_t<E, DK, 8>(mode, a, sg, io, stream);
-    return hipErrorInvalidValue;
+    return heads * slabs > 256;
+}
+
+template <typename E, int DK, int NW, int MODE>
+hipError_t one_t(const Args& a, const Segs& sg, const Ptrs& io, int cols, hipStream_t stream) {
+    hipLaunchKernelGGL((chain_kernel<E, DK, NW, MODE>), dim3((unsigned)groups_of(a, io.places, cols, 16 * NW)), dim3(64 * NW), 0,
+                       stream, a, sg, io);
+    return hipGetLastError();
+}
+
+template <typename E, int DK, int MODE>
+hipError_t one_d(const Args& a, const Segs& sg, Ptrs io, hipStream_t stream) {
+    const int cols = MODE == MAP ? a.dv + DK : a.dv;
+    io.places = (int)places_of(a.nseq, a.T, a.cu != nullptr, seg_unit(sg));
+    if constexpr (sizeof(E) == 2)
+        if (cols > 64 && wide(a, sg, (cols + 63) / 64)) return one_t<E, DK, 8, MODE>(a, sg, io, cols, stream);
+    return one_t<E, DK, 4, MODE>(a, sg, io, cols, stream);
+}
+
+template <typename E, int DK, int NW, int BACKWARDS, int FORWARDS>
+hipError_t pair_t(const Args& a, const Segs& sg, const Ptrs& back, const Ptrs& forth, int fcols, hipStream_t stream) {
+    const int64_t nback = groups_of(a, back.places, a.dv, 16 * NW), nforth = groups_of(a, back.places, fcols, 16 * NW);
+    hipLaunchKernelGGL((pair_kernel<E, DK, NW, BACKWARDS, FORWARDS>), dim3((unsigned)(nback + nforth)), dim3(64 * NW), 0, stream, a,
+                       sg, back, forth, (unsigned)nback);
+    return hipGetLastError();
+}
+
+template <typename E, int DK, int BACKWARDS, int FORWARDS>
+hipError_t pair_d(const Args& a, const Segs& sg, Ptrs back, Ptrs forth, hipStream_t stream) {
+    const int fcols = FORWARDS == MAP ? a.dv + DK : a.dv;
+    back.places = forth.places = (int)places_of(a.nseq, a.T, a.cu != nullptr, seg_unit(sg));
+    if constexpr (sizeof(E) == 2)
+        if (a.dv > 64 && wide(a, sg, (a.dv + 63) / 64 + (fcols + 63) / 64))
+            return pair_t<E, DK, 8, BACKWARDS, FORWARDS>(a, sg, back, forth, fcols, stream);
+    return pair_t<E, DK, 4, BACKWARDS, FORWARDS>(a, sg, back, forth, fcols, stream);
+}
+
+template <typename E, int DK>
+hipError_t fwd_d(const Args& a, const Segs& sg, const Ptrs& io, hipStream_t stream) {
+    return one_d<E, DK, FWD>(a, sg, io, stream);
+}
+template <typename E, int DK>
+hipError_t map_d(const Args& a, const Segs& sg, const Ptrs& io, hipStream_t stream) {
+    return one_d<E, DK, MAP>(a, sg, io, stream);
+}
+template <typename E, int DK>
+hipError_t grads_d(bool maps, const Args& a, const Segs& sg, const Ptrs& back, const Ptrs& forth, hipStream_t stream) {
+    return maps ? pair_d<E, DK, BMAP, MAP>(a, sg, back, forth, stream) : pair_d<E, DK, BACK, SAVE>(a, sg, back, forth, stream);
 }
 
 template <typename E, int DK>
@@ -559,26 +610,28 @@ hipError_t join_d(bool bwd, const Args& a, const Segs& sg, const float* init, co
 hipError_t launch_fwd_chain(bool f32, int dk, const Args& a, const Segs& sg, const void* q, const void* k, const void* v,
                             const float* S0, const float* starts, const char* prep, void* o, float* S_T, hipStream_t stream) {
     const Ptrs io{q, k, v, S0, starts, prep, o, S_T, nullptr, nullptr, false, 0};
-    KDA_GDR_TYPES(chain_d, FWD, a, sg, io, stream);
+    KDA_GDR_TYPES(fwd_d, a, sg, io, stream);
 }
 
-hipError_t launch_save_chain(bool f32, int dk, const Args& a, const Segs& sg, const void* k, const void* v, const float* S0,
-                             const float* starts, const char* prep, char* recs, hipStream_t stream) {
-    const Ptrs io{k, k, v, S0, starts, prep, nullptr, nullptr, recs, nullptr, false, 0};
-    KDA_GDR_TYPES(chain_d, SAVE, a, sg, io, stream);
+hipError_t launch_maps(bool f32, int dk, const Args& a, const Segs& sg, const void* k, const void* v, const char* prep,
+                       float* maps, hipStream_t stream) {
+    const Ptrs io{k, k, v, nullptr, nullptr, prep, nullptr, nullptr, nullptr, maps, false, 0};
+    KDA_GDR_TYPES(map_d, a, sg, io, stream);
 }
 
-hipError_t launch_map_chain(bool f32, int dk, bool bwd, const Args& a, const Segs& sg, const void* k, const void* v,
-                            const char* prep, float* maps, hipStream_t stream) {
-    const Ptrs io{k, k, v, nullptr, nullptr, prep, nullptr, nullptr, nullptr, maps, bwd, 0};
-    KDA_GDR_TYPES(chain_d, MAP, a, sg, io, stream);
+hipError_t launch_bwd_maps(bool f32, int dk, const Args& a, const Segs& sg, const void* q, const void* k, const void* v,
+                           const void* dout, const char* prep, float* maps, float* nmaps, hipStream_t stream) {
+    const Ptrs back{q, k, dout, nullptr, nullptr, prep, nullptr, nullptr, nullptr, nmaps, false, 0};
+    const Ptrs forth{k, k, v, nullptr, nullptr, prep, nullptr, nullptr, nullptr, maps, true, 0};
+    KDA_GDR_TYPES(grads_d, true, a, sg, back, forth, stream);
 }
 
-hipError_t launch_back_chain(bool f32, int dk, bool map, const Args& a, const Segs& sg, const void* q, const void* k,
-                             const void* dout, const float* dS_T, const float* starts, const char* prep, void* dv, float* dS0,
-                             char* recs, float* maps, hipStream_t stream) {
-    const Ptrs io{q, k, dout, dS_T, starts, prep, dv, dS0, recs, maps, false, 0};
-    KDA_GDR_TYPES(chain_d, map ? BMAP : BACK, a, sg, io, stream);
+hipError_t launch_bwd_chains(bool f32, int dk, const Args& a, const Segs& sg, const void* q, const void* k, const void* v,
+                             const void* dout, const float* S0, const float* starts, const float* dS_T, const float* dstarts,
+                             const char* prep, void* dv, float* dS0, char* recs, hipStream_t stream) {
+    const Ptrs back{q, k, dout, dS_T, dstarts, prep, dv, dS0, recs, nullptr, false, 0};
+    const Ptrs forth{k, k, v, S0, starts, prep, nullptr, nullptr, recs, nullptr, false, 0};
+    KDA_GDR_TYPES(grads_d, false, a, sg, back, forth, stream);
 }
 
 hipError_t launch_join(bool f32, int dk, bool bwd, const Args& a, const Segs& sg, const float* init, const float* maps,

@@ -1,8 +1,8 @@
 // kda_gdr_chunk.hip -- the launches of the chunked gated delta rule with one decay a head and
 // the layout of its workspace.
 //   forward:   prep (X and the decays of every chunk) -> [maps -> join] -> chain (states, outputs)
-//   backward:  prep -> [maps, backward maps -> joins] -> chain saving the states ->
-//              chain backwards -> grad
+//   backward:  prep -> [maps both ways -> joins] -> chains both ways, saving the states and
+//              their gradients -> grad
 // The steps in brackets run where sequences are cut into pieces that are walked side by side.
 #include "kda_gdr.hpp"
 #include "kda_launch.hpp"
@@ -14,13 +14,13 @@ hipError_t launch_prep(bool f32, int dk, const Args& a, const void* k, const flo
                        hipStream_t stream);
 hipError_t launch_fwd_chain(bool f32, int dk, const Args& a, const Segs& sg, const void* q, const void* k, const void* v,
                             const float* S0, const float* starts, const char* prep, void* o, float* S_T, hipStream_t stream);
-hipError_t launch_save_chain(bool f32, int dk, const Args& a, const Segs& sg, const void* k, const void* v, const float* S0,
-                             const float* starts, const char* prep, char* recs, hipStream_t stream);
-hipError_t launch_map_chain(bool f32, int dk, bool bwd, const Args& a, const Segs& sg, const void* k, const void* v,
-                            const char* prep, float* maps, hipStream_t stream);
-hipError_t launch_back_chain(bool f32, int dk, bool map, const Args& a, const Segs& sg, const void* q, const void* k,
-                             const void* dout, const float* dS_T, const float* starts, const char* prep, void* dv, float* dS0,
-                             char* recs, float* maps, hipStream_t stream);
+hipError_t launch_maps(bool f32, int dk, const Args& a, const Segs& sg, const void* k, const void* v, const char* prep,
+                       float* maps, hipStream_t stream);
+hipError_t launch_bwd_maps(bool f32, int dk, const Args& a, const Segs& sg, const void* q, const void* k, const void* v,
+                           const void* dout, const char* prep, float* maps, float* nmaps, hipStream_t stream);
+hipError_t launch_bwd_chains(bool f32, int dk, const Args& a, const Segs& sg, const void* q, const void* k, const void* v,
+                             const void* dout, const float* S0, const float* starts, const float* dS_T, const float* dstarts,
+                             const char* prep, void* dv, float* dS0, char* recs, hipStream_t stream);
 hipError_t launch_join(bool f32, int dk, bool bwd, const Args& a, const Segs& sg, const float* init, const float* maps,
                        const float* nmaps, float* starts, hipStream_t stream);
 hipError_t launch_grad(bool f32, int dk_, const Args& a, const void* q, const void* k, const void* dout,
@@ -99,7 +99,7 @@ hipError_t launch_gdr_fwd(const GdrCall& c, void* o, float* S_T, void* workspace
     float *maps = (float*)(ws + p.maps), *starts = (float*)(ws + p.starts);
     KDA_DO(gdr::launch_prep(c.f32, c.dk, a, c.k, c.g, c.beta, ws + p.prep, stream));
     if (p.sg.seg) {
-        KDA_DO(gdr::launch_map_chain(c.f32, c.dk, false, a, p.sg, c.k, c.v, ws + p.prep, maps, stream));
+        KDA_DO(gdr::launch_maps(c.f32, c.dk, a, p.sg, c.k, c.v, ws + p.prep, maps, stream));
         KDA_DO(gdr::launch_join(c.f32, c.dk, false, a, p.sg, c.S0, maps, maps, starts, stream));
     }
     return gdr::launch_fwd_chain(c.f32, c.dk, a, p.sg, c.q, c.k, c.v, c.S0, starts, ws + p.prep, o, S_T, stream);
@@ -114,15 +114,12 @@ hipError_t launch_gdr_bwd(const GdrCall& c, const void* dout, const float* dS_T,
     float *starts = (float*)(ws + p.starts), *dstarts = (float*)(ws + p.dstarts);
     KDA_DO(gdr::launch_prep(c.f32, c.dk, a, c.k, c.g, c.beta, ws + p.prep, stream));
     if (p.sg.seg) {
-        KDA_DO(gdr::launch_map_chain(c.f32, c.dk, true, a, p.sg, c.k, c.v, ws + p.prep, maps, stream));
-        KDA_DO(gdr::launch_back_chain(c.f32, c.dk, true, a, p.sg, c.q, c.k, dout, nullptr, nullptr, ws + p.prep, nullptr,
-                                      nullptr, nullptr, nmaps, stream));
+        KDA_DO(gdr::launch_bwd_maps(c.f32, c.dk, a, p.sg, c.q, c.k, c.v, dout, ws + p.prep, maps, nmaps, stream));
         KDA_DO(gdr::launch_join(c.f32, c.dk, false, a, p.sg, c.S0, maps, maps, starts, stream));
         KDA_DO(gdr::launch_join(c.f32, c.dk, true, a, p.sg, dS_T, maps, nmaps, dstarts, stream));
     }
-    KDA_DO(gdr::launch_save_chain(c.f32, c.dk, a, p.sg, c.k, c.v, c.S0, starts, ws + p.prep, ws + p.recs, stream));
-    KDA_DO(gdr::launch_back_chain(c.f32, c.dk, false, a, p.sg, c.q, c.k, dout, dS_T, dstarts, ws + p.prep, dv, dS0, ws + p.recs,
-                                  nullptr, stream));
+    KDA_DO(gdr::launch_bwd_chains(c.f32, c.dk, a, p.sg, c.q, c.k, c.v, dout, c.S0, starts, dS_T, dstarts, ws + p.prep, dv, dS0,
+                                  ws + p.recs, stream));
     return gdr::launch_grad(c.f32, c.dk, a, c.q, c.k, dout, ws + p.prep, ws + p.recs, dq, dk, dg, dbeta, stream);
 }
 
