@@ -116,12 +116,29 @@ __device__ __forceinline__ Chunk chunk_at(const Args& a, int place, int lane) {
     return Chunk{u.n, u.i, left < C ? left : C, s.row0 + (int64_t)u.i * C};
 }
 
-// Segments: a sequence of more than `over` chunks is walked in pieces of `seg` chunks, joined
-// by their affine maps; others in one piece.  seg = 0: none is cut.
+// Segments: where a sequence has more than `over` chunks, those of more than `seg` are walked in
+// pieces of `seg` chunks, joined by their affine maps; others in one piece.  seg = 0: none is cut.
 struct Segs {
     int seg, over;
 };
 __host__ __device__ inline int64_t seg_unit(const Segs& g) { return g.seg ? (int64_t)g.seg * C : (int64_t)1 << 40; }
+
+// Whether a sequence of nch chunks is cut: the same in every kernel of a call.
+__device__ __forceinline__ bool is_cut(const Args& a, const Segs& g, int nch, int lane) {
+    if (!g.seg || nch <= g.seg) return false;
+    if (nch > g.over || !a.cu) return nch > g.over;
+    for (int n0 = 0; n0 < a.nseq; n0 += 64) {   // is there a longer one?
+        bool more = false;
+        if (n0 + lane < a.nseq) {
+            int lo = a.cu[n0 + lane], hi = a.cu[n0 + lane + 1];
+            lo = lo < 0 ? 0 : lo > a.T ? a.T : lo;
+            hi = hi < lo ? lo : hi > a.T ? a.T : hi;
+            more = ((int64_t)(hi - lo) + C - 1) / C > g.over;
+        }
+        if (__ballot(more)) return true;
+    }
+    return false;
+}
 
 // The piece at a place of seg_unit tokens: chunks [c0, c1) of sequence n, piece i of cnt.
 struct Piece {
@@ -135,7 +152,7 @@ __device__ __forceinline__ Piece piece_at(const Args& a, const Segs& sg, int pla
     if (u.n < 0 || u.i < 0) return p;
     p.s = seq_of(a, u.n);
     const int nch = (int)(((int64_t)p.s.len + C - 1) / C);
-    p.cnt = sg.seg && nch > sg.over ? (nch + sg.seg - 1) / sg.seg : 1;
+    p.cnt = is_cut(a, sg, nch, lane) ? (nch + sg.seg - 1) / sg.seg : 1;
     if (u.i >= p.cnt) return p;
     p.n = u.n;
     p.i = u.i;

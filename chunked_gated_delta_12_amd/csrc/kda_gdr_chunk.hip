@@ -28,21 +28,26 @@ hipError_t launch_grad(bool f32, int dk_, const Args& a, const void* q, const vo
 
 namespace {
 
-// Cutting a sequence costs a second walk of it (the maps, over dv + dk columns), so it pays
-// where one workgroup's walk would outlast the whole call's work spread over the 256
-// compute units by more than about that.  `seg` chunks are the even share, with half a
-// workgroup set aside for the part piece that each sequence ends with; sequences of more than
-// one and a half of it are cut.  Measured: one sequence of 1,024 chunks and 16 heads 5.25 ms
-// whole, 1.0 ms in pieces of 66, 1.1 ms in 32 or 86; eight of 64 chunks 8% slower when cut in
-// two.  Pieces of fewer than eight chunks are not worth their join.
+// Cutting a sequence costs a second walk of it (the maps, over dv + dk columns) and the join of
+// its pieces, so it pays where its own walk would outlast the others' by much.  With a chunk
+// taking about 5 us in a walk and 3.4 us in a map, and a piece 2.6 us in the join (bf16,
+// 128 x 128; fp32 in like proportion), L chunks in pieces of s take 8.4 s + 2.6 L / s us: least at
+// s^2 = 0.31 L, where the chip has room for so many.  `seg` is that, but at least the even share
+// of the call's work over the 256 compute units, half a workgroup set aside for the part piece that
+// each sequence ends with.  Uncut the walk takes 5 L us: longer than the pieces from about
+// L = 1.7 seg + 3 on, which is `over`; once any sequence is longer than that the maps run
+// anyway, and all longer than a piece are cut.  Measured: one sequence of 1,024 chunks and 16 heads 5.25 ms
+// whole, 1.0 ms in pieces of 66, 1.1 ms in 32 or 86; eight of 64 chunks 8% slower when cut in two.
 Segs segs_of(int nseq, int T, int Hv, int dv, bool packed) {
     const int64_t heads = (int64_t)Hv * ((dv + 127) / 128), work = places_of(nseq, T, packed, C) * heads;
+    const int64_t longest = ((int64_t)T + C - 1) / C;   // that a sequence can be
     int64_t share = 256 - nseq * heads / 2;
     if (share < 64) share = 64;
-    int64_t seg = (work + share - 1) / share;
-    if (seg < 8) seg = 8;
-    const int64_t over = seg * 3 / 2;
-    if (((int64_t)T + C - 1) / C <= over) return Segs{0, 0};   // none can be longer
+    int64_t seg = 2;
+    while (100 * seg * seg < 31 * longest) ++seg;
+    if (seg < (work + share - 1) / share) seg = (work + share - 1) / share;
+    const int64_t over = (17 * seg + 30) / 10;
+    if (longest <= over) return Segs{0, 0};
     return Segs{(int)seg, (int)over};
 }
 

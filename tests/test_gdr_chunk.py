@@ -208,7 +208,7 @@ def test_many_workgroups(dk, dv):
 @pytest.mark.parametrize("lens,Hk,Hv,dk,dv", [
     ([1500], 1, 2, 64, 64), ([1217], 1, 1, 128, 128), ([30, 1300, 0, 1153, 64], 1, 2, 32, 96), ([1200, 1160], 2, 2, 64, 160)])
 def test_cut_sequences(lens, Hk, Hv, dk, dv, dtype):
-    """Few heads over sequences of more than 18 chunks: walked in pieces of eight chunks joined
+    """Few heads over long sequences: walked in pieces of a few chunks joined
     by their maps, beside sequences that are not cut."""
     x, cu = make(lens, Hk, Hv, dk, dv, dtype, sum(lens), head=5, tail=2, gmu=-5.0)
     check(x, cu, dk ** -0.5, dtype)
