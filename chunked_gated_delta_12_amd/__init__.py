@@ -93,6 +93,8 @@ def load_library(path: str = LIB_PATH):
     for fn in (lib.kda_gdr_chunk_fwd_workspace_size, lib.kda_gdr_chunk_bwd_workspace_size):
         fn.argtypes = [c_int] * 6 + [ctypes.POINTER(c_size)]
         fn.restype = c_int
+    lib.kda_gdr_clear_rows.argtypes = [c_int, c_int, vp, c_int, ctypes.POINTER(vp), ctypes.POINTER(c_size), vp]
+    lib.kda_gdr_clear_rows.restype = c_int
     lib.kda_gdr_step.argtypes = [c_int] * 8 + [ctypes.c_float] + [vp] * 3 + [fp] * 3 + [vp, vp, vp, vp]
     lib.kda_gdr_step.restype = c_int
     lib.kda_block_norm_fwd.argtypes = [c_int, c_int, ctypes.c_longlong, c_int, ctypes.c_float] + [vp] * 9
@@ -435,6 +437,32 @@ def kda_gdr_chunk_bwd_workspace_size(nseq, T, Hv, dk, dv, packed=False) -> int:
     return int(n.value)
 
 
+def kda_gdr_clear_rows(cu_seqlens, *tensors, stream=None):
+    """Zeros in the rows of no sequence of packed tensors [1,T,..], one to eight, of one T: those
+    before cu_seqlens[0] and from cu_seqlens[-1] on.  Nothing else is touched."""
+    if not tensors:
+        raise ValueError("no tensors")
+    n = _dims(cu_seqlens, "cu_seqlens", 1)[0] - 1
+    for t in tensors:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("tensors must be torch.Tensors")
+        if t.dim() < 2 or t.shape[0] != 1:
+            raise ValueError(f"packed tensors are [1,T,..], got {tuple(t.shape)}")
+    dev, T = tensors[0].device, tensors[0].shape[1]
+    _need(cu_seqlens, "cu_seqlens", torch.int32, (n + 1,), dev)
+    for t in tensors:
+        _need(t, "tensor", t.dtype, (1, T) + tuple(t.shape[2:]), dev)
+    with _On(tensors[0], stream) as st:
+        _clear_rows(n, T, cu_seqlens, tensors, st)
+
+
+def _clear_rows(n, T, cu_seqlens, tensors, st):
+    k = len(tensors)
+    ptrs = (ctypes.c_void_p * k)(*[t.data_ptr() for t in tensors])
+    sizes = (ctypes.c_size_t * k)(*[t.stride(1) * t.element_size() for t in tensors])
+    _check("kda_gdr_clear_rows", load_library().kda_gdr_clear_rows(n, T, _at(cu_seqlens), k, ptrs, sizes, st))
+
+
 def kda_gdr_chunk_fwd(q, k, v, g, beta, S0=None, *, cu_seqlens=None, scale=None, o=None, S_T=None, want_state=True,
                       workspace=None, stream=None):
     """The gated delta rule with one decay a head over whole sequences.  q, k [B,T,Hk,dk],
@@ -452,7 +480,9 @@ def kda_gdr_chunk_fwd(q, k, v, g, beta, S0=None, *, cu_seqlens=None, scale=None,
     nbytes = kda_gdr_chunk_fwd_workspace_size(nseq, T, Hv, dk, dv, cu_seqlens is not None)
     with _On(q, stream) as st:
         if o is None:
-            o = (torch.empty if cu_seqlens is None else torch.zeros)((B, T, Hv, dv), dtype=q.dtype, device=dev)
+            o = torch.empty((B, T, Hv, dv), dtype=q.dtype, device=dev)
+            if cu_seqlens is not None:
+                _clear_rows(nseq, T, cu_seqlens, (o,), st)
         _need(o, "o", q.dtype, (B, T, Hv, dv), dev)
         if S_T is None and want_state:
             S_T = torch.empty((nseq, Hv, dk, dv), dtype=torch.float32, device=dev)
@@ -483,9 +513,11 @@ def kda_gdr_chunk_bwd(q, k, v, g, beta, do, S0=None, dS_T=None, *, cu_seqlens=No
     _check_workspace(workspace, dev)
     nbytes = kda_gdr_chunk_bwd_workspace_size(nseq, T, Hv, dk, dv, cu_seqlens is not None)
     with _On(q, stream) as st:
-        make = torch.empty_like if cu_seqlens is None else torch.zeros_like
-        d = {"dq": make(q), "dk": make(k), "dv": make(v), "dg": make(g), "dbeta": make(beta),
+        d = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
+             "dg": torch.empty_like(g), "dbeta": torch.empty_like(beta),
              "dS0": torch.empty((nseq, Hv, dk, dv), dtype=torch.float32, device=dev) if want_dS0 else None}
+        if cu_seqlens is not None:
+            _clear_rows(nseq, T, cu_seqlens, [d[name] for name in ("dq", "dk", "dv", "dg", "dbeta")], st)
         if workspace is None:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         _check("kda_gdr_chunk_bwd",
@@ -596,7 +628,7 @@ def kda_block_norm_bwd(y, dr, dh=None, *, x=None, z=None, w_post=None, s=None, w
 
 
 __all__ = ["kda_gdr_chunk_fwd", "kda_gdr_chunk_bwd", "kda_gdr_chunk_fwd_workspace_size",
-           "kda_gdr_chunk_bwd_workspace_size", "kda_gdr_step", "kda_block_norm_fwd", "kda_block_norm_bwd", "kda_block_norm_bwd_workspace_size",
+           "kda_gdr_chunk_bwd_workspace_size", "kda_gdr_clear_rows", "kda_gdr_step", "kda_block_norm_fwd", "kda_block_norm_bwd", "kda_block_norm_bwd_workspace_size",
            "KDA_ACT_SIGMOID", "KDA_ACT_SILU", "kda_chunk_fwd", "kda_chunk_fwd_noalloc", "kda_chunk_fwd_gated", "kda_chunk_fwd_unbounded", "kda_chunk_bwd",
            "kda_chunk_bwd_workspace_size", "kda_decode_step",
            "kda_decode_step_gated", "kda_gate", "kda_chunk_fwd_workspace_size",

@@ -510,6 +510,25 @@ int kda_gdr_chunk_bwd(int dtype, int nseq, int T, int Hk, int Hv, int dk, int dv
     return ok();
 }
 
+int kda_gdr_clear_rows(int nseq, int T, const int* cu_seqlens, int n, void* const* tensors, const size_t* row_bytes,
+                       void* stream) {
+    if (nseq < 1 || T < 1) return fail(KDA_ERR_SHAPE, "sequences=%d T=%d must be >= 1", nseq, T);
+    if (n < 1 || n > kda::GDR_CLEAR_MAX) return fail(KDA_ERR_SHAPE, "n=%d tensors outside [1, %d]", n, kda::GDR_CLEAR_MAX);
+    if (!cu_seqlens || !tensors || !row_bytes) return fail(KDA_ERR_NULL, "cu_seqlens, tensors and row_bytes must be non-NULL");
+    Range out[kda::GDR_CLEAR_MAX];
+    for (int i = 0; i < n; ++i) {
+        if (!tensors[i]) return fail(KDA_ERR_NULL, "tensor %d is NULL", i);
+        if (row_bytes[i] < 4 || row_bytes[i] % 4 || row_bytes[i] >= (size_t)1 << 31)
+            return fail(KDA_ERR_SHAPE, "rows of %zu bytes: must be a multiple of 4 below 2^31", row_bytes[i]);
+        out[i] = rng("tensor", tensors[i], (size_t)T * row_bytes[i]);
+    }
+    const Range in[] = {rng("cu_seqlens", cu_seqlens, ((size_t)nseq + 1) * 4)};
+    if (int st = check_ranges(in, 1, out, n)) return st;
+    hipError_t e = kda::launch_gdr_clear(nseq, T, cu_seqlens, n, tensors, row_bytes, reinterpret_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(KDA_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
 // ---------------------------------------------------------------- block norm
 static int check_norm(int dtype, int act, long long rows, int D, float eps) {
     if (dtype != KDA_BF16 && dtype != KDA_F32) return fail(KDA_ERR_DTYPE, "unknown dtype %d", dtype);

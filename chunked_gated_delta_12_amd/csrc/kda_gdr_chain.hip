@@ -456,12 +456,10 @@ pair_kernel(Args a, Segs sg, Ptrs back, Ptrs forth, unsigned nback) {
 // head and 16 columns, a wavefront one tile of rows; X goes from
 // step to step through LDS as split fragments, the next step's M and N are in flight meanwhile.
 template <typename E, int DK, bool BWD>
-__global__ void __launch_bounds__(512)
-join_kernel(Args a, Segs sg, const float* __restrict__ init, const float* __restrict__ maps, const float* __restrict__ nmaps,
-            float* __restrict__ starts) {
+__device__ __forceinline__ void join(const Args& a, const Segs& sg, const float* __restrict__ init, const float* __restrict__ maps,
+                                     const float* __restrict__ nmaps, float* __restrict__ starts, char (&lds)[2][DK / 32 * SPB]) {
     typedef Arith<E> A;
     constexpr int KB = DK / 32, ST = DK / 16;
-    __shared__ alignas(16) char lds[2][KB * SPB];
     const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int nslab = a.dv / 16;
@@ -516,6 +514,16 @@ join_kernel(Args a, Segs sg, const float* __restrict__ init, const float* __rest
 #pragma unroll
         for (int b = 0; b < KB; ++b) X = A::mma(mf[b], A::ld_sp(buf, b, lane), X);
     }
+}
+
+// The backward pass joins both ways in one launch (blockIdx.y).
+template <typename E, int DK>
+__global__ void __launch_bounds__(512)
+join_kernel(Args a, Segs sg, const float* init, const float* maps, float* starts, const float* dinit, const float* nmaps,
+            float* dstarts) {
+    __shared__ alignas(16) char lds[2][DK / 32 * SPB];
+    if (blockIdx.y == 0) join<E, DK, false>(a, sg, init, maps, maps, starts, lds);
+    else join<E, DK, true>(a, sg, dinit, maps, nmaps, dstarts, lds);
 }
 
 // Workgroups of a walk over `cols` columns: a multiple of eight.
@@ -581,11 +589,10 @@ hipError_t grads_d(bool maps, const Args& a, const Segs& sg, const Ptrs& back, c
 }
 
 template <typename E, int DK>
-hipError_t join_d(bool bwd, const Args& a, const Segs& sg, const float* init, const float* maps, const float* nmaps,
-                  float* starts, hipStream_t stream) {
-    const dim3 grid((unsigned)((int64_t)a.nseq * a.Hv * (a.dv / 16)));
-    if (bwd) hipLaunchKernelGGL((join_kernel<E, DK, true>), grid, dim3(512), 0, stream, a, sg, init, maps, nmaps, starts);
-    else hipLaunchKernelGGL((join_kernel<E, DK, false>), grid, dim3(512), 0, stream, a, sg, init, maps, nmaps, starts);
+hipError_t join_d(const Args& a, const Segs& sg, const float* init, const float* maps, float* starts, const float* dinit,
+                  const float* nmaps, float* dstarts, hipStream_t stream) {
+    const dim3 grid((unsigned)((int64_t)a.nseq * a.Hv * (a.dv / 16)), nmaps ? 2 : 1);
+    hipLaunchKernelGGL((join_kernel<E, DK>), grid, dim3(512), 0, stream, a, sg, init, maps, starts, dinit, nmaps, dstarts);
     return hipGetLastError();
 }
 
@@ -634,9 +641,9 @@ hipError_t launch_bwd_chains(bool f32, int dk, const Args& a, const Segs& sg, co
     KDA_GDR_TYPES(grads_d, false, a, sg, back, forth, stream);
 }
 
-hipError_t launch_join(bool f32, int dk, bool bwd, const Args& a, const Segs& sg, const float* init, const float* maps,
-                       const float* nmaps, float* starts, hipStream_t stream) {
-    KDA_GDR_TYPES(join_d, bwd, a, sg, init, maps, nmaps, starts, stream);
+hipError_t launch_join(bool f32, int dk, const Args& a, const Segs& sg, const float* init, const float* maps, float* starts,
+                       const float* dinit, const float* nmaps, float* dstarts, hipStream_t stream) {
+    KDA_GDR_TYPES(join_d, a, sg, init, maps, starts, dinit, nmaps, dstarts, stream);
 }
 
 }  // namespace gdr

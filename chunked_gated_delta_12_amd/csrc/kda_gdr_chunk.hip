@@ -21,8 +21,8 @@ hipError_t launch_bwd_maps(bool f32, int dk, const Args& a, const Segs& sg, cons
 hipError_t launch_bwd_chains(bool f32, int dk, const Args& a, const Segs& sg, const void* q, const void* k, const void* v,
                              const void* dout, const float* S0, const float* starts, const float* dS_T, const float* dstarts,
                              const char* prep, void* dv, float* dS0, char* recs, hipStream_t stream);
-hipError_t launch_join(bool f32, int dk, bool bwd, const Args& a, const Segs& sg, const float* init, const float* maps,
-                       const float* nmaps, float* starts, hipStream_t stream);
+hipError_t launch_join(bool f32, int dk, const Args& a, const Segs& sg, const float* init, const float* maps, float* starts,
+                       const float* dinit, const float* nmaps, float* dstarts, hipStream_t stream);
 hipError_t launch_grad(bool f32, int dk_, const Args& a, const void* q, const void* k, const void* dout,
                        const char* prep, const char* recs, void* dq, void* dk, float* dg, float* dbeta, hipStream_t stream);
 
@@ -78,6 +78,28 @@ Plan plan_of(bool bwd, int nseq, int T, int Hv, int dk, int dv, bool packed) {
     return p;
 }
 
+// Zeros in the rows of no sequence, those before the first and behind the last: words of one
+// tensor (blockIdx.y), 16 bytes a lane where rows are whole pieces of it.
+struct Clear {
+    void* p[GDR_CLEAR_MAX];
+    int64_t row[GDR_CLEAR_MAX];   // bytes
+};
+template <typename W>
+__device__ __forceinline__ void clear_words(W* p, int64_t lo, int64_t hi, int64_t end) {
+    const int64_t step = (int64_t)gridDim.x * blockDim.x;
+    const int64_t n = lo + (end - hi);
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) p[i < lo ? i : hi + (i - lo)] = W{};
+}
+__global__ void __launch_bounds__(256) clear_kernel(int nseq, int T, const int* __restrict__ cu, Clear c) {
+    int lo = cu[0], hi = cu[nseq];
+    lo = lo < 0 ? 0 : lo > T ? T : lo;
+    hi = hi < lo ? lo : hi > T ? T : hi;
+    void* const p = c.p[blockIdx.y];
+    const int64_t row = c.row[blockIdx.y];
+    if (row % 16 == 0) clear_words((u32x4*)p, lo * (row / 16), hi * (row / 16), T * (row / 16));
+    else clear_words((uint32_t*)p, lo * (row / 4), hi * (row / 4), T * (row / 4));
+}
+
 Args args_of(const GdrCall& c) { return Args{c.nseq, c.T, c.Hk, c.Hv, c.dv, c.cu, c.scale}; }
 
 }  // namespace
@@ -105,7 +127,7 @@ hipError_t launch_gdr_fwd(const GdrCall& c, void* o, float* S_T, void* workspace
     KDA_DO(gdr::launch_prep(c.f32, c.dk, a, c.k, c.g, c.beta, ws + p.prep, stream));
     if (p.sg.seg) {
         KDA_DO(gdr::launch_maps(c.f32, c.dk, a, p.sg, c.k, c.v, ws + p.prep, maps, stream));
-        KDA_DO(gdr::launch_join(c.f32, c.dk, false, a, p.sg, c.S0, maps, maps, starts, stream));
+        KDA_DO(gdr::launch_join(c.f32, c.dk, a, p.sg, c.S0, maps, starts, nullptr, nullptr, nullptr, stream));
     }
     return gdr::launch_fwd_chain(c.f32, c.dk, a, p.sg, c.q, c.k, c.v, c.S0, starts, ws + p.prep, o, S_T, stream);
 }
@@ -120,12 +142,22 @@ hipError_t launch_gdr_bwd(const GdrCall& c, const void* dout, const float* dS_T,
     KDA_DO(gdr::launch_prep(c.f32, c.dk, a, c.k, c.g, c.beta, ws + p.prep, stream));
     if (p.sg.seg) {
         KDA_DO(gdr::launch_bwd_maps(c.f32, c.dk, a, p.sg, c.q, c.k, c.v, dout, ws + p.prep, maps, nmaps, stream));
-        KDA_DO(gdr::launch_join(c.f32, c.dk, false, a, p.sg, c.S0, maps, maps, starts, stream));
-        KDA_DO(gdr::launch_join(c.f32, c.dk, true, a, p.sg, dS_T, maps, nmaps, dstarts, stream));
+        KDA_DO(gdr::launch_join(c.f32, c.dk, a, p.sg, c.S0, maps, starts, dS_T, nmaps, dstarts, stream));
     }
     KDA_DO(gdr::launch_bwd_chains(c.f32, c.dk, a, p.sg, c.q, c.k, c.v, dout, c.S0, starts, dS_T, dstarts, ws + p.prep, dv, dS0,
                                   ws + p.recs, stream));
     return gdr::launch_grad(c.f32, c.dk, a, c.q, c.k, dout, ws + p.prep, ws + p.recs, dq, dk, dg, dbeta, stream);
+}
+
+hipError_t launch_gdr_clear(int nseq, int T, const int* cu, int n, void* const* tensors, const size_t* row_bytes,
+                            hipStream_t stream) {
+    gdr::Clear c{};
+    for (int i = 0; i < n; ++i) {
+        c.p[i] = tensors[i];
+        c.row[i] = (int64_t)row_bytes[i];
+    }
+    hipLaunchKernelGGL(gdr::clear_kernel, dim3(128, (unsigned)n), dim3(256), 0, stream, nseq, T, cu, c);
+    return hipGetLastError();
 }
 
 }  // namespace kda

@@ -131,6 +131,9 @@ struct GdrCall {
 };
 size_t gdr_fwd_workspace_bytes(int nseq, int T, int Hv, int dk, int dv, bool packed);
 size_t gdr_bwd_workspace_bytes(int nseq, int T, int Hv, int dk, int dv, bool packed);
+constexpr int GDR_CLEAR_MAX = 8;   // tensors of one launch_gdr_clear
+hipError_t launch_gdr_clear(int nseq, int T, const int* cu, int n, void* const* tensors, const size_t* row_bytes,
+                            hipStream_t stream);
 hipError_t launch_gdr_fwd(const GdrCall& c, void* o, float* S_T, void* workspace, hipStream_t stream);
 hipError_t launch_gdr_bwd(const GdrCall& c, const void* dout, const float* dS_T, void* dq, void* dk, void* dv, float* dg,
                           float* dbeta, float* dS0, void* workspace, hipStream_t stream);

@@ -352,6 +352,20 @@ int kda_gdr_chunk_fwd_workspace_size(int nseq, int T, int Hv, int dk, int dv, in
 int kda_gdr_chunk_bwd_workspace_size(int nseq, int T, int Hv, int dk, int dv, int packed, size_t* bytes);
 
 /* ---------------------------------------------------------------------------
+ * kda_gdr_clear_rows: zeros in the rows of no sequence of packed tensors, which the two
+ * calls above leave as they were: those before cu_seqlens[0] and from
+ * cu_seqlens[nseq] on.  No other row is touched.
+ *
+ *   nseq, T, cu_seqlens   as above, cu_seqlens not NULL
+ *   n            tensors, 1 to 8
+ *   tensors      n device pointers, 16-byte aligned, that overlap nothing; read on the host
+ *   row_bytes    the bytes of a row of each, a multiple of 4 below 2^31; read on the host
+ * Returns a kda_status.
+ * ------------------------------------------------------------------------- */
+int kda_gdr_clear_rows(int nseq, int T, const int* cu_seqlens, int n, void* const* tensors,
+                       const size_t* row_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * kda_gdr_step: T tokens of the rule for each of B rows, from and to a state in a
  * pool, in place (decode: T = 1; proposed tokens: T of a few).  The state is read
  * and written once a call.

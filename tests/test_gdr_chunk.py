@@ -575,3 +575,56 @@ def test_two_graphs_share_a_workspace():
             torch.cuda.synchronize()
             for j, (u, v) in enumerate(zip(want[i], got[i])):
                 assert torch.equal(u, v), (turn, i, j)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cu", [[0, 7], [3, 3, 9], [5, 11], [9, 9], [12, 12], [0, 0], [-4, 30], [8, 2]])
+def test_clear_rows(cu):
+    """Rows before the first and behind the last sequence, in rows of 8, 12, 16 and 64 bytes; offsets are held to
+    the tensors, and the guard around them stays."""
+    T = 12
+    c = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    lo = min(max(cu[0], 0), T)
+    hi = min(max(cu[-1], lo), T)
+    flat = [torch.full((8 * n + T * n + 8 * n,), 3.0, device=DEV) for n in (2, 4, 16, 3)]
+    views = [f[8 * n:8 * n + T * n].view(1, T, n) for f, n in zip(flat, (2, 4, 16, 3))]
+    kda.kda_gdr_clear_rows(c, *views)
+    torch.cuda.synchronize()
+    for f, n in zip(flat, (2, 4, 16, 3)):
+        assert (f[:8 * n] == 3).all() and (f[8 * n + T * n:] == 3).all()
+    for v in views:
+        assert (v[0, :lo] == 0).all() and (v[0, hi:] == 0).all() and (v[0, lo:hi] == 3).all()
+
+
+@pytest.mark.gpu
+def test_made_outputs_are_zero_outside_sequences():
+    """What the binding makes itself is zero in the rows of no sequence, whatever the memory held."""
+    x, cu = make([40, 9], 1, 2, 32, 32, torch.bfloat16, 70, head=6, tail=5)
+    for d in (6.0, 7.0):   # memory that the allocator hands out again
+        junk = [torch.full_like(x["v"], d, device=DEV) for _ in range(12)]
+        del junk
+    o, _ = run_fwd(x, cu, 1.0)
+    g = run_bwd(x, cu, 1.0)
+    for t in (o, *(g[k] for k in ("dq", "dk", "dv", "dg", "dbeta"))):
+        assert (t[0, :6] == 0).all() and (t[0, cu[-1]:] == 0).all()
+
+
+def test_clear_rows_refusals(lib):
+    p = (ctypes.c_void_p * 9)(*[(1 << 40) + (i << 28) for i in range(9)])
+    n = (ctypes.c_size_t * 9)(*[64] * 9)
+    cu = ctypes.c_void_p(1 << 39)
+    f = lib.kda_gdr_clear_rows
+    assert f(0, 8, cu, 1, p, n, None) == 2 and f(1, 0, cu, 1, p, n, None) == 2
+    assert f(1, 8, cu, 0, p, n, None) == 2 and f(1, 8, cu, 9, p, n, None) == 2
+    assert f(1, 8, None, 1, p, n, None) == 1 and f(1, 8, cu, 1, None, n, None) == 1 and f(1, 8, cu, 1, p, None, None) == 1
+    for bad in (0, 2, 66, 1 << 31):
+        assert f(1, 8, cu, 1, p, (ctypes.c_size_t * 1)(bad), None) == 2
+    assert f(1, 8, cu, 1, (ctypes.c_void_p * 1)(None), n, None) == 1
+    assert f(1, 8, cu, 1, (ctypes.c_void_p * 1)((1 << 40) + 4), n, None) == 4
+    assert f(1, 8, cu, 2, (ctypes.c_void_p * 2)(1 << 40, (1 << 40) + 256), n, None) == 6
+    t, c = torch.zeros(1, 8, 4), torch.tensor([0, 8], dtype=torch.int32)
+    for bad in ((t[0],), (t, torch.zeros(1, 9, 4)), (), (t,)):   # no leading 1, another T, none, not on the GPU
+        with pytest.raises(ValueError):
+            kda.kda_gdr_clear_rows(c, *bad)
+    with pytest.raises(TypeError):
+        kda.kda_gdr_clear_rows(c.long(), t)
