@@ -15,7 +15,9 @@
 // half, x = hi + lo up to 2^-18 |x|, and a product is the sum of the halves' products
 // without lo*lo: two matrix instructions against an exact operand, three against a
 // split one.  One rounding to bf16 instead (2^-9) would leave o within its own
-// rounding but the fp32 state and the fp32 gradients of g and beta at 3e-3.
+// rounding but the fp32 state and the fp32 gradients of g and beta at 3e-3.  With the halves
+// the state is within 4e-6 of 64-bit arithmetic (fp32 products throughout: 2e-7);
+// a third part would close that gap for twice the matrix instructions.
 // In fp32 storage all of it runs on the fp32 matrix cores.
 //
 // Operands live in LDS and in the workspace as fragment blocks of 16 rows by 32 columns
@@ -230,8 +232,6 @@ template <> struct Arith<bf16> {
     }
     // Eight natural slots of a row in global memory.
     static __device__ __forceinline__ Ex ld_row(const bf16* p) { return *reinterpret_cast<const bf16x8*>(p); }
-    // Eight accumulator slots of a row: columns 4g.. and 16 + 4g.. from p = row + 4 g.
-    static __device__ __forceinline__ Ex ld_row_acc(const bf16* p) { return cat8(ld_b4(p), ld_b4(p + 16)); }
     // Four rows by 16 columns read transposed: lane r of a group of 16 gives the address of
     // row r >> 2, columns 4 (r & 3).., and receives column r of the four rows.
     static __device__ __forceinline__ bf16x4 ld_tr(const char* p) {
@@ -342,9 +342,6 @@ template <> struct Arith<float> {
     }
     static __device__ __forceinline__ Ex ld_row(const float* p) {
         return Ex{*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 4)};
-    }
-    static __device__ __forceinline__ Ex ld_row_acc(const float* p) {
-        return Ex{*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 16)};
     }
     template <int KB>
     static __device__ __forceinline__ Ex ld_ex_t(const char* base, int kb, int h, int tb, int g, int r) {

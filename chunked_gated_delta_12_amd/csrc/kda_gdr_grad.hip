@@ -18,9 +18,9 @@
 // and dO, which every wavefront needs, lie in LDS.  The ten tiles of X and W on and below the
 // diagonal go to the wavefronts in turn and reach the others through LDS as the operands of the
 // last products, read there as rows of queries and, transposed, as rows of keys.
-// HBM bounds it: 192 KB of states and rows a unit at dk = dv = 128.  The next unit's loads
+// Memory bounds it: 192 KB of states and rows a unit at dk = dv = 128.  The next unit's loads
 // are issued before this unit's last part, as many as fit the registers.  Measured at 8 x 4,096 tokens,
-// 16 heads, dk = dv = 128: 621 us, 2.0 GB, 3.6 TB/s; a workgroup a chunk without loads ahead: 885 us.
+// 16 heads, dk = dv = 128: 620 us, 2.3 GB, 3.7 TB/s; a workgroup a chunk without loads ahead: 885 us.
 #include <type_traits>
 
 #include "kda_gdr.hpp"

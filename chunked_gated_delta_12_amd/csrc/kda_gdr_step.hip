@@ -9,6 +9,9 @@
 // them, a lane dk/8 rows by 4 columns, so the state stays in registers over the tokens,
 // the sums over rows are in the lane and then over 8 lanes, and no wavefront waits for another.
 // 32 columns make 128-byte rows and, at one request of 32 heads, 128 wavefronts.
+// Measured, 128 x 128: 256 requests of 16 heads, one token, 115 us with the call (541 MB, 4.7 TB/s;
+// the kernel alone 85 us, part of the states being in the last-level cache); 32 requests of 16 heads, up to
+// six tokens, 17 us; one request of 32 heads 4.1 us, its call 9 us of host time.
 #include "kda_device.hpp"
 #include "kda_launch.hpp"
 
