@@ -4,7 +4,7 @@
 // Mathematics, precision and layouts: kda_gdr.hpp.
 //
 // Columns of the state (dv) are independent.  A workgroup of NW wavefronts has one head of
-// one piece of a sequence and 16 NW columns, a wavefront 16 of them: its slice of the state
+// one piece of a sequence and 16 NW NC columns, a wavefront NC tiles of 16: its slice of the state
 // stays in fp32 accumulators for the whole walk, and every product of a chunk takes its
 // result straight from the one before it (an accumulator tile is a B operand; read as an A
 // operand it is its transpose), so the wavefronts share nothing but the chunk's operands.
@@ -35,9 +35,9 @@ namespace {
 enum Mode { FWD, SAVE, MAP, BACK, BMAP };
 
 // LDS of one buffer: K, Q, the chunk's record (X and the factors) and the value rows; P once.
-template <typename E, int DK, int NW, int MODE>
+template <typename E, int DK, int NW, int MODE, int NC>
 struct Lay {
-    static constexpr int KB = DK / 32, NTHR = 64 * NW, SLAB = 16 * NW;
+    static constexpr int KB = DK / 32, NTHR = 64 * NW, SLAB = 16 * NC * NW;
     static constexpr bool BWD = MODE >= BACK;                      // rows of dO instead of V
     static constexpr bool HAS_Q = MODE == FWD || BWD, HAS_P = HAS_Q;
     static constexpr int QK = MT * KB * Arith<E>::EXB;
@@ -57,9 +57,9 @@ struct Lay {
 __device__ __forceinline__ f32x4 ld4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
 
 // One chunk's operands on their way from global memory to LDS.
-template <typename E, int DK, int NW, int MODE>
+template <typename E, int DK, int NW, int MODE, int NC>
 struct Stage {
-    typedef Lay<E, DK, NW, MODE> L;
+    typedef Lay<E, DK, NW, MODE, NC> L;
     u32x4 k[L::NQK], q[L::NQK], x[L::NXP], v[L::NV];
     uint32_t kq_off[L::NQK], v_off[L::NV];   // byte offsets in a chunk's rows, the same for every chunk
 
@@ -137,10 +137,12 @@ struct Ptrs {
 };
 
 // One walk by workgroup `block` of those that the walk has.
-template <typename E, int DK, int NW, int MODE>
+// NC: column tiles a wavefront.
+template <typename E, int DK, int NW, int MODE, int NC>
 __device__ __forceinline__ void walk(const Args& a, const Segs& sg, const Ptrs& io, unsigned block, char* lds) {
     typedef Arith<E> A;
-    typedef Lay<E, DK, NW, MODE> L;
+    static_assert(NC == 1 || MODE == MAP, "the other walks' wavefronts have one column tile");
+    typedef Lay<E, DK, NW, MODE, NC> L;
     constexpr int KB = L::KB, ST = DK / 16;
     constexpr bool BWD = L::BWD;
     char* const pl = lds + L::BUFS * L::BYTES;   // P
@@ -163,15 +165,20 @@ __device__ __forceinline__ void walk(const Args& a, const Segs& sg, const Ptrs& 
     if (MODE == BMAP && pc.i == 0) return;
     const int nch = pc.c1 - pc.c0;
     const int64_t ldk = (int64_t)a.Hk * DK, ldv = (int64_t)a.Hv * a.dv;
-    const int c0 = slab * L::SLAB, col0 = c0 + w * 16;   // the slab's and the wavefront's first column
-    const bool act = col0 < ncols;
-    const bool isM = MODE == MAP && col0 >= a.dv;        // a column of the map's linear part: no values
+    const int c0 = slab * L::SLAB, col0 = c0 + w * 16 * NC;   // the slab's and the wavefront's first column
+    bool on[NC], isM[NC];                                     // its tiles; those of the map's linear part have no values
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+        on[j] = col0 + 16 * j < ncols;
+        isM[j] = MODE == MAP && col0 + 16 * j >= a.dv;
+    }
+    const bool act = on[0];
     const E* kp = (const E*)io.k + pc.s.row0 * ldk + (int64_t)hk * DK;
     const E* qp = (const E*)io.q + pc.s.row0 * ldk + (int64_t)hk * DK;
     const E* vp = (const E*)io.v + pc.s.row0 * ldv + (int64_t)h * a.dv + c0;
 
     // the state at the piece's start (backwards: the gradient at its end)
-    f32x4 S[ST];
+    f32x4 S[NC][ST];
     {
         const float* from = nullptr;
         if (MODE != MAP && MODE != BMAP) {
@@ -179,19 +186,23 @@ __device__ __forceinline__ void walk(const Args& a, const Segs& sg, const Ptrs& 
             else if (io.init) from = io.init + ((int64_t)pc.n * a.Hv + h) * DK * a.dv;
         }
 #pragma unroll
-        for (int t = 0; t < ST; ++t)
+        for (int j = 0; j < NC; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = 32 * (t / 2) + 8 * g + 4 * (t & 1) + i;
-                S[t][i] = from && act ? from[(int64_t)row * a.dv + col0 + r] : isM && col0 + r == a.dv + row ? 1.0f : 0.0f;
-            }
+            for (int t = 0; t < ST; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = 32 * (t / 2) + 8 * g + 4 * (t & 1) + i, col = col0 + 16 * j + r;
+                    S[j][t][i] = from && on[j] ? from[(int64_t)row * a.dv + col] : isM[j] && col == a.dv + row ? 1.0f : 0.0f;
+                }
     }
 
     // The start state has arrived before the loop: otherwise the loop would wait for its loads
     // anew in every iteration, and so for the chunk that it has just asked for.
 #pragma unroll
-    for (int t = 0; t < ST; ++t) asm volatile("" : "+v"(S[t]));
-    Stage<E, DK, NW, MODE> st;
+    for (int j = 0; j < NC; ++j)
+#pragma unroll
+        for (int t = 0; t < ST; ++t) asm volatile("" : "+v"(S[j][t]));
+    Stage<E, DK, NW, MODE, NC> st;
     st.init(ldk, ldv, a.dv - c0);
     struct Res { Rsrc k, q, v, x; };
     auto res_of = [&](int c) {
@@ -283,18 +294,20 @@ __device__ __forceinline__ void walk(const Args& a, const Segs& sg, const Ptrs& 
                 }
                 if (BWD) lds_barrier();
             }
-            typename A::Sp sb[KB];
+            typename A::Sp sb[NC][KB];
 #pragma unroll
-            for (int b = 0; b < KB; ++b) sb[b] = A::split(S[2 * b], S[2 * b + 1]);
+            for (int j = 0; j < NC; ++j)
+#pragma unroll
+                for (int b = 0; b < KB; ++b) sb[j][b] = A::split(S[j][2 * b], S[j][2 * b + 1]);
             const int64_t rec = ((int64_t)pc.slot + c) * a.Hv + h;
             if constexpr (MODE == SAVE || MODE == BACK) {
                 const Rsrc to = make_rsrc(io.recs + rec * rec_bytes(DK, a.dv) + (BWD ? state_bytes(DK, a.dv) : 0), (uint32_t)state_bytes(DK, a.dv));
 #pragma unroll
                 for (int b = 0; b < KB; ++b)
 #pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) A::put_t(to, w_off + (uint32_t)((2 * b + hh) * (a.dv / 32) * SPB), sb[b], hh ? pk1 : pk0);
+                    for (int hh = 0; hh < 2; ++hh) A::put_t(to, w_off + (uint32_t)((2 * b + hh) * (a.dv / 32) * SPB), sb[0][b], hh ? pk1 : pk0);
             }
-            f32x4 y[MT], dov[MT];
+            f32x4 y[NC][MT], dov[MT];
             typename A::Ex dob[2];
             if constexpr (BWD) {
 #pragma unroll
@@ -306,47 +319,60 @@ __device__ __forceinline__ void walk(const Args& a, const Segs& sg, const Ptrs& 
             __builtin_amdgcn_sched_barrier(0x1 | 0x2 | 0x4 | 0x8 | 0x100 | 0x200);
             // V - gam (K S), or om beta (K dS) + P^T dO
 #pragma unroll
-            for (int m = 0; m < MT; ++m) y[m] = zero;
+            for (int j = 0; j < NC; ++j)
+#pragma unroll
+                for (int m = 0; m < MT; ++m) y[j][m] = zero;
 #pragma unroll
             for (int b = 0; b < KB; ++b) {
                 typename A::Ex kf[MT];
 #pragma unroll
                 for (int m = 0; m < MT; ++m) kf[m] = A::ld_ex(buf, m * KB + b, lane);
-                A::mma_n(kf, sb[b], y);
+#pragma unroll
+                for (int j = 0; j < NC; ++j) A::mma_n(kf, sb[j][b], y[j]);
             }
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 if constexpr (BWD) {
-                    y[m] *= ld4(ob + 16 * m + 4 * g);
+                    y[0][m] *= ld4(ob + 16 * m + 4 * g);
                 } else {
-                    f32x4 vv = A::ld_col(vl, L::VLD, m, w * 16, g, r);
-                    if (isM) vv = zero;
-                    y[m] = vv - ld4(gam + 16 * m + 4 * g) * y[m];
+                    const f32x4 gm = ld4(gam + 16 * m + 4 * g);
+#pragma unroll
+                    for (int j = 0; j < NC; ++j) {
+                        f32x4 vv = A::ld_col(vl, L::VLD, m, (w * NC + j) * 16, g, r);
+                        if (isM[j]) vv = zero;
+                        y[j][m] = vv - gm * y[j][m];
+                    }
                 }
             }
             if constexpr (BWD) {
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
-                    for (int m = 0; m <= 2 * b + 1; ++m) y[m] = A::mma(A::ld_sp(pl, upper_block(m, b), lane), dob[b], y[m]);
+                    for (int m = 0; m <= 2 * b + 1; ++m) y[0][m] = A::mma(A::ld_sp(pl, upper_block(m, b), lane), dob[b], y[0][m]);
             }
             st.load_v(rs.v);
             __builtin_amdgcn_sched_barrier(0x1 | 0x2 | 0x4 | 0x8 | 0x100 | 0x200);
             // e = X y, or Z = X^T y
-            typename A::Sp yb[2];
+            typename A::Sp yb[NC][2];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) yb[b] = A::split(y[2 * b], y[2 * b + 1]);
+            for (int j = 0; j < NC; ++j) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m) y[m] = zero;
+                for (int b = 0; b < 2; ++b) yb[j][b] = A::split(y[j][2 * b], y[j][2 * b + 1]);
+#pragma unroll
+                for (int m = 0; m < MT; ++m) y[j][m] = zero;
+            }
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int m = BWD ? 0 : 2 * b; m < (BWD ? 2 * b + 2 : MT); ++m)
-                    y[m] = A::mma(BWD ? A::ld_tri_t(buf + L::X_AT, m, b, g, r) : A::ld_sp(buf + L::X_AT, lower_block(m, b), lane), yb[b], y[m]);
-            typename A::Sp eb[2], wb[2], db[2];
+                for (int m = BWD ? 0 : 2 * b; m < (BWD ? 2 * b + 2 : MT); ++m) {
+                    const typename A::Sp xf = BWD ? A::ld_tri_t(buf + L::X_AT, m, b, g, r) : A::ld_sp(buf + L::X_AT, lower_block(m, b), lane);
+#pragma unroll
+                    for (int j = 0; j < NC; ++j) y[j][m] = A::mma(xf, yb[j][b], y[j][m]);
+                }
+            typename A::Sp eb[2], wb[NC][2], db[2];
             if constexpr (MODE != MAP && MODE != BMAP) {
 #pragma unroll
-                for (int b = 0; b < 2; ++b) eb[b] = A::split(y[2 * b], y[2 * b + 1]);
+                for (int b = 0; b < 2; ++b) eb[b] = A::split(y[0][2 * b], y[0][2 * b + 1]);
             }
             if constexpr (MODE == SAVE || MODE == BACK) {
                 const Rsrc to = make_rsrc(io.recs + rec * rec_bytes(DK, a.dv) + 2 * state_bytes(DK, a.dv) + (BWD ? rows_bytes(a.dv) : 0),
@@ -364,33 +390,38 @@ __device__ __forceinline__ void walk(const Args& a, const Segs& sg, const Ptrs& 
             for (int m = 0; m < MT; ++m) {
                 const f32x4 f4 = ld4((BWD ? gam : ob) + 16 * m + 4 * g);
                 if constexpr (BWD) {
-                    y[m] *= -f4;
+                    y[0][m] *= -f4;
                     dov[m] *= f4 * a.scale;
                 } else {
-                    y[m] *= f4;
+#pragma unroll
+                    for (int j = 0; j < NC; ++j) y[j][m] *= f4;
                 }
             }
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                wb[b] = A::split(y[2 * b], y[2 * b + 1]);
+#pragma unroll
+                for (int j = 0; j < NC; ++j) wb[j][b] = A::split(y[j][2 * b], y[j][2 * b + 1]);
                 if constexpr (BWD) db[b] = A::split(dov[2 * b], dov[2 * b + 1]);
             }
             st.load_x(rs.x);
             __builtin_amdgcn_sched_barrier(0x1 | 0x2 | 0x4 | 0x8 | 0x100 | 0x200);
             const float ge = gam[C - 1];
 #pragma unroll
-            for (int t = 0; t < ST; ++t) S[t] *= ge;
+            for (int j = 0; j < NC; ++j)
+#pragma unroll
+                for (int t = 0; t < ST; ++t) S[j][t] *= ge;
 #pragma unroll
             for (int tb = 0; tb < 2; ++tb) {
                 typename A::Ex kt[ST];
                 if constexpr (BWD) {
 #pragma unroll
                     for (int t = 0; t < ST; ++t) kt[t] = A::template ld_ex_t<KB>(buf + L::Q_AT, t / 2, t & 1, tb, g, r);
-                    A::mma_n(kt, db[tb], S);
+                    A::mma_n(kt, db[tb], S[0]);
                 }
 #pragma unroll
                 for (int t = 0; t < ST; ++t) kt[t] = A::template ld_ex_t<KB>(buf, t / 2, t & 1, tb, g, r);
-                A::mma_n(kt, wb[tb], S);
+#pragma unroll
+                for (int j = 0; j < NC; ++j) A::mma_n(kt, wb[j][tb], S[j]);
             }
             if constexpr (MODE == FWD) {
                 // O^T: lane (g, r) has columns 4 g.. of token r
@@ -402,7 +433,7 @@ __device__ __forceinline__ void walk(const Args& a, const Segs& sg, const Ptrs& 
                     typename A::Ex qf[MT];
 #pragma unroll
                     for (int m = 0; m < MT; ++m) qf[m] = A::ld_ex(buf + L::Q_AT, m * KB + b, lane);
-                    A::mma_n(sb[b], qf, ot);
+                    A::mma_n(sb[0][b], qf, ot);
                 }
 #pragma unroll
                 for (int m = 0; m < MT; ++m) ot[m] *= a.scale * gam[16 * m + r];
@@ -429,18 +460,20 @@ __device__ __forceinline__ void walk(const Args& a, const Segs& sg, const Ptrs& 
     } else if (io.last && (BWD ? pc.i == 0 : pc.i + 1 == pc.cnt)) {
         to = io.last + ((int64_t)pc.n * a.Hv + h) * DK * ld;
     }
-    if (to && act)
 #pragma unroll
-        for (int t = 0; t < ST; ++t)
+    for (int j = 0; j < NC; ++j)
+        if (to && on[j])
 #pragma unroll
-            for (int i = 0; i < 4; ++i) to[(32 * (t / 2) + 8 * g + 4 * (t & 1) + i) * ld + col0 + r] = S[t][i];
+            for (int t = 0; t < ST; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) to[(32 * (t / 2) + 8 * g + 4 * (t & 1) + i) * ld + col0 + 16 * j + r] = S[j][t][i];
 }
 
-template <typename E, int DK, int NW, int MODE>
+template <typename E, int DK, int NW, int MODE, int NC>
 __global__ void __launch_bounds__(64 * NW, NW / 4)
 chain_kernel(Args a, Segs sg, Ptrs io) {
-    __shared__ alignas(16) char lds[Lay<E, DK, NW, MODE>::ALL];
-    walk<E, DK, NW, MODE>(a, sg, io, blockIdx.x, lds);
+    __shared__ alignas(16) char lds[Lay<E, DK, NW, MODE, NC>::ALL];
+    walk<E, DK, NW, MODE, NC>(a, sg, io, blockIdx.x, lds);
 }
 
 // Two walks in one launch, the longer one's workgroups first: the backward pass walks each way
@@ -450,10 +483,10 @@ chain_kernel(Args a, Segs sg, Ptrs io) {
 template <typename E, int DK, int NW, int BACKWARDS, int FORWARDS>
 __global__ void __launch_bounds__(64 * NW, NW / 4)
 pair_kernel(Args a, Segs sg, Ptrs back, Ptrs forth, unsigned nback) {
-    constexpr int B = Lay<E, DK, NW, BACKWARDS>::ALL, F = Lay<E, DK, NW, FORWARDS>::ALL;
+    constexpr int B = Lay<E, DK, NW, BACKWARDS, 1>::ALL, F = Lay<E, DK, NW, FORWARDS, 1>::ALL;
     __shared__ alignas(16) char lds[B > F ? B : F];
-    if (blockIdx.x < nback) walk<E, DK, NW, BACKWARDS>(a, sg, back, blockIdx.x, lds);
-    else walk<E, DK, NW, FORWARDS>(a, sg, forth, blockIdx.x - nback, lds);
+    if (blockIdx.x < nback) walk<E, DK, NW, BACKWARDS, 1>(a, sg, back, blockIdx.x, lds);
+    else walk<E, DK, NW, FORWARDS, 1>(a, sg, forth, blockIdx.x - nback, lds);
 }
 
 // Joins the maps of a cut sequence's pieces: forwards X_0 = S0, X_{i+1} = M_i X_i + N_i, backwards
@@ -471,9 +504,9 @@ __device__ __forceinline__ void join(const Args& a, const Segs& sg, const float*
     const int nslab = a.dv / 16;
     const int slab = (int)(blockIdx.x % (unsigned)nslab), h = (int)(blockIdx.x / (unsigned)nslab % (unsigned)a.Hv);
     const int n = (int)(blockIdx.x / (unsigned)nslab / (unsigned)a.Hv);
-    const int p0 = __builtin_amdgcn_readfirstlane(place_of(a, n, seg_unit(sg)));
-    const Piece pc = piece_at(a, sg, p0, lane);
-    if (pc.n != n || pc.cnt < 2) return;
+    const int nch = (int)(((int64_t)seq_of(a, n).len + C - 1) / C);
+    if (!is_cut(a, sg, nch, lane)) return;
+    const int p0 = __builtin_amdgcn_readfirstlane(place_of(a, n, seg_unit(sg))), cnt = (nch + sg.seg - 1) / sg.seg;
     const int col = 16 * slab + r;
     const bool on = w < ST;
     const int t = on ? w : 0;   // wavefronts past the rows work on the first tile and store nothing
@@ -481,7 +514,7 @@ __device__ __forceinline__ void join(const Args& a, const Segs& sg, const float*
     f32x4 X, N, M[KB][2];
     const int row0 = 32 * (t / 2) + 8 * g + 4 * (t & 1);                          // this lane's first row as a result
     const int rowa = 32 * (t / 2) + 8 * (r >> 2) + 4 * (t & 1) + (r & 3);         // and its row as an operand
-    auto place = [&](int s) { return p0 + (BWD ? pc.cnt - 1 - s : s); };
+    auto place = [&](int s) { return p0 + (BWD ? cnt - 1 - s : s); };
     auto fetch = [&](int s) {
         const float* m = maps + ((int64_t)place(s) * a.Hv + h) * DK * mld + a.dv;
         const float* nn = nmaps + ((int64_t)place(s) * a.Hv + h) * DK * nld;
@@ -502,7 +535,7 @@ __device__ __forceinline__ void join(const Args& a, const Segs& sg, const float*
     fetch(0);
 #pragma unroll
     for (int i = 0; i < 4; ++i) X[i] = init ? init[(((int64_t)n * a.Hv + h) * DK + row0 + i) * a.dv + col] : 0.0f;
-    for (int s = 0; s < pc.cnt; ++s) {
+    for (int s = 0; s < cnt; ++s) {
         float* to = starts + ((int64_t)place(s) * a.Hv + h) * DK * a.dv + col;
         char* buf = lds[s & 1];
         if (on) {
@@ -510,12 +543,12 @@ __device__ __forceinline__ void join(const Args& a, const Segs& sg, const float*
             for (int i = 0; i < 4; ++i) to[(int64_t)(row0 + i) * a.dv] = X[i];
             A::put_half(buf, t / 2, lane, t & 1, X);
         }
-        if (s + 1 == pc.cnt) break;
+        if (s + 1 == cnt) break;
         typename A::Sp mf[KB];
         X = N;
 #pragma unroll
         for (int b = 0; b < KB; ++b) mf[b] = A::split(M[b][0], M[b][1]);
-        fetch(s + 2 < pc.cnt ? s + 1 : s);
+        fetch(s + 2 < cnt ? s + 1 : s);
         lds_barrier();
 #pragma unroll
         for (int b = 0; b < KB; ++b) X = A::mma(mf[b], A::ld_sp(buf, b, lane), X);
@@ -537,19 +570,22 @@ int64_t groups_of(const Args& a, int places, int cols, int slab) {
     return ((int64_t)places * a.Hk + 7) / 8 * 8 * (a.Hv / a.Hk) * ((cols + slab - 1) / slab);
 }
 
+// Whether sequences are cut, and pieces times heads to expect.  The lengths of packed sequences
+// are not known here: as if all were equal.
+bool cut_of(const Args& a, const Segs& sg) {
+    return sg.seg && places_of(a.nseq, a.T, a.cu != nullptr, C) / a.nseq > sg.over;
+}
+int64_t walks_of(const Args& a, const Segs& sg) {
+    return (cut_of(a, sg) ? places_of(a.nseq, a.T, a.cu != nullptr, seg_unit(sg)) : a.nseq) * a.Hv;
+}
 // Wavefronts a workgroup: eight share one set of operands over 128 columns; four where a
 // head has no more columns, or where workgroups of eight would leave half the chip empty.
 // `slabs` of 64 columns a head.
-bool wide(const Args& a, const Segs& sg, int slabs) {
-    // Pieces to expect.  The lengths of packed sequences are not known here: as if all were equal.
-    const int64_t chunks = places_of(a.nseq, a.T, a.cu != nullptr, C), places = places_of(a.nseq, a.T, a.cu != nullptr, seg_unit(sg));
-    const int64_t heads = (sg.seg && chunks / a.nseq > sg.over ? places : a.nseq) * a.Hv;
-    return heads * slabs > 256;
-}
+bool wide(const Args& a, const Segs& sg, int slabs) { return walks_of(a, sg) * slabs > 256; }
 
-template <typename E, int DK, int NW, int MODE>
+template <typename E, int DK, int NW, int MODE, int NC>
 hipError_t one_t(const Args& a, const Segs& sg, const Ptrs& io, int cols, hipStream_t stream) {
-    hipLaunchKernelGGL((chain_kernel<E, DK, NW, MODE>), dim3((unsigned)groups_of(a, io.places, cols, 16 * NW)), dim3(64 * NW), 0,
+    hipLaunchKernelGGL((chain_kernel<E, DK, NW, MODE, NC>), dim3((unsigned)groups_of(a, io.places, cols, 16 * NC * NW)), dim3(64 * NW), 0,
                        stream, a, sg, io);
     return hipGetLastError();
 }
@@ -558,9 +594,16 @@ template <typename E, int DK, int MODE>
 hipError_t one_d(const Args& a, const Segs& sg, Ptrs io, hipStream_t stream) {
     const int cols = MODE == MAP ? a.dv + DK : a.dv;
     io.places = (int)places_of(a.nseq, a.T, a.cu != nullptr, seg_unit(sg));
-    if constexpr (sizeof(E) == 2)
-        if (cols > 64 && wide(a, sg, (cols + 63) / 64)) return one_t<E, DK, 8, MODE>(a, sg, io, cols, stream);
-    return one_t<E, DK, 4, MODE>(a, sg, io, cols, stream);
+    if constexpr (sizeof(E) == 2) {
+        // Two column tiles a wavefront read every operand once for both, in 6.0 us a chunk against 3.1:
+        // where workgroups of 128 columns would take a second round (65,536 tokens of 16 heads, the
+        // whole call: 905 us against 980; ten packed sequences with 128 workgroups of 256 columns: 318 against 288).
+        if constexpr (MODE == MAP)
+            if (cols > 128 && cut_of(a, sg) && walks_of(a, sg) * ((cols + 127) / 128) > 256)
+                return one_t<E, DK, 8, MODE, 2>(a, sg, io, cols, stream);
+        if (cols > 64 && wide(a, sg, (cols + 63) / 64)) return one_t<E, DK, 8, MODE, 1>(a, sg, io, cols, stream);
+    }
+    return one_t<E, DK, 4, MODE, 1>(a, sg, io, cols, stream);
 }
 
 template <typename E, int DK, int NW, int BACKWARDS, int FORWARDS>

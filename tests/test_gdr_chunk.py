@@ -628,3 +628,19 @@ def test_clear_rows_refusals(lib):
             kda.kda_gdr_clear_rows(c, *bad)
     with pytest.raises(TypeError):
         kda.kda_gdr_clear_rows(c.long(), t)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,Hk,Hv,dk,dv", [([1500], 16, 48, 32, 128), ([900, 900], 24, 24, 64, 96), ([1300], 40, 40, 128, 256)])
+def test_cut_sequences_of_many_heads(lens, Hk, Hv, dk, dv):
+    """Enough heads that the maps take two column tiles a wavefront, the value columns ending inside its
+    256; three heads are looked at."""
+    x, cu = make(lens, Hk, Hv, dk, dv, torch.bfloat16, sum(lens) + dv, gmu=-5.0)
+    o, S_T = run_fwd(x, cu, dk ** -0.5)
+    rep = Hv // Hk
+    for h in (0, Hv // 2 + 1, Hv - 1):
+        y = {k: v[:, :, h // rep:h // rep + 1] if k in ("q", "k") else v[:, :, h:h + 1] for k, v in x.items() if k not in ("S0", "dS_T")}
+        y["S0"], y["dS_T"] = x["S0"][:, h:h + 1], x["dS_T"][:, h:h + 1]
+        o64, S64, _ = reference(y, cu, dk ** -0.5, False)
+        near(o[:, :, h:h + 1], o64, torch.bfloat16, FWD[torch.bfloat16], f"o of head {h}")
+        near(S_T[:, h:h + 1], S64, torch.float32, FWD[torch.bfloat16], f"S_T of head {h}")
