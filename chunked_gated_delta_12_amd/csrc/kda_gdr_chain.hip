@@ -22,8 +22,9 @@
 //
 // What bounds a walk is one chunk after another: by count its products, splits and LDS reads take about
 // 1.1 us each, and in two wavefronts a SIMD they overlap little.  Measured at 65,536 tokens of 16
-// heads, 128 x 128, bf16, in 16 pieces: the walk with outputs 350-380 us (memory alone 277,
-// compute alone 270), the maps 350-400 us (230 and 316).
+// heads, 128 x 128, bf16, in 16 pieces: the walk with outputs 340-373 us (memory alone 277,
+// compute alone 270), the maps, two column tiles a wavefront, 335-367 us (with one 400-436: memory
+// alone 230, compute alone 316).
 #include "kda_gdr.hpp"
 #include "kda_launch.hpp"
 
@@ -479,7 +480,7 @@ chain_kernel(Args a, Segs sg, Ptrs io) {
 // Two walks in one launch, the longer one's workgroups first: the backward pass walks each way
 // once, neither needs the other, and each alone leaves compute units idle where there are
 // fewer than 256 workgroups (8 sequences of 4,096 tokens, 16 heads of 128 x 128 in bf16: 400 and
-// 470 us one after the other in workgroups of four wavefronts, 728 together in eight).
+// 470 us one after the other in workgroups of four wavefronts, 710 together in eight).
 template <typename E, int DK, int NW, int BACKWARDS, int FORWARDS>
 __global__ void __launch_bounds__(64 * NW, NW / 4)
 pair_kernel(Args a, Segs sg, Ptrs back, Ptrs forth, unsigned nback) {
