@@ -644,3 +644,40 @@ def test_cut_sequences_of_many_heads(lens, Hk, Hv, dk, dv):
         o64, S64, _ = reference(y, cu, dk ** -0.5, False)
         near(o[:, :, h:h + 1], o64, torch.bfloat16, FWD[torch.bfloat16], f"o of head {h}")
         near(S_T[:, h:h + 1], S64, torch.float32, FWD[torch.bfloat16], f"S_T of head {h}")
+
+
+@pytest.mark.gpu
+@both
+def test_growing_state(dtype):
+    """Positive g is used as it is.  Each token multiplies an earlier error by at most e^g, so over a
+    sequence the bounds grow by e^(sum g) = e at most."""
+    x, cu = make([100], 1, 2, 64, 64, dtype, 80)
+    x["g"] = torch.full_like(x["g"], 0.01)
+    grow = 2.72
+    o64, S64, g64 = reference(x, cu, 1.0, True)
+    o, S_T = run_fwd(x, cu, 1.0)
+    near(o, o64, dtype, grow * FWD[dtype], "o")
+    near(S_T, S64, torch.float32, grow * FWD[dtype], "S_T")
+    g = run_bwd(x, cu, 1.0)
+    for k in ("dq", "dk", "dv", "dg", "dbeta", "dS0"):
+        near(g[k], g64[k], dtype if k in ("dq", "dk", "dv") else torch.float32, 2 * grow * FWD[dtype], k)
+
+
+@pytest.mark.gpu
+def test_thousands_of_short_sequences_beside_a_long_one():
+    """5,000 sequences of 0 to 3 tokens around one of 2,000 that is cut; some are looked at."""
+    lens = [i % 4 for i in range(2500)] + [2000] + [(3 * i) % 4 for i in range(2500)]
+    x, cu = make(lens, 1, 1, 32, 32, torch.bfloat16, 81)
+    o, S_T = run_fwd(x, cu, 0.3)
+    g = run_bwd(x, cu, 0.3)
+    for i in (0, 1, 63, 64, 2499, 2500, 2501, 4999, 5000):
+        a = slice(cu[i], cu[i + 1])
+        y = {k: v[:, a] for k, v in x.items() if k not in ("S0", "dS_T")}
+        y["S0"], y["dS_T"] = x["S0"][i:i + 1], x["dS_T"][i:i + 1]
+        o64, S64, g64 = reference(y, [0, lens[i]], 0.3, True)
+        if lens[i]:
+            near(o[:, a], o64, torch.bfloat16, FWD[torch.bfloat16], f"o {i}")
+            for k in ("dq", "dk", "dv", "dg", "dbeta"):
+                near(g[k][:, a], g64[k], torch.bfloat16 if k in ("dq", "dk", "dv") else torch.float32, 2 * FWD[torch.bfloat16], f"{k} {i}")
+        near(S_T[i:i + 1], S64, torch.float32, FWD[torch.bfloat16], f"S_T {i}")
+        near(g["dS0"][i:i + 1], g64["dS0"], torch.float32, 2 * FWD[torch.bfloat16], f"dS0 {i}")
