@@ -11,18 +11,19 @@
 // No factor exceeds one for g <= 0, so the decay needs no bound.
 //
 // Precision: q, k, v and do enter the bf16 matrix cores as they are.  Every other
-// operand (X, P, S, e, Z, ...) is an fp32 value split into an upper and a lower bf16
-// half, x = hi + lo up to 2^-18 |x|, and a product is the sum of the halves' products
-// without lo*lo: two matrix instructions against an exact operand, three against a
-// split one.  One rounding to bf16 instead (2^-9) would leave o within its own
-// rounding but the fp32 state and the fp32 gradients of g and beta at 3e-3.  With the halves
-// the state is within 4e-6 of 64-bit arithmetic (fp32 products throughout: 2e-7);
-// a third part would close that gap for twice the matrix instructions.
+// operand (X, P, S, e, Z, ...) is an fp32 value split into three bf16 parts, x = hi + mid + lo:
+// each part takes 8 bits of the 24 and more, so nothing of x is left over (2^-27 |x|), and a product is the
+// sum of the parts' products down to 2^-18 of it: three matrix instructions against an exact
+// operand, six against a split one (what is left out is below 2^-26).  That is fp32's own
+// precision at 3/16 and 6/16 of the time of its matrix instructions.  Two parts (two and three
+// instructions) left the state 4e-6 and the gradients of g and beta up to 1e-5 off, where fp32
+// products give 2e-7 and 5e-7; one rounding to bf16 leaves 3e-3.
 // In fp32 storage all of it runs on the fp32 matrix cores.
 //
 // Operands live in LDS and in the workspace as fragment blocks of 16 rows by 32 columns
 // of the contraction: lane (g, r) = 16 g + r holds row r and its eight slots of group g
-// contiguously, so reads are 16 bytes a lane without bank conflicts.  Two slot maps:
+// contiguously, so reads are 16 bytes a lane without bank conflicts.  In the workspace values are
+// fp32, and are split on their way into LDS or registers.  Two slot maps:
 //   natural:      slot s of group g is column 8 g + s           (rows of q, k: channels)
 //   accumulator:  slot s < 4 is column 4 g + s, s >= 4 is 16 + 4 g + (s - 4), which is what
 //                 two accumulator tiles hold in place           (tokens, and dv columns)
@@ -37,9 +38,8 @@ namespace gdr {
 
 constexpr int C = 64;                   // tokens a chunk
 constexpr int MT = 4;                   // 16-token tiles a chunk
-constexpr int SPB = 2048;               // bytes of a fragment block of fp32 values, split or not
+constexpr int WSB = 2048;               // bytes of a fragment block of fp32 values in the workspace
 constexpr int TRI = 6;                  // blocks of a triangular 64 x 64 operand that are not zero
-constexpr int TRI_BYTES = TRI * SPB;
 
 typedef short s16x4 __attribute__((__vector_size__(8)));
 typedef uint32_t u32x4 __attribute__((__vector_size__(16)));
@@ -177,37 +177,51 @@ template <typename E> struct Arith;
 
 template <> struct Arith<bf16> {
     typedef bf16x8 Ex;                        // an operand that is exact in bf16
-    struct Sp { bf16x8 hi, lo; };             // an fp32 operand in two halves
+    struct Sp { bf16x8 hi, mid, lo; };        // an fp32 operand in three parts
     static constexpr int EXB = 1024;          // bytes of an exact block
-    // Two values as the halves of their split: (upper pair, lower pair).  Six instructions: two
-    // packed conversions, the upper halves back as floats, two differences.
-    static __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-        hi = __builtin_bit_cast(uint32_t, bf16x2{(bf16)a, (bf16)b});
-        asm("" : "+v"(hi));   // one conversion for both values, not another one for the upper half of each
-        const float ha = __builtin_bit_cast(float, hi << 16), hb = __builtin_bit_cast(float, hi & 0xffff0000u);
-        lo = __builtin_bit_cast(uint32_t, bf16x2{(bf16)(a - ha), (bf16)(b - hb)});
+    static constexpr int SPB = 3072;          // bytes of a split one
+    // One part of two values, and what is left of them: five instructions, a packed
+    // conversion, its values back as floats, two differences (exact).
+    static __device__ __forceinline__ uint32_t part2(float& a, float& b) {
+        uint32_t p = __builtin_bit_cast(uint32_t, bf16x2{(bf16)a, (bf16)b});
+        asm("" : "+v"(p));   // one conversion for both values, not another one for each of the parts
+        a -= __builtin_bit_cast(float, p << 16);
+        b -= __builtin_bit_cast(float, p & 0xffff0000u);
+        return p;
+    }
+    static __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+        hi = part2(a, b);
+        mid = part2(a, b);
+        lo = __builtin_bit_cast(uint32_t, bf16x2{(bf16)a, (bf16)b});
     }
     static __device__ __forceinline__ Sp split(f32x4 a, f32x4 b) {
-        u32x4 h, l;
-        uint32_t x, y;
-        split2(a[0], a[1], x, y); h[0] = x; l[0] = y;
-        split2(a[2], a[3], x, y); h[1] = x; l[1] = y;
-        split2(b[0], b[1], x, y); h[2] = x; l[2] = y;
-        split2(b[2], b[3], x, y); h[3] = x; l[3] = y;
-        return Sp{__builtin_bit_cast(bf16x8, h), __builtin_bit_cast(bf16x8, l)};
+        u32x4 h, m, l;
+        uint32_t x, y, z;
+        split2(a[0], a[1], x, y, z); h[0] = x; m[0] = y; l[0] = z;
+        split2(a[2], a[3], x, y, z); h[1] = x; m[1] = y; l[1] = z;
+        split2(b[0], b[1], x, y, z); h[2] = x; m[2] = y; l[2] = z;
+        split2(b[2], b[3], x, y, z); h[3] = x; m[3] = y; l[3] = z;
+        return Sp{__builtin_bit_cast(bf16x8, h), __builtin_bit_cast(bf16x8, m), __builtin_bit_cast(bf16x8, l)};
     }
     static __device__ __forceinline__ f32x4 mma(Ex a, Ex b, f32x4 c) { return mfma_k32(a, b, c); }
-    static __device__ __forceinline__ f32x4 mma(Ex a, const Sp& b, f32x4 c) { return mfma_k32(a, b.hi, mfma_k32(a, b.lo, c)); }
-    static __device__ __forceinline__ f32x4 mma(const Sp& a, Ex b, f32x4 c) { return mfma_k32(a.hi, b, mfma_k32(a.lo, b, c)); }
-    static __device__ __forceinline__ f32x4 mma(const Sp& a, const Sp& b, f32x4 c) {
-        return mfma_k32(a.hi, b.hi, mfma_k32(a.hi, b.lo, mfma_k32(a.lo, b.hi, c)));
+    static __device__ __forceinline__ f32x4 mma(Ex a, const Sp& b, f32x4 c) {
+        return mfma_k32(a, b.hi, mfma_k32(a, b.mid, mfma_k32(a, b.lo, c)));
     }
-    // The same for N accumulators: one half's product of each before the next, so that no
+    static __device__ __forceinline__ f32x4 mma(const Sp& a, Ex b, f32x4 c) {
+        return mfma_k32(a.hi, b, mfma_k32(a.mid, b, mfma_k32(a.lo, b, c)));
+    }
+    static __device__ __forceinline__ f32x4 mma(const Sp& a, const Sp& b, f32x4 c) {   // the small products first
+        c = mfma_k32(a.mid, b.mid, mfma_k32(a.hi, b.lo, mfma_k32(a.lo, b.hi, c)));
+        return mfma_k32(a.hi, b.hi, mfma_k32(a.hi, b.mid, mfma_k32(a.mid, b.hi, c)));
+    }
+    // The same for N accumulators: one part's product of each before the next, so that no
     // instruction waits for the one before it.
     template <int N>
     static __device__ __forceinline__ void mma_n(const Ex (&a)[N], const Sp& b, f32x4 (&c)[N]) {
 #pragma unroll
         for (int i = 0; i < N; ++i) c[i] = mfma_k32(a[i], b.lo, c[i]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) c[i] = mfma_k32(a[i], b.mid, c[i]);
 #pragma unroll
         for (int i = 0; i < N; ++i) c[i] = mfma_k32(a[i], b.hi, c[i]);
     }
@@ -216,6 +230,8 @@ template <> struct Arith<bf16> {
 #pragma unroll
         for (int i = 0; i < N; ++i) c[i] = mfma_k32(a.lo, b[i], c[i]);
 #pragma unroll
+        for (int i = 0; i < N; ++i) c[i] = mfma_k32(a.mid, b[i], c[i]);
+#pragma unroll
         for (int i = 0; i < N; ++i) c[i] = mfma_k32(a.hi, b[i], c[i]);
     }
     static __device__ __forceinline__ Ex ld_ex(const char* base, int blk, int lane) {
@@ -223,12 +239,8 @@ template <> struct Arith<bf16> {
     }
     static __device__ __forceinline__ Sp ld_sp(const char* base, int blk, int lane) {
         const char* p = base + blk * SPB + lane * 16;
-        return Sp{*reinterpret_cast<const bf16x8*>(p), *reinterpret_cast<const bf16x8*>(p + 1024)};
-    }
-    static __device__ __forceinline__ void st_sp(char* base, int blk, int lane, const Sp& s) {
-        char* p = base + blk * SPB + lane * 16;
-        *reinterpret_cast<bf16x8*>(p) = s.hi;
-        *reinterpret_cast<bf16x8*>(p + 1024) = s.lo;
+        return Sp{*reinterpret_cast<const bf16x8*>(p), *reinterpret_cast<const bf16x8*>(p + 1024),
+                  *reinterpret_cast<const bf16x8*>(p + 2048)};
     }
     // Eight natural slots of a row in global memory.
     static __device__ __forceinline__ Ex ld_row(const bf16* p) { return *reinterpret_cast<const bf16x8*>(p); }
@@ -249,7 +261,7 @@ template <> struct Arith<bf16> {
     static __device__ __forceinline__ Sp ld_tri_t(const char* base, int n, int tb, int g, int r) {
         const int at = ((r & 3) * 16 + 4 * g + (r >> 2)) * 16 + (n & 1) * 8;
         const char *a = base + lower_block(2 * tb, n / 2) * SPB + at, *b = base + lower_block(2 * tb + 1, n / 2) * SPB + at;
-        return Sp{cat8(ld_tr(a), ld_tr(b)), cat8(ld_tr(a + 1024), ld_tr(b + 1024))};
+        return Sp{cat8(ld_tr(a), ld_tr(b)), cat8(ld_tr(a + 1024), ld_tr(b + 1024)), cat8(ld_tr(a + 2048), ld_tr(b + 2048))};
     }
     // Tokens 16 m + 4 g + i of column col + r of a row-major tile with `ld` columns.
     static __device__ __forceinline__ f32x4 ld_col(const char* base, int ld, int m, int col, int g, int r) {
@@ -266,41 +278,26 @@ template <> struct Arith<bf16> {
         for (int i = 0; i < 8; ++i) x[i] = (bf16)(here && i == s ? 1.0f : 0.0f);
         return x;
     }
-    // a's rows, transposed through the product with a picking matrix (exact), as half a
-    // block of accumulator slots at byte `blk` of the record; returns the values.
+    // a's rows, transposed through the product with a picking matrix (exact, and so is the sum
+    // of the parts), as half a block of accumulator slots at byte `blk` of the record; returns the values.
     static __device__ __forceinline__ f32x4 put_t(Rsrc rec, uint32_t blk, const Sp& a, Ex j) {
-        const f32x4 z = {0, 0, 0, 0};
-        const f32x4 hi = mfma_k32(a.hi, j, z), lo = mfma_k32(a.lo, j, z);
-        buf_st_quad(q4(hi), rec, blk);
-        buf_st_quad(q4(lo), rec, blk + 1024);
-        return hi + lo;
-    }
-    // A block of such a record: an upper and a lower plane, each half of the slots contiguous.
-    static __device__ __forceinline__ uint32_t rec_at(int lane, int half) { return (uint32_t)(half * 512 + lane * 8); }
-    static __device__ __forceinline__ Sp ld_rec(const char* base, int blk, int lane) {
-        const char* p = base + blk * SPB + lane * 8;
-        return Sp{cat8(ld_b4((const bf16*)p), ld_b4((const bf16*)(p + 512))),
-                  cat8(ld_b4((const bf16*)(p + 1024)), ld_b4((const bf16*)(p + 1536)))};
-    }
-    static __device__ __forceinline__ Sp ld_rec(Rsrc rec, uint32_t at) {
-        typedef BufQuad<bf16> Q;
-        return Sp{cat8(Q::ld(rec, at, 0), Q::ld(rec, at + 512, 0)), cat8(Q::ld(rec, at + 1024, 0), Q::ld(rec, at + 1536, 0))};
+        const f32x4 x = mma(a, j, f32x4{0, 0, 0, 0});
+        buf_st_quad(x, rec, blk);
+        return x;
     }
     static __device__ __forceinline__ float at(Ex x, int i) { return (float)x[i]; }
-    static __device__ __forceinline__ float dot(const Sp& x, const Sp& y) {
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s += ((float)x.hi[i] + (float)x.lo[i]) * ((float)y.hi[i] + (float)y.lo[i]);
-        return s;
-    }
     typedef bf16x4 Q4;
     static __device__ __forceinline__ Q4 q4(f32x4 x) { return Q4{(bf16)x[0], (bf16)x[1], (bf16)x[2], (bf16)x[3]}; }
     // One accumulator tile as half a split block.
     static __device__ __forceinline__ void put_half(char* base, int blk, int lane, int half, f32x4 x) {
         char* p = base + blk * SPB + lane * 16 + half * 8;
-        const bf16x4 hi = q4(x);
-        *reinterpret_cast<bf16x4*>(p) = hi;
-        *reinterpret_cast<bf16x4*>(p + 1024) = q4(f32x4{x[0] - (float)hi[0], x[1] - (float)hi[1], x[2] - (float)hi[2], x[3] - (float)hi[3]});
+        typedef uint32_t u32x2 __attribute__((__vector_size__(8)));
+        uint32_t h[2], m[2], l[2];
+        split2(x[0], x[1], h[0], m[0], l[0]);
+        split2(x[2], x[3], h[1], m[1], l[1]);
+        *reinterpret_cast<u32x2*>(p) = u32x2{h[0], h[1]};
+        *reinterpret_cast<u32x2*>(p + 1024) = u32x2{m[0], m[1]};
+        *reinterpret_cast<u32x2*>(p + 2048) = u32x2{l[0], l[1]};
     }
     static __device__ __forceinline__ void st4(bf16* p, f32x4 x) {
         *reinterpret_cast<bf16x4*>(p) = bf16x4{(bf16)x[0], (bf16)x[1], (bf16)x[2], (bf16)x[3]};
@@ -310,7 +307,7 @@ template <> struct Arith<bf16> {
 template <> struct Arith<float> {
     struct Ex { f32x4 a, b; };
     typedef Ex Sp;
-    static constexpr int EXB = SPB;
+    static constexpr int EXB = WSB, SPB = WSB;
     static __device__ __forceinline__ Sp split(f32x4 a, f32x4 b) { return Sp{a, b}; }
     static __device__ __forceinline__ f32x4 mma(const Ex& x, const Ex& y, f32x4 c) {
 #pragma unroll
@@ -334,11 +331,6 @@ template <> struct Arith<float> {
     static __device__ __forceinline__ Sp ld_sp(const char* base, int blk, int lane) {
         const char* p = base + blk * SPB + lane * 16;
         return Ex{*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 1024)};
-    }
-    static __device__ __forceinline__ void st_sp(char* base, int blk, int lane, const Sp& s) {
-        char* p = base + blk * SPB + lane * 16;
-        *reinterpret_cast<f32x4*>(p) = s.a;
-        *reinterpret_cast<f32x4*>(p + 1024) = s.b;
     }
     static __device__ __forceinline__ Ex ld_row(const float* p) {
         return Ex{*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 4)};
@@ -378,24 +370,12 @@ template <> struct Arith<float> {
         }
         return x;
     }
-    static __device__ __forceinline__ Sp ld_rec(const char* base, int blk, int lane) { return ld_sp(base, blk, lane); }
-    static __device__ __forceinline__ uint32_t rec_at(int lane, int half) { return (uint32_t)(half * 1024 + lane * 16); }
-    static __device__ __forceinline__ Sp ld_rec(Rsrc rec, uint32_t at) {
-        typedef BufQuad<float> Q;
-        return Sp{Q::ld(rec, at, 0), Q::ld(rec, at + 1024, 0)};
-    }
     static __device__ __forceinline__ f32x4 put_t(Rsrc rec, uint32_t blk, const Sp& a, const Ex& j) {
         const f32x4 x = mma(a, j, f32x4{0, 0, 0, 0});
         buf_st_quad(x, rec, blk);
         return x;
     }
     static __device__ __forceinline__ float at(const Ex& x, int i) { return i < 4 ? x.a[i & 3] : x.b[i & 3]; }
-    static __device__ __forceinline__ float dot(const Sp& x, const Sp& y) {
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s += x.a[i] * y.a[i] + x.b[i] * y.b[i];
-        return s;
-    }
     typedef f32x4 Q4;
     static __device__ __forceinline__ Q4 q4(f32x4 x) { return x; }
     static __device__ __forceinline__ void put_half(char* base, int blk, int lane, int half, f32x4 x) {
@@ -413,15 +393,32 @@ __device__ __forceinline__ typename Arith<E>::Ex pick_half(int h, int g, int r) 
 }
 
 // ---------------------------------------------------------------- workspace
-// A chunk of one head: X as split blocks, then per token gam, om beta, om, beta, and
-// G log2(e) in 64 bits.
-constexpr int PREP_BYTES = TRI_BYTES + 4 * C * 4 + C * 8;
+// A fragment block there: two planes of 16 bytes a lane, slots 0..3 and 4..7.
+__device__ __forceinline__ uint32_t rec_at(int lane, int half) { return (uint32_t)(half * 1024 + lane * 16); }
+struct Rec { f32x4 a, b; };
+__device__ __forceinline__ Rec ld_rec(Rsrc rec, uint32_t at) {
+    typedef BufQuad<float> Q;
+    return Rec{Q::ld(rec, at, 0), Q::ld(rec, at + 1024, 0)};
+}
+__device__ __forceinline__ void st_rec(char* base, int blk, int lane, f32x4 a, f32x4 b) {
+    char* p = base + blk * WSB + lane * 16;
+    *reinterpret_cast<f32x4*>(p) = a;
+    *reinterpret_cast<f32x4*>(p + 1024) = b;
+}
+// 16-byte piece u of consecutive blocks of the workspace, as it lies in LDS.
+template <typename E>
+__device__ __forceinline__ void put_piece(char* base, int u, u32x4 x) {
+    Arith<E>::put_half(base, u >> 7, u & 63, (u >> 6) & 1, __builtin_bit_cast(f32x4, x));
+}
+
+// A chunk of one head: X, then per token gam, om beta, om, beta, and G log2(e) in 64 bits.
+constexpr int X_BYTES = TRI * WSB, F_BYTES = 4 * C * 4 + C * 8, PREP_BYTES = X_BYTES + F_BYTES;
 // The map of a piece of one head, [dk][dv + dk] fp32: N, then M.
 __host__ __device__ constexpr int64_t map_bytes(int dk, int dv) { return (int64_t)dk * (dv + dk) * 4; }
 // The backward pass's records of a chunk of one head: a state (dk / 16 by dv / 32 blocks,
 // rows channels in the order of the accumulator tiles) and a 64 x dv operand (4 by dv / 32 blocks, rows tokens).
-__host__ __device__ constexpr int64_t state_bytes(int dk, int dv) { return (int64_t)(dk / 16) * (dv / 32) * SPB; }
-__host__ __device__ constexpr int64_t rows_bytes(int dv) { return (int64_t)MT * (dv / 32) * SPB; }
+__host__ __device__ constexpr int64_t state_bytes(int dk, int dv) { return (int64_t)(dk / 16) * (dv / 32) * WSB; }
+__host__ __device__ constexpr int64_t rows_bytes(int dv) { return (int64_t)MT * (dv / 32) * WSB; }
 // One behind the other: the start state, the end's gradient, e, Z.
 __host__ __device__ constexpr int64_t rec_bytes(int dk, int dv) { return 2 * (state_bytes(dk, dv) + rows_bytes(dv)); }
 

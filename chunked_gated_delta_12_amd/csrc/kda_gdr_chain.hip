@@ -20,11 +20,12 @@
 // of the chunk's bytes.  A chunk's outputs are stored at the start of the next one: behind the
 // loads they would be waited for at the loop's end.
 //
-// What bounds a walk is one chunk after another: by count its products, splits and LDS reads take about
-// 1.1 us each, and in two wavefronts a SIMD they overlap little.  Measured at 65,536 tokens of 16
-// heads, 128 x 128, bf16, in 16 pieces: the walk with outputs 340-373 us (memory alone 277,
-// compute alone 270), the maps, two column tiles a wavefront, 335-367 us (with one 400-436: memory
-// alone 230, compute alone 316).
+// What bounds a walk is one chunk after another: by count, at 128 x 128, the products of the two
+// wavefronts of a SIMD take 3 us (221 matrix instructions each), their splits 1.5 and the workgroup's LDS
+// reads 2.2, and they overlap little.  Measured at 65,536 tokens of 16 heads, 128 x 128, bf16, in 16 pieces: the walk
+// with outputs 485-531 us (its memory accesses alone 277), the maps, two column tiles a wavefront,
+// 521-564 us (230).  With operands in two parts they took 340-373 and 335-367, at a
+// twentieth of the precision (kda_gdr.hpp).
 #include "kda_gdr.hpp"
 #include "kda_launch.hpp"
 
@@ -45,11 +46,12 @@ struct Lay {
     // a row of values: 32 bytes more than its columns, so that the rows of a transposing read
     // spread over the banks
     static constexpr int VLD = SLAB + 32 / (int)sizeof(E), VROW = SLAB * (int)sizeof(E) / 16, VB = C * VLD * (int)sizeof(E);
-    static constexpr int Q_AT = QK, X_AT = Q_AT + (HAS_Q ? QK : 0), F_AT = X_AT + TRI_BYTES, V_AT = X_AT + PREP_BYTES,
-                         BYTES = V_AT + VB, PB = HAS_P ? TRI_BYTES : 0;
+    static constexpr int TB = TRI * Arith<E>::SPB;   // bytes of X, and of P
+    static constexpr int Q_AT = QK, X_AT = Q_AT + (HAS_Q ? QK : 0), F_AT = X_AT + TB, V_AT = F_AT + F_BYTES,
+                         BYTES = V_AT + VB, PB = HAS_P ? TB : 0;
     static constexpr int BUFS = 2 * BYTES + PB <= 160 * 1024 ? 2 : 1, ALL = BUFS * BYTES + PB;
     // 16-byte pieces, and how many of them a thread moves
-    static constexpr int PQK = QK / 16, PXP = PREP_BYTES / 16, PV = C * VROW;
+    static constexpr int PQK = QK / 16, PX = X_BYTES / 16, PXP = PREP_BYTES / 16, PV = C * VROW;
     static constexpr int NQK = (PQK + NTHR - 1) / NTHR, NXP = (PXP + NTHR - 1) / NTHR, NV = (PV + NTHR - 1) / NTHR;
     // bf16 rows leave through LDS, in the buffer that the chunk is done with
     static constexpr bool ROWS = (MODE == FWD || MODE == BACK) && sizeof(E) == 2 && BUFS == 2;
@@ -113,7 +115,8 @@ struct Stage {
 #pragma unroll
         for (int j = 0; j < L::NXP; ++j) {
             const int u = tid + j * L::NTHR;
-            if (L::PXP % L::NTHR == 0 || u < L::PXP) *reinterpret_cast<u32x4*>(buf + L::X_AT + u * 16) = x[j];
+            if (u < L::PX) put_piece<E>(buf + L::X_AT, u, x[j]);
+            else if (u < L::PXP) *reinterpret_cast<u32x4*>(buf + L::F_AT + (u - L::PX) * 16) = x[j];
         }
 #pragma unroll
         for (int j = 0; j < L::NV; ++j) {
@@ -260,7 +263,7 @@ __device__ __forceinline__ void walk(const Args& a, const Segs& sg, const Ptrs& 
     }
     lds_barrier();
     // where this wavefront's columns are in a record; past its end where it has none
-    const uint32_t w_off = act ? (uint32_t)(col0 / 32 * SPB) + A::rec_at(lane, (col0 >> 4) & 1) : 0x80000000u;
+    const uint32_t w_off = act ? (uint32_t)(col0 / 32 * WSB) + rec_at(lane, (col0 >> 4) & 1) : 0x80000000u;
     const typename A::Ex pk0 = pick_half<E>(0, g, r), pk1 = pick_half<E>(1, g, r);
     for (int it = 0; it < nch; ++it) {
         const char* buf = lds + (L::BUFS == 2 ? (it & 1) * L::BYTES : 0);
@@ -306,7 +309,7 @@ __device__ __forceinline__ void walk(const Args& a, const Segs& sg, const Ptrs& 
 #pragma unroll
                 for (int b = 0; b < KB; ++b)
 #pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) A::put_t(to, w_off + (uint32_t)((2 * b + hh) * (a.dv / 32) * SPB), sb[0][b], hh ? pk1 : pk0);
+                    for (int hh = 0; hh < 2; ++hh) A::put_t(to, w_off + (uint32_t)((2 * b + hh) * (a.dv / 32) * WSB), sb[0][b], hh ? pk1 : pk0);
             }
             f32x4 y[NC][MT], dov[MT];
             typename A::Ex dob[2];
@@ -382,7 +385,7 @@ __device__ __forceinline__ void walk(const Args& a, const Segs& sg, const Ptrs& 
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int hh = 0; hh < 2; ++hh) {
-                        const f32x4 z = A::put_t(to, w_off + (uint32_t)((2 * b + hh) * (a.dv / 32) * SPB), eb[b], hh ? pk1 : pk0);
+                        const f32x4 z = A::put_t(to, w_off + (uint32_t)((2 * b + hh) * (a.dv / 32) * WSB), eb[b], hh ? pk1 : pk0);
                         if constexpr (MODE == BACK) done(buf, 2 * b + hh, z);
                     }
             }
@@ -479,8 +482,8 @@ chain_kernel(Args a, Segs sg, Ptrs io) {
 
 // Two walks in one launch, the longer one's workgroups first: the backward pass walks each way
 // once, neither needs the other, and each alone leaves compute units idle where there are
-// fewer than 256 workgroups (8 sequences of 4,096 tokens, 16 heads of 128 x 128 in bf16: 400 and
-// 470 us one after the other in workgroups of four wavefronts, 710 together in eight).
+// fewer than 256 workgroups (8 sequences of 4,096 tokens, 16 heads of 128 x 128 in bf16: 888 us together in
+// workgroups of eight wavefronts; the whole call 1,660 us, in workgroups of four 1,700).
 template <typename E, int DK, int NW, int BACKWARDS, int FORWARDS>
 __global__ void __launch_bounds__(64 * NW, NW / 4)
 pair_kernel(Args a, Segs sg, Ptrs back, Ptrs forth, unsigned nback) {
@@ -493,12 +496,13 @@ pair_kernel(Args a, Segs sg, Ptrs back, Ptrs forth, unsigned nback) {
 // Joins the maps of a cut sequence's pieces: forwards X_0 = S0, X_{i+1} = M_i X_i + N_i, backwards
 // X_last = dS_T, X_{i-1} = M_i^T X_i + N'_i, every X_i written to `starts`.  A workgroup has one
 // head and 16 columns, a wavefront one tile of rows; X goes from step to step through LDS as
-// split fragments, the next step's M and N are in flight meanwhile.  Bound by a step's way through L2:
+// fragments, the next step's M and N are in flight meanwhile.  On the fp32 matrix cores whatever the
+// storage: M and X come as fp32 values, and nothing is split on the way.  Bound by a step's way through L2:
 // 2.6 us; 16 pieces of 16 heads, 128 x 128: 42 us, with 32 columns a workgroup 70.
-template <typename E, int DK, bool BWD>
+template <int DK, bool BWD>
 __device__ __forceinline__ void join(const Args& a, const Segs& sg, const float* __restrict__ init, const float* __restrict__ maps,
-                                     const float* __restrict__ nmaps, float* __restrict__ starts, char (&lds)[2][DK / 32 * SPB]) {
-    typedef Arith<E> A;
+                                     const float* __restrict__ nmaps, float* __restrict__ starts, char (&lds)[2][DK / 32 * WSB]) {
+    typedef Arith<float> A;
     constexpr int KB = DK / 32, ST = DK / 16;
     const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -557,13 +561,13 @@ __device__ __forceinline__ void join(const Args& a, const Segs& sg, const float*
 }
 
 // The backward pass joins both ways in one launch (blockIdx.y).
-template <typename E, int DK>
+template <int DK>
 __global__ void __launch_bounds__(512)
 join_kernel(Args a, Segs sg, const float* init, const float* maps, float* starts, const float* dinit, const float* nmaps,
             float* dstarts) {
-    __shared__ alignas(16) char lds[2][DK / 32 * SPB];
-    if (blockIdx.y == 0) join<E, DK, false>(a, sg, init, maps, maps, starts, lds);
-    else join<E, DK, true>(a, sg, dinit, maps, nmaps, dstarts, lds);
+    __shared__ alignas(16) char lds[2][DK / 32 * WSB];
+    if (blockIdx.y == 0) join<DK, false>(a, sg, init, maps, maps, starts, lds);
+    else join<DK, true>(a, sg, dinit, maps, nmaps, dstarts, lds);
 }
 
 // Workgroups of a walk over `cols` columns: a multiple of eight.
@@ -596,9 +600,9 @@ hipError_t one_d(const Args& a, const Segs& sg, Ptrs io, hipStream_t stream) {
     const int cols = MODE == MAP ? a.dv + DK : a.dv;
     io.places = (int)places_of(a.nseq, a.T, a.cu != nullptr, seg_unit(sg));
     if constexpr (sizeof(E) == 2) {
-        // Two column tiles a wavefront read every operand once for both, in 6.0 us a chunk against 3.1:
+        // Two column tiles a wavefront read every operand once for both, in 8 us a chunk against 4.4:
         // where workgroups of 128 columns would take a second round (65,536 tokens of 16 heads, the
-        // whole call: 905 us against 980; ten packed sequences with 128 workgroups of 256 columns: 318 against 288).
+        // whole call: 1,165 us against 1,220; ten packed sequences with 128 workgroups of 256 columns: 411 against 340).
         if constexpr (MODE == MAP)
             if (cols > 128 && cut_of(a, sg) && walks_of(a, sg) * ((cols + 127) / 128) > 256)
                 return one_t<E, DK, 8, MODE, 2>(a, sg, io, cols, stream);
@@ -638,11 +642,11 @@ hipError_t grads_d(bool maps, const Args& a, const Segs& sg, const Ptrs& back, c
     return maps ? pair_d<E, DK, BMAP, MAP>(a, sg, back, forth, stream) : pair_d<E, DK, BACK, SAVE>(a, sg, back, forth, stream);
 }
 
-template <typename E, int DK>
+template <int DK>
 hipError_t join_d(const Args& a, const Segs& sg, const float* init, const float* maps, float* starts, const float* dinit,
                   const float* nmaps, float* dstarts, hipStream_t stream) {
     const dim3 grid((unsigned)((int64_t)a.nseq * a.Hv * (a.dv / 16)), nmaps ? 2 : 1);
-    hipLaunchKernelGGL((join_kernel<E, DK>), grid, dim3(512), 0, stream, a, sg, init, maps, starts, dinit, nmaps, dstarts);
+    hipLaunchKernelGGL((join_kernel<DK>), grid, dim3(512), 0, stream, a, sg, init, maps, starts, dinit, nmaps, dstarts);
     return hipGetLastError();
 }
 
@@ -691,9 +695,14 @@ hipError_t launch_bwd_chains(bool f32, int dk, const Args& a, const Segs& sg, co
     KDA_GDR_TYPES(grads_d, false, a, sg, back, forth, stream);
 }
 
-hipError_t launch_join(bool f32, int dk, const Args& a, const Segs& sg, const float* init, const float* maps, float* starts,
+hipError_t launch_join(int dk, const Args& a, const Segs& sg, const float* init, const float* maps, float* starts,
                        const float* dinit, const float* nmaps, float* dstarts, hipStream_t stream) {
-    KDA_GDR_TYPES(join_d, a, sg, init, maps, starts, dinit, nmaps, dstarts, stream);
+    switch (dk) {
+        case 32: return join_d<32>(a, sg, init, maps, starts, dinit, nmaps, dstarts, stream);
+        case 64: return join_d<64>(a, sg, init, maps, starts, dinit, nmaps, dstarts, stream);
+        case 128: return join_d<128>(a, sg, init, maps, starts, dinit, nmaps, dstarts, stream);
+    }
+    return hipErrorInvalidValue;
 }
 
 }  // namespace gdr

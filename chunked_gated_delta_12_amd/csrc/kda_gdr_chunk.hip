@@ -21,7 +21,7 @@ hipError_t launch_bwd_maps(bool f32, int dk, const Args& a, const Segs& sg, cons
 hipError_t launch_bwd_chains(bool f32, int dk, const Args& a, const Segs& sg, const void* q, const void* k, const void* v,
                              const void* dout, const float* S0, const float* starts, const float* dS_T, const float* dstarts,
                              const char* prep, void* dv, float* dS0, char* recs, hipStream_t stream);
-hipError_t launch_join(bool f32, int dk, const Args& a, const Segs& sg, const float* init, const float* maps, float* starts,
+hipError_t launch_join(int dk, const Args& a, const Segs& sg, const float* init, const float* maps, float* starts,
                        const float* dinit, const float* nmaps, float* dstarts, hipStream_t stream);
 hipError_t launch_grad(bool f32, int dk_, const Args& a, const void* q, const void* k, const void* dout,
                        const char* prep, const char* recs, void* dq, void* dk, float* dg, float* dbeta, hipStream_t stream);
@@ -30,14 +30,16 @@ namespace {
 
 // Cutting a sequence costs a second walk of it (the maps, over dv + dk columns) and the join of
 // its pieces, so it pays where its own walk would outlast the others' by much.  With a chunk
-// taking about 5 us in a walk and 3.4 us in a map, and a piece 2.6 us in the join (bf16,
-// 128 x 128; fp32 in like proportion), L chunks in pieces of s take 8.4 s + 2.6 L / s us: least at
-// s^2 = 0.31 L, where the chip has room for so many.  `seg` is that, but at least the even share
+// taking about 6.8 us in a walk and 4.4 us in a map, and a piece 2.6 us in the join (bf16,
+// 128 x 128), L chunks in pieces of s take 11.2 s + 2.6 L / s us: least at s^2 = 0.23 L, and flat
+// around it.  `seg` is from s^2 = 0.31 L, but at least the even share
 // of the call's work over the 256 compute units, half a workgroup set aside for the part piece that
-// each sequence ends with.  Uncut the walk takes 5 L us: longer than the pieces from about
+// each sequence ends with.  Uncut the walk takes 6.8 L us: longer than the pieces from about
 // L = 1.7 seg + 3 on, which is `over`; once any sequence is longer than that the maps run
-// anyway, and all longer than a piece are cut.  Measured: one sequence of 1,024 chunks and 16 heads 5.25 ms
-// whole, 1.0 ms in pieces of 66, 1.1 ms in 32 or 86; eight of 64 chunks 8% slower when cut in two.
+// anyway, and all longer than a piece are cut.  0.23 and 0.31 were measured over both passes and types,
+// 32 x 64 to 128 x 256, one to eight heads, 2,000 to 30,000 tokens: prefill in bf16 of 8,492 tokens, 4 heads of
+// 128 x 256, 164 and 147 us, of 2 x 1,000 tokens, 4 heads of 64 x 64, 49 and 53; fp32 forwards
+// 4,096 tokens, one head of 128 x 128, 140 and 151; the others within 10% either way.
 Segs segs_of(int nseq, int T, int Hv, int dv, bool packed) {
     const int64_t heads = (int64_t)Hv * ((dv + 127) / 128), work = places_of(nseq, T, packed, C) * heads;
     const int64_t longest = ((int64_t)T + C - 1) / C;   // that a sequence can be
@@ -127,7 +129,7 @@ hipError_t launch_gdr_fwd(const GdrCall& c, void* o, float* S_T, void* workspace
     KDA_DO(gdr::launch_prep(c.f32, c.dk, a, c.k, c.g, c.beta, ws + p.prep, stream));
     if (p.sg.seg) {
         KDA_DO(gdr::launch_maps(c.f32, c.dk, a, p.sg, c.k, c.v, ws + p.prep, maps, stream));
-        KDA_DO(gdr::launch_join(c.f32, c.dk, a, p.sg, c.S0, maps, starts, nullptr, nullptr, nullptr, stream));
+        KDA_DO(gdr::launch_join(c.dk, a, p.sg, c.S0, maps, starts, nullptr, nullptr, nullptr, stream));
     }
     return gdr::launch_fwd_chain(c.f32, c.dk, a, p.sg, c.q, c.k, c.v, c.S0, starts, ws + p.prep, o, S_T, stream);
 }
@@ -142,7 +144,7 @@ hipError_t launch_gdr_bwd(const GdrCall& c, const void* dout, const float* dS_T,
     KDA_DO(gdr::launch_prep(c.f32, c.dk, a, c.k, c.g, c.beta, ws + p.prep, stream));
     if (p.sg.seg) {
         KDA_DO(gdr::launch_bwd_maps(c.f32, c.dk, a, p.sg, c.q, c.k, c.v, dout, ws + p.prep, maps, nmaps, stream));
-        KDA_DO(gdr::launch_join(c.f32, c.dk, a, p.sg, c.S0, maps, starts, dS_T, nmaps, dstarts, stream));
+        KDA_DO(gdr::launch_join(c.dk, a, p.sg, c.S0, maps, starts, dS_T, nmaps, dstarts, stream));
     }
     KDA_DO(gdr::launch_bwd_chains(c.f32, c.dk, a, p.sg, c.q, c.k, c.v, dout, c.S0, starts, dS_T, dstarts, ws + p.prep, dv, dS0,
                                   ws + p.recs, stream));

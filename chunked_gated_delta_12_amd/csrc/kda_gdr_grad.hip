@@ -20,7 +20,7 @@
 // last products, read there as rows of queries and, transposed, as rows of keys.
 // Memory bounds it: 192 KB of states and rows a unit at dk = dv = 128.  The next unit's loads
 // are issued before this unit's last part, as many as fit the registers.  Measured at 8 x 4,096 tokens,
-// 16 heads, dk = dv = 128: 620 us, 2.3 GB, 3.7 TB/s; a workgroup a chunk without loads ahead: 885 us.
+// 16 heads, dk = dv = 128: 660-680 us, 2.3 GB, 3.4 TB/s.
 #include <type_traits>
 
 #include "kda_gdr.hpp"
@@ -39,8 +39,10 @@ struct GradLay {
     static constexpr int SPLIT = 8 / ST, TT = MT / SPLIT;     // wavefronts a channel tile, token tiles of each
     static constexpr int GB = sizeof(E) == 2 ? 4 : 1;         // 32-column blocks of a unit in LDS at once
     static constexpr int QK = MT * KB * EXB;
+    static constexpr int SPB = Arith<E>::SPB, TB = TRI * SPB;
     static constexpr int E_AT = 0, Z_AT = MT * SPB, O_AT = 2 * MT * SPB, BLK = O_AT + MT * EXB;   // one column block
     static constexpr int BUF = GB * BLK;
+    static_assert(2 * TB <= BUF, "the exchanged tiles lie over the column blocks");
     static constexpr int PQK = QK / 16, NQK = (PQK + GTHR - 1) / GTHR;
     static constexpr int PO = MT * EXB / 16, NO = (GB * PO + GTHR - 1) / GTHR;   // pieces of do in a block; a thread's in all
 };
@@ -63,7 +65,6 @@ grad_kernel(Args a, int items, const E* __restrict__ q, const E* __restrict__ k,
     __shared__ alignas(16) char kl[L::QK];
     __shared__ alignas(16) char ql[L::QK];
     __shared__ alignas(16) char lds[L::BUF];
-    __shared__ alignas(16) char xch[2 * TRI_BYTES];   // scale D X beta_s and M, [t][s]
     __shared__ double Gs[C];
     __shared__ alignas(16) float csum[10][16];
     __shared__ float gam[C], om[C], bts[C], part[3][ST][C], rsum[10][16], dots[8];
@@ -83,6 +84,7 @@ grad_kernel(Args a, int items, const E* __restrict__ q, const E* __restrict__ k,
     const int rep = a.Hv / a.Hk, nb = a.dv / 32, ngrp = (nb + GB - 1) / GB;
     const int64_t ldk = (int64_t)a.Hk * DK, ldv = (int64_t)a.Hv * a.dv;
     const f32x4 zero = {0, 0, 0, 0};
+    char* const xch = lds;   // scale D X beta_s and M, [t][s], once a unit's column blocks have been read
 
     // A unit: group `grp` of value head vh of an item, the item's chunk in ch.
     struct Unit3 {
@@ -106,7 +108,7 @@ grad_kernel(Args a, int items, const E* __restrict__ q, const E* __restrict__ k,
     };
 
     const uint32_t sbytes = (uint32_t)state_bytes(DK, a.dv), ebytes = (uint32_t)rows_bytes(a.dv), rbytes = 2 * (sbytes + ebytes);
-    Sp sf[GB], df[GB];
+    Rec sf[GB], df[GB];
     u32x4 se[GB], sz[GB], so[L::NO], sk[L::NQK], sq[L::NQK];
     float fac[3] = {0, 0, 0};
     double facG = 0.0;
@@ -118,9 +120,9 @@ grad_kernel(Args a, int items, const E* __restrict__ q, const E* __restrict__ k,
         const int b0 = u.grp * GB;
 #pragma unroll
         for (int b = decltype(lo)::value; b < decltype(hi)::value; ++b) {
-            const uint32_t at = b0 + b < nb ? (uint32_t)((ct * nb + b0 + b) * SPB) + A::rec_at(lane, 0) : 0x80000000u;
-            sf[b] = A::ld_rec(rs, at);
-            df[b] = A::ld_rec(rs, at + sbytes);
+            const uint32_t at = b0 + b < nb ? (uint32_t)((ct * nb + b0 + b) * WSB) + rec_at(lane, 0) : 0x80000000u;
+            sf[b] = ld_rec(rs, at);
+            df[b] = ld_rec(rs, at + sbytes);
         }
     };
     typedef std::integral_constant<int, 0> B0;
@@ -131,7 +133,7 @@ grad_kernel(Args a, int items, const E* __restrict__ q, const E* __restrict__ k,
         const Rsrc rs = make_rsrc(recs + rec_of(u) * rbytes, rbytes);
 #pragma unroll
         for (int b = 0; b < GB; ++b) {   // 512 pieces of e and of Z a block: one a thread
-            const uint32_t at = b0 + b < nb ? 2 * sbytes + (uint32_t)(((tid >> 7) * nb + b0 + b) * SPB + (tid & 127) * 16) : 0x80000000u;
+            const uint32_t at = b0 + b < nb ? 2 * sbytes + (uint32_t)(((tid >> 7) * nb + b0 + b) * WSB + (tid & 127) * 16) : 0x80000000u;
             se[b] = buf_ld128(rs, at);
             sz[b] = buf_ld128(rs, at + ebytes);
         }
@@ -164,7 +166,7 @@ grad_kernel(Args a, int items, const E* __restrict__ q, const E* __restrict__ k,
             sq[j] = buf_ld128(rq, at);
         }
         if (tid < C) {
-            const float* f = reinterpret_cast<const float*>(prep + rec_of(u) * PREP_BYTES + TRI_BYTES);
+            const float* f = reinterpret_cast<const float*>(prep + rec_of(u) * PREP_BYTES + X_BYTES);
             fac[0] = f[tid];
             fac[1] = f[2 * C + tid];
             fac[2] = f[3 * C + tid];
@@ -195,8 +197,8 @@ grad_kernel(Args a, int items, const E* __restrict__ q, const E* __restrict__ k,
         lds_barrier();   // the unit before is done with LDS
 #pragma unroll
         for (int b = 0; b < GB; ++b) {
-            *reinterpret_cast<u32x4*>(lds + b * L::BLK + L::E_AT + tid * 16) = se[b];
-            *reinterpret_cast<u32x4*>(lds + b * L::BLK + L::Z_AT + tid * 16) = sz[b];
+            put_piece<E>(lds + b * L::BLK + L::E_AT, tid, se[b]);
+            put_piece<E>(lds + b * L::BLK + L::Z_AT, tid, sz[b]);
         }
 #pragma unroll
         for (int j = 0; j < L::NO; ++j) {
@@ -210,23 +212,30 @@ grad_kernel(Args a, int items, const E* __restrict__ q, const E* __restrict__ k,
         for (int b = 0; b < GB; ++b) {
             const char* buf = lds + b * L::BLK;
             if (b == GB / 2) load_kq(u);   // into the registers that the first states have left
-            const Sp &s = sf[b], &d = df[b];
+            if (L::SPLIT == 1 || m0 == 0)
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                const Sp z = A::ld_rec(buf + L::Z_AT, m0 + t, lane), e = A::ld_rec(buf + L::E_AT, m0 + t, lane);
-                dos[t] = A::mma(s, A::ld_ex(buf + L::O_AT, m0 + t, swz(lane)), dos[t]);
-                zs[t] = A::mma(s, z, zs[t]);
-                eds[t] = A::mma(d, e, eds[t]);
-            }
-            if (L::SPLIT == 1 || m0 == 0) dot += A::dot(s, d);
+                for (int i = 0; i < 4; ++i) dot += sf[b].a[i] * df[b].a[i] + sf[b].b[i] * df[b].b[i];
             asm volatile("" : "+v"(dot));   // here, while the states' registers are needed anyway
+            {
+                const Sp s = A::split(sf[b].a, sf[b].b);
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
+                    dos[t] = A::mma(s, A::ld_ex(buf + L::O_AT, m0 + t, swz(lane)), dos[t]);
+                    zs[t] = A::mma(s, A::ld_sp(buf + L::Z_AT, m0 + t, lane), zs[t]);
+                }
+            }
+            {
+                const Sp d = A::split(df[b].a, df[b].b);
+#pragma unroll
+                for (int t = 0; t < TT; ++t) eds[t] = A::mma(d, A::ld_sp(buf + L::E_AT, m0 + t, lane), eds[t]);
+            }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 int m, n;
                 if (!tile_of(j, m, n)) continue;
-                const Sp e = A::ld_rec(buf + L::E_AT, n, lane);
+                const Sp e = A::ld_sp(buf + L::E_AT, n, lane);
                 x[j] = A::mma(e, A::ld_ex(buf + L::O_AT, m, swz(lane)), x[j]);
-                mm[j] = A::mma(e, A::ld_rec(buf + L::Z_AT, m, lane), mm[j]);
+                mm[j] = A::mma(e, A::ld_sp(buf + L::Z_AT, m, lane), mm[j]);
             }
         }
         const Unit3 nu = next(u);
@@ -278,7 +287,7 @@ grad_kernel(Args a, int items, const E* __restrict__ q, const E* __restrict__ k,
                     mv[l] *= b;
                 }
                 A::put_half(xch, lower_block(m, n / 2), lane, n & 1, xv);
-                A::put_half(xch + TRI_BYTES, lower_block(m, n / 2), lane, n & 1, mv);
+                A::put_half(xch + L::TB, lower_block(m, n / 2), lane, n & 1, mv);
                 row = over_groups(row);
 #pragma unroll
                 for (int s = 1; s < 16; s <<= 1)
@@ -289,7 +298,7 @@ grad_kernel(Args a, int items, const E* __restrict__ q, const E* __restrict__ k,
                 if (r == 0) *reinterpret_cast<f32x4*>(&csum[t][4 * g]) = col;
                 x[j] = mm[j] = zero;
             }
-            if (w < 4) A::put_half(xch + (w & 1) * TRI_BYTES, w < 2 ? lower_block(0, 0) : lower_block(2, 1), lane, 1, zero);   // beyond the diagonal
+            if (w < 4) A::put_half(xch + (w & 1) * L::TB, w < 2 ? lower_block(0, 0) : lower_block(2, 1), lane, 1, zero);   // beyond the diagonal
             // the states' parts, and their products with q and k over this channel tile
 #pragma unroll
             for (int t = 0; t < TT; ++t) {
@@ -336,11 +345,11 @@ grad_kernel(Args a, int items, const E* __restrict__ q, const E* __restrict__ k,
                     for (int tb = 0; tb < 2; ++tb) {
                         if (tb <= m / 2) {
                             aq[t] = A::mma(kt[tb], A::ld_sp(xch, lower_block(m, tb), lane), aq[t]);
-                            ak[t] = A::mma(kt[tb], A::ld_sp(xch + TRI_BYTES, lower_block(m, tb), lane), ak[t]);
+                            ak[t] = A::mma(kt[tb], A::ld_sp(xch + L::TB, lower_block(m, tb), lane), ak[t]);
                         }
                         if (tb >= m / 2) {
                             ak[t] = A::mma(qt[tb], A::ld_tri_t(xch, m, tb, g, r), ak[t]);
-                            ak[t] = A::mma(kt[tb], A::ld_tri_t(xch + TRI_BYTES, m, tb, g, r), ak[t]);
+                            ak[t] = A::mma(kt[tb], A::ld_tri_t(xch + L::TB, m, tb, g, r), ak[t]);
                         }
                     }
                 }

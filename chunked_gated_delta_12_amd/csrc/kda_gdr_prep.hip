@@ -85,7 +85,7 @@ prep_kernel(Args a, const E* __restrict__ k, const float* __restrict__ gate, con
         Bs[lane] = bt;
         const double end = __shfl(G, 63);
         const float om = __builtin_amdgcn_exp2f((float)(end - G));
-        float* f = reinterpret_cast<float*>(out + TRI_BYTES);
+        float* f = reinterpret_cast<float*>(out + X_BYTES);
         f[lane] = __builtin_amdgcn_exp2f((float)G);
         f[C + lane] = om * bt;
         f[2 * C + lane] = om;
@@ -160,7 +160,7 @@ prep_kernel(Args a, const E* __restrict__ k, const float* __restrict__ gate, con
         if (b <= w / 2) {
             const f32x4 lo = *reinterpret_cast<const f32x4*>(&tiles[x_tile(w, 2 * b) + r * LD + 4 * g]);
             const f32x4 hi = 2 * b + 1 <= w ? *reinterpret_cast<const f32x4*>(&tiles[x_tile(w, 2 * b + 1) + r * LD + 4 * g]) : zero;
-            A::st_sp(out, lower_block(w, b), lane, A::split(lo, hi));
+            st_rec(out, lower_block(w, b), lane, lo, hi);
         }
     }
 }

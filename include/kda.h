@@ -292,9 +292,9 @@ int kda_gate(int B, int T, int H, int dk, const float* theta, float* g, float* g
  *    as given.  Positive g is used as it is (the state grows).
  *  - KDA_BF16 means bf16 storage of q, k, v, o (and of do, dq, dk, dv).  The state,
  *    g, beta and their gradients are fp32, and so is the arithmetic: products of
- *    intermediate results run on the bf16 matrix cores as sums over their upper and
- *    lower halves, which keeps 16 bits of each factor.  KDA_F32 keeps fp32
- *    storage and fp32 products throughout.
+ *    intermediate results run on the bf16 matrix cores as sums over three parts of
+ *    each factor, which keep all its 24 bits.  KDA_F32 keeps fp32 storage and the
+ *    fp32 matrix cores throughout.
  * ------------------------------------------------------------------------- */
 
 /* ---------------------------------------------------------------------------

@@ -681,3 +681,27 @@ def test_thousands_of_short_sequences_beside_a_long_one():
                 near(g[k][:, a], g64[k], torch.bfloat16 if k in ("dq", "dk", "dv") else torch.float32, 2 * FWD[torch.bfloat16], f"{k} {i}")
         near(S_T[i:i + 1], S64, torch.float32, FWD[torch.bfloat16], f"S_T {i}")
         near(g["dS0"][i:i + 1], g64["dS0"], torch.float32, 2 * FWD[torch.bfloat16], f"dS0 {i}")
+
+
+@pytest.mark.gpu
+@both
+@pytest.mark.parametrize("lens,Hk,Hv,dk,dv", [
+    ([13, 268], 2, 2, 32, 128), ([88, 1], 1, 4, 128, 64), ([257], 2, 4, 32, 128), ([1500], 1, 2, 64, 64), ([700, 1217], 1, 2, 128, 96)])
+def test_fp32_results_keep_fp32_precision(lens, Hk, Hv, dk, dv, dtype):
+    """The last state and the gradients of g, beta and the start state are fp32 whatever the storage,
+    and so is their precision, sequences cut in pieces among them; in the 2-norm, relative.  An
+    operand in three bf16 parts leaves 2^-27 of itself and its products leave out 2^-26, less than the
+    accumulators' rounding of 2^-24.  Eight products one behind another, each a sum of at most 128 terms with one
+    rounding a term, their signs independent: sqrt(8 * 128) * 2^-24 / sqrt(3) = 1.1e-6.  dS0 runs through both chains:
+    sqrt(2) times that.  dg and dbeta are differences of sums twice their size besides: 2 sqrt(2) times."""
+    unit = (8 * 128 / 3) ** 0.5 * 2.0 ** -24
+    x, cu = make(lens, Hk, Hv, dk, dv, dtype, 90 + sum(lens), gmu=-4.0)
+    print(f"gdr precision lens={lens} {Hk} {Hv} {dk} {dv} {dtype}", flush=True)
+    _, S64, g64 = reference(x, cu, dk ** -0.5, True)
+    got = dict(run_bwd(x, cu, dk ** -0.5), S_T=run_fwd(x, cu, dk ** -0.5)[1])
+    off = {}
+    for k, want, times in (("S_T", S64, 1.0), ("dS0", g64["dS0"], 2 ** 0.5), ("dg", g64["dg"], 8 ** 0.5), ("dbeta", g64["dbeta"], 8 ** 0.5)):
+        e = float((got[k].double().cpu() - want).norm() / want.norm())
+        if not e <= times * unit:
+            off[k] = f"{e:.2e} > {times * unit:.2e}"
+    assert not off, off
