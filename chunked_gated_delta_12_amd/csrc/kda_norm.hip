@@ -256,7 +256,7 @@ norm_bwd_kernel(int64_t rows, int D, float eps, bool silu, const E* __restrict__
     if (AHEAD) fetch((int64_t)blockIdx.x * G + grp);
     for (int64_t base = (int64_t)blockIdx.x * G; base < rows; base += (int64_t)gridDim.x * G) {
         const int64_t row = base + grp;
-        const bool in = row < rows;
+        const bool in = G == 1 || row < rows;
         if (!AHEAD) fetch(row);
         V8 vy[NV], vx[NV], vz[NV], vd[NV], vh[NV];
 #pragma unroll
@@ -276,7 +276,7 @@ norm_bwd_kernel(int64_t rows, int D, float eps, bool silu, const E* __restrict__
 #pragma unroll
                 for (int e = 0; e < 8; ++e) q[0] += vy[i].f[e] * vy[i].f[e];
             row_sum<L>(q, lds, turn);
-            rho = 1.0f / sqrtf(q[0] * inv + eps);
+            rho = in ? 1.0f / sqrtf(q[0] * inv + eps) : 0.0f;   // eps may be 0: lanes without a row add nothing to the weights' sums
         }
         if (dh) {
             // r from its parts, then the norm's backward into dr'
@@ -298,7 +298,7 @@ norm_bwd_kernel(int64_t rows, int D, float eps, bool silu, const E* __restrict__
                     q[1] += on[i] ? vh[i].f[e] * wn[i].f[e] * vx[i].f[e] : 0.0f;
                 }
             row_sum<L>(q, lds, turn);
-            const float rr = 1.0f / sqrtf(q[0] * inv + eps);
+            const float rr = in ? 1.0f / sqrtf(q[0] * inv + eps) : 0.0f;
             const float k = rr * rr * rr * q[1] * inv;
 #pragma unroll
             for (int i = 0; i < NV; ++i)

@@ -359,3 +359,15 @@ def test_two_calls_at_once():
     for p, q in zip(want, got):
         for j, (u, v) in enumerate(zip(p, q)):
             assert torch.equal(u, v), j
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("eps", [0.0, 1e-38, 1e-30])
+@pytest.mark.parametrize("rows,D,dtype", [(17, 8, torch.float32), (17, 128, torch.bfloat16), (5, 64, torch.float32), (2049, 1000, torch.bfloat16),
+                                          (3, 1000, torch.float32), (1, 24, torch.bfloat16), (3, 2048, torch.bfloat16)])
+def test_eps_of_zero_and_part_groups(rows, D, dtype, eps):
+    """Rows that do not fill the last group of lanes: where no row is, the root of zero stands under nothing,
+    and the weights' gradients are those of the rows."""
+    check((rows,), D, dtype, 100 + rows + D, ALL, "silu", eps=eps)
+    check((rows,), D, dtype, 101 + rows + D, ("w_pre",), "sigmoid", eps=eps)
+    check((rows,), D, dtype, 102 + rows + D, ("z", "w_post"), "sigmoid", eps=eps)
