@@ -299,14 +299,15 @@ norm_bwd_kernel(int64_t rows, int D, float eps, bool silu, const E* __restrict__
                 }
             row_sum<L>(q, lds, turn);
             const float rr = in ? 1.0f / sqrtf(q[0] * inv + eps) : 0.0f;
-            const float k = rr * rr * rr * q[1] * inv;
+            const float k = rr * (rr * (q[1] * inv));   // times r rr: rr^3 alone would leave fp32's range from |r| of 1e13 and 1e-13 on
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    vd[i].f[e] += rr * vh[i].f[e] * wn[i].f[e] - vx[i].f[e] * k;
-                    if constexpr (PRE_LDS) pre_lds[(i * 8 + e) * L + lane] += vh[i].f[e] * (vx[i].f[e] * rr);
-                    else a_pre[i].f[e] += vh[i].f[e] * (vx[i].f[e] * rr);
+                    const float u = vx[i].f[e] * rr;
+                    vd[i].f[e] += rr * vh[i].f[e] * wn[i].f[e] - u * k;
+                    if constexpr (PRE_LDS) pre_lds[(i * 8 + e) * L + lane] += vh[i].f[e] * u;
+                    else a_pre[i].f[e] += vh[i].f[e] * u;
                 }
         }
         if (dx)
@@ -346,13 +347,14 @@ norm_bwd_kernel(int64_t rows, int D, float eps, bool silu, const E* __restrict__
 #pragma unroll
                 for (int e = 0; e < 8; ++e) q[0] += on[i] ? vd[i].f[e] * wp[i].f[e] * vy[i].f[e] : 0.0f;
             row_sum<L>(q, lds, turn);
-            const float k = rho * rho * rho * q[0] * inv;
+            const float k = rho * (rho * (q[0] * inv));
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    a_post[i].f[e] += vd[i].f[e] * (vy[i].f[e] * rho);
-                    vd[i].f[e] = rho * vd[i].f[e] * wp[i].f[e] - vy[i].f[e] * k;
+                    const float u = vy[i].f[e] * rho;
+                    a_post[i].f[e] += vd[i].f[e] * u;
+                    vd[i].f[e] = rho * vd[i].f[e] * wp[i].f[e] - u * k;
                 }
         }
 #pragma unroll

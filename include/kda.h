@@ -405,7 +405,9 @@ int kda_gdr_step(int dtype, int B, int T, int Hk, int Hv, int dk, int dv, int ns
  *   dtype        storage of y, x, z, r, h and of their gradients
  *   act          KDA_ACT_SIGMOID: act(z) = 1/(1+e^-z);  KDA_ACT_SILU: z/(1+e^-z)
  *   rows, D      rows >= 1; D a multiple of 8 from 8 to 8192
- *   eps          in [0, 1]
+ *   eps          in [0, 1]; with 0 a row of zeros is 0 / 0, NaN.  The sum of a row's squares
+ *                is fp32: values up to 1e19 / sqrt(D) are in its range, and with eps 0 a row
+ *                of values all below 1e-19 loses digits
  *   y, x, z      [rows, D]  dtype
  *   w_post, s, w_pre   [D]  fp32
  *   r            [rows, D]  dtype, written; may be x itself

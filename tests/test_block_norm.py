@@ -371,3 +371,25 @@ def test_eps_of_zero_and_part_groups(rows, D, dtype, eps):
     check((rows,), D, dtype, 100 + rows + D, ALL, "silu", eps=eps)
     check((rows,), D, dtype, 101 + rows + D, ("w_pre",), "sigmoid", eps=eps)
     check((rows,), D, dtype, 102 + rows + D, ("z", "w_post"), "sigmoid", eps=eps)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 1000, 8192])
+@pytest.mark.parametrize("power", [-50, -43, 43, 50])
+def test_rows_of_any_scale(power, D):
+    """With eps 0 the norms do not see a row's scale.  Scaled by a power of two every step scales with it
+    exactly, while it stays in range: the same bits, times the power or over it."""
+    by = 2.0 ** power
+    a = gpu(make((7,), D, torch.float32, 120 + D, ("z", "s", "w_post", "w_pre")))
+    kw = dict(z=a["z"], s=a["s"], act="silu", eps=0.0)
+    # the norm after the block: r is the same, y's gradient over the scale
+    one, two = (kda.kda_block_norm_bwd(y, a["dr"], w_post=a["w_post"], **kw) for y in (a["y"], a["y"] * by))
+    assert torch.equal(one["dy"], two["dy"] * by)
+    for k in ("dz", "ds", "dw_post"):
+        assert torch.equal(one[k], two[k]), k
+    # the norm before the next one alone
+    h1, h2 = (kda.kda_block_norm_fwd(y, w_pre=a["w_pre"], **kw)[1] for y in (a["y"], a["y"] * by))
+    one, two = (kda.kda_block_norm_bwd(y, None, a["dh"], w_pre=a["w_pre"], **kw) for y in (a["y"], a["y"] * by))
+    assert torch.equal(h1, h2) and torch.equal(one["dy"], two["dy"] * by)
+    for k in ("dz", "ds", "dw_pre"):
+        assert torch.equal(one[k], two[k]), k
