@@ -74,9 +74,10 @@ gdr_step_kernel(int T, int Hk, int Hv, int dv, int nslot, float scale, const E* 
     f32x4 s[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) s[i] = *reinterpret_cast<const f32x4*>(Sp + (int64_t)i * dv);
-    if (slots) {   // of the rows that name one slot, the first has it; the others are padding
+    if (slots) {   // of the rows with tokens that name one slot, the first has it; the others are padding
         int twice = 0;
-        for (int i = lane; i < b; i += 64) twice |= slots[i] == slot;
+        for (int i = lane; i < b; i += 64)
+            if (slots[i] == slot) twice |= !ntok || ntok[i] > 0;
         if (__ballot(twice)) return;
     }
     const int hk = h / (Hv / Hk);

@@ -377,8 +377,8 @@ int kda_gdr_clear_rows(int nseq, int T, const int* cu_seqlens, int n, void* cons
  *   S            [nslot, Hv, dk, dv]  fp32, the rows' states read and overwritten
  *   slots        [B] int32, the state of each row, or NULL: row b has state b
  *                (nslot >= B).  A slot outside [0, nslot) marks a padded row.  Of the
- *                rows that name one slot the first has it and the others count as
- *                padded.
+ *                rows with tokens that name one slot the first has it and the others
+ *                count as padded.
  *   ntok         [B] int32, how many of a row's T tokens are real (more than T counts
  *                as T), or NULL: all.  With none the row is padded.
  *   o            [B, T, Hv, dv]  dtype, written for the real tokens of rows that are not

@@ -210,3 +210,23 @@ def test_binding_refusals(lib):
         kda.kda_gdr_step(*args, x["S"].to(torch.bfloat16))
     with pytest.raises(ValueError):
         kda.kda_gdr_step(x["q"], x["k"], x["v"], x["g"][:1], x["beta"], x["S"])
+
+
+@pytest.mark.gpu
+def test_padded_row_does_not_hold_its_slot():
+    """A row without tokens is padding and has no state: the slot that it names belongs to the first
+    row behind it that has tokens."""
+    B, T, Hk, Hv, dk, dv, P = 7, 2, 1, 2, 64, 96, 6
+    x = setup(B, T, Hk, Hv, dk, dv, torch.bfloat16, 12, P)
+    slots, ntok = [5, 5, 0, 0, 0, 3, 5], [0, 2, -1, 0, 1, 2, 1]
+    real = {1: 2, 4: 1, 5: 2}
+    o0 = torch.full((B, T, Hv, dv), 7.0).to(torch.bfloat16)
+    o, S = run(x, 0.25, slots=torch.tensor(slots, dtype=torch.int32, device=DEV),
+               ntok=torch.tensor(ntok, dtype=torch.int32, device=DEV), o=o0.to(DEV))
+    for b, n in real.items():
+        check_row(x, o, S, b, slots[b], n, 0.25, torch.bfloat16, dk)
+        assert torch.equal(o[b, n:], o0[b, n:])
+    for b in set(range(B)) - set(real):
+        assert torch.equal(o[b], o0[b]), b
+    for s in set(range(P)) - {slots[b] for b in real}:
+        assert torch.equal(S[s], x["S"][s]), s
