@@ -459,7 +459,8 @@ def kda_gdr_clear_rows(cu_seqlens, *tensors, stream=None):
 def _clear_rows(n, T, cu_seqlens, tensors, st):
     k = len(tensors)
     ptrs = (ctypes.c_void_p * k)(*[t.data_ptr() for t in tensors])
-    sizes = (ctypes.c_size_t * k)(*[t.stride(1) * t.element_size() for t in tensors])
+    # from the shape: the stride of an axis of one is not the size of its row
+    sizes = (ctypes.c_size_t * k)(*[t.numel() // max(1, T) * t.element_size() for t in tensors])
     _check("kda_gdr_clear_rows", load_library().kda_gdr_clear_rows(n, T, _at(cu_seqlens), k, ptrs, sizes, st))
 
 

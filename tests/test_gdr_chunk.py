@@ -705,3 +705,45 @@ def test_fp32_results_keep_fp32_precision(lens, Hk, Hv, dk, dv, dtype):
         if not e <= times * unit:
             off[k] = f"{e:.2e} > {times * unit:.2e}"
     assert not off, off
+
+
+def one_row_view(*shape, dtype=torch.float32, device="cpu", fill=3.0):
+    """(a contiguous view of one row [1, 1, *shape] whose row stride is five rows, the memory around it)"""
+    big = torch.full((1, 5, *shape), fill, dtype=dtype, device=device)
+    t = big[:, ::5]
+    assert t.is_contiguous() and t.shape == (1, 1, *shape) and t.stride(1) != big.stride(1)
+    return t, big
+
+
+def test_row_bytes_of_one_row_views(monkeypatch):
+    """The stride of an axis of one says nothing of a row's size: what the library is told to clear is the tensor."""
+    seen = []
+
+    class Lib:
+        @staticmethod
+        def kda_gdr_clear_rows(n, T, cu, k, ptrs, sizes, st):
+            seen.extend(sizes)
+            return 0
+
+    monkeypatch.setattr(kda, "load_library", lambda: Lib)
+    t, _ = one_row_view(4, 8)
+    none = torch.zeros(1, 1, 6).as_strided((1, 1, 6), (6, 0, 1))
+    kda._clear_rows(1, 1, torch.tensor([0, 0], dtype=torch.int32), (t, none, torch.zeros(1, 1, 2, dtype=torch.bfloat16)), None)
+    kda._clear_rows(1, 3, torch.tensor([0, 0], dtype=torch.int32), (torch.zeros(1, 3, 4, 8),), None)
+    assert seen == [128, 24, 4, 128]
+
+
+@pytest.mark.gpu
+def test_one_row_views_keep_what_is_around():
+    """Clearing, and a backward pass whose gradients are made with the inputs' strides."""
+    cu = torch.tensor([0, 0], dtype=torch.int32, device=DEV)
+    t, big = one_row_view(4, 8, device=DEV)
+    kda.kda_gdr_clear_rows(cu, t)
+    torch.cuda.synchronize()
+    assert (big[:, 0] == 0).all() and (big[:, 1:] == 3).all()
+    q, v = (one_row_view(2, 32, dtype=torch.bfloat16, device=DEV, fill=0.5)[0] for _ in range(2))
+    g = one_row_view(2, device=DEV, fill=-0.5)[0]
+    d = kda.kda_gdr_chunk_bwd(q, q, v, g, g, v, cu_seqlens=cu, scale=1.0)
+    torch.cuda.synchronize()
+    for k in ("dq", "dk", "dv", "dg", "dbeta"):
+        assert d[k].shape[:2] == (1, 1) and not d[k].any(), k
