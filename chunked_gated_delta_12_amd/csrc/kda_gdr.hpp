@@ -120,10 +120,25 @@ __device__ __forceinline__ Chunk chunk_at(const Args& a, int place, int lane) {
 
 // Segments: where a sequence has more than `over` chunks, those of more than `seg` are walked in
 // pieces of `seg` chunks, joined by their affine maps; others in one piece.  seg = 0: none is cut.
+//
+// A piece's map and start state are at its place.  Few sequences have the places of units of seg_unit
+// tokens, cut or not.  Many packed ones (`apart`: more than whole units fit the rows) would
+// leave nearly all of those empty, so the pieces of cut ones have places of their own: those of a
+// sequence that starts at row lo from 2 floor(lo / unit) on.  A cut sequence is longer than a unit, len / unit = l > 1,
+// so that 2 floor(l) >= ceil(l): its pieces end before those of the next one begin, and
+// before 2 floor(rows / unit).
 struct Segs {
     int seg, over;
+    bool apart;
 };
 __host__ __device__ inline int64_t seg_unit(const Segs& g) { return g.seg ? (int64_t)g.seg * C : (int64_t)1 << 40; }
+// Places of pieces (where sequences are cut at all), and of walks: apart, one a sequence goes before the pieces'.
+__host__ __device__ inline int64_t pieces_of(int nseq, int T, bool packed, const Segs& g) {
+    return g.apart ? 2 * (T / seg_unit(g)) : places_of(nseq, T, packed, seg_unit(g));
+}
+__host__ __device__ inline int64_t walk_places(int nseq, int T, bool packed, const Segs& g) {
+    return pieces_of(nseq, T, packed, g) + (g.apart ? nseq : 0);
+}
 
 // Whether a sequence of nch chunks is cut: the same in every kernel of a call.
 __device__ __forceinline__ bool is_cut(const Args& a, const Segs& g, int nch, int lane) {
@@ -142,21 +157,59 @@ __device__ __forceinline__ bool is_cut(const Args& a, const Segs& g, int nch, in
     return false;
 }
 
-// The piece at a place of seg_unit tokens: chunks [c0, c1) of sequence n, piece i of cnt.
+// The first place of a cut sequence's pieces.
+__device__ __forceinline__ int first_piece(const Args& a, const Segs& sg, int n) {
+    if (!sg.apart) return place_of(a, n, seg_unit(sg));
+    int lo = a.cu[n];
+    lo = lo < 0 ? 0 : lo > a.T ? a.T : lo;
+    return 2 * (lo / (sg.seg * C));
+}
+
+// Apart: the cut sequence whose pieces hold place `at`, the last one that begins there or before, and
+// which of its pieces; n < 0: none.
+__device__ __forceinline__ Unit cut_unit_at(const Args& a, const Segs& sg, int at, int lane) {
+    int n = -1;
+    bool any = false;   // is any sequence long enough for the cut?
+    for (int n0 = 0; n0 < a.nseq; n0 += 64) {
+        bool cut = false, longer = false, behind = false;
+        if (n0 + lane < a.nseq) {
+            int lo = a.cu[n0 + lane], hi = a.cu[n0 + lane + 1];
+            lo = lo < 0 ? 0 : lo > a.T ? a.T : lo;
+            hi = hi < lo ? lo : hi > a.T ? a.T : hi;
+            const int nch = (int)(((int64_t)(hi - lo) + C - 1) / C);
+            longer = nch > sg.over;
+            behind = 2 * (lo / (sg.seg * C)) > at;
+            cut = nch > sg.seg && !behind;
+        }
+        any |= __ballot(longer) != 0;
+        const uint64_t m = __ballot(cut);
+        if (m) n = n0 + 63 - __builtin_clzll(m);
+        if (any && __ballot(behind)) break;
+    }
+    if (!any || n < 0) return Unit{-1, 0};
+    return Unit{n, at - __builtin_amdgcn_readfirstlane(first_piece(a, sg, n))};
+}
+
+// The piece at a place of walk_places: chunks [c0, c1) of sequence n, piece i of cnt.
 struct Piece {
     int n, i, cnt, c0, c1;
+    int at;         // its place among the pieces, where it is one of several
     int slot;       // the sequence's first place among the chunks
     Seq s;
 };
 __device__ __forceinline__ Piece piece_at(const Args& a, const Segs& sg, int place, int lane) {
-    const Unit u = unit_at(a, place, seg_unit(sg), lane);
-    Piece p{-1, 0, 0, 0, 0, 0, Seq{0, 0}};
+    const bool whole = sg.apart && place < a.nseq;   // a place for a sequence that is not cut
+    const int at = sg.apart ? place - a.nseq : place;
+    const Unit u = whole ? Unit{place, 0} : sg.apart ? cut_unit_at(a, sg, at, lane) : unit_at(a, place, seg_unit(sg), lane);
+    Piece p{-1, 0, 0, 0, 0, 0, 0, Seq{0, 0}};
     if (u.n < 0 || u.i < 0) return p;
     p.s = seq_of(a, u.n);
     const int nch = (int)(((int64_t)p.s.len + C - 1) / C);
-    p.cnt = is_cut(a, sg, nch, lane) ? (nch + sg.seg - 1) / sg.seg : 1;
-    if (u.i >= p.cnt) return p;
+    const bool cut = is_cut(a, sg, nch, lane);
+    p.cnt = cut ? (nch + sg.seg - 1) / sg.seg : 1;
+    if (u.i >= p.cnt || (sg.apart && cut == whole)) return p;
     p.n = u.n;
+    p.at = at;
     p.i = u.i;
     p.c0 = p.cnt > 1 ? u.i * sg.seg : 0;
     p.c1 = p.cnt > 1 && u.i + 1 < p.cnt ? p.c0 + sg.seg : nch;

@@ -158,9 +158,11 @@ __device__ __forceinline__ void walk(const Args& a, const Segs& sg, const Ptrs& 
     // which read the same K and Q, are eight apart and share one XCD's L2.
     const unsigned inner = (unsigned)(a.Hv / a.Hk * nslab), grp = block / (8 * inner), in8 = block % (8 * inner);
     const unsigned outer = grp * 8 + in8 % 8, sub = in8 / 8;
-    const int place = (int)(outer / (unsigned)a.Hk), hk = (int)(outer % (unsigned)a.Hk);
+    int place = (int)(outer / (unsigned)a.Hk);
+    const int hk = (int)(outer % (unsigned)a.Hk);
     const int h = hk * (a.Hv / a.Hk) + (int)(sub / (unsigned)nslab), slab = (int)(sub % (unsigned)nslab);
     if (place >= io.places) return;
+    if ((MODE == MAP || MODE == BMAP) && sg.apart) place += a.nseq;   // a launch over the pieces alone
     const Piece pc = piece_at(a, sg, place, lane);
     if (pc.n < 0) return;
     // maps: forwards of every piece but the last one (all where both directions are joined),
@@ -186,7 +188,7 @@ __device__ __forceinline__ void walk(const Args& a, const Segs& sg, const Ptrs& 
     {
         const float* from = nullptr;
         if (MODE != MAP && MODE != BMAP) {
-            if (pc.cnt > 1) from = io.starts + ((int64_t)place * a.Hv + h) * DK * a.dv;
+            if (pc.cnt > 1) from = io.starts + ((int64_t)pc.at * a.Hv + h) * DK * a.dv;
             else if (io.init) from = io.init + ((int64_t)pc.n * a.Hv + h) * DK * a.dv;
         }
 #pragma unroll
@@ -460,7 +462,7 @@ __device__ __forceinline__ void walk(const Args& a, const Segs& sg, const Ptrs& 
     int64_t ld = a.dv;
     if (MODE == MAP || MODE == BMAP) {
         ld = ncols;
-        to = io.maps + ((int64_t)place * a.Hv + h) * DK * ld;
+        to = io.maps + ((int64_t)pc.at * a.Hv + h) * DK * ld;
     } else if (io.last && (BWD ? pc.i == 0 : pc.i + 1 == pc.cnt)) {
         to = io.last + ((int64_t)pc.n * a.Hv + h) * DK * ld;
     }
@@ -511,7 +513,7 @@ __device__ __forceinline__ void join(const Args& a, const Segs& sg, const float*
     const int n = (int)(blockIdx.x / (unsigned)nslab / (unsigned)a.Hv);
     const int nch = (int)(((int64_t)seq_of(a, n).len + C - 1) / C);
     if (!is_cut(a, sg, nch, lane)) return;
-    const int p0 = __builtin_amdgcn_readfirstlane(place_of(a, n, seg_unit(sg))), cnt = (nch + sg.seg - 1) / sg.seg;
+    const int p0 = __builtin_amdgcn_readfirstlane(first_piece(a, sg, n)), cnt = (nch + sg.seg - 1) / sg.seg;
     const int col = 16 * slab + r;
     const bool on = w < ST;
     const int t = on ? w : 0;   // wavefronts past the rows work on the first tile and store nothing
@@ -575,6 +577,11 @@ int64_t groups_of(const Args& a, int places, int cols, int slab) {
     return ((int64_t)places * a.Hk + 7) / 8 * 8 * (a.Hv / a.Hk) * ((cols + slab - 1) / slab);
 }
 
+// Places of a launch: the maps' is over the pieces alone.
+int places_for(const Args& a, const Segs& sg, bool maps) {
+    return (int)(maps ? pieces_of(a.nseq, a.T, a.cu != nullptr, sg) : walk_places(a.nseq, a.T, a.cu != nullptr, sg));
+}
+
 // Whether sequences are cut, and pieces times heads to expect.  The lengths of packed sequences
 // are not known here: as if all were equal.
 bool cut_of(const Args& a, const Segs& sg) {
@@ -598,7 +605,7 @@ hipError_t one_t(const Args& a, const Segs& sg, const Ptrs& io, int cols, hipStr
 template <typename E, int DK, int MODE>
 hipError_t one_d(const Args& a, const Segs& sg, Ptrs io, hipStream_t stream) {
     const int cols = MODE == MAP ? a.dv + DK : a.dv;
-    io.places = (int)places_of(a.nseq, a.T, a.cu != nullptr, seg_unit(sg));
+    io.places = places_for(a, sg, MODE == MAP);
     if constexpr (sizeof(E) == 2) {
         // Two column tiles a wavefront read every operand once for both, in 8 us a chunk against 4.4:
         // where workgroups of 128 columns would take a second round (65,536 tokens of 16 heads, the
@@ -622,7 +629,7 @@ hipError_t pair_t(const Args& a, const Segs& sg, const Ptrs& back, const Ptrs& f
 template <typename E, int DK, int BACKWARDS, int FORWARDS>
 hipError_t pair_d(const Args& a, const Segs& sg, Ptrs back, Ptrs forth, hipStream_t stream) {
     const int fcols = FORWARDS == MAP ? a.dv + DK : a.dv;
-    back.places = forth.places = (int)places_of(a.nseq, a.T, a.cu != nullptr, seg_unit(sg));
+    back.places = forth.places = places_for(a, sg, BACKWARDS == BMAP);
     if constexpr (sizeof(E) == 2)
         if (a.dv > 64 && wide(a, sg, (a.dv + 63) / 64 + (fcols + 63) / 64))
             return pair_t<E, DK, 8, BACKWARDS, FORWARDS>(a, sg, back, forth, fcols, stream);

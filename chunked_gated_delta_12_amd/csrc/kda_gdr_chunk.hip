@@ -49,8 +49,8 @@ Segs segs_of(int nseq, int T, int Hv, int dv, bool packed) {
     while (100 * seg * seg < 31 * longest) ++seg;
     if (seg < (work + share - 1) / share) seg = (work + share - 1) / share;
     const int64_t over = (17 * seg + 30) / 10;
-    if (longest <= over) return Segs{0, 0};
-    return Segs{(int)seg, (int)over};
+    if (longest <= over) return Segs{0, 0, false};
+    return Segs{(int)seg, (int)over, packed && nseq > T / (seg * C)};
 }
 
 // The parts of a workspace, in order; each a multiple of 16 bytes.
@@ -62,7 +62,7 @@ Plan plan_of(bool bwd, int nseq, int T, int Hv, int dk, int dv, bool packed) {
     Plan p{};
     p.sg = segs_of(nseq, T, Hv, dv, packed);
     const int64_t n = places_of(nseq, T, packed, C) * Hv;
-    const int64_t m = p.sg.seg ? places_of(nseq, T, packed, seg_unit(p.sg)) * Hv : 0;
+    const int64_t m = p.sg.seg ? pieces_of(nseq, T, packed, p.sg) * Hv : 0;
     int64_t at = 0;
     auto take = [&](int64_t& x, int64_t bytes) {
         x = at;

@@ -747,3 +747,71 @@ def test_one_row_views_keep_what_is_around():
     torch.cuda.synchronize()
     for k in ("dq", "dk", "dv", "dg", "dbeta"):
         assert d[k].shape[:2] == (1, 1) and not d[k].any(), k
+
+
+@pytest.mark.parametrize("nseq,T,Hv", [(4096, 262144, 16), (1024, 65536, 8), (8000, 65536, 4), (100000, 2000000, 1), (3, 65536, 16), (600, 9000, 2), (1, 65536, 32)])
+def test_workspace_of_many_packed_sequences(lib, nseq, T, Hv):
+    """Beside what every chunk takes, the maps and states of pieces: pieces are cut for 256 compute units, and
+    sequences that are not cut have none, however many they are.  Rows hold at most 256 / heads whole pieces, and twice
+    that many places are enough."""
+    dk = dv = 128
+    chunks = (T // 64 + nseq) * Hv
+    one, two = kda.kda_gdr_chunk_fwd_workspace_size(1, 64, 1, dk, dv), kda.kda_gdr_chunk_bwd_workspace_size(1, 64, 1, dk, dv)
+    f = kda.kda_gdr_chunk_fwd_workspace_size(nseq, T, Hv, dk, dv, True) - chunks * one
+    b = kda.kda_gdr_chunk_bwd_workspace_size(nseq, T, Hv, dk, dv, True) - chunks * two
+    assert 0 <= f <= 512 * 4 * (dk * (dv + dk) + dk * dv)
+    assert 0 <= b <= 512 * 4 * (dk * (dv + dk) + 3 * dk * dv)
+
+
+MANY = [i % 4 for i in range(400)] + [4500] + [(3 * i) % 4 for i in range(300)] + [2500, 2300, 1, 2700] + [1] * 300
+
+
+@pytest.mark.gpu
+@both
+@pytest.mark.parametrize("Hk,Hv,dk,dv", [(1, 2, 64, 64), (1, 1, 32, 96)])
+def test_cut_sequences_among_a_thousand_short_ones(Hk, Hv, dk, dv, dtype):
+    """More sequences than pieces fit the rows: three are cut, one long one is not; those and some short ones are looked at."""
+    x, cu = make(MANY, Hk, Hv, dk, dv, dtype, 95 + dv, head=3, tail=70, gmu=-5.0)
+    print(f"gdr many {Hk} {Hv} {dk} {dv} {dtype}", flush=True)
+    o, S_T = run_fwd(x, cu, 0.3)
+    g = run_bwd(x, cu, 0.3)
+    for i in (0, 3, 399, 400, 401, 699, 700, 701, 702, 703, 704, 705, 1003):
+        a = slice(cu[i], cu[i + 1])
+        y = {k: v[:, a] for k, v in x.items() if k not in ("S0", "dS_T")}
+        y["S0"], y["dS_T"] = x["S0"][i:i + 1], x["dS_T"][i:i + 1]
+        o64, S64, g64 = reference(y, [0, MANY[i]], 0.3, True)
+        near(S_T[i:i + 1], S64, torch.float32, FWD[dtype], f"S_T {i}")
+        near(g["dS0"][i:i + 1], g64["dS0"], torch.float32, 2 * FWD[dtype], f"dS0 {i}")
+        if MANY[i]:
+            near(o[:, a], o64, dtype, FWD[dtype], f"o {i}")
+            for k in ("dq", "dk", "dv", "dg", "dbeta"):
+                near(g[k][:, a], g64[k], dtype if k in ("dq", "dk", "dv") else torch.float32, 2 * FWD[dtype], f"{k} {i}")
+    S = x["S0"].to(DEV)   # and the last states written over the start states
+    d = to(x)
+    c = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    o2, _ = kda.kda_gdr_chunk_fwd(*(d[k] for k in ("q", "k", "v", "g", "beta")), S, cu_seqlens=c, S_T=S, scale=0.3)
+    assert torch.equal(o, o2) and torch.equal(S, S_T)
+
+
+@pytest.mark.gpu
+def test_many_offsets_out_of_order_touch_nothing_else():
+    """As above with so many sequences that pieces have places of their own: the tensors and a workspace of just the
+    size asked for keep the guards around them."""
+    rows, n, Hv = 9000, 600, 1
+    x, _ = make([rows], 1, Hv, 32, 32, torch.bfloat16, 96)
+    d = to(x)
+    a = [d[k] for k in ("q", "k", "v", "g", "beta")]
+    pad = torch.full((rows + 256, Hv, 32), 5.0, dtype=torch.bfloat16, device=DEV)
+    o = pad[128:128 + rows].unsqueeze(0)
+    need = kda.kda_gdr_chunk_bwd_workspace_size(n, rows, Hv, 32, 32, True)
+    mem = torch.full((need + (1 << 21),), 9, dtype=torch.uint8, device=DEV)
+    ws = mem[1 << 20:(1 << 20) + need]
+    gen = torch.Generator().manual_seed(5)
+    for cu in ([0] + [rows] * n, [0, rows] * 300 + [0], [rows] * n + [0], torch.randint(-rows, 2 * rows, (n + 1,), generator=gen).tolist(),
+               torch.randint(0, rows + 1, (n + 1,), generator=gen).tolist()):
+        c = torch.tensor(cu, dtype=torch.int32, device=DEV)
+        kda.kda_gdr_chunk_fwd(*a, cu_seqlens=c, scale=1.0, o=o, workspace=ws)
+        kda.kda_gdr_chunk_bwd(*a, d["do"], cu_seqlens=c, scale=1.0, workspace=ws)
+        torch.cuda.synchronize()
+        assert (pad[:128] == 5).all() and (pad[128 + rows:] == 5).all(), cu[:4]
+        assert (mem[:1 << 20] == 9).all() and (mem[(1 << 20) + need:] == 9).all(), cu[:4]
