@@ -431,8 +431,10 @@ int kda_gdr_step(int dtype, int B, int T, int Hk, int Hv, int dk, int dv, int ns
 static int check_gdr_chunk(int dtype, int nseq, int T, int Hk, int Hv, int dk, int dv, float scale, bool packed) {
     int st = check_gdr(dtype, nseq, T, Hk, Hv, dk, dv, scale);
     if (st) return st;
-    // a launch has at most 2^32 threads: one workgroup of 256 a chunk and head, up to eight of
-    // 512 a sequence and head
+    // A launch has at most 2^32 threads.  The preparation has 256 a chunk and head.  Two walks
+    // together have eight a column, up to 2^11 a sequence and head, and as many again for each of
+    // the pieces, of which there are 512 heads' at most (two for each of 256 compute units); a join has up to 2^14
+    // for each head of a sequence that may be cut, 256 at most.
     const int64_t slots = packed ? (int64_t)T / 64 + nseq : (int64_t)nseq * (((int64_t)T + 63) / 64);
     if (slots >= (1LL << 24) / Hv || (int64_t)nseq * Hv >= 1LL << 20)
         return fail(KDA_ERR_SHAPE, "sequences*chunks*Hv too large");

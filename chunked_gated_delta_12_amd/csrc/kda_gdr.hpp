@@ -136,6 +136,8 @@ __host__ __device__ inline int64_t seg_unit(const Segs& g) { return g.seg ? (int
 __host__ __device__ inline int64_t pieces_of(int nseq, int T, bool packed, const Segs& g) {
     return g.apart ? 2 * (T / seg_unit(g)) : places_of(nseq, T, packed, seg_unit(g));
 }
+// Sequences that a join has workgroups for: apart, of those that start in the same unit one at most is cut.
+__host__ __device__ inline int64_t joins_of(int nseq, int T, const Segs& g) { return g.apart ? T / seg_unit(g) : nseq; }
 __host__ __device__ inline int64_t walk_places(int nseq, int T, bool packed, const Segs& g) {
     return pieces_of(nseq, T, packed, g) + (g.apart ? nseq : 0);
 }

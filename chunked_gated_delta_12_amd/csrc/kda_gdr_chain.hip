@@ -510,7 +510,12 @@ __device__ __forceinline__ void join(const Args& a, const Segs& sg, const float*
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int nslab = a.dv / 16;
     const int slab = (int)(blockIdx.x % (unsigned)nslab), h = (int)(blockIdx.x / (unsigned)nslab % (unsigned)a.Hv);
-    const int n = (int)(blockIdx.x / (unsigned)nslab / (unsigned)a.Hv);
+    int n = (int)(blockIdx.x / (unsigned)nslab / (unsigned)a.Hv);
+    if (sg.apart) {   // the cut sequence whose first piece is at place 2 n
+        const Unit u = cut_unit_at(a, sg, 2 * n, lane);
+        if (u.n < 0 || u.i != 0) return;
+        n = u.n;
+    }
     const int nch = (int)(((int64_t)seq_of(a, n).len + C - 1) / C);
     if (!is_cut(a, sg, nch, lane)) return;
     const int p0 = __builtin_amdgcn_readfirstlane(first_piece(a, sg, n)), cnt = (nch + sg.seg - 1) / sg.seg;
@@ -652,7 +657,7 @@ hipError_t grads_d(bool maps, const Args& a, const Segs& sg, const Ptrs& back, c
 template <int DK>
 hipError_t join_d(const Args& a, const Segs& sg, const float* init, const float* maps, float* starts, const float* dinit,
                   const float* nmaps, float* dstarts, hipStream_t stream) {
-    const dim3 grid((unsigned)((int64_t)a.nseq * a.Hv * (a.dv / 16)), nmaps ? 2 : 1);
+    const dim3 grid((unsigned)(joins_of(a.nseq, a.T, sg) * a.Hv * (a.dv / 16)), nmaps ? 2 : 1);
     hipLaunchKernelGGL((join_kernel<DK>), grid, dim3(512), 0, stream, a, sg, init, maps, starts, dinit, nmaps, dstarts);
     return hipGetLastError();
 }

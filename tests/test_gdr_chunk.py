@@ -815,3 +815,27 @@ def test_many_offsets_out_of_order_touch_nothing_else():
         torch.cuda.synchronize()
         assert (pad[:128] == 5).all() and (pad[128 + rows:] == 5).all(), cu[:4]
         assert (mem[:1 << 20] == 9).all() and (mem[(1 << 20) + need:] == 9).all(), cu[:4]
+
+
+@pytest.mark.gpu
+def test_cut_sequence_among_half_a_million():
+    """2^19 sequences, 256 columns: joins for every sequence would be 2^32 threads; only those that may be
+    cut have any.  One holds all the rows and is cut; alone it is cut elsewhere, so both are off by the
+    tolerance at most."""
+    n, rows = 1 << 19, 64 * 30000
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    r = lambda *s, dt=torch.bfloat16: torch.randn(*s, generator=gen, device=DEV, dtype=dt)   # noqa: E731
+    q, k = (torch.nn.functional.normalize(r(1, rows, 1, 32), dim=-1) for _ in range(2))
+    v, g, beta = r(1, rows, 1, 256), -0.02 * r(1, rows, 1, dt=torch.float32).abs(), torch.sigmoid(r(1, rows, 1, dt=torch.float32))
+    cu = torch.zeros(n + 1, dtype=torch.int32, device=DEV)
+    cu[n // 2 + 7:] = rows
+    S0 = 0.2 * r(1, 1, 32, 256, dt=torch.float32)
+    states = torch.zeros(n, 1, 32, 256, device=DEV)
+    states[n // 2 + 6] = S0[0]
+    print(f"gdr {n} sequences, {rows} rows", flush=True)
+    o, S = kda.kda_gdr_chunk_fwd(q, k, v, g, beta, states, cu_seqlens=cu, scale=1.0)
+    o2, S2 = kda.kda_gdr_chunk_fwd(q, k, v, g, beta, S0, scale=1.0)
+    torch.cuda.synchronize()
+    assert torch.equal(S[:n // 2 + 6], states[:n // 2 + 6]) and torch.equal(S[n // 2 + 7:], states[n // 2 + 7:])
+    near(S[n // 2 + 6:n // 2 + 7], S2.double().cpu(), torch.float32, 2 * FWD[torch.bfloat16], "S_T")
+    near(o, o2.double().cpu(), torch.bfloat16, 2 * FWD[torch.bfloat16] + 2 * HALF_STEP[torch.bfloat16], "o")
