@@ -90,15 +90,21 @@ __device__ __forceinline__ Unit unit_at(const Args& a, int place, int64_t unit, 
     int n;
     if (!a.cu) {
         n = (int)(place / ((a.T + unit - 1) / unit));
-    } else {   // places rise with the sequence: count those that start at or before this one
-        int cnt = 0;
-        for (int n0 = 0; n0 < a.nseq; n0 += 64) {
-            const bool le = n0 + lane < a.nseq && place_of(a, n0 + lane, unit) <= place;
-            const int k = __popcll(__ballot(le));
-            cnt += k;
-            if (k < 64) break;
+    } else {
+        // Places rise with the sequence: the last that starts at or before this one, 64 evenly spaced
+        // sequences a step (two steps for 4,096; counting them all was most of a short sequence's time).
+        // With offsets out of order any of them, but one of the call's.
+        int first = 0, cnt = a.nseq;
+        for (;;) {
+            const int step = (cnt + 63) / 64, at = lane * step;
+            const int k = __popcll(__ballot(at < cnt && place_of(a, first + at, unit) <= place));
+            if (k == 0) return Unit{-1, 0};
+            first += (k - 1) * step;
+            cnt -= (k - 1) * step;
+            if (step == 1) break;
+            cnt = cnt < step ? cnt : step;
         }
-        n = cnt - 1;
+        n = first;
     }
     if (n < 0) return Unit{-1, 0};
     return Unit{n, place - __builtin_amdgcn_readfirstlane(place_of(a, n, unit))};
@@ -200,7 +206,7 @@ struct Piece {
     Seq s;
 };
 __device__ __forceinline__ Piece piece_at(const Args& a, const Segs& sg, int place, int lane) {
-    const bool whole = sg.apart && place < a.nseq;   // a place for a sequence that is not cut
+    const bool whole = !sg.seg || (sg.apart && place < a.nseq);   // a place for a sequence that is not cut
     const int at = sg.apart ? place - a.nseq : place;
     const Unit u = whole ? Unit{place, 0} : sg.apart ? cut_unit_at(a, sg, at, lane) : unit_at(a, place, seg_unit(sg), lane);
     Piece p{-1, 0, 0, 0, 0, 0, 0, Seq{0, 0}};
