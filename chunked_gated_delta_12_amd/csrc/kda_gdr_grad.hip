@@ -331,7 +331,9 @@ grad_kernel(Args a, int items, const E* __restrict__ q, const E* __restrict__ k,
             dot = 0.0f;
             lds_barrier();
             anew();
-            {
+            // Tokens' block by block from the transposed K and Q.  bf16: both blocks' operands at once, token tiles
+            // outside; fp32, where an operand is eight registers, one block after the other (the sums' order is the same).
+            if constexpr (sizeof(E) == 2) {
                 Ex kt[2], qt[2];
 #pragma unroll
                 for (int tb = 0; tb < 2; ++tb) {
@@ -353,6 +355,24 @@ grad_kernel(Args a, int items, const E* __restrict__ q, const E* __restrict__ k,
                         }
                     }
                 }
+            } else {
+                auto block = [&](int tb, const Ex& kt, const Ex& qt) {
+#pragma unroll
+                    for (int t = 0; t < TT; ++t) {
+                        const int m = m0 + t;
+                        if (tb <= m / 2) {
+                            aq[t] = A::mma(kt, A::ld_sp(xch, lower_block(m, tb), lane), aq[t]);
+                            ak[t] = A::mma(kt, A::ld_sp(xch + L::TB, lower_block(m, tb), lane), ak[t]);
+                        }
+                        if (tb >= m / 2) {
+                            ak[t] = A::mma(qt, A::ld_tri_t(xch, m, tb, g, r), ak[t]);
+                            ak[t] = A::mma(kt, A::ld_tri_t(xch + L::TB, m, tb, g, r), ak[t]);
+                        }
+                    }
+                };
+#pragma unroll
+                for (int tb = 0; tb < 2; ++tb)
+                    block(tb, A::template ld_ex_t<KB>(kl, ct / 2, ct & 1, tb, g, r), A::template ld_ex_t<KB>(ql, ct / 2, ct & 1, tb, g, r));
             }
             if (w == 0) {   // g's and beta's: lane is the token
                 float qs = 0.0f, kz = 0.0f, ke = 0.0f, ab = 0.0f, ac = 0.0f, sd = 0.0f;
