@@ -23,8 +23,8 @@
 // What bounds a walk is one chunk after another: by count, at 128 x 128, the products of the two
 // wavefronts of a SIMD take 3 us (221 matrix instructions each), their splits 1.5 and the workgroup's LDS
 // reads 2.2, and they overlap little.  Measured at 65,536 tokens of 16 heads, 128 x 128, bf16, in 16 pieces: the walk
-// with outputs 485-531 us (its memory accesses alone 277), the maps, two column tiles a wavefront,
-// 521-564 us (230).  With operands in two parts they took 340-373 and 335-367, at a
+// with outputs 450-530 us (its memory accesses alone 277), the maps, two column tiles a wavefront,
+// 480-560 us (230).  With operands in two parts they took 340-373 and 335-367, at a
 // twentieth of the precision (kda_gdr.hpp).
 #include "kda_gdr.hpp"
 #include "kda_launch.hpp"
@@ -484,7 +484,7 @@ chain_kernel(Args a, Segs sg, Ptrs io) {
 
 // Two walks in one launch, the longer one's workgroups first: the backward pass walks each way
 // once, neither needs the other, and each alone leaves compute units idle where there are
-// fewer than 256 workgroups (8 sequences of 4,096 tokens, 16 heads of 128 x 128 in bf16: 888 us together in
+// fewer than 256 workgroups (8 sequences of 4,096 tokens, 16 heads of 128 x 128 in bf16: 880-900 us together in
 // workgroups of eight wavefronts; the whole call 1,660 us, in workgroups of four 1,700).
 template <typename E, int DK, int NW, int BACKWARDS, int FORWARDS>
 __global__ void __launch_bounds__(64 * NW, NW / 4)

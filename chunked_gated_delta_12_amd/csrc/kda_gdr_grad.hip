@@ -20,7 +20,7 @@
 // last products, read there as rows of queries and, transposed, as rows of keys.
 // Memory bounds it: 192 KB of states and rows a unit at dk = dv = 128.  The next unit's loads
 // are issued before this unit's last part, as many as fit the registers.  Measured at 8 x 4,096 tokens,
-// 16 heads, dk = dv = 128: 660-680 us, 2.3 GB, 3.4 TB/s.
+// 16 heads, dk = dv = 128: 650-690 us, 2.3 GB, 3.4 TB/s.
 #include <type_traits>
 
 #include "kda_gdr.hpp"

@@ -20,8 +20,9 @@
 // exchange alone, and rows above 512 channels span wavefronts and reduce through LDS.
 // Workgroups walk over the rows with the weights in registers.
 // Measured: forwards 1,048,576 rows of 128 channels in bf16 with y, w_post and z 160 us (805 MB, 5.0
-// TB/s); backwards 16,384 rows of 2,048 channels in bf16, all parts, 120 us (537 MB, 4.5 TB/s);
-// small calls are bound by their host time, 11 us forwards and 16 us backwards.
+// TB/s); backwards 16,384 rows of 2,048 channels in bf16, all parts, 120 us (537 MB, 4.5 TB/s), but
+// 8,192 of 4,096 211 us and 4,096 of 8,192 182 us, where a row is eight and sixteen wavefronts', and
+// 16,384 of 2,056, nearly half of the lanes idle, 356 us (all 537 MB); small calls are bound by their host time, 11 us forwards and 16 us backwards.
 #include "kda_device.hpp"
 #include "kda_launch.hpp"
 
