@@ -12,7 +12,7 @@
 //
 // Precision: q, k, v and do enter the bf16 matrix cores as they are.  Every other
 // operand (X, P, S, e, Z, ...) is an fp32 value split into three bf16 parts, x = hi + mid + lo:
-// each part takes 8 bits of the 24 and more, so nothing of x is left over (2^-27 |x|), and a product is the
+// each takes 8 bits and a sign of what the one before left, so 2^-27 |x| at most is left over, and a product is the
 // sum of the parts' products down to 2^-18 of it: three matrix instructions against an exact
 // operand, six against a split one (what is left out is below 2^-26).  That is fp32's own
 // precision at 3/16 and 6/16 of the time of its matrix instructions.  Two parts (two and three
@@ -240,7 +240,7 @@ template <> struct Arith<bf16> {
     typedef bf16x8 Ex;                        // an operand that is exact in bf16
     struct Sp { bf16x8 hi, mid, lo; };        // an fp32 operand in three parts
     static constexpr int EXB = 1024;          // bytes of an exact block
-    static constexpr int SPB = 3072;          // bytes of a split one
+    static constexpr int SPB = 3 * EXB;       // bytes of a split one: three planes
     // One part of two values, and what is left of them: five instructions, a packed
     // conversion, its values back as floats, two differences (exact).
     static __device__ __forceinline__ uint32_t part2(float& a, float& b) {

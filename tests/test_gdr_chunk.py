@@ -690,7 +690,8 @@ def test_thousands_of_short_sequences_beside_a_long_one():
 def test_fp32_results_keep_fp32_precision(lens, Hk, Hv, dk, dv, dtype):
     """The last state and the gradients of g, beta and the start state are fp32 whatever the storage,
     and so is their precision, sequences cut in pieces among them; in the 2-norm, relative.  An
-    operand in three bf16 parts leaves 2^-27 of itself and its products leave out 2^-26, less than the
+    operand in three bf16 parts leaves 2^-27 of itself and its products leave out 2^-26 (the bounds at the top
+    of this file allow for two parts), less than the
     accumulators' rounding of 2^-24.  Eight products one behind another, each a sum of at most 128 terms with one
     rounding a term, their signs independent: sqrt(8 * 128) * 2^-24 / sqrt(3) = 1.1e-6.  dS0 runs through both chains:
     sqrt(2) times that.  dg and dbeta are differences of sums twice their size besides: 2 sqrt(2) times."""
