@@ -21,6 +21,17 @@ Beside KDA, the gated delta rule with one decay a head, and the norms around a b
     o      = kda_gdr_step(q, k, v, g, beta, S, slots=slots)  # S updated in place
     r, h   = kda_block_norm_fwd(y, x=x, z=z, w_post=w_post, s=s, w_pre=w_pre)
     grads  = kda_block_norm_bwd(y, dr, dh, x=x, z=z, w_post=w_post, s=s, w_pre=w_pre)
+
+and the operators of a state-space block:
+
+    y, S_T = kda_short_conv_fwd(x, w, S0, bias=bias, act="silu", cu_seqlens=cu_seqlens)
+    grads  = kda_short_conv_bwd(x, w, dy, S0, dS_T, bias=bias, act="silu", cu_seqlens=cu_seqlens)
+    y      = kda_short_conv_step(x, w, S, bias=bias, act="silu", slots=slots)  # S updated in place
+    y, S_T = kda_sel_scan_fwd(x, dt, A, b, c, S0, skip=skip, z=z, dt_bias=dt_bias, cu_seqlens=cu_seqlens)
+    grads  = kda_sel_scan_bwd(x, dt, A, b, c, dy, S0, dS_T, skip=skip, z=z, dt_bias=dt_bias, cu_seqlens=cu_seqlens)
+    y      = kda_sel_scan_step(x, dt, A, b, c, S, skip=skip, z=z, dt_bias=dt_bias, slots=slots)
+    r, h   = kda_layer_norm_fwd(y, x=x, w=w, b=b)
+    grads  = kda_layer_norm_bwd(y, dh, dr, x=x, w=w)
 """
 from __future__ import annotations
 
@@ -36,6 +47,7 @@ HEADER_PATH = os.path.join(_HERE, "..", "include", "kda.h")
 
 KDA_BF16, KDA_F32 = 0, 1
 KDA_ACT_SIGMOID, KDA_ACT_SILU = 0, 1
+KDA_CONV_LINEAR, KDA_CONV_SILU = 0, 1
 KDA_CHUNK = 16
 KDA_G_MIN = -5.0
 
@@ -104,6 +116,18 @@ def load_library(path: str = LIB_PATH):
     lib.kda_block_norm_bwd.restype = c_int
     lib.kda_block_norm_bwd_workspace_size.argtypes = [ctypes.c_longlong, c_int, ctypes.POINTER(c_size)]
     lib.kda_block_norm_bwd_workspace_size.restype = c_int
+    ll, f32 = ctypes.c_longlong, ctypes.c_float
+    for name, args in (("sel_scan_fwd", [c_int] * 7 + [vp] * 13 + [c_size, vp]), ("sel_scan_bwd", [c_int] * 7 + [vp] * 22 + [c_size, vp]),
+                       ("sel_scan_fwd_workspace_size", [c_int] * 6 + [ctypes.POINTER(c_size)]),
+                       ("sel_scan_bwd_workspace_size", [c_int] * 6 + [ctypes.POINTER(c_size)]),
+                       ("sel_scan_step", [c_int] * 8 + [vp] * 13), ("short_conv_fwd", [c_int] * 6 + [vp] * 8),
+                       ("short_conv_bwd", [c_int] * 6 + [vp] * 12 + [c_size, vp]),
+                       ("short_conv_bwd_workspace_size", [ll, c_int, c_int, ctypes.POINTER(c_size)]),
+                       ("short_conv_step", [c_int] * 7 + [vp] * 8), ("layer_norm_fwd", [c_int, ll, c_int, f32] + [vp] * 7),
+                       ("layer_norm_bwd", [c_int, ll, c_int, f32] + [vp] * 9 + [c_size, vp]),
+                       ("layer_norm_bwd_workspace_size", [ll, c_int, ctypes.POINTER(c_size)])):
+        fn = getattr(lib, "kda_" + name)
+        fn.argtypes, fn.restype = args, c_int
     _lib = lib
     return lib
 
@@ -628,7 +652,279 @@ def kda_block_norm_bwd(y, dr, dh=None, *, x=None, z=None, w_post=None, s=None, w
     return d
 
 
-__all__ = ["kda_gdr_chunk_fwd", "kda_gdr_chunk_bwd", "kda_gdr_chunk_fwd_workspace_size",
+# ----------------------------------------------------------------------------- the operators of a state-space block
+def _size(fn, *args) -> int:
+    n = ctypes.c_size_t(0)
+    _check(fn, getattr(load_library(), fn)(*args, ctypes.byref(n)))
+    return int(n.value)
+
+
+def _bytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _made(t, name, dtype, shape, device, make=torch.empty):
+    """The caller's output, checked, or a new one."""
+    if t is None:
+        return make(shape, dtype=dtype, device=device)
+    _need(t, name, dtype, shape, device)
+    return t
+
+
+def _pool(S, n, dtype, tail, slots, ntok, B, device):
+    nslot = _dims(S, "S", n)[0]
+    _need(S, "S", dtype, (nslot,) + tail, device)
+    for name, t in (("slots", slots), ("ntok", ntok)):
+        if t is not None:
+            _need(t, name, torch.int32, (B,), device)
+    return nslot
+
+
+def _scan_inputs(x, dt, A, b, c, skip, z, dt_bias):
+    B, T, D = _dims(x, "x", 3)
+    G, N = _dims(b, "b", 4)[2:]
+    dev, ty = x.device, x.dtype
+    code = _dtype_code(x)
+    for name, t in (("x", x), ("dt", dt), ("z", z)):
+        if t is not None or name == "dt":
+            _need(t, name, ty, (B, T, D), dev)
+    _need(A, "A", torch.float32, (D, N), dev)
+    _need(b, "b", ty, (B, T, G, N), dev)
+    _need(c, "c", ty, (B, T, G, N), dev)
+    for name, t in (("skip", skip), ("dt_bias", dt_bias)):
+        if t is not None:
+            _need(t, name, torch.float32, (D,), dev)
+    return code, B, T, D, N, G
+
+
+def kda_sel_scan_fwd_workspace_size(nseq, T, D, N, G, packed=False) -> int:
+    return _size("kda_sel_scan_fwd_workspace_size", nseq, T, D, N, G, int(packed))
+
+
+def kda_sel_scan_bwd_workspace_size(nseq, T, D, N, G, packed=False) -> int:
+    return _size("kda_sel_scan_bwd_workspace_size", nseq, T, D, N, G, int(packed))
+
+
+def kda_sel_scan_fwd(x, dt, A, b, c, S0=None, *, skip=None, z=None, dt_bias=None, softplus=True, cu_seqlens=None, y=None, S_T=None,
+                     want_state=True, workspace=None, stream=None):
+    """The selective scan over whole sequences.  x, dt, z [B,T,D], b, c [B,T,G,N] (bf16 or fp32), A
+    [D,N], skip, dt_bias [D] fp32, S0 [n,D,N] fp32 or None; n = B, or with cu_seqlens [n+1] int32
+    (then B = 1) the packed sequences.  The step size is softplus(dt + dt_bias), or dt + dt_bias.
+    Returns (y, S_T); S_T is None when want_state is False.  Rows of no sequence are left as they
+    were in y (zero where y is made here)."""
+    lib = load_library()
+    code, B, T, D, N, G = _scan_inputs(x, dt, A, b, c, skip, z, dt_bias)
+    dev = x.device
+    nseq, T = _gdr_sequences(B, T, cu_seqlens, dev)
+    if S0 is not None:
+        _need(S0, "S0", torch.float32, (nseq, D, N), dev)
+    _check_workspace(workspace, dev)
+    with _On(x, stream) as st:
+        made = y is None
+        y = _made(y, "y", x.dtype, (B, x.shape[1], D), dev)
+        if S_T is not None or want_state:
+            S_T = _made(S_T, "S_T", torch.float32, (nseq, D, N), dev)
+        if workspace is None:
+            nbytes = kda_sel_scan_fwd_workspace_size(nseq, T, D, N, G, cu_seqlens is not None)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        if made and cu_seqlens is not None:
+            _clear_rows(nseq, T, cu_seqlens, (y,), st)
+        _check("kda_sel_scan_fwd",
+               lib.kda_sel_scan_fwd(code, nseq, T, D, N, G, int(softplus), _at(cu_seqlens), _at(x), _at(dt), _at(A), _at(b), _at(c),
+                                    _at(skip), _at(z), _at(dt_bias), _at(S0), _at(y), _at(S_T), _at(workspace), _bytes(workspace), st))
+    return y, S_T
+
+
+def kda_sel_scan_bwd(x, dt, A, b, c, dy, S0=None, dS_T=None, *, skip=None, z=None, dt_bias=None, softplus=True, cu_seqlens=None,
+                     want_dS0=True, workspace=None, stream=None):
+    """Backward of kda_sel_scan_fwd for L = sum <dy, y> + <dS_T, S_T>, from its inputs alone.
+    Returns a dict of dx, ddt, dz, db, dc (x's dtype), dA, dskip, ddt_bias and dS0 (fp32); None for
+    parts that were not given, and for dS0 unless want_dS0.  The gradients of rows of no sequence are zero."""
+    lib = load_library()
+    code, B, T, D, N, G = _scan_inputs(x, dt, A, b, c, skip, z, dt_bias)
+    dev = x.device
+    nseq, T = _gdr_sequences(B, T, cu_seqlens, dev)
+    _need(dy, "dy", x.dtype, x.shape, dev)
+    for name, t in (("S0", S0), ("dS_T", dS_T)):
+        if t is not None:
+            _need(t, name, torch.float32, (nseq, D, N), dev)
+    _check_workspace(workspace, dev)
+    with _On(x, stream) as st:
+        d = {name: None if t is None else torch.empty_like(t)
+             for name, t in (("dx", x), ("ddt", dt), ("dA", A), ("db", b), ("dc", c), ("dskip", skip), ("dz", z), ("ddt_bias", dt_bias))}
+        d["dS0"] = torch.empty((nseq, D, N), dtype=torch.float32, device=dev) if want_dS0 else None
+        if workspace is None:
+            workspace = torch.empty(kda_sel_scan_bwd_workspace_size(nseq, T, D, N, G, cu_seqlens is not None), dtype=torch.uint8, device=dev)
+        if cu_seqlens is not None:
+            _clear_rows(nseq, T, cu_seqlens, [d[name] for name in ("dx", "ddt", "db", "dc", "dz") if d[name] is not None], st)
+        _check("kda_sel_scan_bwd",
+               lib.kda_sel_scan_bwd(code, nseq, T, D, N, G, int(softplus), _at(cu_seqlens), _at(x), _at(dt), _at(A), _at(b), _at(c),
+                                    _at(skip), _at(z), _at(dt_bias), _at(S0), _at(dy), _at(dS_T), _at(d["dx"]), _at(d["ddt"]),
+                                    _at(d["dA"]), _at(d["db"]), _at(d["dc"]), _at(d["dskip"]), _at(d["dz"]), _at(d["ddt_bias"]),
+                                    _at(d["dS0"]), _at(workspace), _bytes(workspace), st))
+    return d
+
+
+def kda_sel_scan_step(x, dt, A, b, c, S, *, skip=None, z=None, dt_bias=None, softplus=True, slots=None, ntok=None, y=None, stream=None):
+    """T tokens of the selective scan for each of B rows, the states in a pool S [nslot,D,N] fp32
+    updated in place.  x, dt, z [B,T,D], b, c [B,T,G,N]; slots and ntok as kda_gdr_step.  Returns y
+    [B,T,D]; what belongs to padded rows and tokens is left as it was (zero where y is made here)."""
+    lib = load_library()
+    code, B, T, D, N, G = _scan_inputs(x, dt, A, b, c, skip, z, dt_bias)
+    nslot = _pool(S, 3, torch.float32, (D, N), slots, ntok, B, x.device)
+    with _On(x, stream) as st:
+        y = _made(y, "y", x.dtype, (B, T, D), x.device, torch.empty if slots is None and ntok is None else torch.zeros)
+        _check("kda_sel_scan_step",
+               lib.kda_sel_scan_step(code, B, T, D, N, G, nslot, int(softplus), _at(x), _at(dt), _at(A), _at(b), _at(c), _at(skip), _at(z),
+                                     _at(dt_bias), _at(S), _at(slots), _at(ntok), _at(y), st))
+    return y
+
+
+_CONV_ACTS = {None: KDA_CONV_LINEAR, "silu": KDA_CONV_SILU}
+
+
+def _conv_inputs(x, w, bias, act):
+    B, T, D = _dims(x, "x", 3)
+    W = _dims(w, "w", 2)[1]
+    if act not in _CONV_ACTS:
+        raise ValueError(f"act must be None or 'silu', got {act!r}")
+    code = _dtype_code(x)
+    _need(x, "x", x.dtype, (B, T, D), x.device)
+    _need(w, "w", torch.float32, (D, W), x.device)
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (D,), x.device)
+    return code, _CONV_ACTS[act], B, T, D, W
+
+
+def kda_short_conv_fwd(x, w, S0=None, *, bias=None, act=None, cu_seqlens=None, y=None, S_T=None, want_state=True, stream=None):
+    """The short causal convolution of every channel: y_t = act(bias + sum_j w[:, j] x_{t-W+1+j}).  x
+    [B,T,D] (bf16 or fp32), w [D,W] (W 2 to 4), bias [D] fp32, S0 [n,W-1,D] of x's dtype, the inputs
+    before the first, oldest first, or None for zero; act None or "silu"; cu_seqlens as
+    kda_gdr_chunk_fwd.  Returns (y, S_T), S_T the last W - 1 inputs (None when want_state is
+    False).  Rows of no sequence are left as they were in y (zero where y is made here)."""
+    lib = load_library()
+    code, a, B, T, D, W = _conv_inputs(x, w, bias, act)
+    dev = x.device
+    nseq, T = _gdr_sequences(B, T, cu_seqlens, dev)
+    if S0 is not None:
+        _need(S0, "S0", x.dtype, (nseq, W - 1, D), dev)
+    with _On(x, stream) as st:
+        made = y is None
+        y = _made(y, "y", x.dtype, x.shape, dev)
+        if S_T is not None or want_state:
+            S_T = _made(S_T, "S_T", x.dtype, (nseq, W - 1, D), dev)
+        if made and cu_seqlens is not None:
+            _clear_rows(nseq, T, cu_seqlens, (y,), st)
+        _check("kda_short_conv_fwd",
+               lib.kda_short_conv_fwd(code, a, nseq, T, D, W, _at(cu_seqlens), _at(x), _at(w), _at(bias), _at(S0), _at(y), _at(S_T), st))
+    return y, S_T
+
+
+def kda_short_conv_bwd_workspace_size(rows, D, W) -> int:
+    return _size("kda_short_conv_bwd_workspace_size", rows, D, W)
+
+
+def kda_short_conv_bwd(x, w, dy, S0=None, dS_T=None, *, bias=None, act=None, cu_seqlens=None, want_dS0=True, workspace=None, stream=None):
+    """Backward of kda_short_conv_fwd for L = sum <dy, y> + <dS_T, S_T>, from its inputs alone.
+    Returns a dict of dx, dS0 (x's dtype; dS0 None unless want_dS0), dw and dbias (fp32; dbias None
+    without bias).  The gradients of rows of no sequence are zero."""
+    lib = load_library()
+    code, a, B, T, D, W = _conv_inputs(x, w, bias, act)
+    dev = x.device
+    nseq, T = _gdr_sequences(B, T, cu_seqlens, dev)
+    _need(dy, "dy", x.dtype, x.shape, dev)
+    for name, t in (("S0", S0), ("dS_T", dS_T)):
+        if t is not None:
+            _need(t, name, x.dtype, (nseq, W - 1, D), dev)
+    _check_workspace(workspace, dev)
+    with _On(x, stream) as st:
+        d = {"dx": torch.empty_like(x), "dw": torch.empty_like(w), "dbias": None if bias is None else torch.empty_like(bias),
+             "dS0": torch.empty((nseq, W - 1, D), dtype=x.dtype, device=dev) if want_dS0 else None}
+        if workspace is None:
+            workspace = torch.empty(kda_short_conv_bwd_workspace_size(B * x.shape[1], D, W), dtype=torch.uint8, device=dev)
+        if cu_seqlens is not None:
+            _clear_rows(nseq, T, cu_seqlens, (d["dx"],), st)
+        _check("kda_short_conv_bwd",
+               lib.kda_short_conv_bwd(code, a, nseq, T, D, W, _at(cu_seqlens), _at(x), _at(w), _at(bias), _at(S0), _at(dy), _at(dS_T),
+                                      _at(d["dx"]), _at(d["dw"]), _at(d["dbias"]), _at(d["dS0"]), _at(workspace), _bytes(workspace), st))
+    return d
+
+
+def kda_short_conv_step(x, w, S, *, bias=None, act=None, slots=None, ntok=None, y=None, stream=None):
+    """T tokens of the short convolution for each of B rows, the states in a pool S [nslot,W-1,D]
+    of x's dtype updated in place.  x [B,T,D]; slots and ntok as kda_gdr_step.  Returns y [B,T,D];
+    what belongs to padded rows and tokens is left as it was (zero where y is made here)."""
+    lib = load_library()
+    code, a, B, T, D, W = _conv_inputs(x, w, bias, act)
+    nslot = _pool(S, 3, x.dtype, (W - 1, D), slots, ntok, B, x.device)
+    with _On(x, stream) as st:
+        y = _made(y, "y", x.dtype, (B, T, D), x.device, torch.empty if slots is None and ntok is None else torch.zeros)
+        _check("kda_short_conv_step",
+               lib.kda_short_conv_step(code, a, B, T, D, W, nslot, _at(x), _at(w), _at(bias), _at(S), _at(slots), _at(ntok), _at(y), st))
+    return y
+
+
+# ----------------------------------------------------------------------------- layer norm
+def _layer_norm_inputs(y, x, w, b):
+    if not isinstance(y, torch.Tensor) or y.dim() < 1:
+        raise TypeError("y must be a torch.Tensor with at least one dimension")
+    code = _dtype_code(y)
+    D = y.shape[-1]
+    for name, t in (("y", y), ("x", x)):
+        if t is not None:
+            _need(t, name, y.dtype, y.shape, y.device)
+    for name, t in (("w", w), ("b", b)):
+        if t is not None:
+            _need(t, name, torch.float32, (D,), y.device)
+    return code, y.numel() // max(1, D), D
+
+
+def kda_layer_norm_fwd(y, *, x=None, w=None, b=None, eps=1e-5, r=None, h=None, stream=None):
+    """The layer norm behind a residual sum: r = x + y and h = (r - mean) / sqrt(var + eps) w + b over
+    the last dimension.  y, x [..., D] (bf16 or fp32), w, b [D] fp32, every part but y optional.
+    r may be x itself.  Returns (r, h); r is None without x."""
+    lib = load_library()
+    code, rows, D = _layer_norm_inputs(y, x, w, b)
+    if r is not None and x is None:
+        raise ValueError("r without x")
+    with _On(y, stream) as st:
+        r = None if x is None else _made(r, "r", y.dtype, y.shape, y.device)
+        h = _made(h, "h", y.dtype, y.shape, y.device)
+        _check("kda_layer_norm_fwd", lib.kda_layer_norm_fwd(code, rows, D, eps, _at(y), _at(x), _at(w), _at(b), _at(r), _at(h), st))
+    return r, h
+
+
+def kda_layer_norm_bwd_workspace_size(rows, D) -> int:
+    return _size("kda_layer_norm_bwd_workspace_size", rows, D)
+
+
+def kda_layer_norm_bwd(y, dh, dr=None, *, x=None, w=None, want_db=True, eps=1e-5, workspace=None, stream=None):
+    """Backward of kda_layer_norm_fwd for L = sum <dr, r> + <dh, h>, from its inputs alone (dr goes
+    with x and may be None).  Returns a dict of dy (y's dtype; x has the same gradient), dw (fp32;
+    None without w) and db (fp32; None unless want_db)."""
+    lib = load_library()
+    code, rows, D = _layer_norm_inputs(y, x, w, None)
+    for name, t in (("dh", dh), ("dr", dr)):
+        if t is not None or name == "dh":
+            _need(t, name, y.dtype, y.shape, y.device)
+    if dr is not None and x is None:
+        raise ValueError("dr without x")
+    _check_workspace(workspace, y.device)
+    with _On(y, stream) as st:
+        d = {"dy": torch.empty_like(y), "dw": None if w is None else torch.empty_like(w),
+             "db": torch.empty(D, dtype=torch.float32, device=y.device) if want_db else None}
+        if workspace is None and (w is not None or want_db):
+            workspace = torch.empty(kda_layer_norm_bwd_workspace_size(rows, D), dtype=torch.uint8, device=y.device)
+        _check("kda_layer_norm_bwd",
+               lib.kda_layer_norm_bwd(code, rows, D, eps, _at(y), _at(x), _at(w), _at(dr), _at(dh), _at(d["dy"]), _at(d["dw"]), _at(d["db"]),
+                                      _at(workspace), _bytes(workspace), st))
+    return d
+
+
+__all__ = ["kda_sel_scan_fwd", "kda_sel_scan_bwd", "kda_sel_scan_step", "kda_sel_scan_fwd_workspace_size", "kda_sel_scan_bwd_workspace_size",
+           "kda_short_conv_fwd", "kda_short_conv_bwd", "kda_short_conv_step", "kda_short_conv_bwd_workspace_size", "kda_layer_norm_fwd",
+           "kda_layer_norm_bwd", "kda_layer_norm_bwd_workspace_size", "KDA_CONV_LINEAR", "KDA_CONV_SILU",
+           "kda_gdr_chunk_fwd", "kda_gdr_chunk_bwd", "kda_gdr_chunk_fwd_workspace_size",
            "kda_gdr_chunk_bwd_workspace_size", "kda_gdr_clear_rows", "kda_gdr_step", "kda_block_norm_fwd", "kda_block_norm_bwd", "kda_block_norm_bwd_workspace_size",
            "KDA_ACT_SIGMOID", "KDA_ACT_SILU", "kda_chunk_fwd", "kda_chunk_fwd_noalloc", "kda_chunk_fwd_gated", "kda_chunk_fwd_unbounded", "kda_chunk_bwd",
            "kda_chunk_bwd_workspace_size", "kda_decode_step",

@@ -23,10 +23,10 @@ LIB = os.path.join(HERE, "libkda.so")
 PEAKS_LIB = os.path.join(HERE, "libkda_peaks.so")
 PEAKS_SOURCES = ["kda_peaks.hip"]
 SOURCES = ["kda_api.cpp", "kda_gate.hip", "kda_decode.hip", "kda_chunk.hip", "kda_map.hip", "kda_out.hip", "kda_bwd.hip", "kda_bwd2.hip", "kda_gmap.hip"]
-# the operators beside KDA (the gated delta rule with one decay a head, the block norm),
-# linked into libkda.so with the sources above
+# the operators beside KDA (the gated delta rule with one decay a head, the norms, the
+# selective scan, the short convolution), linked into libkda.so with the sources above
 MORE_SOURCES = ["kda_gdr_step.hip", "kda_gdr_chunk.hip", "kda_gdr_prep.hip", "kda_gdr_chain.hip", "kda_gdr_grad.hip",
-                "kda_norm.hip"]
+                "kda_norm.hip", "kda_layer_norm.hip", "kda_conv.hip", "kda_scan_fwd.hip", "kda_scan_bwd.hip", "kda_scan_step.hip"]
 ARCH = "gfx950"
 
 

@@ -594,4 +594,256 @@ int kda_block_norm_bwd(int dtype, int act, long long rows, int D, float eps, con
     return ok();
 }
 
+// ---------------------------------------------------------------- selective scan
+static int check_scan(int dtype, int a, int T, int D, int N, int G, int softplus) {
+    if (dtype != KDA_BF16 && dtype != KDA_F32) return fail(KDA_ERR_DTYPE, "unknown dtype %d", dtype);
+    if (a < 1 || T < 1) return fail(KDA_ERR_SHAPE, "sequences=%d T=%d must be >= 1", a, T);
+    if (T > 1 << 30) return fail(KDA_ERR_SHAPE, "T=%d above 2^30", T);
+    if (G < 1 || D < 8 || D > 1 << 20 || D % G || D / G % 8)
+        return fail(KDA_ERR_SHAPE, "D=%d, G=%d: D must be at most 2^20 and D / G a multiple of 8", D, G);
+    if (N != 8 && N != 16 && N != 32 && N != 64) return fail(KDA_ERR_SHAPE, "N=%d not in {8, 16, 32, 64}", N);
+    if (softplus != 0 && softplus != 1) return fail(KDA_ERR_SHAPE, "softplus=%d must be 0 or 1", softplus);
+    if (!sizes_fit(a, T, D, N)) return fail(KDA_ERR_SHAPE, "sequences*T*D*N too large");
+    return KDA_OK;
+}
+
+// A launch has at most 2^32 threads, 256 a workgroup.
+static int check_workgroups(int64_t n) {
+    if (n >= 1LL << 24) return fail(KDA_ERR_SHAPE, "sequences, T and D need %lld workgroups: 2^24 is too many", (long long)n);
+    return KDA_OK;
+}
+
+static int scan_workspace_size(bool bwd, int nseq, int T, int D, int N, int G, int packed, size_t* bytes) {
+    if (!bytes) return fail(KDA_ERR_NULL, "bytes is NULL");
+    int st = check_scan(KDA_BF16, nseq, T, D, N, G, 1);
+    if (st) return st;
+    if ((st = check_workgroups(bwd ? kda::scan_bwd_workgroups(nseq, T, D, G, packed != 0)
+                                   : kda::scan_fwd_workgroups(nseq, T, D, G, packed != 0))))
+        return st;
+    *bytes = bwd ? kda::scan_bwd_workspace_bytes(nseq, T, D, N, G, packed != 0)
+                 : kda::scan_fwd_workspace_bytes(nseq, T, D, N, G, packed != 0);
+    return ok();
+}
+
+int kda_sel_scan_fwd_workspace_size(int nseq, int T, int D, int N, int G, int packed, size_t* bytes) {
+    return scan_workspace_size(false, nseq, T, D, N, G, packed, bytes);
+}
+
+int kda_sel_scan_bwd_workspace_size(int nseq, int T, int D, int N, int G, int packed, size_t* bytes) {
+    return scan_workspace_size(true, nseq, T, D, N, G, packed, bytes);
+}
+
+int kda_sel_scan_fwd(int dtype, int nseq, int T, int D, int N, int G, int softplus, const int* cu_seqlens, const void* x,
+                     const void* dt, const float* A, const void* b, const void* c, const float* skip, const void* z,
+                     const float* dt_bias, const float* S0, void* y, float* S_T, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+    int st = check_scan(dtype, nseq, T, D, N, G, softplus);
+    if (st) return st;
+    const bool packed = cu_seqlens != nullptr;
+    if ((st = check_workgroups(kda::scan_fwd_workgroups(nseq, T, D, G, packed)))) return st;
+    if (!x || !dt || !A || !b || !c || !y) return fail(KDA_ERR_NULL, "x, dt, A, b, c and y must be non-NULL");
+    const size_t need = kda::scan_fwd_workspace_bytes(nseq, T, D, N, G, packed);
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(KDA_ERR_WORKSPACE, "workspace of %zu bytes needed, got %zu%s", need, workspace_bytes,
+                    workspace ? "" : " (NULL)");
+    const size_t es = dtype == KDA_BF16 ? 2 : 4, tok = packed ? (size_t)T : (size_t)nseq * T;
+    const size_t nx = tok * D * es, nb = tok * G * N * es, nd = (size_t)D * 4, ns = (size_t)nseq * D * N * 4;
+    const Range in[] = {rng("x", x, nx), rng("dt", dt, nx), rng("A", A, nd * N), rng("b", b, nb), rng("c", c, nb),
+                        rng("skip", skip, nd), rng("z", z, nx), rng("dt_bias", dt_bias, nd),
+                        rng("cu_seqlens", cu_seqlens, ((size_t)nseq + 1) * 4), rng("S0", S0 == S_T ? nullptr : S0, ns)};
+    const Range out[] = {rng("y", y, nx), rng("S_T", S_T, ns), rng("workspace", need ? workspace : nullptr, need)};
+    if ((st = check_ranges(in, 10, out, 3))) return st;
+    const kda::ScanCall call{dtype == KDA_F32, nseq, T, D, N, G, softplus != 0, cu_seqlens, x, dt, b, c, z, A, skip, dt_bias, S0};
+    hipError_t e = kda::launch_scan_fwd(call, y, S_T, need ? workspace : nullptr, reinterpret_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(KDA_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
+int kda_sel_scan_bwd(int dtype, int nseq, int T, int D, int N, int G, int softplus, const int* cu_seqlens, const void* x,
+                     const void* dt, const float* A, const void* b, const void* c, const float* skip, const void* z,
+                     const float* dt_bias, const float* S0, const void* dy, const float* dS_T, void* dx, void* ddt, float* dA,
+                     void* db, void* dc, float* dskip, void* dz, float* ddt_bias, float* dS0, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+    int st = check_scan(dtype, nseq, T, D, N, G, softplus);
+    if (st) return st;
+    const bool packed = cu_seqlens != nullptr;
+    if ((st = check_workgroups(kda::scan_bwd_workgroups(nseq, T, D, G, packed)))) return st;
+    if (!x || !dt || !A || !b || !c || !dy || !dx || !ddt || !dA || !db || !dc)
+        return fail(KDA_ERR_NULL, "x, dt, A, b, c, dy, dx, ddt, dA, db and dc must be non-NULL");
+    if (!z != !dz || (dskip && !skip) || (ddt_bias && !dt_bias))
+        return fail(KDA_ERR_NULL, "z and dz go together, and dskip and ddt_bias need skip and dt_bias");
+    const size_t need = kda::scan_bwd_workspace_bytes(nseq, T, D, N, G, packed);
+    if (!workspace || workspace_bytes < need)
+        return fail(KDA_ERR_WORKSPACE, "workspace of %zu bytes needed, got %zu%s", need, workspace_bytes,
+                    workspace ? "" : " (NULL)");
+    const size_t es = dtype == KDA_BF16 ? 2 : 4, tok = packed ? (size_t)T : (size_t)nseq * T;
+    const size_t nx = tok * D * es, nb = tok * G * N * es, nd = (size_t)D * 4, ns = (size_t)nseq * D * N * 4;
+    const Range in[] = {rng("x", x, nx), rng("dt", dt, nx), rng("A", A, nd * N), rng("b", b, nb), rng("c", c, nb),
+                        rng("skip", skip, nd), rng("z", z, nx), rng("dt_bias", dt_bias, nd),
+                        rng("cu_seqlens", cu_seqlens, ((size_t)nseq + 1) * 4), rng("S0", S0, ns), rng("dy", dy, nx),
+                        rng("dS_T", dS_T, ns)};
+    const Range out[] = {rng("dx", dx, nx), rng("ddt", ddt, nx), rng("dA", dA, nd * N), rng("db", db, nb), rng("dc", dc, nb),
+                         rng("dskip", dskip, nd), rng("dz", dz, nx), rng("ddt_bias", ddt_bias, nd), rng("dS0", dS0, ns),
+                         rng("workspace", workspace, need)};
+    if ((st = check_ranges(in, 12, out, 10))) return st;
+    const kda::ScanCall call{dtype == KDA_F32, nseq, T, D, N, G, softplus != 0, cu_seqlens, x, dt, b, c, z, A, skip, dt_bias, S0};
+    hipError_t e = kda::launch_scan_bwd(call, dy, dS_T, dx, ddt, dA, db, dc, dskip, dz, ddt_bias, dS0, workspace,
+                                        reinterpret_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(KDA_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
+int kda_sel_scan_step(int dtype, int B, int T, int D, int N, int G, int nslot, int softplus, const void* x, const void* dt,
+                      const float* A, const void* b, const void* c, const float* skip, const void* z, const float* dt_bias,
+                      float* S, const int* slots, const int* ntok, void* y, void* stream) {
+    int st = check_scan(dtype, B, T, D, N, G, softplus);
+    if (st) return st;
+    if (nslot < 1 || (!slots && nslot < B))
+        return fail(KDA_ERR_SHAPE, "nslot=%d states for B=%d rows%s", nslot, B, slots ? "" : " without slots");
+    if (!sizes_fit(nslot, D, N, 1)) return fail(KDA_ERR_SHAPE, "nslot*D*N too large");
+    if ((st = check_workgroups(kda::scan_step_workgroups(B, D, G)))) return st;
+    if (!x || !dt || !A || !b || !c || !S || !y) return fail(KDA_ERR_NULL, "x, dt, A, b, c, S and y must be non-NULL");
+    const size_t es = dtype == KDA_BF16 ? 2 : 4, tok = (size_t)B * T;
+    const size_t nx = tok * D * es, nb = tok * G * N * es, nd = (size_t)D * 4;
+    const Range in[] = {rng("x", x, nx), rng("dt", dt, nx), rng("A", A, nd * N), rng("b", b, nb), rng("c", c, nb),
+                        rng("skip", skip, nd), rng("z", z, nx), rng("dt_bias", dt_bias, nd), rng("slots", slots, (size_t)B * 4),
+                        rng("ntok", ntok, (size_t)B * 4)};
+    const Range out[] = {rng("S", S, (size_t)nslot * nd * N), rng("y", y, nx)};
+    if ((st = check_ranges(in, 10, out, 2))) return st;
+    hipError_t e = kda::launch_scan_step(dtype == KDA_F32, B, T, D, N, G, nslot, softplus != 0, x, dt, A, b, c, skip, z, dt_bias,
+                                         S, slots, ntok, y, reinterpret_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(KDA_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
+// ---------------------------------------------------------------- short convolution
+static int check_conv(int dtype, int act, int a, int T, int D, int W) {
+    if (dtype != KDA_BF16 && dtype != KDA_F32) return fail(KDA_ERR_DTYPE, "unknown dtype %d", dtype);
+    if (act != KDA_CONV_LINEAR && act != KDA_CONV_SILU) return fail(KDA_ERR_SHAPE, "unknown act %d", act);
+    if (a < 1 || T < 1) return fail(KDA_ERR_SHAPE, "sequences=%d T=%d must be >= 1", a, T);
+    if (T > 1 << 30) return fail(KDA_ERR_SHAPE, "T=%d above 2^30", T);
+    if (D < 8 || D > 1 << 20 || D % 8) return fail(KDA_ERR_SHAPE, "D=%d must be a multiple of 8 from 8 to 2^20", D);
+    if (W < 2 || W > 4) return fail(KDA_ERR_SHAPE, "W=%d not in {2, 3, 4}", W);
+    // a launch has at most 2^32 threads: one for eight channels of eight rows at the least, and of each sequence's state
+    if (((int64_t)a * T / 8 + 2 * (int64_t)a + 1) >= (1LL << 31) / (D / 8)) return fail(KDA_ERR_SHAPE, "sequences*T*D too large");
+    return KDA_OK;
+}
+
+int kda_short_conv_fwd(int dtype, int act, int nseq, int T, int D, int W, const int* cu_seqlens, const void* x, const float* w,
+                       const float* bias, const void* S0, void* y, void* S_T, void* stream) {
+    int st = check_conv(dtype, act, cu_seqlens ? 1 : nseq, T, D, W);
+    if (st) return st;
+    if (cu_seqlens && (st = check_conv(dtype, act, nseq, 1, D, W))) return st;
+    if (!x || !w || !y) return fail(KDA_ERR_NULL, "x, w and y must be non-NULL");
+    const size_t es = dtype == KDA_BF16 ? 2 : 4, tok = cu_seqlens ? (size_t)T : (size_t)nseq * T;
+    const size_t nx = tok * D * es, ns = (size_t)nseq * (W - 1) * D * es;
+    const Range in[] = {rng("x", x, nx), rng("w", w, (size_t)D * W * 4), rng("bias", bias, (size_t)D * 4),
+                        rng("cu_seqlens", cu_seqlens, ((size_t)nseq + 1) * 4), rng("S0", S0 == S_T ? nullptr : S0, ns)};
+    const Range out[] = {rng("y", y, nx), rng("S_T", S_T, ns)};
+    if ((st = check_ranges(in, 5, out, 2))) return st;
+    const kda::ConvCall call{dtype == KDA_F32, nseq, T, D, W, act == KDA_CONV_SILU, cu_seqlens, x, S0, w, bias};
+    hipError_t e = kda::launch_conv_fwd(call, y, S_T, reinterpret_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(KDA_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
+int kda_short_conv_bwd_workspace_size(long long rows, int D, int W, size_t* bytes) {
+    if (!bytes) return fail(KDA_ERR_NULL, "bytes is NULL");
+    if (rows < 1 || rows > 1LL << 40) return fail(KDA_ERR_SHAPE, "rows=%lld outside [1, 2^40]", rows);
+    int st = check_conv(KDA_BF16, KDA_CONV_LINEAR, 1, 1, D, W);
+    if (st) return st;
+    *bytes = kda::conv_bwd_workspace_bytes(rows, D, W);
+    return ok();
+}
+
+int kda_short_conv_bwd(int dtype, int act, int nseq, int T, int D, int W, const int* cu_seqlens, const void* x, const float* w,
+                       const float* bias, const void* S0, const void* dy, const void* dS_T, void* dx, float* dw, float* dbias,
+                       void* dS0, void* workspace, size_t workspace_bytes, void* stream) {
+    int st = check_conv(dtype, act, cu_seqlens ? 1 : nseq, T, D, W);
+    if (st) return st;
+    if (cu_seqlens && (st = check_conv(dtype, act, nseq, 1, D, W))) return st;
+    if (!x || !w || !dy || !dx || !dw) return fail(KDA_ERR_NULL, "x, w, dy, dx and dw must be non-NULL");
+    if (dbias && !bias) return fail(KDA_ERR_NULL, "dbias needs bias");
+    const size_t es = dtype == KDA_BF16 ? 2 : 4, tok = cu_seqlens ? (size_t)T : (size_t)nseq * T;
+    const size_t nx = tok * D * es, ns = (size_t)nseq * (W - 1) * D * es, nw = (size_t)D * W * 4, nb = (size_t)D * 4;
+    const size_t need = kda::conv_bwd_workspace_bytes((int64_t)tok, D, W);
+    if (!workspace || workspace_bytes < need)
+        return fail(KDA_ERR_WORKSPACE, "workspace of %zu bytes needed, got %zu%s", need, workspace_bytes,
+                    workspace ? "" : " (NULL)");
+    const Range in[] = {rng("x", x, nx), rng("w", w, nw), rng("bias", bias, nb),
+                        rng("cu_seqlens", cu_seqlens, ((size_t)nseq + 1) * 4), rng("S0", S0, ns), rng("dy", dy, nx),
+                        rng("dS_T", dS_T, ns)};
+    const Range out[] = {rng("dx", dx, nx), rng("dw", dw, nw), rng("dbias", dbias, nb), rng("dS0", dS0, ns),
+                         rng("workspace", workspace, need)};
+    if ((st = check_ranges(in, 7, out, 5))) return st;
+    const kda::ConvCall call{dtype == KDA_F32, nseq, T, D, W, act == KDA_CONV_SILU, cu_seqlens, x, S0, w, bias};
+    hipError_t e = kda::launch_conv_bwd(call, dy, dS_T, dx, dw, dbias, dS0, (float*)workspace, reinterpret_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(KDA_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
+int kda_short_conv_step(int dtype, int act, int B, int T, int D, int W, int nslot, const void* x, const float* w,
+                        const float* bias, void* S, const int* slots, const int* ntok, void* y, void* stream) {
+    int st = check_conv(dtype, act, B, T, D, W);
+    if (st) return st;
+    if (nslot < 1 || (!slots && nslot < B))
+        return fail(KDA_ERR_SHAPE, "nslot=%d states for B=%d rows%s", nslot, B, slots ? "" : " without slots");
+    if ((int64_t)B * ((D / 8 + 63) / 64) >= 1LL << 26) return fail(KDA_ERR_SHAPE, "B*D too large");   // workgroups of 64 threads
+    if (!x || !w || !S || !y) return fail(KDA_ERR_NULL, "x, w, S and y must be non-NULL");
+    const size_t es = dtype == KDA_BF16 ? 2 : 4, nx = (size_t)B * T * D * es;
+    const Range in[] = {rng("x", x, nx), rng("w", w, (size_t)D * W * 4), rng("bias", bias, (size_t)D * 4),
+                        rng("slots", slots, (size_t)B * 4), rng("ntok", ntok, (size_t)B * 4)};
+    const Range out[] = {rng("S", S, (size_t)nslot * (W - 1) * D * es), rng("y", y, nx)};
+    if ((st = check_ranges(in, 5, out, 2))) return st;
+    const kda::ConvCall call{dtype == KDA_F32, B, T, D, W, act == KDA_CONV_SILU, nullptr, x, nullptr, w, bias};
+    hipError_t e = kda::launch_conv_step(call, B, nslot, S, slots, ntok, y, reinterpret_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(KDA_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
+// ---------------------------------------------------------------- layer norm
+int kda_layer_norm_fwd(int dtype, long long rows, int D, float eps, const void* y, const void* x, const float* w, const float* b,
+                       void* r, void* h, void* stream) {
+    int st = check_norm(dtype, KDA_ACT_SIGMOID, rows, D, eps);
+    if (st) return st;
+    if (!y || !h) return fail(KDA_ERR_NULL, "y and h must be non-NULL");
+    if (!x != !r) return fail(KDA_ERR_NULL, "r and x go together: both or neither may be NULL");
+    const size_t n = (size_t)rows * D * (dtype == KDA_BF16 ? 2 : 4), nw = (size_t)D * 4;
+    // r may be x itself: the residual stream updated in place
+    const Range in[] = {rng("y", y, n), rng("x", x == r ? nullptr : x, n), rng("w", w, nw), rng("b", b, nw)};
+    const Range out[] = {rng("r", r, n), rng("h", h, n)};
+    if ((st = check_ranges(in, 4, out, 2))) return st;
+    hipError_t e = kda::launch_layer_norm_fwd(dtype == KDA_F32, rows, D, eps, y, x, w, b, r, h, reinterpret_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(KDA_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
+int kda_layer_norm_bwd_workspace_size(long long rows, int D, size_t* bytes) {
+    if (!bytes) return fail(KDA_ERR_NULL, "bytes is NULL");
+    int st = check_norm(KDA_BF16, KDA_ACT_SIGMOID, rows, D, 0.0f);
+    if (st) return st;
+    *bytes = kda::layer_norm_bwd_workspace_bytes(rows, D);
+    return ok();
+}
+
+int kda_layer_norm_bwd(int dtype, long long rows, int D, float eps, const void* y, const void* x, const float* w, const void* dr,
+                       const void* dh, void* dy, float* dw, float* db, void* workspace, size_t workspace_bytes, void* stream) {
+    int st = check_norm(dtype, KDA_ACT_SIGMOID, rows, D, eps);
+    if (st) return st;
+    if (!y || !dh || !dy) return fail(KDA_ERR_NULL, "y, dh and dy must be non-NULL");
+    if (dr && !x) return fail(KDA_ERR_NULL, "dr without x: the norm alone has no residual stream");
+    const size_t n = (size_t)rows * D * (dtype == KDA_BF16 ? 2 : 4), nw = (size_t)D * 4;
+    const size_t need = dw || db ? kda::layer_norm_bwd_workspace_bytes(rows, D) : 0;
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(KDA_ERR_WORKSPACE, "workspace of %zu bytes needed, got %zu%s", need, workspace_bytes,
+                    workspace ? "" : " (NULL)");
+    const Range in[] = {rng("y", y, n), rng("x", x, n), rng("w", w, nw), rng("dr", dr, n), rng("dh", dh, n)};
+    const Range out[] = {rng("dy", dy, n), rng("dw", dw, nw), rng("db", db, nw), rng("workspace", need ? workspace : nullptr, need)};
+    if ((st = check_ranges(in, 5, out, 4))) return st;
+    hipError_t e = kda::launch_layer_norm_bwd(dtype == KDA_F32, rows, D, eps, y, x, w, dr, dh, dy, dw, db, (float*)workspace,
+                                              reinterpret_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(KDA_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
+    return ok();
+}
+
 }  // extern "C"

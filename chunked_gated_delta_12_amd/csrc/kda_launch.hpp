@@ -150,4 +150,52 @@ hipError_t launch_norm_bwd(bool f32, int64_t rows, int D, float eps, bool silu, 
                            const void* dh, void* dy, void* dx, void* dz, float* dw_post, float* ds, float* dw_pre,
                            float* part, hipStream_t stream);
 
+// The selective scan (kda_scan.hpp): over sequences of T tokens each (cu NULL) or packed into T
+// rows; skip, z, bias and S0 may be NULL.  The workgroup counts bound a launch's threads.
+struct ScanCall {
+    bool f32;
+    int nseq, T, D, N, G;
+    bool softplus;
+    const int* cu;
+    const void *x, *dt, *b, *c, *z;
+    const float *A, *skip, *bias, *S0;
+};
+int64_t scan_fwd_workgroups(int nseq, int T, int D, int G, bool packed);
+int64_t scan_bwd_workgroups(int nseq, int T, int D, int G, bool packed);
+int64_t scan_step_workgroups(int B, int D, int G);
+size_t scan_fwd_workspace_bytes(int nseq, int T, int D, int N, int G, bool packed);
+size_t scan_bwd_workspace_bytes(int nseq, int T, int D, int N, int G, bool packed);
+hipError_t launch_scan_fwd(const ScanCall& c, void* y, float* S_T, void* workspace, hipStream_t stream);
+hipError_t launch_scan_bwd(const ScanCall& c, const void* dy, const float* dS_T, void* dx, void* ddt, float* dA, void* db,
+                           void* dc, float* dskip, void* dz, float* dbias, float* dS0, void* workspace,
+                           hipStream_t stream);
+hipError_t launch_scan_step(bool f32, int B, int T, int D, int N, int G, int nslot, bool softplus, const void* x,
+                            const void* dt, const float* A, const void* b, const void* c, const float* skip,
+                            const void* z, const float* bias, float* S, const int* slots, const int* ntok, void* y,
+                            hipStream_t stream);
+
+// The short convolution (kda_conv.hip), sequences as above; bias and S0 may be NULL.
+struct ConvCall {
+    bool f32;
+    int nseq, T, D, W;
+    bool silu;
+    const int* cu;
+    const void *x, *S0;
+    const float *w, *bias;
+};
+hipError_t launch_conv_fwd(const ConvCall& c, void* y, void* S_T, hipStream_t stream);
+size_t conv_bwd_workspace_bytes(int64_t rows, int D, int W);
+hipError_t launch_conv_bwd(const ConvCall& c, const void* dy, const void* dS_T, void* dx, float* dw, float* dbias, void* dS0,
+                           float* part, hipStream_t stream);
+hipError_t launch_conv_step(const ConvCall& c, int B, int nslot, void* S, const int* slots, const int* ntok, void* y,
+                            hipStream_t stream);
+
+// The layer norm and its backward (kda_layer_norm.hip): x, w, b, r, dr, dw and db may be NULL.
+hipError_t launch_layer_norm_fwd(bool f32, int64_t rows, int D, float eps, const void* y, const void* x, const float* w,
+                                 const float* b, void* r, void* h, hipStream_t stream);
+size_t layer_norm_bwd_workspace_bytes(int64_t rows, int D);
+hipError_t launch_layer_norm_bwd(bool f32, int64_t rows, int D, float eps, const void* y, const void* x, const float* w,
+                                 const void* dr, const void* dh, void* dy, float* dw, float* db, float* part,
+                                 hipStream_t stream);
+
 }  // namespace kda

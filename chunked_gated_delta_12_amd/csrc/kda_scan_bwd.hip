@@ -1,0 +1,508 @@
+// kda_scan_bwd.hip -- the backward pass of the selective scan (kda_scan.hpp has the forward's
+// formulas and how lanes and pieces are laid out).
+//
+// With dy' = dy silu(z), a_t,n = exp(delta_t A_n), and from the last token to the first, mu
+// starting as the last state's gradient:
+//     lam_n  = c_t,n dy'_t + mu_n                       gradient of h_t
+//     dc_t,n = dy'_t h_t,n,   db_t,n = u_t lam_n        summed over a group's channels, u = delta x
+//     w_n    = lam_n a_t,n h_t-1,n
+//     ddelta = x_t sum_n lam_n b_t,n + sum_n A_n w_n    dx_t = delta_t sum_n lam_n b_t,n + skip dy'_t
+//     dA_n  += delta_t w_n                              mu_n = a_t,n lam_n
+// and ddt = ddelta softplus'(dt + bias), dz = dy (sum_n c h + skip x) silu'(z).
+//
+// Three launches.  Maps: every piece forwards from nothing, leaving the state before each 16
+// tokens, the piece's end state, and its part of the state's gradient before it (which needs the running product of
+// the decays only, so it is formed in the same sweep).  Gradients: every piece backwards, 16 tokens at a time; a
+// state's 16 decays and products stay in registers between the sweep forwards and the one back.  Sums: what
+// several workgroups have parts of, always in the same order.
+#include <utility>
+
+#include "kda_rows.hpp"
+#include "kda_scan.hpp"
+
+namespace kda {
+namespace scan {
+
+constexpr int CH = 16;         // tokens at a time
+constexpr int BPAD = CH + 4;   // floats a state's row of b or c in LDS: four lanes' rows start in different banks
+
+struct BwdArgs {
+    Seqs seqs;
+    int D, G;
+    bool softplus;
+    const void *x, *dt, *b, *c, *z, *dy;
+    const float *A, *skip, *bias, *S0, *dS_T;
+    void *dx, *ddt, *dz;
+    float* dS0;
+    // workspace.  Of each piece: end state [slot][D][N], gradient before it [slot][D][N], sum of delta [slot][D].  Of each
+    // 16 tokens of a sequence: state before them [chunk][D][N], sum of delta before them within the piece [chunk][D].
+    float *local, *grad, *sums, *start, *before;
+    // parts: dA [slot][D][N], dskip and dbias [slot][D], db and dc [workgroup of channels][row][2][N]
+    float *pA, *pskip, *pbias, *pbc;
+    int64_t rows;
+};
+
+// The chunks of sequence n start at its first row / 16 + n.
+__device__ __forceinline__ int64_t first_chunk(const Seqs& s, const Place& p) {
+    return s.cu ? p.row0 / CH + p.seq : (int64_t)p.seq * ((s.T + CH - 1) / CH);
+}
+
+template <typename E, int NS>
+__global__ void __launch_bounds__(BLOCK) scan_bwd_map(BwdArgs a) {
+    constexpr int N = 4 * NS, GROUPS = TILE / 4;
+    __shared__ float rows[2][2 * TILE * N];
+    const int per = (a.D / a.G + BLOCK_CH - 1) / BLOCK_CH, nblk = a.G * per;
+    const int blk = (int)(blockIdx.x % (unsigned)nblk);
+    const int64_t slot = blockIdx.x / (unsigned)nblk;
+    Place pl;
+    if (!place_of(a.seqs, slot, pl)) return;
+    const int grp = blk / per, Dg = a.D / a.G;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, q = lane & 3;
+    const int in_group = (blk % per) * BLOCK_CH + wave * WAVE_CH + (lane >> 2);
+    const bool real = in_group < Dg;
+    const int ch = grp * Dg + (real ? in_group : Dg - 1);
+    const int t_first = pl.k * a.seqs.piece;
+    const int n = pl.len - t_first < a.seqs.piece ? pl.len - t_first : a.seqs.piece;
+    const int64_t row = pl.row0 + t_first;
+    const bool gated = a.z != nullptr;
+    const uint32_t own = (uint32_t)ch * sizeof(E), ld_x = (uint32_t)a.D * sizeof(E);
+    const int64_t ld = (int64_t)a.G * N;
+    const E *b = (const E*)a.b + grp * N, *c = (const E*)a.c + grp * N;
+    const float bias = a.bias ? a.bias[ch] : 0.0f;
+    const int64_t at_state = (int64_t)ch * N + q * NS, states = (int64_t)a.D * N;
+    const bool back = pl.k > 0;   // the gradient before the piece is asked for
+    float* start = a.start + (first_chunk(a.seqs, pl) + t_first / CH) * states + at_state;
+    float* before = a.before + (first_chunk(a.seqs, pl) + t_first / CH) * a.D + ch;
+
+    Rows<E, N> next;
+    E nx[GROUPS], nt[GROUPS], nz[GROUPS], nd[GROUPS];
+    auto fetch = [&](int t0) {
+        next.fetch(b, c, row, ld, t0, n);
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+            const int t = 4 * g + q, last = n - 1 - t0;
+            const uint32_t off = own + (uint32_t)(t < last ? t : last) * ld_x;
+            const int64_t base = (row + t0) * a.D;
+            nx[g] = ld_off((const E*)a.x + base, off);
+            nt[g] = ld_off((const E*)a.dt + base, off);
+            if (back) {
+                nd[g] = ld_off((const E*)a.dy + base, off);
+                if (gated) nz[g] = ld_off((const E*)a.z + base, off);
+            }
+        }
+    };
+    if (n > 0) fetch(0);
+    float A2[NS], h[NS], m[NS], P[NS];
+    ld_states<NS>(a.A + at_state, A2);
+#pragma unroll
+    for (int i = 0; i < NS; ++i) A2[i] *= LOG2E, h[i] = m[i] = 0.0f, P[i] = 1.0f;
+    if (pl.k == 0 && a.S0) ld_states<NS>(a.S0 + (int64_t)pl.seq * states + at_state, h);
+    float sum = 0.0f;
+    for (int t0 = 0, buf = 0; t0 < n; t0 += TILE, buf ^= 1) {
+        next.store(rows[buf]);
+        E cx[GROUPS], ct[GROUPS], cz[GROUPS], cd[GROUPS];
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) cx[g] = nx[g], ct[g] = nt[g], cz[g] = nz[g], cd[g] = nd[g];
+        lds_barrier();
+        if (t0 + TILE < n) fetch(t0 + TILE);
+        const float* bl = rows[buf] + q * NS;
+        const float* cl = bl + TILE * N;
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+            if (t0 + 4 * g >= n) break;
+            if (g % (CH / 4) == 0) {
+                const int chunk = (t0 + 4 * g) / CH;
+                const float s = quad_sum(sum);
+                if (real) {
+                    st_states<NS>(start + chunk * states, h);
+                    if (q == 0) before[(int64_t)chunk * a.D] = s;
+                }
+            }
+            const int t = t0 + 4 * g + q;
+            float d = (float)ct[g] + bias, v = 0.0f;
+            if (a.softplus) d = softplus(d);
+            float u = d * (float)cx[g];
+            if (back) {
+                v = (float)cd[g];
+                if (gated) {
+                    const float zv = (float)cz[g];
+                    v *= zv * sigmoid(zv);
+                }
+            }
+            if (t >= n) d = u = v = 0.0f;   // a step of nothing
+            sum += d;
+            const float dj[4] = {quad_lane<0>(d), quad_lane<1>(d), quad_lane<2>(d), quad_lane<3>(d)};
+            const float uj[4] = {quad_lane<0>(u), quad_lane<1>(u), quad_lane<2>(u), quad_lane<3>(u)};
+            const float vj[4] = {quad_lane<0>(v), quad_lane<1>(v), quad_lane<2>(v), quad_lane<3>(v)};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float bv[NS], cv[NS];
+                ld_states<NS>(bl + (4 * g + j) * N, bv);
+                if (back) ld_states<NS>(cl + (4 * g + j) * N, cv);
+#pragma unroll
+                for (int i = 0; i < NS; ++i) {
+                    const float e = __builtin_amdgcn_exp2f(dj[j] * A2[i]);
+                    h[i] = __builtin_fmaf(e, h[i], uj[j] * bv[i]);
+                    if (back) {
+                        P[i] *= e;
+                        m[i] = __builtin_fmaf(P[i], vj[j] * cv[i], m[i]);
+                    }
+                }
+            }
+        }
+    }
+    sum = quad_sum(sum);
+    if (real) {
+        st_states<NS>(a.local + slot * states + at_state, h);
+        if (back) st_states<NS>(a.grad + slot * states + at_state, m);
+        if (q == 0) a.sums[slot * a.D + ch] = sum;
+    }
+}
+
+// ---------------------------------------------------------------- sums over a wavefront's channels
+typedef unsigned u32x2 __attribute__((__vector_size__(8)));
+
+__device__ __forceinline__ float sum_of(u32x2 r) {
+    const unsigned a = r[0], b = r[1];   // a bit cast of r[1] itself takes r[0]
+    return __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b);
+}
+
+// The sum over the 16 channels (lane bits 5 to 2) of a value a token, each lane left with token
+// (lane >> 2)'s of its quad place.  Every step halves the values: a lane keeps one of a pair and sends
+// the other.
+__device__ __forceinline__ float channel_sums(float (&v)[CH], int lane) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = sum_of(__builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, v[i]), __builtin_bit_cast(unsigned, v[i + 8]), false, false));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = sum_of(__builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, v[i]), __builtin_bit_cast(unsigned, v[i + 4]), false, false));
+    const bool b3 = lane & 8, b2 = lane & 4;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)   // row_ror:8, the lane with bit 3 turned
+        v[i] = (b3 ? v[i + 2] : v[i]) + quad_perm<0x128>(b3 ? v[i] : v[i + 2]);
+    // bit 2 turned: from four lanes above where it is 0, below where it is 1 (row_ror:12 and row_ror:4)
+    const float send = b2 ? v[0] : v[1], up = quad_perm<0x12c>(send), down = quad_perm<0x124>(send);
+    return (b2 ? v[1] : v[0]) + (b2 ? down : up);
+}
+
+// Token T of 16's value, which lane T % 4 of the quad holds in v[T / 4].
+template <int T>
+__device__ __forceinline__ float token(const float* v) { return quad_lane<T % 4>(v[T / 4]); }
+template <typename F, int... T>
+__device__ __forceinline__ void each_token_(F f, std::integer_sequence<int, T...>) { (f(std::integral_constant<int, T>{}), ...); }
+template <typename F>
+__device__ __forceinline__ void each_token(F f) { each_token_(f, std::make_integer_sequence<int, CH>{}); }
+
+template <typename E, int NS>
+__global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(2))) scan_bwd_grad(BwdArgs a) {
+    constexpr int N = 4 * NS, GROUPS = CH / 4, WAVES = BLOCK / 64;
+    __shared__ float bc[2][N * BPAD];
+    __shared__ float part[WAVES][CH][2][N];
+    // A lane's states, one word each, in turn in registers: 16 tokens' work on one fill those.
+    __shared__ float sA[NS][BLOCK], smu[NS][BLOCK], sdA[NS][BLOCK], sh0[NS][BLOCK], sh[NS][BLOCK];
+    // what the outputs need of a lane's own tokens beside, while the registers are the states'
+    __shared__ float aside[2][GROUPS][BLOCK];
+    const int me = threadIdx.x;
+    const int per = (a.D / a.G + BLOCK_CH - 1) / BLOCK_CH, nblk = a.G * per;
+    const int blk = (int)(blockIdx.x % (unsigned)nblk);
+    const int64_t slot = blockIdx.x / (unsigned)nblk;
+    const int grp = blk / per, Dg = a.D / a.G;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, q = lane & 3;
+    const int in_group = (blk % per) * BLOCK_CH + wave * WAVE_CH + (lane >> 2);
+    const bool real = in_group < Dg;
+    const int ch = grp * Dg + (real ? in_group : Dg - 1);
+    const int64_t at_state = (int64_t)ch * N + q * NS, states = (int64_t)a.D * N;
+    Place pl;
+    if (!place_of(a.seqs, slot, pl)) {   // its parts are read all the same
+        if (real) {
+            const float zero[NS] = {};
+            st_states<NS>(a.pA + slot * states + at_state, zero);
+            if (q == 0) a.pskip[slot * a.D + ch] = a.pbias[slot * a.D + ch] = 0.0f;
+        }
+        return;
+    }
+    const int t_first = pl.k * a.seqs.piece;
+    const int n = pl.len - t_first < a.seqs.piece ? pl.len - t_first : a.seqs.piece;
+    const int64_t row = pl.row0 + t_first;
+    const bool gated = a.z != nullptr;
+    const uint32_t own = (uint32_t)ch * sizeof(E), ld_x = (uint32_t)a.D * sizeof(E);
+    const int64_t ld = (int64_t)a.G * N;
+    const E *b = (const E*)a.b + row * ld + grp * N, *c = (const E*)a.c + row * ld + grp * N;
+    const float bias = a.bias ? a.bias[ch] : 0.0f, skip = a.skip ? a.skip[ch] : 0.0f;
+    const int64_t chunk0 = first_chunk(a.seqs, pl) + t_first / CH;
+
+    float A2[NS], mu[NS], h0[NS];
+    ld_states<NS>(a.A + at_state, A2);
+#pragma unroll
+    for (int i = 0; i < NS; ++i) A2[i] *= LOG2E, mu[i] = h0[i] = 0.0f;
+    if (a.dS_T) ld_states<NS>(a.dS_T + (int64_t)pl.seq * states + at_state, mu);
+    for (int j = pl.pieces - 1; j > pl.k; --j) {   // what the pieces behind make of it
+        float l[NS];
+        ld_states<NS>(a.grad + (pl.first + j) * states + at_state, l);
+        const float s = a.sums[(pl.first + j) * a.D + ch];
+#pragma unroll
+        for (int i = 0; i < NS; ++i) mu[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(s * A2[i]), mu[i], l[i]);
+    }
+    for (int j = 0; j < pl.k; ++j) {   // the state that the pieces before leave
+        float l[NS];
+        ld_states<NS>(a.local + (pl.first + j) * states + at_state, l);
+        const float s = a.sums[(pl.first + j) * a.D + ch];
+#pragma unroll
+        for (int i = 0; i < NS; ++i) h0[i] = j ? __builtin_fmaf(__builtin_amdgcn_exp2f(s * A2[i]), h0[i], l[i]) : l[i];
+    }
+
+#pragma unroll
+    for (int i = 0; i < NS; ++i) sA[i][me] = A2[i], smu[i][me] = mu[i], sh0[i][me] = h0[i], sdA[i][me] = 0.0f;
+
+    // a chunk's operands are asked for one chunk ahead
+    constexpr int VECS = 2 * CH * N / 4, PER = (VECS + BLOCK - 1) / BLOCK;
+    typename Four<E>::T nbc[PER];
+    E nx[GROUPS], nt[GROUPS], nz[GROUPS], nd[GROUPS];
+    float nh[NS], ns = 0.0f;
+    auto fetch = [&](int chunk) {
+#pragma unroll
+        for (int p = 0; p < PER; ++p) {
+            const int i = p * BLOCK + (int)threadIdx.x, t = CH * chunk + i % (VECS / 2) / (N / 4);
+            nbc[p] = typename Four<E>::T{};
+            if (i < VECS && t < n)
+                nbc[p] = *reinterpret_cast<const typename Four<E>::T*>((i < VECS / 2 ? b : c) + t * ld + i % (N / 4) * 4);
+        }
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+            const int t = 4 * g + q, last = n - 1 - CH * chunk;
+            const uint32_t off = own + (uint32_t)(t < last ? t : last) * ld_x;
+            const int64_t base = (row + CH * chunk) * a.D;
+            nx[g] = ld_off((const E*)a.x + base, off);
+            nt[g] = ld_off((const E*)a.dt + base, off);
+            nd[g] = ld_off((const E*)a.dy + base, off);
+            if (gated) nz[g] = ld_off((const E*)a.z + base, off);
+        }
+        ld_states<NS>(a.start + (chunk0 + chunk) * states + (uint32_t)at_state, nh);
+        ns = ld_off(a.before + (chunk0 + chunk) * a.D, (uint32_t)ch * 4);
+    };
+    float dskip = 0.0f, dbias = 0.0f;
+    const int chunks = (n + CH - 1) / CH;
+    if (chunks > 0) fetch(chunks - 1);
+    for (int k = chunks - 1; k >= 0; --k) {
+        float xv[GROUPS], dv[GROUPS], uv[GROUPS], vy[GROUPS];
+#pragma unroll
+        for (int p = 0; p < PER; ++p) {
+            const int i = p * BLOCK + (int)threadIdx.x;
+            if (VECS % BLOCK && i >= VECS) continue;
+            const f32x4 v = to_f4<E>(nbc[p]);
+            float* to = bc[i < VECS / 2 ? 0 : 1] + i % (N / 4) * 4 * BPAD + i % (VECS / 2) / (N / 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) to[j * BPAD] = v[j];
+        }
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+            const bool in = CH * k + 4 * g + q < n;
+            xv[g] = (float)nx[g];
+            const float raw = (float)nt[g] + bias;
+            dv[g] = a.softplus ? softplus(raw) : raw;
+            aside[0][g][me] = a.softplus ? sigmoid(raw) : 1.0f;
+            vy[g] = (float)nd[g];
+            if (gated) {
+                const float zv = (float)nz[g], sg = sigmoid(zv);
+                aside[1][g][me] = vy[g] * (sg * (1.0f + zv * (1.0f - sg)));
+                vy[g] *= zv * sg;
+            }
+            uv[g] = dv[g] * xv[g];
+            if (!in) dv[g] = uv[g] = vy[g] = 0.0f;   // a step of nothing
+        }
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            sh[i][me] = pl.k > 0 ? __builtin_fmaf(__builtin_amdgcn_exp2f(ns * sA[i][me]), sh0[i][me], nh[i]) : nh[i];
+        lds_barrier();
+        if (k > 0) fetch(k - 1);
+
+        float s1[CH], s2[CH], sy[CH];
+#pragma unroll
+        for (int t = 0; t < CH; ++t) s1[t] = s2[t] = sy[t] = 0.0f;
+#pragma unroll 1
+        for (int i = 0; i < NS; ++i) {
+            // handed round the quad anew for each state: 48 values kept over the loop do not fit the registers
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g) asm volatile("" : "+v"(dv[g]), "+v"(uv[g]), "+v"(vy[g]));
+            float bv[CH], cv[CH], e[CH], ah[CH], v[CH];
+            ld_states<CH>(bc[0] + (q * NS + i) * BPAD, bv);
+            ld_states<CH>(bc[1] + (q * NS + i) * BPAD, cv);
+            float h = sh[i][me];
+            const float A2i = sA[i][me], Ai = A2i * (1.0f / LOG2E);
+            each_token([&](auto T) {
+                constexpr int t = decltype(T)::value;
+                e[t] = __builtin_amdgcn_exp2f(token<t>(dv) * A2i);
+                ah[t] = e[t] * h;
+                h = __builtin_fmaf(token<t>(uv), bv[t], ah[t]);
+                sy[t] = __builtin_fmaf(cv[t], h, sy[t]);
+                v[t] = real ? token<t>(vy) * h : 0.0f;
+            });
+            const int t_mine = lane >> 2;
+            part[wave][t_mine][1][q * NS + i] = channel_sums(v, lane);
+            float m = smu[i][me], s = 0.0f;
+            each_token([&](auto T) {
+                constexpr int t = CH - 1 - decltype(T)::value;
+                const float lam = __builtin_fmaf(token<t>(vy), cv[t], m), w = lam * ah[t];
+                s1[t] = __builtin_fmaf(lam, bv[t], s1[t]);
+                s2[t] = __builtin_fmaf(Ai, w, s2[t]);
+                s = __builtin_fmaf(token<t>(dv), w, s);
+                v[t] = real ? token<t>(uv) * lam : 0.0f;
+                m = e[t] * lam;
+            });
+            smu[i][me] = m;
+            sdA[i][me] += s;
+            part[wave][t_mine][0][q * NS + i] = channel_sums(v, lane);
+        }
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+            const int t = CH * k + 4 * g + q;
+            const float lb = quad_sums(s1 + 4 * g, q), lw = quad_sums(s2 + 4 * g, q);
+            const float ddt = __builtin_fmaf(xv[g], lb, lw) * aside[0][g][me];
+            const float dxv = __builtin_fmaf(skip, vy[g], dv[g] * lb);
+            const float ych = quad_sums(sy + 4 * g, q);
+            if (t < n) {
+                dskip = __builtin_fmaf(vy[g], xv[g], dskip);
+                dbias += ddt;
+                if (real) {
+                    const uint32_t off = own + (uint32_t)(4 * g + q) * ld_x;
+                    const int64_t base = (row + CH * k) * a.D;
+                    st_off((E*)a.dx + base, off, dxv);
+                    st_off((E*)a.ddt + base, off, ddt);
+                    if (gated) st_off((E*)a.dz + base, off, aside[1][g][me] * __builtin_fmaf(skip, xv[g], ych));
+                }
+            }
+        }
+        lds_barrier();
+        // the workgroup's part of db and dc
+        float* to = a.pbc + ((int64_t)blk * a.rows + row + CH * k) * 2 * N;
+        for (int i = threadIdx.x; i < CH * 2 * N; i += BLOCK) {
+            if (CH * k + i / (2 * N) >= n) break;
+            float s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) s += (&part[w][0][0][0])[i];
+            to[i] = s;
+        }
+    }
+    dskip = quad_sum(dskip);
+    dbias = quad_sum(dbias);
+    float dA[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) dA[i] = sdA[i][me], mu[i] = smu[i][me];
+    if (real) {
+        st_states<NS>(a.pA + slot * states + at_state, dA);
+        if (q == 0) {
+            a.pskip[slot * a.D + ch] = dskip;
+            a.pbias[slot * a.D + ch] = dbias;
+        }
+        if (pl.k == 0 && a.dS0) st_states<NS>(a.dS0 + (int64_t)pl.seq * states + at_state, mu);
+    }
+}
+
+// db and dc: the parts of a group's workgroups of channels.  Rows of no sequence have none.
+template <typename E>
+__global__ void __launch_bounds__(BLOCK)
+scan_bwd_bc(Seqs s, int64_t rows, int G, int N, int per, const float* __restrict__ part, E* __restrict__ db, E* __restrict__ dc) {
+    const int64_t each = 2 * (int64_t)G * N, total = rows * each;
+    int64_t lo = 0, hi = rows;
+    if (s.cu) {
+        lo = held(s.cu[0], 0, s.T);
+        hi = held(s.cu[s.nseq], 0, s.T);
+    }
+    for (int64_t i = (int64_t)blockIdx.x * BLOCK + threadIdx.x; i < total; i += (int64_t)gridDim.x * BLOCK) {
+        const int64_t row = i / each;
+        const int r = (int)(i - row * each), g = r / (2 * N), j = r - g * 2 * N;
+        if (row < lo || row >= hi) continue;
+        float t = 0.0f;
+        for (int k = 0; k < per; ++k) t += part[((int64_t)(g * per + k) * rows + row) * 2 * N + j];
+        (j < N ? db : dc)[(row * G + g) * N + (j < N ? j : j - N)] = from_f<E>(t);
+    }
+}
+
+static int bwd_piece(int nseq, int T, int D, int G, bool packed) {
+    const int64_t blocks = blocks_of(D, G), rows = packed ? T : (int64_t)nseq * T;
+    const int64_t whole = ((int64_t)T + TILE - 1) / TILE * TILE;
+    const int64_t pieces = 1024 / blocks > 1 ? 1024 / blocks : 1;
+    int64_t len = rows / pieces;
+    if (len < 2 * TILE) len = 2 * TILE;
+    if (len < T / 256) len = T / 256;
+    len = (len + TILE - 1) / TILE * TILE;
+    return (int)(len < whole ? len : whole);
+}
+
+struct BwdPlan {
+    int piece;
+    int64_t rows, slots, chunks;
+    int64_t local, grad, sums, start, before, pA, pskip, pbias, pbc, floats;
+};
+static BwdPlan plan_of(int nseq, int T, int D, int N, int G, bool packed) {
+    BwdPlan p;
+    p.piece = bwd_piece(nseq, T, D, G, packed);
+    p.rows = packed ? T : (int64_t)nseq * T;
+    p.slots = slots_of(nseq, T, p.piece, packed);
+    p.chunks = slots_of(nseq, T, CH, packed);
+    int64_t at = 0;
+    auto take = [&](int64_t n) {
+        const int64_t r = at;
+        at += (n + 3) / 4 * 4;
+        return r;
+    };
+    const int64_t states = (int64_t)D * N;
+    p.local = take(p.slots * states);
+    p.grad = take(p.slots * states);
+    p.pA = take(p.slots * states);
+    p.start = take(p.chunks * states);
+    p.pbc = take((int64_t)blocks_of(D, G) * p.rows * 2 * N);
+    p.sums = take(p.slots * D);
+    p.pskip = take(p.slots * D);
+    p.pbias = take(p.slots * D);
+    p.before = take(p.chunks * D);
+    p.floats = at;
+    return p;
+}
+
+template <typename E, int NS>
+static hipError_t bwd_t(const BwdArgs& a, const BwdPlan& p, void* db, void* dc, float* dA, float* dskip, float* dbias, hipStream_t stream) {
+    constexpr int N = 4 * NS;
+    const int blocks = blocks_of(a.D, a.G);
+    const unsigned grid = (unsigned)(p.slots * blocks);
+    hipLaunchKernelGGL((scan_bwd_map<E, NS>), dim3(grid), dim3(BLOCK), 0, stream, a);
+    hipLaunchKernelGGL((scan_bwd_grad<E, NS>), dim3(grid), dim3(BLOCK), 0, stream, a);
+    launch_part_sums(PartSums{{a.pA, a.pskip, a.pbias}, {dA, dskip, dbias}, {(int64_t)a.D * N, a.D, a.D}, p.slots}, stream);
+    const int64_t want = (p.rows * 2 * a.G * N + BLOCK - 1) / BLOCK;
+    hipLaunchKernelGGL(scan_bwd_bc<E>, dim3((unsigned)(want < 8192 ? want : 8192)), dim3(BLOCK), 0, stream, a.seqs, p.rows, a.G, N, blocks / a.G,
+                       a.pbc, (E*)db, (E*)dc);
+    return hipGetLastError();
+}
+
+}  // namespace scan
+
+int64_t scan_bwd_workgroups(int nseq, int T, int D, int G, bool packed) {
+    return scan::slots_of(nseq, T, scan::bwd_piece(nseq, T, D, G, packed), packed) * scan::blocks_of(D, G);
+}
+
+size_t scan_bwd_workspace_bytes(int nseq, int T, int D, int N, int G, bool packed) {
+    return (size_t)scan::plan_of(nseq, T, D, N, G, packed).floats * sizeof(float);
+}
+
+hipError_t launch_scan_bwd(const ScanCall& c, const void* dy, const float* dS_T, void* dx, void* ddt, float* dA, void* db, void* dc,
+                           float* dskip, void* dz, float* dbias, float* dS0, void* workspace, hipStream_t stream) {
+    const scan::BwdPlan p = scan::plan_of(c.nseq, c.T, c.D, c.N, c.G, c.cu != nullptr);
+    float* w = (float*)workspace;
+    const scan::BwdArgs a{{c.nseq, c.T, p.piece, c.cu}, c.D, c.G, c.softplus, c.x, c.dt, c.b, c.c, c.z, dy, c.A, c.skip, c.bias, c.S0, dS_T,
+                          dx, ddt, dz, dS0, w + p.local, w + p.grad, w + p.sums, w + p.start, w + p.before, w + p.pA, w + p.pskip,
+                          w + p.pbias, w + p.pbc, p.rows};
+#define KDA_SB(N)                                                                                          \
+    return c.f32 ? scan::bwd_t<float, N / 4>(a, p, db, dc, dA, dskip, dbias, stream)                       \
+                 : scan::bwd_t<bf16, N / 4>(a, p, db, dc, dA, dskip, dbias, stream)
+    switch (c.N) {
+        case 8: KDA_SB(8);
+        case 16: KDA_SB(16);
+        case 32: KDA_SB(32);
+        case 64: KDA_SB(64);
+    }
+#undef KDA_SB
+    return hipErrorInvalidValue;
+}
+
+}  // namespace kda

@@ -446,6 +446,161 @@ int kda_block_norm_bwd(int dtype, int act, long long rows, int D, float eps,
 /* Bytes of workspace kda_block_norm_bwd needs.  Writes *bytes; returns a kda_status. */
 int kda_block_norm_bwd_workspace_size(long long rows, int D, size_t* bytes);
 
+/* ===========================================================================
+ * The operators of a state-space block.
+ *
+ * Conventions as above; D, the channels, lie side by side in a row, a row a token.  Sequences
+ * are nseq times T tokens, or packed as for kda_gdr_chunk_fwd (cu_seqlens, with what is said
+ * there of offsets and of rows of no sequence; kda_gdr_clear_rows zeroes those).  The step calls take slots and
+ * ntok as kda_gdr_step does.
+ * ------------------------------------------------------------------------- */
+
+/* ---------------------------------------------------------------------------
+ * kda_sel_scan_fwd: the selective scan, a state-space recurrence whose step size, input and output
+ * vectors depend on the token.  Channel d keeps N states h_n and belongs to group d / (D / G):
+ *     delta_t = softplus(dt_t + dt_bias)        (softplus = 0: dt_t + dt_bias)
+ *     h_n    <- exp(delta_t A_n) h_n + delta_t x_t b_t,n
+ *     y_t     = (sum_n c_t,n h_n + skip x_t) z_t / (1 + e^-z_t)
+ *
+ *   dtype        storage of x, dt, b, c, z and y; all arithmetic, A and the states are fp32
+ *   T            at most 2^30;  D at most 2^20, D / G a multiple of 8;  N 8, 16, 32 or 64
+ *   x, dt, z     [.., D]     dtype; z NULL: no gate
+ *   A            [D, N]      fp32, used as given (negative in a model that forgets); finite
+ *   b, c         [.., G, N]  dtype
+ *   skip, dt_bias  [D]       fp32, or NULL for zero
+ *   S0           [nseq, D, N]  fp32, or NULL for zero
+ *   y            [.., D]     dtype, written
+ *   S_T          [nseq, D, N]  fp32, written; or NULL to skip.  May be S0 itself.
+ *   workspace    kda_sel_scan_fwd_workspace_size bytes (NULL where that is 0); contents on entry do not matter
+ *   A value that is not finite reaches what follows it in its sequence (in b and c in all channels of the group, elsewhere in its own).
+ * Returns a kda_status.
+ * ------------------------------------------------------------------------- */
+int kda_sel_scan_fwd(int dtype, int nseq, int T, int D, int N, int G, int softplus, const int* cu_seqlens,
+                     const void* x, const void* dt, const float* A, const void* b, const void* c, const float* skip,
+                     const void* z, const float* dt_bias, const float* S0, void* y, float* S_T,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * kda_sel_scan_bwd: gradients of L = sum <dy, y> + <dS_T, S_T> with respect to every input, from
+ * the forward's inputs (nothing of it is saved).
+ *
+ *   dy           as y;  dS_T  as S_T, or NULL for zero
+ *   dx, ddt, dz  as x; dz goes with z;  db, dc  as b, summed over a group's channels: dtype, written
+ *   dA           [D, N] fp32, written;  dskip, ddt_bias  [D] fp32, written, or NULL to skip
+ *   dS0          as S0, fp32, written; or NULL to skip
+ *   workspace    kda_sel_scan_bwd_workspace_size bytes (about 4 D N / 16 + 8 N D / 64 bytes a token)
+ *   No output may overlap anything.  Sums over rows and channels are in a fixed order.
+ * Returns a kda_status.
+ * ------------------------------------------------------------------------- */
+int kda_sel_scan_bwd(int dtype, int nseq, int T, int D, int N, int G, int softplus, const int* cu_seqlens,
+                     const void* x, const void* dt, const float* A, const void* b, const void* c, const float* skip,
+                     const void* z, const float* dt_bias, const float* S0, const void* dy, const float* dS_T,
+                     void* dx, void* ddt, float* dA, void* db, void* dc, float* dskip, void* dz, float* ddt_bias,
+                     float* dS0, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of the two calls; packed: whether cu_seqlens is given.  Writes *bytes;
+ * returns a kda_status. */
+int kda_sel_scan_fwd_workspace_size(int nseq, int T, int D, int N, int G, int packed, size_t* bytes);
+int kda_sel_scan_bwd_workspace_size(int nseq, int T, int D, int N, int G, int packed, size_t* bytes);
+
+/* ---------------------------------------------------------------------------
+ * kda_sel_scan_step: T tokens of the scan for each of B rows, from and to a state in a pool, in
+ * place.  The state is read and written once a call.
+ *
+ *   x, dt, z     [B, T, D]  dtype;  b, c  [B, T, G, N]  dtype;  A, skip, dt_bias as above
+ *   S            [nslot, D, N]  fp32, the rows' states read and overwritten
+ *   slots, ntok  [B] int32, as for kda_gdr_step
+ *   y            [B, T, D]  dtype, written for the real tokens of rows that are not padded
+ * Returns a kda_status.
+ * ------------------------------------------------------------------------- */
+int kda_sel_scan_step(int dtype, int B, int T, int D, int N, int G, int nslot, int softplus, const void* x,
+                      const void* dt, const float* A, const void* b, const void* c, const float* skip, const void* z,
+                      const float* dt_bias, float* S, const int* slots, const int* ntok, void* y, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * kda_short_conv_fwd: the short causal convolution of every channel over its own last W inputs,
+ * before the scan or before the queries, keys and values of a delta rule:
+ *     y_t = act(bias + sum_j w_j x_{t-W+1+j})
+ * where inputs before the first are S0's (the last W - 1 before the sequence, oldest first).
+ *
+ *   act          KDA_CONV_LINEAR: the identity;  KDA_CONV_SILU: p / (1 + e^-p)
+ *   T            at most 2^30;  D a multiple of 8, at most 2^20;  W 2, 3 or 4
+ *   x            [.., D]   dtype
+ *   w            [D, W]    fp32;  bias  [D] fp32, or NULL for zero
+ *   S0           [nseq, W - 1, D]  dtype, or NULL for zero
+ *   y            [.., D]   dtype, written
+ *   S_T          [nseq, W - 1, D]  dtype, the last W - 1 inputs, S0's among them where a
+ *                sequence is short; or NULL to skip.  May be S0 itself.
+ * Returns a kda_status.
+ * ------------------------------------------------------------------------- */
+typedef enum kda_conv_act { KDA_CONV_LINEAR = 0, KDA_CONV_SILU = 1 } kda_conv_act;
+
+int kda_short_conv_fwd(int dtype, int act, int nseq, int T, int D, int W, const int* cu_seqlens, const void* x,
+                       const float* w, const float* bias, const void* S0, void* y, void* S_T, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * kda_short_conv_bwd: gradients of L = sum <dy, y> + <dS_T, S_T>, from the forward's inputs.
+ *
+ *   dy           as y;  dS_T  as S_T, or NULL for zero
+ *   dx           as x, dtype, written;  dw  [D, W] fp32, written
+ *   dbias        [D] fp32, written, or NULL to skip;  dS0  as S0, dtype, written, or NULL to skip
+ *   workspace    kda_short_conv_bwd_workspace_size bytes, rows being all rows of x
+ *   No output may overlap anything.  Sums over rows are in a fixed order.
+ * Returns a kda_status.
+ * ------------------------------------------------------------------------- */
+int kda_short_conv_bwd(int dtype, int act, int nseq, int T, int D, int W, const int* cu_seqlens, const void* x,
+                       const float* w, const float* bias, const void* S0, const void* dy, const void* dS_T,
+                       void* dx, float* dw, float* dbias, void* dS0,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace kda_short_conv_bwd needs.  Writes *bytes; returns a kda_status. */
+int kda_short_conv_bwd_workspace_size(long long rows, int D, int W, size_t* bytes);
+
+/* ---------------------------------------------------------------------------
+ * kda_short_conv_step: T tokens of the convolution for each of B rows, from and to a state in
+ * a pool, in place.
+ *
+ *   x            [B, T, D]  dtype;  w, bias as above
+ *   S            [nslot, W - 1, D]  dtype, the rows' states read and overwritten
+ *   slots, ntok  [B] int32, as for kda_gdr_step
+ *   y            [B, T, D]  dtype, written for the real tokens of rows that are not padded
+ * Returns a kda_status.
+ * ------------------------------------------------------------------------- */
+int kda_short_conv_step(int dtype, int act, int B, int T, int D, int W, int nslot, const void* x, const float* w,
+                        const float* bias, void* S, const int* slots, const int* ntok, void* y, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * kda_layer_norm_fwd: the layer norm behind a residual sum, per row of D channels:
+ *     r = x + y                                              (x NULL: r = y, not written)
+ *     h = (r - mean(r)) / sqrt(mean((r - mean(r))^2) + eps) * w + b    (w, b NULL: 1 and 0)
+ * All arithmetic is fp32; h is formed from r before r is rounded.
+ *
+ *   rows, D, eps as for kda_block_norm_fwd; with eps 0 a row of equal values is 0 / 0, NaN
+ *   y, x         [rows, D]  dtype;  w, b  [D] fp32
+ *   r            [rows, D]  dtype, written; may be x itself; NULL exactly when x is
+ *   h            [rows, D]  dtype, written
+ * Returns a kda_status.
+ * ------------------------------------------------------------------------- */
+int kda_layer_norm_fwd(int dtype, long long rows, int D, float eps, const void* y, const void* x, const float* w,
+                       const float* b, void* r, void* h, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * kda_layer_norm_bwd: gradients of L = sum <dr, r> + <dh, h>, from the inputs of the forward alone.
+ *
+ *   dr           [rows, D]  dtype, or NULL (zero; it goes with x);  dh  [rows, D]  dtype
+ *   dy           [rows, D]  dtype, written: the gradient of y, and of x, which has the same
+ *   dw, db       [D] fp32, written (sums over the rows, in a fixed order); or NULL to skip
+ *   workspace    kda_layer_norm_bwd_workspace_size bytes when dw or db is asked for
+ *   No output may overlap an input, another output or the workspace.
+ * Returns a kda_status.
+ * ------------------------------------------------------------------------- */
+int kda_layer_norm_bwd(int dtype, long long rows, int D, float eps, const void* y, const void* x, const float* w,
+                       const void* dr, const void* dh, void* dy, float* dw, float* db,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace kda_layer_norm_bwd needs.  Writes *bytes; returns a kda_status. */
+int kda_layer_norm_bwd_workspace_size(long long rows, int D, size_t* bytes);
+
 /* Static description of a status code (never NULL). */
 const char* kda_status_string(int status);
 
