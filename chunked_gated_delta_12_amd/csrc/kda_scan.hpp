@@ -19,6 +19,8 @@
 // which leaves room for each sequence's last, part piece.
 #pragma once
 
+#include <type_traits>
+
 #include "kda_device.hpp"
 #include "kda_launch.hpp"
 
@@ -40,13 +42,20 @@ struct Place {
     int64_t row0, first;
 };
 
+// A value that all lanes share, in a scalar register: what was loaded may have come through vector ones.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+    return (int64_t)(((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32) | (uint32_t)uniform((int)v));
+}
+
 __device__ __forceinline__ int held(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
 
 // False where the slot has no piece.  Offsets out of order or range are held to both.
 __device__ __forceinline__ bool place_of(const Seqs& s, int64_t slot, Place& p) {
     if (!s.cu) {
         const int pieces = (s.T + s.piece - 1) / s.piece;
-        p.seq = (int)(slot / pieces);
+        p.seq = uniform((int)(slot / pieces));
         p.k = (int)(slot - (int64_t)p.seq * pieces);
         p.pieces = pieces;
         p.len = s.T;
@@ -60,7 +69,8 @@ __device__ __forceinline__ bool place_of(const Seqs& s, int64_t slot, Place& p) 
         if (held(s.cu[mid], 0, s.T) / s.piece + (int64_t)mid <= slot) lo = mid;
         else hi = mid - 1;
     }
-    const int r0 = held(s.cu[lo], 0, s.T), r1 = held(s.cu[lo + 1], r0, s.T);
+    lo = uniform(lo);
+    const int r0 = uniform(held(s.cu[lo], 0, s.T)), r1 = uniform(held(s.cu[lo + 1], r0, s.T));
     p.seq = lo;
     p.row0 = r0;
     p.len = r1 - r0;
@@ -71,41 +81,40 @@ __device__ __forceinline__ bool place_of(const Seqs& s, int64_t slot, Place& p) 
     return k >= 0 && k < p.pieces;
 }
 
-// e^v to an ulp or two: the product's rounding is put back.
-__device__ __forceinline__ float exp_full(float v) {
-    const float t = v * LOG2E;
-    const float r = __builtin_fmaf(v, LOG2E, -t) + v * 1.9259629911266175e-8f;   // log2(e) - LOG2E
-    const float e = __builtin_amdgcn_exp2f(t);
-    return __builtin_fmaf(e, r * 0.6931471805599453f, e);
+// e^-|v|, exactly 0 from 104 on, without a branch: NaN is not above 104 and stays.  The product's
+// rounding is put back; log2(e)'s own leaves 1.3e-8 |v| of the result.
+__device__ __forceinline__ float exp_minus(float v) {
+    float a = __builtin_fabsf(v);
+    a = a > 104.0f ? 104.0f : a;
+    const float t = a * -LOG2E, e = __builtin_amdgcn_exp2f(t);
+    return __builtin_fmaf(e, __builtin_fmaf(a, -LOG2E, -t) * 0.6931471805599453f, e);
 }
 
-// softplus(v) = max(v, 0) + log(1 + e^-|v|), with log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3,
-// from atanh's series: relative error below 2^-22 for every v, also where e is small and a
-// logarithm of the rounded 1 + e would lose it.  The series' terms left out start at s^16 / 17 = 1.4e-9.
+// softplus(v) = max(v, 0) + log(1 + e^-|v|), with log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3: a relative
+// error of a few 2^-24 for every v, also where e is small and a logarithm of the rounded 1 + e would
+// lose it.  atanh(s) / s is interpolated in s^2 on [0, 1/9] at Chebyshev's points, off by at most 4e-9.
 __device__ __forceinline__ float softplus(float v) {
-    const float a = __builtin_fabsf(v);
-    // e^-a is 0 in fp32 from 104 on; holding the argument keeps exp_full's correction finite at infinity
-    const float e = a < 104.0f ? exp_full(-a) : a != a ? a : 0.0f;
+    const float e = exp_minus(v);
     const float s = e * __builtin_amdgcn_rcpf(2.0f + e), q = s * s;
-    float p = 1.0f / 15.0f;
-    p = __builtin_fmaf(p, q, 1.0f / 13.0f);
-    p = __builtin_fmaf(p, q, 1.0f / 11.0f);
-    p = __builtin_fmaf(p, q, 1.0f / 9.0f);
-    p = __builtin_fmaf(p, q, 1.0f / 7.0f);
-    p = __builtin_fmaf(p, q, 1.0f / 5.0f);
-    p = __builtin_fmaf(p, q, 1.0f / 3.0f);
+    float p = 1.4078889183e-01f;
+    p = __builtin_fmaf(p, q, 1.3982578873e-01f);
+    p = __builtin_fmaf(p, q, 2.0012297615e-01f);
+    p = __builtin_fmaf(p, q, 3.3333160821e-01f);
     p = __builtin_fmaf(p, q, 1.0f);
-    return __builtin_fmaf(2.0f * s, p, v > 0.0f ? v : 0.0f);
+    float m;
+    asm("v_max_f32 %0, 0, %1" : "=v"(m) : "v"(v));   // the compiler's is two instructions; NaN comes through p
+    return __builtin_fmaf(2.0f * s, p, m);
 }
 
-// sigmoid(v) to a few ulp; exactly 0 and 1 in the tails.
-__device__ __forceinline__ float sigmoid(float v) {
-    const float a = __builtin_fabsf(v);
-    const float e = a < 104.0f ? exp_full(-a) : a != a ? a : 0.0f;
-    const float d = 1.0f + e, r = __builtin_amdgcn_rcpf(d);
+// sigmoid(v): in fp32 storage to a few ulp; in bf16 storage from the hardware exponential and
+// reciprocal, whose error of a few 2^-24 |v| is far below a result's rounding.  Exactly 0 and 1 in the tails.
+template <typename E> __device__ __forceinline__ float sigmoid(float v);
+template <> __device__ __forceinline__ float sigmoid<float>(float v) {
+    const float e = exp_minus(v), d = 1.0f + e, r = __builtin_amdgcn_rcpf(d);
     const float i = __builtin_fmaf(r, __builtin_fmaf(-d, r, 1.0f), r);   // one step: 1 / (1 + e)
     return v < 0.0f ? e * i : i;
 }
+template <> __device__ __forceinline__ float sigmoid<bf16>(float v) { return out_sigmoid(v); }
 
 // ---------------------------------------------------------------- quads
 template <int CTRL>
@@ -120,6 +129,19 @@ __device__ __forceinline__ float quad_sum(float v) {
     v += quad_xor1(v);
     return v + quad_xor2(v);
 }
+// f for the quad's four lanes, the lane's number a constant.
+template <typename F>
+__device__ __forceinline__ void each_of_quad(F f) {
+    f(std::integral_constant<int, 0>{}), f(std::integral_constant<int, 1>{}), f(std::integral_constant<int, 2>{}), f(std::integral_constant<int, 3>{});
+}
+// out[i] = lane J's v times x[i].  The products follow the exchange directly, so that it becomes a
+// modifier of theirs: a multiplication takes a neighbour's operand, a fused one does not.
+template <int J, int NS>
+__device__ __forceinline__ void quad_times(float v, const float* x, float* out) {
+    const float w = quad_lane<J>(v);
+#pragma unroll
+    for (int i = 0; i < NS; ++i) out[i] = w * x[i];
+}
 // Lane j of the quad gets the sum of v[j] over the quad.
 __device__ __forceinline__ float quad_sums(const float* v, int q) {
     const bool b0 = q & 1, b1 = q & 2;
@@ -129,17 +151,32 @@ __device__ __forceinline__ float quad_sums(const float* v, int q) {
 }
 
 // ---------------------------------------------------------------- memory
-// A value `bytes` behind a base that all lanes share: the base stays in scalar registers, and a
-// lane's part is 32 bits (a tile of tokens is at most TILE * 2^20 channels * 4 bytes).
+// Rows of a tile of tokens through a buffer resource that ends behind the last one: the base is in
+// scalar registers, a lane's part 32 bits and the same for every tile, and what lies behind is
+// read as zero and not written.  NOWHERE keeps a lane without a channel out.
+constexpr uint32_t NOWHERE = 0x80000000u;   // a tile has less than half of that, so what is added to it does not wrap
 template <typename E>
-__device__ __forceinline__ E ld_off(const E* base, uint32_t bytes) {
-    return *reinterpret_cast<const E*>(reinterpret_cast<const char*>(base) + bytes);
+__device__ __forceinline__ Rsrc rows_rsrc(const void* p, int64_t row, int64_t ld, int tokens) {
+    // at most TILE tokens of 2^20 channels of 4 bytes
+    return make_rsrc((const E*)p + row * ld, (uint32_t)tokens * (uint32_t)ld * (uint32_t)sizeof(E));
+}
+// A value on its way, 32 bits wide: two of bf16 would be packed into one register and taken apart again.
+template <typename E> __device__ __forceinline__ uint32_t ld_one(Rsrc r, uint32_t off);
+template <> __device__ __forceinline__ uint32_t ld_one<float>(Rsrc r, uint32_t off) { return __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0); }
+template <> __device__ __forceinline__ uint32_t ld_one<bf16>(Rsrc r, uint32_t off) {
+    return (uint32_t)(unsigned short)__builtin_amdgcn_raw_buffer_load_b16(r, (int)off, 0, 0);
 }
 template <typename E>
-__device__ __forceinline__ void st_off(E* base, uint32_t bytes, float v) {
-    *reinterpret_cast<E*>(reinterpret_cast<char*>(base) + bytes) = from_f<E>(v);
+__device__ __forceinline__ float value(uint32_t raw) { return __builtin_bit_cast(float, sizeof(E) == 2 ? raw << 16 : raw); }
+template <typename E> __device__ __forceinline__ void st_one(Rsrc r, uint32_t off, float v);
+template <> __device__ __forceinline__ void st_one<float>(Rsrc r, uint32_t off, float v) {
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), r, (int)off, 0, 0);
+}
+template <> __device__ __forceinline__ void st_one<bf16>(Rsrc r, uint32_t off, float v) {
+    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, (bf16)v), r, (int)off, 0, 0);
 }
 
+// ---------------------------------------------------------------- vectors of states
 template <int NS>
 __device__ __forceinline__ void ld_states(const float* p, float* out) {
     if constexpr (NS % 4 == 0) {
@@ -165,6 +202,28 @@ __device__ __forceinline__ void st_states(float* p, const float* x) {
     }
 }
 
+// v <- exp(A2 sum_j) v + local_j along `count` pieces from j0 on in steps of `by`, the loads of eight at a time in
+// flight: a chain of dependent loads takes half a microsecond a piece.
+template <int NS>
+__device__ __forceinline__ void along_pieces(float (&v)[NS], const float (&A2)[NS], const float* local, const float* sums, int64_t j0, int by,
+                                             int count, int64_t states, int D) {
+    constexpr int AT_ONCE = NS <= 4 ? 8 : NS == 8 ? 4 : 2;
+    for (int k = 0; k < count; k += AT_ONCE) {
+        float l[AT_ONCE][NS], s[AT_ONCE];
+#pragma unroll
+        for (int u = 0; u < AT_ONCE; ++u) {
+            const int64_t j = j0 + (int64_t)by * (k + u < count ? k + u : count - 1);
+            ld_states<NS>(local + j * states, l[u]);
+            s[u] = sums[j * D];
+        }
+#pragma unroll
+        for (int u = 0; u < AT_ONCE; ++u)
+            if (k + u < count)
+#pragma unroll
+                for (int i = 0; i < NS; ++i) v[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(s[u] * A2[i]), v[i], l[u][i]);
+    }
+}
+
 // Four neighbouring values as they are stored, and as fp32.
 template <typename E> struct Four;
 template <> struct Four<float> { typedef f32x4 T; };
@@ -172,33 +231,39 @@ template <> struct Four<bf16> { typedef bf16x4 T; };
 template <typename E>
 __device__ __forceinline__ f32x4 to_f4(typename Four<E>::T v) { return f32x4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]}; }
 
-// b and c of a tile of tokens on their way from memory to LDS, fp32 there: [2][TILE][N].
-// Every token's row is the same for all channels of a group, so the workgroup converts it once.
-// Rows behind the last token are zero, whatever follows them in memory.
-template <typename E, int N>
+// b and c of T tokens on their way from memory to LDS, fp32 there.  Every token's row is the same
+// for all channels of a group, so the workgroup converts it once.  Rows behind the last token are zero.
+// A wavefront's vectors are all of b or all of c, each filled up to whole wavefronts.
+template <typename E, int N, int T>
 struct Rows {
-    static constexpr int VECS = 2 * TILE * N / 4, PER = (VECS + BLOCK - 1) / BLOCK;
+    static constexpr int VECS = T * N / 4, HALF = (VECS + 63) / 64 * 64, PER = (2 * HALF + BLOCK - 1) / BLOCK;
     typename Four<E>::T v[PER];
 
-    __device__ __forceinline__ static int token_of(int i) { return i % (VECS / 2) / (N / 4); }
-
-    __device__ __forceinline__ void fetch(const E* b, const E* c, int64_t row, int64_t ld, int t0, int n) {
+    // b, c: at the group's first state of the first token; ld: elements a token
+    __device__ __forceinline__ void fetch(const E* b, const E* c, int64_t ld, int tokens) {
+        const int wave = uniform((int)threadIdx.x >> 6);
+        const uint32_t bytes = ((uint32_t)(tokens - 1) * (uint32_t)ld + N) * (uint32_t)sizeof(E);
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
-            const int i = p * BLOCK + (int)threadIdx.x;
-            v[p] = typename Four<E>::T{};
-            if (VECS % BLOCK && i >= VECS) continue;
-            const int t = t0 + token_of(i);
-            if (t < n) v[p] = *reinterpret_cast<const typename Four<E>::T*>((i < VECS / 2 ? b : c) + (row + t) * ld + i % (N / 4) * 4);
+            const int first = p * BLOCK + wave * 64;
+            if (first >= 2 * HALF) break;
+            const int i = (p * BLOCK + (int)threadIdx.x) % HALF;   // tokens from T on are behind the end
+            v[p] = BufQuad<E>::ld(make_rsrc(first < HALF ? b : c, bytes),
+                                  ((uint32_t)(i / (N / 4)) * (uint32_t)ld + i % (N / 4) * 4) * (uint32_t)sizeof(E), 0);
         }
     }
-    __device__ __forceinline__ void store(float* lds) const {
+    // f(of c?, token, first of four states, the four)
+    template <typename F>
+    __device__ __forceinline__ void each(F f) const {
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
-            const int i = p * BLOCK + (int)threadIdx.x;
-            if (VECS % BLOCK && i >= VECS) continue;
-            *reinterpret_cast<f32x4*>(lds + 4 * i) = to_f4<E>(v[p]);
+            const int at = p * BLOCK + (int)threadIdx.x, i = at % HALF;
+            if (at < 2 * HALF && i < VECS) f(at >= HALF, i / (N / 4), i % (N / 4) * 4, to_f4<E>(v[p]));
         }
+    }
+    // [2][T][N]
+    __device__ __forceinline__ void store(float* lds) const {
+        each([&](bool of_c, int t, int n, f32x4 x) { *reinterpret_cast<f32x4*>(lds + ((of_c ? T : 0) + t) * N + n) = x; });
     }
 };
 

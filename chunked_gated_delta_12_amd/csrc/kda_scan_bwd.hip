@@ -47,7 +47,8 @@ __device__ __forceinline__ int64_t first_chunk(const Seqs& s, const Place& p) {
     return s.cu ? p.row0 / CH + p.seq : (int64_t)p.seq * ((s.T + CH - 1) / CH);
 }
 
-template <typename E, int NS>
+// BACK: sequences may be cut, and the gradient before a piece is asked for (the first piece's goes unused).
+template <typename E, int NS, bool SOFTPLUS, bool BACK>
 __global__ void __launch_bounds__(BLOCK) scan_bwd_map(BwdArgs a) {
     constexpr int N = 4 * NS, GROUPS = TILE / 4;
     __shared__ float rows[2][2 * TILE * N];
@@ -57,41 +58,51 @@ __global__ void __launch_bounds__(BLOCK) scan_bwd_map(BwdArgs a) {
     Place pl;
     if (!place_of(a.seqs, slot, pl)) return;
     const int grp = blk / per, Dg = a.D / a.G;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, q = lane & 3;
-    const int in_group = (blk % per) * BLOCK_CH + wave * WAVE_CH + (lane >> 2);
+    const int lane = threadIdx.x & 63, q = lane & 3;
+    const int in_group = (blk % per) * BLOCK_CH + (int)(threadIdx.x >> 6) * WAVE_CH + (lane >> 2);
     const bool real = in_group < Dg;
     const int ch = grp * Dg + (real ? in_group : Dg - 1);
     const int t_first = pl.k * a.seqs.piece;
-    const int n = pl.len - t_first < a.seqs.piece ? pl.len - t_first : a.seqs.piece;
-    const int64_t row = pl.row0 + t_first;
-    const bool gated = a.z != nullptr;
-    const uint32_t own = (uint32_t)ch * sizeof(E), ld_x = (uint32_t)a.D * sizeof(E);
+    const int n = uniform(pl.len - t_first < a.seqs.piece ? pl.len - t_first : a.seqs.piece);
+    const int64_t row = uniform64(pl.row0 + t_first);
     const int64_t ld = (int64_t)a.G * N;
-    const E *b = (const E*)a.b + grp * N, *c = (const E*)a.c + grp * N;
+    const bool gated = a.z != nullptr;
+    uint32_t own[GROUPS];
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) own[g] = real ? ((uint32_t)(4 * g + q) * (uint32_t)a.D + ch) * (uint32_t)sizeof(E) : NOWHERE;
     const float bias = a.bias ? a.bias[ch] : 0.0f;
     const int64_t at_state = (int64_t)ch * N + q * NS, states = (int64_t)a.D * N;
-    const bool back = pl.k > 0;   // the gradient before the piece is asked for
     float* start = a.start + (first_chunk(a.seqs, pl) + t_first / CH) * states + at_state;
     float* before = a.before + (first_chunk(a.seqs, pl) + t_first / CH) * a.D + ch;
 
-    Rows<E, N> next;
-    E nx[GROUPS], nt[GROUPS], nz[GROUPS], nd[GROUPS];
-    auto fetch = [&](int t0) {
-        next.fetch(b, c, row, ld, t0, n);
-#pragma unroll
-        for (int g = 0; g < GROUPS; ++g) {
-            const int t = 4 * g + q, last = n - 1 - t0;
-            const uint32_t off = own + (uint32_t)(t < last ? t : last) * ld_x;
-            const int64_t base = (row + t0) * a.D;
-            nx[g] = ld_off((const E*)a.x + base, off);
-            nt[g] = ld_off((const E*)a.dt + base, off);
-            if (back) {
-                nd[g] = ld_off((const E*)a.dy + base, off);
-                if (gated) nz[g] = ld_off((const E*)a.z + base, off);
-            }
+    Rows<E, N, TILE> next;
+    uint32_t nx[GROUPS], nt[GROUPS], nz[GROUPS], nd[GROUPS];
+    auto tokens_at = [&](int t0) { return uniform(n - t0 < 0 ? 0 : n - t0 < TILE ? n - t0 : TILE); };
+    auto fetch_rows = [&](int t0) {
+        const int64_t at = (row + t0) * ld + grp * N;
+        next.fetch((const E*)a.b + at, (const E*)a.c + at, ld, tokens_at(t0));
+    };
+    // a lane's own tokens are asked for a tile ahead, each as soon as the one in its place is used
+    Rsrc rx, rt, rd, rz;
+    auto at_tile = [&](int t0) {
+        const int tokens = tokens_at(t0);
+        rx = rows_rsrc<E>(a.x, row + t0, a.D, tokens), rt = rows_rsrc<E>(a.dt, row + t0, a.D, tokens);
+        if (BACK) rd = rows_rsrc<E>(a.dy, row + t0, a.D, tokens), rz = rows_rsrc<E>(a.z, gated ? row + t0 : 0, a.D, gated ? tokens : 0);
+    };
+    auto fetch = [&](int g) {
+        nx[g] = ld_one<E>(rx, own[g]);
+        nt[g] = ld_one<E>(rt, own[g]);
+        if (BACK) {
+            nd[g] = ld_one<E>(rd, own[g]);
+            nz[g] = ld_one<E>(rz, own[g]);
         }
     };
-    if (n > 0) fetch(0);
+    if (n > 0) {
+        fetch_rows(0);
+        at_tile(0);
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) fetch(g);
+    }
     float A2[NS], h[NS], m[NS], P[NS];
     ld_states<NS>(a.A + at_state, A2);
 #pragma unroll
@@ -100,17 +111,16 @@ __global__ void __launch_bounds__(BLOCK) scan_bwd_map(BwdArgs a) {
     float sum = 0.0f;
     for (int t0 = 0, buf = 0; t0 < n; t0 += TILE, buf ^= 1) {
         next.store(rows[buf]);
-        E cx[GROUPS], ct[GROUPS], cz[GROUPS], cd[GROUPS];
-#pragma unroll
-        for (int g = 0; g < GROUPS; ++g) cx[g] = nx[g], ct[g] = nt[g], cz[g] = nz[g], cd[g] = nd[g];
         lds_barrier();
-        if (t0 + TILE < n) fetch(t0 + TILE);
+        if (t0 + TILE < n) fetch_rows(t0 + TILE);
         const float* bl = rows[buf] + q * NS;
         const float* cl = bl + TILE * N;
+        const int left = n - t0 - q;
+        at_tile(t0 + TILE);
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
-            if (t0 + 4 * g >= n) break;
             if (g % (CH / 4) == 0) {
+                if (t0 + 4 * g >= n) break;
                 const int chunk = (t0 + 4 * g) / CH;
                 const float s = quad_sum(sum);
                 if (real) {
@@ -118,43 +128,40 @@ __global__ void __launch_bounds__(BLOCK) scan_bwd_map(BwdArgs a) {
                     if (q == 0) before[(int64_t)chunk * a.D] = s;
                 }
             }
-            const int t = t0 + 4 * g + q;
-            float d = (float)ct[g] + bias, v = 0.0f;
-            if (a.softplus) d = softplus(d);
-            float u = d * (float)cx[g];
-            if (back) {
-                v = (float)cd[g];
-                if (gated) {
-                    const float zv = (float)cz[g];
-                    v *= zv * sigmoid(zv);
-                }
-            }
-            if (t >= n) d = u = v = 0.0f;   // a step of nothing
+            const float xv = value<E>(nx[g]), raw = value<E>(nt[g]) + bias, dyv = BACK ? value<E>(nd[g]) : 0.0f, zv = BACK ? value<E>(nz[g]) : 0.0f;
+            fetch(g);
+            float d = SOFTPLUS ? softplus(raw) : raw;
+            d = 4 * g < left ? d : 0.0f;   // a step of nothing behind the last token: x and dy are zero there
+            const float u = d * xv, v = dyv * (gated ? zv * sigmoid<E>(zv) : 1.0f);
             sum += d;
-            const float dj[4] = {quad_lane<0>(d), quad_lane<1>(d), quad_lane<2>(d), quad_lane<3>(d)};
-            const float uj[4] = {quad_lane<0>(u), quad_lane<1>(u), quad_lane<2>(u), quad_lane<3>(u)};
-            const float vj[4] = {quad_lane<0>(v), quad_lane<1>(v), quad_lane<2>(v), quad_lane<3>(v)};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float bv[NS], cv[NS];
+            each_of_quad([&](auto J) {
+                constexpr int j = decltype(J)::value;
+                float bv[NS], cv[NS], e[NS];
                 ld_states<NS>(bl + (4 * g + j) * N, bv);
-                if (back) ld_states<NS>(cl + (4 * g + j) * N, cv);
+                if (BACK) ld_states<NS>(cl + (4 * g + j) * N, cv);
+                quad_times<j, NS>(d, A2, e);
+                quad_times<j, NS>(u, bv, bv);
+                if (BACK) quad_times<j, NS>(v, cv, cv);
 #pragma unroll
                 for (int i = 0; i < NS; ++i) {
-                    const float e = __builtin_amdgcn_exp2f(dj[j] * A2[i]);
-                    h[i] = __builtin_fmaf(e, h[i], uj[j] * bv[i]);
-                    if (back) {
-                        P[i] *= e;
-                        m[i] = __builtin_fmaf(P[i], vj[j] * cv[i], m[i]);
+                    e[i] = __builtin_amdgcn_exp2f(e[i]);
+                    h[i] = __builtin_fmaf(e[i], h[i], bv[i]);
+                    if (BACK) {
+                        P[i] *= e[i];
+                        m[i] = __builtin_fmaf(P[i], cv[i], m[i]);
                     }
                 }
-            }
+            });
+            // a group at a time: drawn together, a tile's operands do not fit the registers and its exchanges lie too far from
+            // the products that take them
+#pragma unroll
+            for (int i = 0; i < NS; ++i) asm volatile("" : : "v"(h[i]), "v"(m[i]));
         }
     }
     sum = quad_sum(sum);
     if (real) {
         st_states<NS>(a.local + slot * states + at_state, h);
-        if (back) st_states<NS>(a.grad + slot * states + at_state, m);
+        if (BACK) st_states<NS>(a.grad + slot * states + at_state, m);
         if (q == 0) a.sums[slot * a.D + ch] = sum;
     }
 }
@@ -208,7 +215,7 @@ __global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(2)))
     const int blk = (int)(blockIdx.x % (unsigned)nblk);
     const int64_t slot = blockIdx.x / (unsigned)nblk;
     const int grp = blk / per, Dg = a.D / a.G;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, q = lane & 3;
+    const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, q = lane & 3;
     const int in_group = (blk % per) * BLOCK_CH + wave * WAVE_CH + (lane >> 2);
     const bool real = in_group < Dg;
     const int ch = grp * Dg + (real ? in_group : Dg - 1);
@@ -223,12 +230,11 @@ __global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(2)))
         return;
     }
     const int t_first = pl.k * a.seqs.piece;
-    const int n = pl.len - t_first < a.seqs.piece ? pl.len - t_first : a.seqs.piece;
-    const int64_t row = pl.row0 + t_first;
+    const int n = uniform(pl.len - t_first < a.seqs.piece ? pl.len - t_first : a.seqs.piece);
+    const int64_t row = uniform64(pl.row0 + t_first);
     const bool gated = a.z != nullptr;
-    const uint32_t own = (uint32_t)ch * sizeof(E), ld_x = (uint32_t)a.D * sizeof(E);
+    const uint32_t own = real ? ((uint32_t)q * (uint32_t)a.D + ch) * (uint32_t)sizeof(E) : NOWHERE, four = 4 * (uint32_t)a.D * (uint32_t)sizeof(E);
     const int64_t ld = (int64_t)a.G * N;
-    const E *b = (const E*)a.b + row * ld + grp * N, *c = (const E*)a.c + row * ld + grp * N;
     const float bias = a.bias ? a.bias[ch] : 0.0f, skip = a.skip ? a.skip[ch] : 0.0f;
     const int64_t chunk0 = first_chunk(a.seqs, pl) + t_first / CH;
 
@@ -237,79 +243,76 @@ __global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(2)))
 #pragma unroll
     for (int i = 0; i < NS; ++i) A2[i] *= LOG2E, mu[i] = h0[i] = 0.0f;
     if (a.dS_T) ld_states<NS>(a.dS_T + (int64_t)pl.seq * states + at_state, mu);
-    for (int j = pl.pieces - 1; j > pl.k; --j) {   // what the pieces behind make of it
-        float l[NS];
-        ld_states<NS>(a.grad + (pl.first + j) * states + at_state, l);
-        const float s = a.sums[(pl.first + j) * a.D + ch];
-#pragma unroll
-        for (int i = 0; i < NS; ++i) mu[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(s * A2[i]), mu[i], l[i]);
+    // what the pieces behind make of it, and the state that the pieces before leave
+    along_pieces<NS>(mu, A2, a.grad + at_state, a.sums + ch, pl.first + pl.pieces - 1, -1, pl.pieces - 1 - pl.k, states, a.D);
+    if (pl.k > 0) {
+        ld_states<NS>(a.local + pl.first * states + at_state, h0);
+        along_pieces<NS>(h0, A2, a.local + at_state, a.sums + ch, pl.first + 1, 1, pl.k - 1, states, a.D);
     }
-    for (int j = 0; j < pl.k; ++j) {   // the state that the pieces before leave
-        float l[NS];
-        ld_states<NS>(a.local + (pl.first + j) * states + at_state, l);
-        const float s = a.sums[(pl.first + j) * a.D + ch];
-#pragma unroll
-        for (int i = 0; i < NS; ++i) h0[i] = j ? __builtin_fmaf(__builtin_amdgcn_exp2f(s * A2[i]), h0[i], l[i]) : l[i];
-    }
-
 #pragma unroll
     for (int i = 0; i < NS; ++i) sA[i][me] = A2[i], smu[i][me] = mu[i], sh0[i][me] = h0[i], sdA[i][me] = 0.0f;
 
     // a chunk's operands are asked for one chunk ahead
-    constexpr int VECS = 2 * CH * N / 4, PER = (VECS + BLOCK - 1) / BLOCK;
-    typename Four<E>::T nbc[PER];
-    E nx[GROUPS], nt[GROUPS], nz[GROUPS], nd[GROUPS];
+    Rows<E, N, CH> next;
+    uint32_t nx[GROUPS], nt[GROUPS], nz[GROUPS], nd[GROUPS];
     float nh[NS], ns = 0.0f;
     auto fetch = [&](int chunk) {
-#pragma unroll
-        for (int p = 0; p < PER; ++p) {
-            const int i = p * BLOCK + (int)threadIdx.x, t = CH * chunk + i % (VECS / 2) / (N / 4);
-            nbc[p] = typename Four<E>::T{};
-            if (i < VECS && t < n)
-                nbc[p] = *reinterpret_cast<const typename Four<E>::T*>((i < VECS / 2 ? b : c) + t * ld + i % (N / 4) * 4);
-        }
+        const int tokens = n - CH * chunk < CH ? n - CH * chunk : CH;
+        const int64_t from = row + CH * chunk, at = from * ld + grp * N;
+        next.fetch((const E*)a.b + at, (const E*)a.c + at, ld, tokens);
+        const Rsrc rx = rows_rsrc<E>(a.x, from, a.D, tokens), rt = rows_rsrc<E>(a.dt, from, a.D, tokens),
+                   rd = rows_rsrc<E>(a.dy, from, a.D, tokens);
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
-            const int t = 4 * g + q, last = n - 1 - CH * chunk;
-            const uint32_t off = own + (uint32_t)(t < last ? t : last) * ld_x;
-            const int64_t base = (row + CH * chunk) * a.D;
-            nx[g] = ld_off((const E*)a.x + base, off);
-            nt[g] = ld_off((const E*)a.dt + base, off);
-            nd[g] = ld_off((const E*)a.dy + base, off);
-            if (gated) nz[g] = ld_off((const E*)a.z + base, off);
+            nx[g] = ld_one<E>(rx, own + g * four);
+            nt[g] = ld_one<E>(rt, own + g * four);
+            nd[g] = ld_one<E>(rd, own + g * four);
+        }
+        if (gated) {
+            const Rsrc rz = rows_rsrc<E>(a.z, from, a.D, tokens);
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g) nz[g] = ld_one<E>(rz, own + g * four);
         }
         ld_states<NS>(a.start + (chunk0 + chunk) * states + (uint32_t)at_state, nh);
-        ns = ld_off(a.before + (chunk0 + chunk) * a.D, (uint32_t)ch * 4);
+        ns = a.before[(chunk0 + chunk) * a.D + (uint32_t)ch];
     };
     float dskip = 0.0f, dbias = 0.0f;
     const int chunks = (n + CH - 1) / CH;
     if (chunks > 0) fetch(chunks - 1);
     for (int k = chunks - 1; k >= 0; --k) {
         float xv[GROUPS], dv[GROUPS], uv[GROUPS], vy[GROUPS];
+        next.each([&](bool of_c, int t, int n0, f32x4 x) {
 #pragma unroll
-        for (int p = 0; p < PER; ++p) {
-            const int i = p * BLOCK + (int)threadIdx.x;
-            if (VECS % BLOCK && i >= VECS) continue;
-            const f32x4 v = to_f4<E>(nbc[p]);
-            float* to = bc[i < VECS / 2 ? 0 : 1] + i % (N / 4) * 4 * BPAD + i % (VECS / 2) / (N / 4);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) to[j * BPAD] = v[j];
-        }
+            for (int j = 0; j < 4; ++j) bc[of_c ? 1 : 0][(n0 + j) * BPAD + t] = x[j];
+        });
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
-            const bool in = CH * k + 4 * g + q < n;
-            xv[g] = (float)nx[g];
-            const float raw = (float)nt[g] + bias;
-            dv[g] = a.softplus ? softplus(raw) : raw;
-            aside[0][g][me] = a.softplus ? sigmoid(raw) : 1.0f;
-            vy[g] = (float)nd[g];
-            if (gated) {
-                const float zv = (float)nz[g], sg = sigmoid(zv);
+            dv[g] = value<E>(nt[g]) + bias;
+            xv[g] = value<E>(nx[g]);
+            vy[g] = value<E>(nd[g]);
+        }
+        if (a.softplus) {
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g) {
+                aside[0][g][me] = sigmoid<float>(dv[g]);
+                dv[g] = softplus(dv[g]);
+            }
+        } else {
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g) aside[0][g][me] = 1.0f;
+        }
+        if (gated)
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g) {
+                const float zv = value<E>(nz[g]), sg = sigmoid<E>(zv);
                 aside[1][g][me] = vy[g] * (sg * (1.0f + zv * (1.0f - sg)));
                 vy[g] *= zv * sg;
             }
+        const int left = n - CH * k - q;
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+            if (4 * g >= left) dv[g] = aside[0][g][me] = 0.0f;   // a step of nothing behind the last token: x and dy are zero there
             uv[g] = dv[g] * xv[g];
-            if (!in) dv[g] = uv[g] = vy[g] = 0.0f;   // a step of nothing
         }
 #pragma unroll
         for (int i = 0; i < NS; ++i)
@@ -322,56 +325,61 @@ __global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(2)))
         for (int t = 0; t < CH; ++t) s1[t] = s2[t] = sy[t] = 0.0f;
 #pragma unroll 1
         for (int i = 0; i < NS; ++i) {
-            // handed round the quad anew for each state: 48 values kept over the loop do not fit the registers
+            // Operands are handed round the quad as modifiers of multiplications, which have to follow one another closely for
+            // that; the empty statements keep the compiler from drawing the tokens together.
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g) asm volatile("" : "+v"(dv[g]), "+v"(uv[g]), "+v"(vy[g]));
-            float bv[CH], cv[CH], e[CH], ah[CH], v[CH];
+            float bv[CH], cv[CH], e[CH], hp[CH], v[CH];
             ld_states<CH>(bc[0] + (q * NS + i) * BPAD, bv);
             ld_states<CH>(bc[1] + (q * NS + i) * BPAD, cv);
             float h = sh[i][me];
             const float A2i = sA[i][me], Ai = A2i * (1.0f / LOG2E);
             each_token([&](auto T) {
                 constexpr int t = decltype(T)::value;
+                hp[t] = h;
                 e[t] = __builtin_amdgcn_exp2f(token<t>(dv) * A2i);
-                ah[t] = e[t] * h;
-                h = __builtin_fmaf(token<t>(uv), bv[t], ah[t]);
+                h = __builtin_fmaf(e[t], h, token<t>(uv) * bv[t]);
                 sy[t] = __builtin_fmaf(cv[t], h, sy[t]);
-                v[t] = real ? token<t>(vy) * h : 0.0f;
+                v[t] = token<t>(vy) * h;   // zero of lanes without a channel: they read nothing
+                if (t % 2) asm volatile("" : : "v"(v[t]), "v"(sy[t]));
             });
             const int t_mine = lane >> 2;
             part[wave][t_mine][1][q * NS + i] = channel_sums(v, lane);
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g) asm volatile("" : "+v"(dv[g]), "+v"(uv[g]), "+v"(vy[g]));
             float m = smu[i][me], s = 0.0f;
             each_token([&](auto T) {
                 constexpr int t = CH - 1 - decltype(T)::value;
-                const float lam = __builtin_fmaf(token<t>(vy), cv[t], m), w = lam * ah[t];
+                const float lam = token<t>(vy) * cv[t] + m;
+                v[t] = token<t>(uv) * lam;
+                m = e[t] * lam;
+                const float w = m * hp[t];   // lam a_t h_t-1
                 s1[t] = __builtin_fmaf(lam, bv[t], s1[t]);
                 s2[t] = __builtin_fmaf(Ai, w, s2[t]);
-                s = __builtin_fmaf(token<t>(dv), w, s);
-                v[t] = real ? token<t>(uv) * lam : 0.0f;
-                m = e[t] * lam;
+                s += token<t>(dv) * w;
+                if (t % 2 == 0) asm volatile("" : : "v"(v[t]), "v"(s));
             });
             smu[i][me] = m;
             sdA[i][me] += s;
             part[wave][t_mine][0][q * NS + i] = channel_sums(v, lane);
         }
+        const int64_t from = row + CH * k;
+        const int tokens = n - CH * k < CH ? n - CH * k : CH;
+        const Rsrc wx = rows_rsrc<E>(a.dx, from, a.D, tokens), wt = rows_rsrc<E>(a.ddt, from, a.D, tokens);
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
-            const int t = CH * k + 4 * g + q;
             const float lb = quad_sums(s1 + 4 * g, q), lw = quad_sums(s2 + 4 * g, q);
             const float ddt = __builtin_fmaf(xv[g], lb, lw) * aside[0][g][me];
-            const float dxv = __builtin_fmaf(skip, vy[g], dv[g] * lb);
-            const float ych = quad_sums(sy + 4 * g, q);
-            if (t < n) {
-                dskip = __builtin_fmaf(vy[g], xv[g], dskip);
-                dbias += ddt;
-                if (real) {
-                    const uint32_t off = own + (uint32_t)(4 * g + q) * ld_x;
-                    const int64_t base = (row + CH * k) * a.D;
-                    st_off((E*)a.dx + base, off, dxv);
-                    st_off((E*)a.ddt + base, off, ddt);
-                    if (gated) st_off((E*)a.dz + base, off, aside[1][g][me] * __builtin_fmaf(skip, xv[g], ych));
-                }
-            }
+            st_one<E>(wx, own + g * four, __builtin_fmaf(skip, vy[g], dv[g] * lb));
+            st_one<E>(wt, own + g * four, ddt);
+            dskip = __builtin_fmaf(vy[g], xv[g], dskip);
+            dbias += ddt;   // zero where there is no token
+        }
+        if (gated) {
+            const Rsrc wz = rows_rsrc<E>(a.dz, from, a.D, tokens);
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g)
+                st_one<E>(wz, own + g * four, aside[1][g][me] * __builtin_fmaf(skip, xv[g], quad_sums(sy + 4 * g, q)));
         }
         lds_barrier();
         // the workgroup's part of db and dc
@@ -466,7 +474,9 @@ static hipError_t bwd_t(const BwdArgs& a, const BwdPlan& p, void* db, void* dc, 
     constexpr int N = 4 * NS;
     const int blocks = blocks_of(a.D, a.G);
     const unsigned grid = (unsigned)(p.slots * blocks);
-    hipLaunchKernelGGL((scan_bwd_map<E, NS>), dim3(grid), dim3(BLOCK), 0, stream, a);
+    auto map = p.piece < a.seqs.T ? (a.softplus ? scan_bwd_map<E, NS, true, true> : scan_bwd_map<E, NS, false, true>)
+                                  : (a.softplus ? scan_bwd_map<E, NS, true, false> : scan_bwd_map<E, NS, false, false>);
+    hipLaunchKernelGGL(map, dim3(grid), dim3(BLOCK), 0, stream, a);
     hipLaunchKernelGGL((scan_bwd_grad<E, NS>), dim3(grid), dim3(BLOCK), 0, stream, a);
     launch_part_sums(PartSums{{a.pA, a.pskip, a.pbias}, {dA, dskip, dbias}, {(int64_t)a.D * N, a.D, a.D}, p.slots}, stream);
     const int64_t want = (p.rows * 2 * a.G * N + BLOCK - 1) / BLOCK;

@@ -12,14 +12,13 @@ namespace scan {
 struct FwdArgs {
     Seqs seqs;
     int D, G;
-    bool softplus;
     const void *x, *dt, *b, *c, *z;
     const float *A, *skip, *bias, *S0;
     void* y;
     float *S_T, *local, *sums;   // maps: end state from nothing [slot][D][N], sum of delta [slot][D]
 };
 
-template <typename E, int NS, bool MAP>
+template <typename E, int NS, bool SOFTPLUS, bool MAP, bool GATED>
 __global__ void __launch_bounds__(BLOCK) scan_walk(FwdArgs a) {
     constexpr int N = 4 * NS, GROUPS = TILE / 4;
     __shared__ float rows[2][2 * TILE * N];
@@ -30,35 +29,39 @@ __global__ void __launch_bounds__(BLOCK) scan_walk(FwdArgs a) {
     if (!place_of(a.seqs, slot, pl)) return;
     if (MAP && pl.k == pl.pieces - 1) return;
     const int grp = blk / per, Dg = a.D / a.G;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, q = lane & 3;
-    const int in_group = (blk % per) * BLOCK_CH + wave * WAVE_CH + (lane >> 2);
+    const int lane = threadIdx.x & 63, q = lane & 3;
+    const int in_group = (blk % per) * BLOCK_CH + (int)(threadIdx.x >> 6) * WAVE_CH + (lane >> 2);
     const bool real = in_group < Dg;
-    const int ch = grp * Dg + (real ? in_group : Dg - 1);   // lanes without a channel repeat the last and store nothing
+    const int ch = grp * Dg + (real ? in_group : Dg - 1);   // lanes without a channel repeat the last one's states and store nothing
     const int t_first = pl.k * a.seqs.piece;
-    const int n = pl.len - t_first < a.seqs.piece ? pl.len - t_first : a.seqs.piece;
-    const int64_t row = pl.row0 + t_first;
-    const bool gated = a.z != nullptr;
-    const uint32_t own = (uint32_t)ch * sizeof(E), ld_x = (uint32_t)a.D * sizeof(E);
+    const int n = uniform(pl.len - t_first < a.seqs.piece ? pl.len - t_first : a.seqs.piece);
+    const int64_t row = uniform64(pl.row0 + t_first);
     const int64_t ld = (int64_t)a.G * N;
-    const E *b = (const E*)a.b + grp * N, *c = (const E*)a.c + grp * N;
+    uint32_t own[GROUPS];   // a lane's own tokens of a tile: every fourth
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) own[g] = real ? ((uint32_t)(4 * g + q) * (uint32_t)a.D + ch) * (uint32_t)sizeof(E) : NOWHERE;
     const float bias = a.bias ? a.bias[ch] : 0.0f, skip = a.skip ? a.skip[ch] : 0.0f;
     const int64_t at_state = (int64_t)ch * N + q * NS, states = (int64_t)a.D * N;
 
-    Rows<E, N> next;
-    E nx[GROUPS], nt[GROUPS], nz[GROUPS];
-    auto fetch = [&](int t0) {
-        next.fetch(b, c, row, ld, t0, n);
+    Rows<E, N, TILE> next;
+    uint32_t nx[GROUPS], nt[GROUPS], nz[GROUPS];
+    auto tokens_at = [&](int t0) { return uniform(n - t0 < 0 ? 0 : n - t0 < TILE ? n - t0 : TILE); };   // a median of three is a vector instruction
+    auto fetch_rows = [&](int t0) {
+        const int64_t at = (row + t0) * ld + grp * N;
+        next.fetch((const E*)a.b + at, (const E*)a.c + at, ld, tokens_at(t0));
+    };
+    if (n > 0) {
+        fetch_rows(0);
+        const Rsrc rx = rows_rsrc<E>(a.x, row, a.D, tokens_at(0)), rt = rows_rsrc<E>(a.dt, row, a.D, tokens_at(0));
+        Rsrc rz;
+        if (GATED) rz = rows_rsrc<E>(a.z, row, a.D, tokens_at(0));
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
-            const int t = 4 * g + q, last = n - 1 - t0;
-            const uint32_t off = own + (uint32_t)(t < last ? t : last) * ld_x;
-            const int64_t base = (row + t0) * a.D;
-            nx[g] = ld_off((const E*)a.x + base, off);
-            nt[g] = ld_off((const E*)a.dt + base, off);
-            if (!MAP && gated) nz[g] = ld_off((const E*)a.z + base, off);
+            nx[g] = ld_one<E>(rx, own[g]);
+            nt[g] = ld_one<E>(rt, own[g]);
+            if (GATED) nz[g] = ld_one<E>(rz, own[g]);
         }
-    };
-    if (n > 0) fetch(0);
+    }
 
     float A2[NS], h[NS];
     ld_states<NS>(a.A + at_state, A2);
@@ -72,58 +75,57 @@ __global__ void __launch_bounds__(BLOCK) scan_walk(FwdArgs a) {
         if (a.S0) ld_states<NS>(from, h);
         if (MAP && a.S0 && real) st_states<NS>(local + (pl.first + pl.pieces - 1) * states, h);
     } else if (!MAP) {
-        for (int j = 0; j < pl.k; ++j) {
-            float l[NS];
-            ld_states<NS>(local + (pl.first + j) * states, l);
-            const float s = a.sums[(pl.first + j) * a.D + ch];
-#pragma unroll
-            for (int i = 0; i < NS; ++i) h[i] = j ? __builtin_fmaf(__builtin_amdgcn_exp2f(s * A2[i]), h[i], l[i]) : l[i];
-        }
+        ld_states<NS>(local + pl.first * states, h);   // the first piece's map starts from S0
+        along_pieces<NS>(h, A2, local, a.sums + ch, pl.first + 1, 1, pl.k - 1, states, a.D);
     }
     float sum = 0.0f;
     for (int t0 = 0, buf = 0; t0 < n; t0 += TILE, buf ^= 1) {
         next.store(rows[buf]);
-        E cx[GROUPS], ct[GROUPS], cz[GROUPS];
-#pragma unroll
-        for (int g = 0; g < GROUPS; ++g) cx[g] = nx[g], ct[g] = nt[g], cz[g] = nz[g];
         lds_barrier();   // one a tile: a buffer is written again only after the barrier of the other's tile
-        if (t0 + TILE < n) fetch(t0 + TILE);
+        if (t0 + TILE < n) fetch_rows(t0 + TILE);
         const float* bl = rows[buf] + q * NS;
         const float* cl = bl + TILE * N;
+        // a lane's own tokens are asked for a tile ahead, each as soon as the one in its place is used
+        const int ahead = tokens_at(t0 + TILE), left = n - t0 - q;
+        const Rsrc rx = rows_rsrc<E>(a.x, row + t0 + TILE, a.D, ahead), rt = rows_rsrc<E>(a.dt, row + t0 + TILE, a.D, ahead);
+        Rsrc rz, ry;
+        if (GATED) rz = rows_rsrc<E>(a.z, row + t0 + TILE, a.D, ahead);
+        if (!MAP) ry = rows_rsrc<E>(a.y, row + t0, a.D, tokens_at(t0));
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
-            if (t0 + 4 * g >= n) break;
-            const int t = t0 + 4 * g + q;
-            const float xv = (float)cx[g];
-            float d = (float)ct[g] + bias;
-            if (a.softplus) d = softplus(d);
-            float u = d * xv;
-            if (t >= n) d = u = 0.0f;   // a step of nothing
-            sum += d;
-            float dj[4] = {quad_lane<0>(d), quad_lane<1>(d), quad_lane<2>(d), quad_lane<3>(d)};
-            float uj[4] = {quad_lane<0>(u), quad_lane<1>(u), quad_lane<2>(u), quad_lane<3>(u)};
+            if (g % 4 == 0 && t0 + 4 * g >= n) break;
+            const float xv = value<E>(nx[g]), raw = value<E>(nt[g]) + bias, zv = GATED ? value<E>(nz[g]) : 0.0f;
+            nx[g] = ld_one<E>(rx, own[g]);
+            nt[g] = ld_one<E>(rt, own[g]);
+            if (GATED) nz[g] = ld_one<E>(rz, own[g]);
+            float d = SOFTPLUS ? softplus(raw) : raw;
+            d = 4 * g < left ? d : 0.0f;   // a step of nothing behind the last token: x is zero there
+            const float u = d * xv, ys = a.skip ? skip * xv : 0.0f, gate = GATED ? zv * sigmoid<E>(zv) : 1.0f;
+            if (MAP) sum += d;
             float yj[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float bv[NS], cv[NS];
+            each_of_quad([&](auto J) {
+                constexpr int j = decltype(J)::value;
+                float bv[NS], cv[NS], e[NS];
                 ld_states<NS>(bl + (4 * g + j) * N, bv);
                 if (!MAP) ld_states<NS>(cl + (4 * g + j) * N, cv);
+                quad_times<j, NS>(d, A2, e);
+                quad_times<j, NS>(u, bv, bv);
                 float s = 0.0f;
 #pragma unroll
                 for (int i = 0; i < NS; ++i) {
-                    h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(dj[j] * A2[i]), h[i], uj[j] * bv[i]);
+                    h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(e[i]), h[i], bv[i]);
                     if (!MAP) s = i ? __builtin_fmaf(cv[i], h[i], s) : cv[i] * h[i];
                 }
                 yj[j] = s;
-            }
-            if (!MAP) {
-                float yv = quad_sums(yj, q);
-                if (a.skip) yv = __builtin_fmaf(skip, xv, yv);
-                if (gated) {
-                    const float zv = (float)cz[g];
-                    yv *= zv * sigmoid(zv);
-                }
-                if (t < n && real) st_off((E*)a.y + (row + t0) * a.D, own + (uint32_t)(4 * g + q) * ld_x, yv);
+            });
+            if (MAP) {
+                // a group at a time, as the walk's stores have it: drawn together, a tile's exchanges lie too far from the
+                // products that take them
+#pragma unroll
+                for (int i = 0; i < NS; ++i) asm volatile("" : : "v"(h[i]));
+            } else {
+                const float yv = quad_sums(yj, q) + ys;
+                st_one<E>(ry, own[g], GATED ? yv * gate : yv);
             }
         }
     }
@@ -142,8 +144,8 @@ __global__ void __launch_bounds__(BLOCK) scan_walk(FwdArgs a) {
 static int fwd_piece(int nseq, int T, int D, int G, bool packed) {
     const int64_t blocks = blocks_of(D, G), rows = packed ? T : (int64_t)nseq * T;
     const int64_t whole = ((int64_t)T + TILE - 1) / TILE * TILE;
-    if (!packed && nseq * blocks >= 256) return (int)whole;
-    const int64_t pieces = 512 / blocks > 1 ? 512 / blocks : 1;
+    if (!packed && nseq * blocks >= 512) return (int)whole;
+    const int64_t pieces = 2048 / blocks > 1 ? 2048 / blocks : 1;
     int64_t len = rows / pieces;
     if (len < 2 * TILE) len = 2 * TILE;
     if (len < T / 256) len = T / 256;
@@ -151,11 +153,12 @@ static int fwd_piece(int nseq, int T, int D, int G, bool packed) {
     return (int)(len < whole ? len : whole);
 }
 
-template <typename E, int NS>
+template <typename E, int NS, bool SOFTPLUS>
 static hipError_t fwd_t(const FwdArgs& a, int64_t slots, bool cut, hipStream_t stream) {
     const unsigned grid = (unsigned)(slots * blocks_of(a.D, a.G));
-    if (cut) hipLaunchKernelGGL((scan_walk<E, NS, true>), dim3(grid), dim3(BLOCK), 0, stream, a);
-    hipLaunchKernelGGL((scan_walk<E, NS, false>), dim3(grid), dim3(BLOCK), 0, stream, a);
+    if (cut) hipLaunchKernelGGL((scan_walk<E, NS, SOFTPLUS, true, false>), dim3(grid), dim3(BLOCK), 0, stream, a);
+    if (a.z) hipLaunchKernelGGL((scan_walk<E, NS, SOFTPLUS, false, true>), dim3(grid), dim3(BLOCK), 0, stream, a);
+    else hipLaunchKernelGGL((scan_walk<E, NS, SOFTPLUS, false, false>), dim3(grid), dim3(BLOCK), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -176,10 +179,12 @@ hipError_t launch_scan_fwd(const ScanCall& c, void* y, float* S_T, void* workspa
     const int piece = scan::fwd_piece(c.nseq, c.T, c.D, c.G, packed);
     const int64_t slots = scan::slots_of(c.nseq, c.T, piece, packed);
     float* local = (float*)workspace;
-    const scan::FwdArgs a{{c.nseq, c.T, piece, c.cu}, c.D, c.G, c.softplus, c.x, c.dt, c.b, c.c, c.z, c.A, c.skip, c.bias, c.S0,
+    const scan::FwdArgs a{{c.nseq, c.T, piece, c.cu}, c.D, c.G, c.x, c.dt, c.b, c.c, c.z, c.A, c.skip, c.bias, c.S0,
                           y, S_T, local, local ? local + slots * c.D * c.N : nullptr};
     const bool cut = piece < c.T;
-#define KDA_SF(N) return c.f32 ? scan::fwd_t<float, N / 4>(a, slots, cut, stream) : scan::fwd_t<bf16, N / 4>(a, slots, cut, stream)
+#define KDA_SF(N)                                                                                                          \
+    return c.f32 ? c.softplus ? scan::fwd_t<float, N / 4, true>(a, slots, cut, stream) : scan::fwd_t<float, N / 4, false>(a, slots, cut, stream) \
+                 : c.softplus ? scan::fwd_t<bf16, N / 4, true>(a, slots, cut, stream) : scan::fwd_t<bf16, N / 4, false>(a, slots, cut, stream)
     switch (c.N) {
         case 8: KDA_SF(8);
         case 16: KDA_SF(16);

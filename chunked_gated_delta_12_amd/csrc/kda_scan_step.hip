@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(BLOCK) scan_step(StepArgs a) {
         }
         float yv = quad_sums(yj, q);
         if (a.skip) yv = __builtin_fmaf(skip, xv, yv);
-        if (a.z) yv *= zv * sigmoid(zv);
+        if (a.z) yv *= zv * sigmoid<E>(zv);
         if (t < n && real) ((E*)a.y)[off] = from_f<E>(yv);
     }
     if (real) st_states<NS>(Sp, h);
