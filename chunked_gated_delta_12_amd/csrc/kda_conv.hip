@@ -175,6 +175,7 @@ __device__ __forceinline__ V8 through_act(bool silu, const V8& p, const V8& dy) 
 // VB lanes side by side hold eight channels each, 256 / VB runs of rows a workgroup.
 template <typename E, int W>
 __global__ void __launch_bounds__(256) conv_bwd_kernel(ConvArgs a, int VB, int state_blocks) {
+    constexpr int AHEAD = 2;
     __shared__ float lds[8 * 256];
     const int nvec = a.D / 8, nvb = (nvec + VB - 1) / VB;
     if ((int)blockIdx.x < state_blocks) {   // the start states' gradients
@@ -227,60 +228,73 @@ __global__ void __launch_bounds__(256) conv_bwd_kernel(ConvArgs a, int VB, int s
 #pragma unroll
             for (int k = 1; k < W; ++k) win[k - 1] = input_at<E, W>(a, s, r0 - k, vec);
         const int64_t last = r1 + W - 1 < a.rows ? r1 + W - 1 : a.rows;
-        Raw<E> nx, nd;
+        // rows are asked for AHEAD at a time, one batch ahead of their use
+        Raw<E> nx[AHEAD], nd[AHEAD];
         auto fetch = [&](int64_t t) {
-            ld_raw((const E*)a.x + t * a.D + 8 * vec, nx);
-            ld_raw((const E*)a.dy + t * a.D + 8 * vec, nd);
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                const int64_t at = (t + i < last ? t + i : last - 1) * a.D + 8 * vec;
+                ld_raw((const E*)a.x + at, nx[i]);
+                ld_raw((const E*)a.dy + at, nd[i]);
+            }
+        };
+        // The rows that wait at the end of a sequence have all that comes, but the last state's gradient.
+        auto flush = [&](int64_t t) {
+#pragma unroll
+            for (int k = W - 1; k > 0; --k) {
+                const int64_t row = t - k;
+                if (row < s.lo || row < r0 || row >= r1 || t > s.hi) continue;
+                V8 g = out[k - 1];
+                if (a.dS_T) {
+                    const V8 d = ld_row<E>(a.dS_T, (int64_t)s.n * (W - 1) + (W - 1) - k, a.D, vec);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) g.f[e] += d.f[e];
+                }
+                st8((E*)a.dx + row * a.D + 8 * vec, g);
+            }
         };
         fetch(r0);
-        for (int64_t t = r0;; ++t) {
-            if (t >= s.hi || t >= last) {
-                if (t >= s.hi) {   // the sequence is at its end: the rows that wait have all that comes, but the last state's gradient
+        for (int64_t t0 = r0; t0 < last; t0 += AHEAD) {
+            Raw<E> cx[AHEAD], cd[AHEAD];
 #pragma unroll
-                    for (int k = W - 1; k > 0; --k) {
-                        const int64_t row = t - k;
-                        if (row < s.lo || row < r0 || row >= r1 || t > s.hi) continue;
-                        V8 g = out[k - 1];
-                        if (a.dS_T) {
-                            const V8 d = ld_row<E>(a.dS_T, (int64_t)s.n * (W - 1) + (W - 1) - k, a.D, vec);
+            for (int i = 0; i < AHEAD; ++i) cx[i] = nx[i], cd[i] = nd[i];
+            if (t0 + AHEAD < last) fetch(t0 + AHEAD);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) g.f[e] += d.f[e];
-                        }
-                        st8((E*)a.dx + row * a.D + 8 * vec, g);
+            for (int i = 0; i < AHEAD; ++i) {
+                const int64_t t = t0 + i;
+                if (t >= last) break;
+                if (t >= s.hi) {
+                    flush(t);
+                    while (t >= s.hi && s.n + 1 < a.nseq) s = span_at(a, s.n + 1);
+                }
+                if (t == s.lo) {
+#pragma unroll
+                    for (int k = 0; k < W; ++k) out[k] = V8{};
+#pragma unroll
+                    for (int k = 1; k < W; ++k) win[k - 1] = input_at<E, W>(a, s, t - k, vec);
+                }
+                if (t < s.lo || t >= s.hi) continue;   // a row of no sequence
+                shift<W>(win);
+                win[0] = to_f8(cx[i]);
+                const V8 d = through_act<E>(a.silu, taps.apply(win), to_f8(cd[i]));
+                if (t < r1)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+#pragma unroll
+                        for (int j = 0; j < W; ++j) dw[j].f[e] = __builtin_fmaf(d.f[e], win[W - 1 - j].f[e], dw[j].f[e]);
+                        db.f[e] += d.f[e];
                     }
-                }
-                if (t >= r1 || t >= last) break;
-                while (s.n + 1 < a.nseq && t >= s.hi) s = span_at(a, s.n + 1);
-                if (t >= s.hi) break;   // rows behind the last sequence
+                shift<W>(out);
+                out[0] = V8{};
+#pragma unroll
+                for (int k = 0; k < W; ++k)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) out[k].f[e] = __builtin_fmaf(taps.w[W - 1 - k].f[e], d.f[e], out[k].f[e]);
+                const int64_t row = t - (W - 1);
+                if (row >= s.lo && row >= r0) st8((E*)a.dx + row * a.D + 8 * vec, out[W - 1]);
             }
-            if (t == s.lo) {
-#pragma unroll
-                for (int k = 0; k < W; ++k) out[k] = V8{};
-#pragma unroll
-                for (int k = 1; k < W; ++k) win[k - 1] = input_at<E, W>(a, s, t - k, vec);
-            }
-            const V8 xv = to_f8(nx), dv = to_f8(nd);
-            if (t + 1 < last) fetch(t + 1);
-            if (t < s.lo) continue;   // before the first sequence
-            shift<W>(win);
-            win[0] = xv;
-            const V8 d = through_act<E>(a.silu, taps.apply(win), dv);
-            if (t < r1)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-#pragma unroll
-                    for (int j = 0; j < W; ++j) dw[j].f[e] = __builtin_fmaf(d.f[e], win[W - 1 - j].f[e], dw[j].f[e]);
-                    db.f[e] += d.f[e];
-                }
-            shift<W>(out);
-            out[0] = V8{};
-#pragma unroll
-            for (int k = 0; k < W; ++k)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) out[k].f[e] = __builtin_fmaf(taps.w[W - 1 - k].f[e], d.f[e], out[k].f[e]);
-            const int64_t row = t - (W - 1);
-            if (row >= s.lo && row >= r0) st8((E*)a.dx + row * a.D + 8 * vec, out[W - 1]);
         }
+        if (last >= s.hi) flush(last);
     }
     // the workgroup's runs, always in the same order
     float* pw = a.pw + blk / nvb * a.D * W + (int64_t)8 * vec * W;

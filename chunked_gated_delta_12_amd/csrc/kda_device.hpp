@@ -94,6 +94,11 @@ template <typename E> __device__ __forceinline__ E from_f(float x);
 template <> __device__ __forceinline__ float from_f<float>(float x) { return x; }
 template <> __device__ __forceinline__ bf16 from_f<bf16>(float x) { return (bf16)x; }  // RNE
 
+// Four adjacent elements of a storage type.
+template <typename E> struct Four;
+template <> struct Four<float> { typedef f32x4 T; };
+template <> struct Four<bf16> { typedef bf16x4 T; };
+
 // Two adjacent elements of a storage type, loaded/stored as one unit.
 template <typename E> struct Pair;
 template <> struct Pair<float> { typedef f32x2 T; };

@@ -93,8 +93,7 @@ __device__ __forceinline__ float exp_minus(float v) {
 // softplus(v) = max(v, 0) + log(1 + e^-|v|), with log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3: a relative
 // error of a few 2^-24 for every v, also where e is small and a logarithm of the rounded 1 + e would
 // lose it.  atanh(s) / s is interpolated in s^2 on [0, 1/9] at Chebyshev's points, off by at most 4e-9.
-__device__ __forceinline__ float softplus(float v) {
-    const float e = exp_minus(v);
+__device__ __forceinline__ float softplus_of(float v, float e) {   // e = e^-|v|
     const float s = e * __builtin_amdgcn_rcpf(2.0f + e), q = s * s;
     float p = 1.4078889183e-01f;
     p = __builtin_fmaf(p, q, 1.3982578873e-01f);
@@ -104,6 +103,14 @@ __device__ __forceinline__ float softplus(float v) {
     float m;
     asm("v_max_f32 %0, 0, %1" : "=v"(m) : "v"(v));   // the compiler's is two instructions; NaN comes through p
     return __builtin_fmaf(2.0f * s, p, m);
+}
+
+__device__ __forceinline__ float softplus(float v) { return softplus_of(v, exp_minus(v)); }
+// softplus(v) and its slope sigmoid(v), from one exponential.
+__device__ __forceinline__ float softplus(float v, float& slope) {
+    const float e = exp_minus(v), i = __builtin_amdgcn_rcpf(1.0f + e);
+    slope = v < 0.0f ? e * i : i;
+    return softplus_of(v, e);
 }
 
 // sigmoid(v): in fp32 storage to a few ulp; in bf16 storage from the hardware exponential and
@@ -141,6 +148,17 @@ __device__ __forceinline__ void quad_times(float v, const float* x, float* out) 
     const float w = quad_lane<J>(v);
 #pragma unroll
     for (int i = 0; i < NS; ++i) out[i] = w * x[i];
+}
+// s += sum over j of lane j's v times x[j].  The compiler takes the exchange into a multiplication but not into
+// a fused one; the two wait states are those between a write of v and its exchange, wherever that write stands.
+__device__ __forceinline__ void quad_fma(float& s, float v, const float (&x)[4]) {
+    asm("s_nop 1\n\t"
+        "v_fmac_f32_dpp %0, %1, %2 quad_perm:[0,0,0,0] row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %1, %3 quad_perm:[1,1,1,1] row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %1, %4 quad_perm:[2,2,2,2] row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %0, %1, %5 quad_perm:[3,3,3,3] row_mask:0xf bank_mask:0xf"
+        : "+v"(s)
+        : "v"(v), "v"(x[0]), "v"(x[1]), "v"(x[2]), "v"(x[3]));
 }
 // Lane j of the quad gets the sum of v[j] over the quad.
 __device__ __forceinline__ float quad_sums(const float* v, int q) {
@@ -224,10 +242,7 @@ __device__ __forceinline__ void along_pieces(float (&v)[NS], const float (&A2)[N
     }
 }
 
-// Four neighbouring values as they are stored, and as fp32.
-template <typename E> struct Four;
-template <> struct Four<float> { typedef f32x4 T; };
-template <> struct Four<bf16> { typedef bf16x4 T; };
+// Four neighbouring values as they are stored as fp32.
 template <typename E>
 __device__ __forceinline__ f32x4 to_f4(typename Four<E>::T v) { return f32x4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]}; }
 

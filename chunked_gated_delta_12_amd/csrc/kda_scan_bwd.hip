@@ -15,8 +15,6 @@
 // the decays only, so it is formed in the same sweep).  Gradients: every piece backwards, 16 tokens at a time; a
 // state's 16 decays and products stay in registers between the sweep forwards and the one back.  Sums: what
 // several workgroups have parts of, always in the same order.
-#include <utility>
-
 #include "kda_rows.hpp"
 #include "kda_scan.hpp"
 
@@ -188,28 +186,25 @@ __device__ __forceinline__ float channel_sums(float (&v)[CH], int lane) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)   // row_ror:8, the lane with bit 3 turned
         v[i] = (b3 ? v[i + 2] : v[i]) + quad_perm<0x128>(b3 ? v[i] : v[i + 2]);
-    // bit 2 turned: from four lanes above where it is 0, below where it is 1 (row_ror:12 and row_ror:4)
-    const float send = b2 ? v[0] : v[1], up = quad_perm<0x12c>(send), down = quad_perm<0x124>(send);
-    return (b2 ? v[1] : v[0]) + (b2 ? down : up);
+    // bit 2 turned: row_shr:4 for all, then row_shl:4 over it in the banks of four lanes where the bit is 0
+    const int send = __builtin_bit_cast(int, b2 ? v[0] : v[1]);
+    const int down = __builtin_amdgcn_update_dpp(0, send, 0x114, 0xf, 0xf, false);
+    return (b2 ? v[1] : v[0]) + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(down, send, 0x104, 0xf, 0x5, false));
 }
 
 // Token T of 16's value, which lane T % 4 of the quad holds in v[T / 4].
 template <int T>
 __device__ __forceinline__ float token(const float* v) { return quad_lane<T % 4>(v[T / 4]); }
-template <typename F, int... T>
-__device__ __forceinline__ void each_token_(F f, std::integer_sequence<int, T...>) { (f(std::integral_constant<int, T>{}), ...); }
-template <typename F>
-__device__ __forceinline__ void each_token(F f) { each_token_(f, std::make_integer_sequence<int, CH>{}); }
-
 template <typename E, int NS>
-__global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(2))) scan_bwd_grad(BwdArgs a) {
+__global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(NS == 4 && sizeof(E) == 2 ? 3 : NS <= 8 ? 2 : 1))) scan_bwd_grad(BwdArgs a) {
     constexpr int N = 4 * NS, GROUPS = CH / 4, WAVES = BLOCK / 64;
     __shared__ float bc[2][N * BPAD];
     __shared__ float part[WAVES][CH][2][N];
     // A lane's states, one word each, in turn in registers: 16 tokens' work on one fill those.
     __shared__ float sA[NS][BLOCK], smu[NS][BLOCK], sdA[NS][BLOCK], sh0[NS][BLOCK], sh[NS][BLOCK];
     // what the outputs need of a lane's own tokens beside, while the registers are the states'
-    __shared__ float aside[2][GROUPS][BLOCK];
+    __shared__ float aside[3][GROUPS][BLOCK];
+    __shared__ float chan[4][BLOCK];   // a channel's bias and skip, and its parts of their gradients
     const int me = threadIdx.x;
     const int per = (a.D / a.G + BLOCK_CH - 1) / BLOCK_CH, nblk = a.G * per;
     const int blk = (int)(blockIdx.x % (unsigned)nblk);
@@ -235,7 +230,9 @@ __global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(2)))
     const bool gated = a.z != nullptr;
     const uint32_t own = real ? ((uint32_t)q * (uint32_t)a.D + ch) * (uint32_t)sizeof(E) : NOWHERE, four = 4 * (uint32_t)a.D * (uint32_t)sizeof(E);
     const int64_t ld = (int64_t)a.G * N;
-    const float bias = a.bias ? a.bias[ch] : 0.0f, skip = a.skip ? a.skip[ch] : 0.0f;
+    chan[0][me] = a.bias ? a.bias[ch] : 0.0f;
+    chan[1][me] = a.skip ? a.skip[ch] : 0.0f;
+    chan[2][me] = chan[3][me] = 0.0f;
     const int64_t chunk0 = first_chunk(a.seqs, pl) + t_first / CH;
 
     float A2[NS], mu[NS], h0[NS];
@@ -276,26 +273,26 @@ __global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(2)))
         ld_states<NS>(a.start + (chunk0 + chunk) * states + (uint32_t)at_state, nh);
         ns = a.before[(chunk0 + chunk) * a.D + (uint32_t)ch];
     };
-    float dskip = 0.0f, dbias = 0.0f;
     const int chunks = (n + CH - 1) / CH;
     if (chunks > 0) fetch(chunks - 1);
     for (int k = chunks - 1; k >= 0; --k) {
-        float xv[GROUPS], dv[GROUPS], uv[GROUPS], vy[GROUPS];
+        float dv[GROUPS], uv[GROUPS], vy[GROUPS];
         next.each([&](bool of_c, int t, int n0, f32x4 x) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) bc[of_c ? 1 : 0][(n0 + j) * BPAD + t] = x[j];
         });
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
-            dv[g] = value<E>(nt[g]) + bias;
-            xv[g] = value<E>(nx[g]);
+            dv[g] = value<E>(nt[g]) + chan[0][me];
+            uv[g] = aside[2][g][me] = value<E>(nx[g]);
             vy[g] = value<E>(nd[g]);
         }
         if (a.softplus) {
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g) {
-                aside[0][g][me] = sigmoid<float>(dv[g]);
-                dv[g] = softplus(dv[g]);
+                float slope;
+                dv[g] = softplus(dv[g], slope);
+                aside[0][g][me] = slope;
             }
         } else {
 #pragma unroll
@@ -312,7 +309,7 @@ __global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(2)))
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
             if (4 * g >= left) dv[g] = aside[0][g][me] = 0.0f;   // a step of nothing behind the last token: x and dy are zero there
-            uv[g] = dv[g] * xv[g];
+            uv[g] *= dv[g];
         }
 #pragma unroll
         for (int i = 0; i < NS; ++i)
@@ -329,35 +326,47 @@ __global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(2)))
             // that; the empty statements keep the compiler from drawing the tokens together.
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g) asm volatile("" : "+v"(dv[g]), "+v"(uv[g]), "+v"(vy[g]));
-            float bv[CH], cv[CH], e[CH], hp[CH], v[CH];
-            ld_states<CH>(bc[0] + (q * NS + i) * BPAD, bv);
-            ld_states<CH>(bc[1] + (q * NS + i) * BPAD, cv);
+            float e[CH], hp[CH], v[CH];
+            const float *bi = bc[0] + (q * NS + i) * BPAD, *ci = bc[1] + (q * NS + i) * BPAD;
             float h = sh[i][me];
             const float A2i = sA[i][me], Ai = A2i * (1.0f / LOG2E);
-            each_token([&](auto T) {
-                constexpr int t = decltype(T)::value;
-                hp[t] = h;
-                e[t] = __builtin_amdgcn_exp2f(token<t>(dv) * A2i);
-                h = __builtin_fmaf(e[t], h, token<t>(uv) * bv[t]);
-                sy[t] = __builtin_fmaf(cv[t], h, sy[t]);
-                v[t] = token<t>(vy) * h;   // zero of lanes without a channel: they read nothing
-                if (t % 2) asm volatile("" : : "v"(v[t]), "v"(sy[t]));
+            each_of_quad([&](auto Gr) {
+                constexpr int t0 = 4 * decltype(Gr)::value;
+                float bv[4], cv[4];
+                ld_states<4>(bi + t0, bv);
+                ld_states<4>(ci + t0, cv);
+                each_of_quad([&](auto J) {
+                    constexpr int j = decltype(J)::value, t = t0 + j;
+                    hp[t] = h;
+                    e[t] = __builtin_amdgcn_exp2f(token<t>(dv) * A2i);
+                    h = __builtin_fmaf(e[t], h, token<t>(uv) * bv[j]);
+                    sy[t] = __builtin_fmaf(cv[j], h, sy[t]);
+                    v[t] = token<t>(vy) * h;   // zero of lanes without a channel: they read nothing
+                });
+                asm volatile("" : : "v"(v[t0]), "v"(v[t0 + 1]), "v"(v[t0 + 2]), "v"(v[t0 + 3]), "v"(sy[t0 + 3]) : "memory");
             });
             const int t_mine = lane >> 2;
             part[wave][t_mine][1][q * NS + i] = channel_sums(v, lane);
 #pragma unroll
-            for (int g = 0; g < GROUPS; ++g) asm volatile("" : "+v"(dv[g]), "+v"(uv[g]), "+v"(vy[g]));
+            for (int g = 0; g < GROUPS; ++g) asm volatile("" : "+v"(dv[g]), "+v"(uv[g]), "+v"(vy[g]) : : "memory");
             float m = smu[i][me], s = 0.0f;
-            each_token([&](auto T) {
-                constexpr int t = CH - 1 - decltype(T)::value;
-                const float lam = token<t>(vy) * cv[t] + m;
-                v[t] = token<t>(uv) * lam;
-                m = e[t] * lam;
-                const float w = m * hp[t];   // lam a_t h_t-1
-                s1[t] = __builtin_fmaf(lam, bv[t], s1[t]);
-                s2[t] = __builtin_fmaf(Ai, w, s2[t]);
-                s += token<t>(dv) * w;
-                if (t % 2 == 0) asm volatile("" : : "v"(v[t]), "v"(s));
+            each_of_quad([&](auto Gr) {
+                constexpr int t0 = CH - 4 - 4 * decltype(Gr)::value;
+                float bv[4], cv[4];
+                ld_states<4>(bi + t0, bv);
+                ld_states<4>(ci + t0, cv);
+                float w[4];
+                each_of_quad([&](auto J) {
+                    constexpr int j = 3 - decltype(J)::value, t = t0 + j;
+                    const float lam = token<t>(vy) * cv[j] + m;
+                    v[t] = token<t>(uv) * lam;
+                    m = e[t] * lam;
+                    w[j] = m * hp[t];   // lam a_t h_t-1
+                    s1[t] = __builtin_fmaf(lam, bv[j], s1[t]);
+                    s2[t] = __builtin_fmaf(Ai, w[j], s2[t]);
+                });
+                quad_fma(s, dv[t0 / 4], w);
+                asm volatile("" : : "v"(v[t0]), "v"(v[t0 + 1]), "v"(v[t0 + 2]), "v"(v[t0 + 3]), "v"(s) : "memory");
             });
             smu[i][me] = m;
             sdA[i][me] += s;
@@ -366,21 +375,25 @@ __global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(2)))
         const int64_t from = row + CH * k;
         const int tokens = n - CH * k < CH ? n - CH * k : CH;
         const Rsrc wx = rows_rsrc<E>(a.dx, from, a.D, tokens), wt = rows_rsrc<E>(a.ddt, from, a.D, tokens);
+        const float skip = chan[1][me];
+        float dskip = chan[3][me], dbias = chan[2][me];
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
             const float lb = quad_sums(s1 + 4 * g, q), lw = quad_sums(s2 + 4 * g, q);
-            const float ddt = __builtin_fmaf(xv[g], lb, lw) * aside[0][g][me];
+            const float xv = aside[2][g][me], ddt = __builtin_fmaf(xv, lb, lw) * aside[0][g][me];
             st_one<E>(wx, own + g * four, __builtin_fmaf(skip, vy[g], dv[g] * lb));
             st_one<E>(wt, own + g * four, ddt);
-            dskip = __builtin_fmaf(vy[g], xv[g], dskip);
+            dskip = __builtin_fmaf(vy[g], xv, dskip);
             dbias += ddt;   // zero where there is no token
         }
         if (gated) {
             const Rsrc wz = rows_rsrc<E>(a.dz, from, a.D, tokens);
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g)
-                st_one<E>(wz, own + g * four, aside[1][g][me] * __builtin_fmaf(skip, xv[g], quad_sums(sy + 4 * g, q)));
+                st_one<E>(wz, own + g * four, aside[1][g][me] * __builtin_fmaf(skip, aside[2][g][me], quad_sums(sy + 4 * g, q)));
         }
+        chan[3][me] = dskip;
+        chan[2][me] = dbias;
         lds_barrier();
         // the workgroup's part of db and dc
         float* to = a.pbc + ((int64_t)blk * a.rows + row + CH * k) * 2 * N;
@@ -392,8 +405,7 @@ __global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(2)))
             to[i] = s;
         }
     }
-    dskip = quad_sum(dskip);
-    dbias = quad_sum(dbias);
+    const float dskip = quad_sum(chan[3][me]), dbias = quad_sum(chan[2][me]);
     float dA[NS];
 #pragma unroll
     for (int i = 0; i < NS; ++i) dA[i] = sdA[i][me], mu[i] = smu[i][me];
@@ -421,8 +433,15 @@ scan_bwd_bc(Seqs s, int64_t rows, int G, int N, int per, const float* __restrict
         const int64_t row = i / each;
         const int r = (int)(i - row * each), g = r / (2 * N), j = r - g * 2 * N;
         if (row < lo || row >= hi) continue;
-        float t = 0.0f;
-        for (int k = 0; k < per; ++k) t += part[((int64_t)(g * per + k) * rows + row) * 2 * N + j];
+        const float* p = part + ((int64_t)g * per * rows + row) * 2 * N + j;
+        const int64_t ld = rows * 2 * N;
+        float u[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        int k = 0;
+        for (; k + 8 <= per; k += 8)   // eight loads in flight
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[e] += p[(k + e) * ld];
+        for (; k < per; ++k) u[0] += p[k * ld];
+        const float t = ((u[0] + u[1]) + (u[2] + u[3])) + ((u[4] + u[5]) + (u[6] + u[7]));
         (j < N ? db : dc)[(row * G + g) * N + (j < N ? j : j - N)] = from_f<E>(t);
     }
 }
@@ -430,7 +449,7 @@ scan_bwd_bc(Seqs s, int64_t rows, int G, int N, int per, const float* __restrict
 static int bwd_piece(int nseq, int T, int D, int G, bool packed) {
     const int64_t blocks = blocks_of(D, G), rows = packed ? T : (int64_t)nseq * T;
     const int64_t whole = ((int64_t)T + TILE - 1) / TILE * TILE;
-    const int64_t pieces = 1024 / blocks > 1 ? 1024 / blocks : 1;
+    const int64_t pieces = 2048 / blocks > 1 ? 2048 / blocks : 1;
     int64_t len = rows / pieces;
     if (len < 2 * TILE) len = 2 * TILE;
     if (len < T / 256) len = T / 256;

@@ -19,6 +19,19 @@ struct StepArgs {
     void* y;
 };
 
+// NS values as they are stored.
+template <typename E, int NS>
+struct StateVec {
+    static constexpr int V = NS < 4 ? NS : 4;
+    typedef E T __attribute__((__vector_size__(V * sizeof(E))));
+    T v[NS / V];
+    __device__ __forceinline__ void load(const E* p) {
+#pragma unroll
+        for (int i = 0; i < NS / V; ++i) v[i] = *reinterpret_cast<const T*>(p + V * i);
+    }
+    __device__ __forceinline__ float at(int i) const { return (float)v[i / V][i % V]; }
+};
+
 template <typename E, int NS>
 __global__ void __launch_bounds__(BLOCK) scan_step(StepArgs a) {
     constexpr int N = 4 * NS;
@@ -37,45 +50,61 @@ __global__ void __launch_bounds__(BLOCK) scan_step(StepArgs a) {
     const bool real = in_group < Dg;
     const int ch = grp * Dg + (real ? in_group : Dg - 1);
     float* Sp = a.S + ((int64_t)slot * a.D + ch) * N + q * NS;
+    const int64_t row = (int64_t)r * a.T, ld = (int64_t)a.G * N;
+    const E *b = (const E*)a.b + row * ld + grp * N + q * NS, *c = (const E*)a.c + row * ld + grp * N + q * NS;
+    // everything that the first tokens take is asked for before the search for an earlier row of the slot
     float h[NS], A2[NS];
     ld_states<NS>(Sp, h);
     ld_states<NS>(a.A + (int64_t)ch * N + q * NS, A2);
+    const float bias = a.bias ? a.bias[ch] : 0.0f, skip = a.skip ? a.skip[ch] : 0.0f;
+    E xr, dr, zr;
+    auto fetch = [&](int t0) {
+        const int64_t off = (row + (t0 + q < n ? t0 + q : n - 1)) * a.D + ch;
+        xr = ((const E*)a.x)[off];
+        dr = ((const E*)a.dt)[off];
+        if (a.z) zr = ((const E*)a.z)[off];
+    };
+    StateVec<E, NS> nb, nc;
+    fetch(0);
+    nb.load(b);
+    nc.load(c);
     if (a.slots) {   // of the rows with tokens that name one slot, the first has it; the others are padding
         int twice = 0;
+#pragma unroll 4
         for (int i = lane; i < r; i += 64)
             if (a.slots[i] == slot) twice |= !a.ntok || a.ntok[i] > 0;
         if (__ballot(twice)) return;
     }
 #pragma unroll
     for (int i = 0; i < NS; ++i) A2[i] *= LOG2E;
-    const float bias = a.bias ? a.bias[ch] : 0.0f, skip = a.skip ? a.skip[ch] : 0.0f;
-    const int64_t row = (int64_t)r * a.T, ld = (int64_t)a.G * N;
-    const E *b = (const E*)a.b + row * ld + grp * N + q * NS, *c = (const E*)a.c + row * ld + grp * N + q * NS;
     for (int t0 = 0; t0 < n; t0 += 4) {
-        const int t = t0 + q;
-        const int64_t off = (row + (t < n ? t : n - 1)) * a.D + ch;
-        const float xv = (float)((const E*)a.x)[off];
-        float d = (float)((const E*)a.dt)[off] + bias;
+        const float xv = (float)xr, zv = a.z ? (float)zr : 0.0f;
+        float d = (float)dr + bias;
+        if (t0 + 4 < n) fetch(t0 + 4);
         if (a.softplus) d = softplus(d);
         const float u = d * xv;
-        const float zv = a.z ? (float)((const E*)a.z)[off] : 0.0f;
-        const float dj[4] = {quad_lane<0>(d), quad_lane<1>(d), quad_lane<2>(d), quad_lane<3>(d)};
-        const float uj[4] = {quad_lane<0>(u), quad_lane<1>(u), quad_lane<2>(u), quad_lane<3>(u)};
         float yj[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (t0 + j >= n) break;
-            const E *bp = b + (t0 + j) * ld, *cp = c + (t0 + j) * ld;
+        each_of_quad([&](auto J) {
+            constexpr int j = decltype(J)::value;
+            if (t0 + j >= n) return;
+            const StateVec<E, NS> bv = nb, cv = nc;
+            if (t0 + j + 1 < n) {   // the next token's
+                nb.load(b + (t0 + j + 1) * ld);
+                nc.load(c + (t0 + j + 1) * ld);
+            }
+            const float dj = quad_lane<j>(d), uj = quad_lane<j>(u);
+            float s = 0.0f;
 #pragma unroll
             for (int i = 0; i < NS; ++i) {
-                h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(dj[j] * A2[i]), h[i], uj[j] * (float)bp[i]);
-                yj[j] = i ? __builtin_fmaf((float)cp[i], h[i], yj[j]) : (float)cp[i] * h[i];
+                h[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(dj * A2[i]), h[i], uj * bv.at(i));
+                s = i ? __builtin_fmaf(cv.at(i), h[i], s) : cv.at(i) * h[i];
             }
-        }
+            yj[j] = s;
+        });
         float yv = quad_sums(yj, q);
         if (a.skip) yv = __builtin_fmaf(skip, xv, yv);
         if (a.z) yv *= zv * sigmoid<E>(zv);
-        if (t < n && real) ((E*)a.y)[off] = from_f<E>(yv);
+        if (t0 + q < n && real) ((E*)a.y)[(row + t0 + q) * a.D + ch] = from_f<E>(yv);
     }
     if (real) st_states<NS>(Sp, h);
 }
