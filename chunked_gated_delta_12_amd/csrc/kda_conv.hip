@@ -296,22 +296,26 @@ __global__ void __launch_bounds__(256) conv_bwd_kernel(ConvArgs a, int VB, int s
         }
         if (last >= s.hi) flush(last);
     }
-    // the workgroup's runs, always in the same order
+    // the workgroup's runs, halved step by step in a fixed order
     float* pw = a.pw + blk / nvb * a.D * W + (int64_t)8 * vec * W;
 #pragma unroll
     for (int j = 0; j <= W; ++j) {
-        const V8 v = j < W ? dw[j < W ? j : 0] : db;
-        __syncthreads();
+        V8 v = j < W ? dw[j < W ? j : 0] : db;
+        for (int half = runs / 2; half > 0; half /= 2) {
+            __syncthreads();
+            if (sub >= half && sub < 2 * half)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) lds[e * 256 + threadIdx.x] = v.f[e];
-        __syncthreads();
+                for (int e = 0; e < 8; ++e) lds[e * 256 + threadIdx.x] = v.f[e];
+            __syncthreads();
+            if (sub < half)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v.f[e] += lds[e * 256 + threadIdx.x + half * VB];
+        }
         if (sub == 0 && vec < nvec)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float u = 0.0f;
-                for (int i = 0; i < runs; ++i) u += lds[e * 256 + i * VB + lane];
-                if (j < W) pw[e * W + j] = u;
-                else a.pb[blk / nvb * a.D + 8 * vec + e] = u;
+                if (j < W) pw[e * W + j] = v.f[e];
+                else a.pb[blk / nvb * a.D + 8 * vec + e] = v.f[e];
             }
     }
 }
@@ -335,10 +339,7 @@ __global__ void __launch_bounds__(64) conv_step_kernel(ConvStepArgs a) {
     const int slot = a.slots ? a.slots[r] : r;
     if (n <= 0 || slot < 0 || slot >= a.nslot) return;   // a padded row: nothing of it is touched
     if (a.slots) {   // of the rows with tokens that name one slot, the first has it; the others are padding
-        int twice = 0;
-        for (int i = (int)threadIdx.x; i < r; i += 64)
-            if (a.slots[i] == slot) twice |= !a.ntok || a.ntok[i] > 0;
-        if (__ballot(twice)) return;
+        if (earlier_row(a.slots, a.ntok, r, slot, (int)threadIdx.x)) return;
     }
     if (vec >= nvec) return;
     E* Sp = (E*)a.S + (int64_t)slot * (W - 1) * D + 8 * vec;

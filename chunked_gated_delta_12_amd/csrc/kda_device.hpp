@@ -117,6 +117,25 @@ __device__ __forceinline__ void store_pair(E* p, float a, float b) {
     *reinterpret_cast<typename Pair<E>::T*>(p) = v;
 }
 
+// ---------------------------------------------------------------- rows and slots
+// Whether a row before row r that has tokens (ntok NULL: every one) names the same slot; the answer is the
+// wavefront's.  256 rows at a time: the search is every wavefront's own and grows with the rows before it.
+__device__ __forceinline__ bool earlier_row(const int* __restrict__ slots, const int* __restrict__ ntok, int r, int slot, int lane) {
+    typedef int i32x4 __attribute__((__vector_size__(16)));
+    int twice = 0;
+    const int whole = r & ~3;   // slots is 16-byte aligned
+#pragma unroll 2
+    for (int i = 4 * lane; i < whole; i += 256) {
+        const i32x4 s = *reinterpret_cast<const i32x4*>(slots + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (s[j] == slot) twice |= !ntok || ntok[i + j] > 0;
+    }
+    const int i = whole + lane;
+    if (i < r && slots[i] == slot) twice |= !ntok || ntok[i] > 0;
+    return __ballot(twice) != 0;
+}
+
 // ---------------------------------------------------------------- MFMA wrappers
 // K = 16 bf16 products run on the 16x16x32 instruction with the upper four
 // k-slots of each lane group zeroed on both operands.  The legacy 16x16x16

@@ -63,13 +63,19 @@ __device__ __forceinline__ bool place_of(const Seqs& s, int64_t slot, Place& p) 
         p.first = (int64_t)p.seq * pieces;
         return true;
     }
-    int lo = 0, hi = s.nseq - 1;   // the last sequence whose first slot is not behind this one
-    while (lo < hi) {
-        const int mid = lo + (hi - lo + 1) / 2;
-        if (held(s.cu[mid], 0, s.T) / s.piece + (int64_t)mid <= slot) lo = mid;
-        else hi = mid - 1;
+    // The last sequence whose first slot is not behind this one: 64 candidates at a time, so that 4,096 sequences take
+    // two loads one after the other.
+    const int lane = (int)threadIdx.x & 63;
+    int lo = 0, n = s.nseq;   // it is one of lo .. lo + n - 1
+    while (n > 1) {
+        const int by = (n + 63) / 64, i = lane * by;
+        const bool behind = i < n && held(s.cu[lo + i], 0, s.T) / s.piece + (int64_t)(lo + i) > slot;
+        const uint64_t before = __ballot(i < n && !behind);
+        // offsets that rise leave one run of candidates before; the first is taken where there is none
+        const int k = before ? 63 - __builtin_clzll(before) : 0;
+        lo = uniform(lo + k * by);
+        n = uniform(n - k * by < by ? n - k * by : by);
     }
-    lo = uniform(lo);
     const int r0 = uniform(held(s.cu[lo], 0, s.T)), r1 = uniform(held(s.cu[lo + 1], r0, s.T));
     p.seq = lo;
     p.row0 = r0;

@@ -157,9 +157,9 @@ __global__ void __launch_bounds__(BLOCK) scan_bwd_map(BwdArgs a) {
         }
     }
     sum = quad_sum(sum);
-    if (real) {
-        st_states<NS>(a.local + slot * states + at_state, h);
-        if (BACK) st_states<NS>(a.grad + slot * states + at_state, m);
+    if (BACK && real && pl.pieces > 1) {   // what the other pieces of the sequence ask for
+        if (pl.k < pl.pieces - 1) st_states<NS>(a.local + slot * states + at_state, h);
+        if (pl.k > 0) st_states<NS>(a.grad + slot * states + at_state, m);
         if (q == 0) a.sums[slot * a.D + ch] = sum;
     }
 }

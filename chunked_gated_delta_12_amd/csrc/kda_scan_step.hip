@@ -69,11 +69,7 @@ __global__ void __launch_bounds__(BLOCK) scan_step(StepArgs a) {
     nb.load(b);
     nc.load(c);
     if (a.slots) {   // of the rows with tokens that name one slot, the first has it; the others are padding
-        int twice = 0;
-#pragma unroll 4
-        for (int i = lane; i < r; i += 64)
-            if (a.slots[i] == slot) twice |= !a.ntok || a.ntok[i] > 0;
-        if (__ballot(twice)) return;
+        if (earlier_row(a.slots, a.ntok, r, slot, lane)) return;
     }
 #pragma unroll
     for (int i = 0; i < NS; ++i) A2[i] *= LOG2E;
