@@ -724,8 +724,9 @@ static int check_conv(int dtype, int act, int a, int T, int D, int W) {
     if (T > 1 << 30) return fail(KDA_ERR_SHAPE, "T=%d above 2^30", T);
     if (D < 8 || D > 1 << 20 || D % 8) return fail(KDA_ERR_SHAPE, "D=%d must be a multiple of 8 from 8 to 2^20", D);
     if (W < 2 || W > 4) return fail(KDA_ERR_SHAPE, "W=%d not in {2, 3, 4}", W);
-    // a launch has at most 2^32 threads: one for eight channels of eight rows at the least, and of each sequence's state
-    if (((int64_t)a * T / 8 + 2 * (int64_t)a + 1) >= (1LL << 31) / (D / 8)) return fail(KDA_ERR_SHAPE, "sequences*T*D too large");
+    // a launch has at most 2^32 threads: one for eight channels of eight rows at the least, filled up to whole
+    // wavefronts, and one for eight channels of each sequence's state
+    if (((int64_t)a * T / 8 + 2 * (int64_t)a + 1) >= (1LL << 30) / (D / 8)) return fail(KDA_ERR_SHAPE, "sequences*T*D too large");
     return KDA_OK;
 }
 

@@ -7,6 +7,11 @@
 //     dx_s = sum_j w_j dp_{s+W-1-j} (+ the last state's gradient),  dw_j = sum_t dp_t x_{t-W+1+j},  dbias = sum_t dp_t
 // All arithmetic is fp32, rounded once.  Both passes are bound by HBM: a lane owns eight channels and
 // a run of rows, whose last W inputs stay in registers; a run reads W - 1 rows of its neighbour's.
+// Measured, bf16, 4 taps, silu: forwards 65,536 rows of 6,144 channels 316 us (1.61 GB, 5.1 TB/s, a large copy's rate);
+// backwards 32,768 rows of 2,048 channels in six packed sequences 102 us (403 MB, 3.9 TB/s; 12 us of it two other
+// launches), where the taps, their sums, the inputs and the waiting gradients are 200 registers and a SIMD
+// has two wavefronts.  Four channels a lane (119), two (114 to 120), rows without branches in the middle of
+// a run (114 beside 110) and other lengths of runs gained nothing there.
 #include "kda_launch.hpp"
 #include "kda_rows.hpp"
 
@@ -15,7 +20,7 @@ namespace kda {
 namespace {
 
 struct ConvArgs {
-    int nseq, T, D, W, run;   // run: rows a lane
+    int nseq, T, D, run;   // run: rows a lane
     int64_t rows;
     bool silu;
     const int* cu;
@@ -362,7 +367,8 @@ __global__ void __launch_bounds__(64) conv_step_kernel(ConvStepArgs a) {
     for (int k = 1; k < W; ++k) st8(Sp + (int64_t)(W - 1 - k) * D, win[k - 1]);
 }
 
-// Rows a lane: long runs read little of their neighbours', short ones fill the device.
+// Rows a lane: long runs read little of their neighbours' (3 rows in 32), short ones fill the device: 2^18 lanes
+// are 16 wavefronts a compute unit.
 int fwd_run(int64_t rows, int D) {
     int run = 32;
     while (run > 8 && (rows + run - 1) / run * (D / 8) < 1 << 18) run /= 2;
@@ -415,7 +421,7 @@ hipError_t conv_step_t(int B, const ConvStepArgs& a, hipStream_t stream) {
 
 ConvArgs args_of(const ConvCall& c) {
     ConvArgs a{};
-    a.nseq = c.nseq, a.T = c.T, a.D = c.D, a.W = c.W, a.silu = c.silu, a.cu = c.cu;
+    a.nseq = c.nseq, a.T = c.T, a.D = c.D, a.silu = c.silu, a.cu = c.cu;
     a.rows = c.cu ? c.T : (int64_t)c.nseq * c.T;
     a.x = c.x, a.S0 = c.S0, a.w = c.w, a.bias = c.bias;
     return a;

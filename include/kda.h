@@ -575,7 +575,9 @@ int kda_short_conv_step(int dtype, int act, int B, int T, int D, int W, int nslo
  *     h = (r - mean(r)) / sqrt(mean((r - mean(r))^2) + eps) * w + b    (w, b NULL: 1 and 0)
  * All arithmetic is fp32; h is formed from r before r is rounded.
  *
- *   rows, D, eps as for kda_block_norm_fwd; with eps 0 a row of equal values is 0 / 0, NaN
+ *   rows, D, eps as for kda_block_norm_fwd; with eps 0 a row of equal values has no
+ *                direction and comes out as NaN or as rounding errors.  The sum of the squares
+ *                is fp32: values within 1e19 / sqrt(D) of their mean are in its range
  *   y, x         [rows, D]  dtype;  w, b  [D] fp32
  *   r            [rows, D]  dtype, written; may be x itself; NULL exactly when x is
  *   h            [rows, D]  dtype, written
