@@ -117,10 +117,10 @@ def load_library(path: str = LIB_PATH):
     lib.kda_block_norm_bwd_workspace_size.argtypes = [ctypes.c_longlong, c_int, ctypes.POINTER(c_size)]
     lib.kda_block_norm_bwd_workspace_size.restype = c_int
     ll, f32 = ctypes.c_longlong, ctypes.c_float
-    for name, args in (("sel_scan_fwd", [c_int] * 7 + [vp] * 13 + [c_size, vp]), ("sel_scan_bwd", [c_int] * 7 + [vp] * 22 + [c_size, vp]),
+    for name, args in (("sel_scan_fwd", [c_int] * 7 + [vp, c_int] + [vp] * 12 + [c_size, vp]), ("sel_scan_bwd", [c_int] * 7 + [vp] * 22 + [c_size, vp]),
                        ("sel_scan_fwd_workspace_size", [c_int] * 6 + [ctypes.POINTER(c_size)]),
                        ("sel_scan_bwd_workspace_size", [c_int] * 6 + [ctypes.POINTER(c_size)]),
-                       ("sel_scan_step", [c_int] * 8 + [vp] * 13), ("short_conv_fwd", [c_int] * 6 + [vp] * 8),
+                       ("sel_scan_step", [c_int] * 8 + [vp] * 13), ("short_conv_fwd", [c_int] * 6 + [vp, c_int] + [vp] * 7),
                        ("short_conv_bwd", [c_int] * 6 + [vp] * 12 + [c_size, vp]),
                        ("short_conv_bwd_workspace_size", [ll, c_int, c_int, ctypes.POINTER(c_size)]),
                        ("short_conv_step", [c_int] * 7 + [vp] * 8), ("layer_norm_fwd", [c_int, ll, c_int, f32] + [vp] * 7),
@@ -727,11 +727,9 @@ def kda_sel_scan_fwd(x, dt, A, b, c, S0=None, *, skip=None, z=None, dt_bias=None
         if workspace is None:
             nbytes = kda_sel_scan_fwd_workspace_size(nseq, T, D, N, G, cu_seqlens is not None)
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-        if made and cu_seqlens is not None:
-            _clear_rows(nseq, T, cu_seqlens, (y,), st)
         _check("kda_sel_scan_fwd",
-               lib.kda_sel_scan_fwd(code, nseq, T, D, N, G, int(softplus), _at(cu_seqlens), _at(x), _at(dt), _at(A), _at(b), _at(c),
-                                    _at(skip), _at(z), _at(dt_bias), _at(S0), _at(y), _at(S_T), _at(workspace), _bytes(workspace), st))
+               lib.kda_sel_scan_fwd(code, nseq, T, D, N, G, int(softplus), _at(cu_seqlens), int(made), _at(x), _at(dt), _at(A), _at(b),
+                                    _at(c), _at(skip), _at(z), _at(dt_bias), _at(S0), _at(y), _at(S_T), _at(workspace), _bytes(workspace), st))
     return y, S_T
 
 
@@ -755,8 +753,6 @@ def kda_sel_scan_bwd(x, dt, A, b, c, dy, S0=None, dS_T=None, *, skip=None, z=Non
         d["dS0"] = torch.empty((nseq, D, N), dtype=torch.float32, device=dev) if want_dS0 else None
         if workspace is None:
             workspace = torch.empty(kda_sel_scan_bwd_workspace_size(nseq, T, D, N, G, cu_seqlens is not None), dtype=torch.uint8, device=dev)
-        if cu_seqlens is not None:
-            _clear_rows(nseq, T, cu_seqlens, [d[name] for name in ("dx", "ddt", "db", "dc", "dz") if d[name] is not None], st)
         _check("kda_sel_scan_bwd",
                lib.kda_sel_scan_bwd(code, nseq, T, D, N, G, int(softplus), _at(cu_seqlens), _at(x), _at(dt), _at(A), _at(b), _at(c),
                                     _at(skip), _at(z), _at(dt_bias), _at(S0), _at(dy), _at(dS_T), _at(d["dx"]), _at(d["ddt"]),
@@ -813,10 +809,9 @@ def kda_short_conv_fwd(x, w, S0=None, *, bias=None, act=None, cu_seqlens=None, y
         y = _made(y, "y", x.dtype, x.shape, dev)
         if S_T is not None or want_state:
             S_T = _made(S_T, "S_T", x.dtype, (nseq, W - 1, D), dev)
-        if made and cu_seqlens is not None:
-            _clear_rows(nseq, T, cu_seqlens, (y,), st)
         _check("kda_short_conv_fwd",
-               lib.kda_short_conv_fwd(code, a, nseq, T, D, W, _at(cu_seqlens), _at(x), _at(w), _at(bias), _at(S0), _at(y), _at(S_T), st))
+               lib.kda_short_conv_fwd(code, a, nseq, T, D, W, _at(cu_seqlens), int(made), _at(x), _at(w), _at(bias), _at(S0), _at(y), _at(S_T),
+                                      st))
     return y, S_T
 
 
@@ -842,8 +837,6 @@ def kda_short_conv_bwd(x, w, dy, S0=None, dS_T=None, *, bias=None, act=None, cu_
              "dS0": torch.empty((nseq, W - 1, D), dtype=x.dtype, device=dev) if want_dS0 else None}
         if workspace is None:
             workspace = torch.empty(kda_short_conv_bwd_workspace_size(B * x.shape[1], D, W), dtype=torch.uint8, device=dev)
-        if cu_seqlens is not None:
-            _clear_rows(nseq, T, cu_seqlens, (d["dx"],), st)
         _check("kda_short_conv_bwd",
                lib.kda_short_conv_bwd(code, a, nseq, T, D, W, _at(cu_seqlens), _at(x), _at(w), _at(bias), _at(S0), _at(dy), _at(dS_T),
                                       _at(d["dx"]), _at(d["dw"]), _at(d["dbias"]), _at(d["dS0"]), _at(workspace), _bytes(workspace), st))

@@ -633,14 +633,15 @@ int kda_sel_scan_bwd_workspace_size(int nseq, int T, int D, int N, int G, int pa
     return scan_workspace_size(true, nseq, T, D, N, G, packed, bytes);
 }
 
-int kda_sel_scan_fwd(int dtype, int nseq, int T, int D, int N, int G, int softplus, const int* cu_seqlens, const void* x,
-                     const void* dt, const float* A, const void* b, const void* c, const float* skip, const void* z,
+int kda_sel_scan_fwd(int dtype, int nseq, int T, int D, int N, int G, int softplus, const int* cu_seqlens, int zero_rest,
+                     const void* x, const void* dt, const float* A, const void* b, const void* c, const float* skip, const void* z,
                      const float* dt_bias, const float* S0, void* y, float* S_T, void* workspace, size_t workspace_bytes,
                      void* stream) {
     int st = check_scan(dtype, nseq, T, D, N, G, softplus);
     if (st) return st;
     const bool packed = cu_seqlens != nullptr;
     if ((st = check_workgroups(kda::scan_fwd_workgroups(nseq, T, D, G, packed)))) return st;
+    if (zero_rest != 0 && zero_rest != 1) return fail(KDA_ERR_SHAPE, "zero_rest=%d not in {0, 1}", zero_rest);
     if (!x || !dt || !A || !b || !c || !y) return fail(KDA_ERR_NULL, "x, dt, A, b, c and y must be non-NULL");
     const size_t need = kda::scan_fwd_workspace_bytes(nseq, T, D, N, G, packed);
     if (need && (!workspace || workspace_bytes < need))
@@ -654,7 +655,7 @@ int kda_sel_scan_fwd(int dtype, int nseq, int T, int D, int N, int G, int softpl
     const Range out[] = {rng("y", y, nx), rng("S_T", S_T, ns), rng("workspace", need ? workspace : nullptr, need)};
     if ((st = check_ranges(in, 10, out, 3))) return st;
     const kda::ScanCall call{dtype == KDA_F32, nseq, T, D, N, G, softplus != 0, cu_seqlens, x, dt, b, c, z, A, skip, dt_bias, S0};
-    hipError_t e = kda::launch_scan_fwd(call, y, S_T, need ? workspace : nullptr, reinterpret_cast<hipStream_t>(stream));
+    hipError_t e = kda::launch_scan_fwd(call, zero_rest != 0, y, S_T, need ? workspace : nullptr, reinterpret_cast<hipStream_t>(stream));
     if (e != hipSuccess) return fail(KDA_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
     return ok();
 }
@@ -730,11 +731,12 @@ static int check_conv(int dtype, int act, int a, int T, int D, int W) {
     return KDA_OK;
 }
 
-int kda_short_conv_fwd(int dtype, int act, int nseq, int T, int D, int W, const int* cu_seqlens, const void* x, const float* w,
-                       const float* bias, const void* S0, void* y, void* S_T, void* stream) {
+int kda_short_conv_fwd(int dtype, int act, int nseq, int T, int D, int W, const int* cu_seqlens, int zero_rest, const void* x,
+                       const float* w, const float* bias, const void* S0, void* y, void* S_T, void* stream) {
     int st = check_conv(dtype, act, cu_seqlens ? 1 : nseq, T, D, W);
     if (st) return st;
     if (cu_seqlens && (st = check_conv(dtype, act, nseq, 1, D, W))) return st;
+    if (zero_rest != 0 && zero_rest != 1) return fail(KDA_ERR_SHAPE, "zero_rest=%d not in {0, 1}", zero_rest);
     if (!x || !w || !y) return fail(KDA_ERR_NULL, "x, w and y must be non-NULL");
     const size_t es = dtype == KDA_BF16 ? 2 : 4, tok = cu_seqlens ? (size_t)T : (size_t)nseq * T;
     const size_t nx = tok * D * es, ns = (size_t)nseq * (W - 1) * D * es;
@@ -743,7 +745,7 @@ int kda_short_conv_fwd(int dtype, int act, int nseq, int T, int D, int W, const 
     const Range out[] = {rng("y", y, nx), rng("S_T", S_T, ns)};
     if ((st = check_ranges(in, 5, out, 2))) return st;
     const kda::ConvCall call{dtype == KDA_F32, nseq, T, D, W, act == KDA_CONV_SILU, cu_seqlens, x, S0, w, bias};
-    hipError_t e = kda::launch_conv_fwd(call, y, S_T, reinterpret_cast<hipStream_t>(stream));
+    hipError_t e = kda::launch_conv_fwd(call, zero_rest != 0, y, S_T, reinterpret_cast<hipStream_t>(stream));
     if (e != hipSuccess) return fail(KDA_ERR_HIP, "launch failed: %s", hipGetErrorString(e));
     return ok();
 }

@@ -22,7 +22,7 @@ namespace {
 struct ConvArgs {
     int nseq, T, D, run;   // run: rows a lane
     int64_t rows;
-    bool silu;
+    bool silu, zero_rest;   // zero_rest: zeros in y's rows of no sequence (in dx's always)
     const int* cu;
     const void *x, *S0, *dy, *dS_T;
     const float *w, *bias;
@@ -154,7 +154,10 @@ __global__ void __launch_bounds__(256) conv_fwd_kernel(ConvArgs a) {
                 for (int k = 1; k < W; ++k) win[k - 1] = input_at<E, W>(a, s, row - k, vec);
             shift<W>(win);
             win[0] = to_f8(now[i]);
-            if (row < s.lo || row >= s.hi) continue;   // a row of no sequence
+            if (row < s.lo || row >= s.hi) {   // a row of no sequence
+                if (a.zero_rest) st8((E*)a.y + row * a.D + 8 * vec, V8{});
+                continue;
+            }
             V8 p = taps.apply(win);
             if (a.silu)
 #pragma unroll
@@ -278,7 +281,10 @@ __global__ void __launch_bounds__(256) conv_bwd_kernel(ConvArgs a, int VB, int s
 #pragma unroll
                     for (int k = 1; k < W; ++k) win[k - 1] = input_at<E, W>(a, s, t - k, vec);
                 }
-                if (t < s.lo || t >= s.hi) continue;   // a row of no sequence
+                if (t < s.lo || t >= s.hi) {   // a row of no sequence
+                    if (t < r1) st8((E*)a.dx + t * a.D + 8 * vec, V8{});
+                    continue;
+                }
                 shift<W>(win);
                 win[0] = to_f8(cx[i]);
                 const V8 d = through_act<E>(a.silu, taps.apply(win), to_f8(cd[i]));
@@ -436,10 +442,10 @@ ConvArgs args_of(const ConvCall& c) {
 
 }  // namespace
 
-hipError_t launch_conv_fwd(const ConvCall& c, void* y, void* S_T, hipStream_t stream) {
+hipError_t launch_conv_fwd(const ConvCall& c, bool zero_rest, void* y, void* S_T, hipStream_t stream) {
     ConvArgs a = args_of(c);
     a.run = fwd_run(a.rows, a.D);
-    a.y = y, a.S_T = S_T;
+    a.zero_rest = zero_rest, a.y = y, a.S_T = S_T;
 #define KDA_CF(W) return c.f32 ? conv_fwd_t<float, W>(a, stream) : conv_fwd_t<bf16, W>(a, stream)
     KDA_CONV_TAPS(c.W, KDA_CF)
 #undef KDA_CF

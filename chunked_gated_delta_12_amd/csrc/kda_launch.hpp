@@ -165,7 +165,7 @@ int64_t scan_bwd_workgroups(int nseq, int T, int D, int G, bool packed);
 int64_t scan_step_workgroups(int B, int D, int G);
 size_t scan_fwd_workspace_bytes(int nseq, int T, int D, int N, int G, bool packed);
 size_t scan_bwd_workspace_bytes(int nseq, int T, int D, int N, int G, bool packed);
-hipError_t launch_scan_fwd(const ScanCall& c, void* y, float* S_T, void* workspace, hipStream_t stream);
+hipError_t launch_scan_fwd(const ScanCall& c, bool zero_rest, void* y, float* S_T, void* workspace, hipStream_t stream);
 hipError_t launch_scan_bwd(const ScanCall& c, const void* dy, const float* dS_T, void* dx, void* ddt, float* dA, void* db,
                            void* dc, float* dskip, void* dz, float* dbias, float* dS0, void* workspace,
                            hipStream_t stream);
@@ -183,7 +183,7 @@ struct ConvCall {
     const void *x, *S0;
     const float *w, *bias;
 };
-hipError_t launch_conv_fwd(const ConvCall& c, void* y, void* S_T, hipStream_t stream);
+hipError_t launch_conv_fwd(const ConvCall& c, bool zero_rest, void* y, void* S_T, hipStream_t stream);
 size_t conv_bwd_workspace_bytes(int64_t rows, int D, int W);
 hipError_t launch_conv_bwd(const ConvCall& c, const void* dy, const void* dS_T, void* dx, float* dw, float* dbias, void* dS0,
                            float* part, hipStream_t stream);

@@ -51,6 +51,18 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
 
 __device__ __forceinline__ int held(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
 
+// Zeros in the rows of no sequence, those before the first and behind the last, of a tensor of D values a row: workgroup blk of
+// the REST_BLOCKS that a launch has for that behind its others.
+constexpr int REST_BLOCKS = 64;
+template <typename E>
+__device__ __forceinline__ void clear_rest(const Seqs& s, E* p, int D, int64_t blk) {
+    const int lo = held(s.cu[0], 0, s.T), hi = held(s.cu[s.nseq], lo, s.T);
+    const int64_t words = D / (int)(16 / sizeof(E));   // 16 bytes each; D is a multiple of 8
+    const int64_t first = lo * words, gap = (hi - lo) * words, n = s.T * words - gap;
+    for (int64_t i = blk * blockDim.x + threadIdx.x; i < n; i += (int64_t)REST_BLOCKS * blockDim.x)
+        ((f32x4*)p)[i < first ? i : gap + i] = f32x4{};
+}
+
 // False where the slot has no piece.  Offsets out of order or range are held to both.
 __device__ __forceinline__ bool place_of(const Seqs& s, int64_t slot, Place& p) {
     if (!s.cu) {

@@ -429,16 +429,24 @@ __global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(NS =
 }
 
 // What several workgroups have parts of: the first workgroups sum those of dA, dskip and ddt_bias, the others those
-// of db and dc, of which rows of no sequence have none.
+// of db and dc, and the last clear all gradients' rows of no sequence.
 template <typename E>
 __global__ void __launch_bounds__(1024)
 scan_bwd_sums(PartSums params, int64_t nparams, Seqs s, int64_t rows, int G, int N, int per, const float* __restrict__ part,
-              E* __restrict__ db, E* __restrict__ dc) {
+              E* __restrict__ db, E* __restrict__ dc, E* dx, E* ddt, E* dz, int D) {
     if ((int64_t)blockIdx.x < nparams) {
         part_sums(params, blockIdx.x);
         return;
     }
-    const int64_t blk = blockIdx.x - nparams, nblk = gridDim.x - nparams;
+    const int64_t blk = blockIdx.x - nparams, nblk = gridDim.x - nparams - (s.cu ? REST_BLOCKS : 0);
+    if (blk >= nblk) {
+        E* const rest[] = {dx, ddt, dz};
+        for (E* p : rest)
+            if (p) clear_rest(s, p, D, blk - nblk);
+        clear_rest(s, db, G * N, blk - nblk);
+        clear_rest(s, dc, G * N, blk - nblk);
+        return;
+    }
     const int64_t each = 2 * (int64_t)G * N, total = rows * each;
     int64_t lo = 0, hi = rows;
     if (s.cu) {
@@ -517,8 +525,8 @@ static hipError_t bwd_t(const BwdArgs& a, const BwdPlan& p, void* db, void* dc, 
     hipLaunchKernelGGL((scan_bwd_grad<E, NS>), dim3(grid), dim3(BLOCK), 0, stream, a);
     const PartSums params{{a.pA, a.pskip, a.pbias}, {dA, dskip, dbias}, {(int64_t)a.D * N, a.D, a.D}, p.slots};
     const int64_t nparams = part_sums_blocks(params), want = (p.rows * 2 * a.G * N + 1023) / 1024;
-    hipLaunchKernelGGL(scan_bwd_sums<E>, dim3((unsigned)(nparams + (want < 2048 ? want : 2048))), dim3(1024), 0, stream, params, nparams, a.seqs,
-                       p.rows, a.G, N, blocks / a.G, a.pbc, (E*)db, (E*)dc);
+    hipLaunchKernelGGL(scan_bwd_sums<E>, dim3((unsigned)(nparams + (want < 2048 ? want : 2048) + (a.seqs.cu ? REST_BLOCKS : 0))), dim3(1024), 0, stream, params, nparams, a.seqs,
+                       p.rows, a.G, N, blocks / a.G, a.pbc, (E*)db, (E*)dc, (E*)a.dx, (E*)a.ddt, (E*)a.dz, a.D);
     return hipGetLastError();
 }
 

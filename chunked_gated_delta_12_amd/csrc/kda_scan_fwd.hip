@@ -26,6 +26,7 @@ struct FwdArgs {
     const void *x, *dt, *b, *c, *z;
     const float *A, *skip, *bias, *S0;
     void* y;
+    unsigned walks;   // workgroups with a piece; those behind them clear y's rows of no sequence
     float *S_T, *local, *sums;   // maps: end state from nothing [slot][D][N], sum of delta [slot][D]
 };
 
@@ -36,6 +37,10 @@ __global__ void __launch_bounds__(BLOCK) scan_walk(FwdArgs a) {
     const int per = (a.D / a.G + BLOCK_CH - 1) / BLOCK_CH, nblk = a.G * per;
     const int blk = (int)(blockIdx.x % (unsigned)nblk);
     const int64_t slot = blockIdx.x / (unsigned)nblk;
+    if (!MAP && blockIdx.x >= a.walks) {
+        clear_rest(a.seqs, (E*)a.y, a.D, blockIdx.x - a.walks);
+        return;
+    }
     Place pl;
     if (!place_of(a.seqs, slot, pl)) return;
     if (MAP && pl.k == pl.pieces - 1) return;
@@ -171,9 +176,9 @@ static int fwd_piece(int nseq, int T, int D, int G, bool packed) {
 }
 
 template <typename E, int NS, bool SOFTPLUS>
-static hipError_t fwd_t(const FwdArgs& a, int64_t slots, bool cut, hipStream_t stream) {
-    const unsigned grid = (unsigned)(slots * blocks_of(a.D, a.G));
-    if (cut) hipLaunchKernelGGL((scan_walk<E, NS, SOFTPLUS, true, false>), dim3(grid), dim3(BLOCK), 0, stream, a);
+static hipError_t fwd_t(const FwdArgs& a, bool cut, bool zero_rest, hipStream_t stream) {
+    const unsigned grid = a.walks + (zero_rest ? REST_BLOCKS : 0);
+    if (cut) hipLaunchKernelGGL((scan_walk<E, NS, SOFTPLUS, true, false>), dim3(a.walks), dim3(BLOCK), 0, stream, a);
     if (a.z) hipLaunchKernelGGL((scan_walk<E, NS, SOFTPLUS, false, true>), dim3(grid), dim3(BLOCK), 0, stream, a);
     else hipLaunchKernelGGL((scan_walk<E, NS, SOFTPLUS, false, false>), dim3(grid), dim3(BLOCK), 0, stream, a);
     return hipGetLastError();
@@ -182,7 +187,7 @@ static hipError_t fwd_t(const FwdArgs& a, int64_t slots, bool cut, hipStream_t s
 }  // namespace scan
 
 int64_t scan_fwd_workgroups(int nseq, int T, int D, int G, bool packed) {
-    return scan::slots_of(nseq, T, scan::fwd_piece(nseq, T, D, G, packed), packed) * scan::blocks_of(D, G);
+    return scan::slots_of(nseq, T, scan::fwd_piece(nseq, T, D, G, packed), packed) * scan::blocks_of(D, G) + (packed ? scan::REST_BLOCKS : 0);
 }
 
 size_t scan_fwd_workspace_bytes(int nseq, int T, int D, int N, int G, bool packed) {
@@ -191,17 +196,17 @@ size_t scan_fwd_workspace_bytes(int nseq, int T, int D, int N, int G, bool packe
     return (size_t)scan::slots_of(nseq, T, piece, packed) * D * (N + 1) * sizeof(float);
 }
 
-hipError_t launch_scan_fwd(const ScanCall& c, void* y, float* S_T, void* workspace, hipStream_t stream) {
+hipError_t launch_scan_fwd(const ScanCall& c, bool zero_rest, void* y, float* S_T, void* workspace, hipStream_t stream) {
     const bool packed = c.cu != nullptr;
     const int piece = scan::fwd_piece(c.nseq, c.T, c.D, c.G, packed);
     const int64_t slots = scan::slots_of(c.nseq, c.T, piece, packed);
     float* local = (float*)workspace;
     const scan::FwdArgs a{{c.nseq, c.T, piece, c.cu}, c.D, c.G, c.x, c.dt, c.b, c.c, c.z, c.A, c.skip, c.bias, c.S0,
-                          y, S_T, local, local ? local + slots * c.D * c.N : nullptr};
+                          y, (unsigned)(slots * scan::blocks_of(c.D, c.G)), S_T, local, local ? local + slots * c.D * c.N : nullptr};
     const bool cut = piece < c.T;
 #define KDA_SF(N)                                                                                                          \
-    return c.f32 ? c.softplus ? scan::fwd_t<float, N / 4, true>(a, slots, cut, stream) : scan::fwd_t<float, N / 4, false>(a, slots, cut, stream) \
-                 : c.softplus ? scan::fwd_t<bf16, N / 4, true>(a, slots, cut, stream) : scan::fwd_t<bf16, N / 4, false>(a, slots, cut, stream)
+    return c.f32 ? c.softplus ? scan::fwd_t<float, N / 4, true>(a, cut, zero_rest && packed, stream) : scan::fwd_t<float, N / 4, false>(a, cut, zero_rest && packed, stream) \
+                 : c.softplus ? scan::fwd_t<bf16, N / 4, true>(a, cut, zero_rest && packed, stream) : scan::fwd_t<bf16, N / 4, false>(a, cut, zero_rest && packed, stream)
     switch (c.N) {
         case 8: KDA_SF(8);
         case 16: KDA_SF(16);

@@ -451,8 +451,9 @@ int kda_block_norm_bwd_workspace_size(long long rows, int D, size_t* bytes);
  *
  * Conventions as above; D, the channels, lie side by side in a row, a row a token.  Sequences
  * are nseq times T tokens, or packed as for kda_gdr_chunk_fwd (cu_seqlens, with what is said
- * there of offsets and of rows of no sequence; kda_gdr_clear_rows zeroes those).  The step calls take slots and
- * ntok as kda_gdr_step does.
+ * there of offsets).  Rows of no sequence: the forward calls leave those of y alone, or zero
+ * them with zero_rest = 1; the backward calls zero those of all gradients.  The step calls take
+ * slots and ntok as kda_gdr_step does.
  * ------------------------------------------------------------------------- */
 
 /* ---------------------------------------------------------------------------
@@ -476,7 +477,7 @@ int kda_block_norm_bwd_workspace_size(long long rows, int D, size_t* bytes);
  * Returns a kda_status.
  * ------------------------------------------------------------------------- */
 int kda_sel_scan_fwd(int dtype, int nseq, int T, int D, int N, int G, int softplus, const int* cu_seqlens,
-                     const void* x, const void* dt, const float* A, const void* b, const void* c, const float* skip,
+                     int zero_rest, const void* x, const void* dt, const float* A, const void* b, const void* c, const float* skip,
                      const void* z, const float* dt_bias, const float* S0, void* y, float* S_T,
                      void* workspace, size_t workspace_bytes, void* stream);
 
@@ -535,8 +536,8 @@ int kda_sel_scan_step(int dtype, int B, int T, int D, int N, int G, int nslot, i
  * ------------------------------------------------------------------------- */
 typedef enum kda_conv_act { KDA_CONV_LINEAR = 0, KDA_CONV_SILU = 1 } kda_conv_act;
 
-int kda_short_conv_fwd(int dtype, int act, int nseq, int T, int D, int W, const int* cu_seqlens, const void* x,
-                       const float* w, const float* bias, const void* S0, void* y, void* S_T, void* stream);
+int kda_short_conv_fwd(int dtype, int act, int nseq, int T, int D, int W, const int* cu_seqlens, int zero_rest,
+                       const void* x, const float* w, const float* bias, const void* S0, void* y, void* S_T, void* stream);
 
 /* ---------------------------------------------------------------------------
  * kda_short_conv_bwd: gradients of L = sum <dy, y> + <dS_T, S_T>, from the forward's inputs.

@@ -269,6 +269,24 @@ def test_rows_of_no_sequence(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("first,lens", [(9000, [40]), (0, [0, 1]), (0, [0]), (9001, [0, 0]), (18000, [0]), (17999, [1])])
+def test_many_rows_of_no_sequence(first, lens):
+    """More rows than the workgroups that clear them have lanes, before, behind and on both sides of little or nothing."""
+    D, N, rows = 72, 8, 18000
+    d = to_dev(inputs(1, rows, D, N, 1, F32, 9, "z", n=len(lens)))
+    cu, dy = cu_of(lens, first), torch.ones(1, rows, D, device=DEV)
+    args = (d["x"], d["dt"], d["A"], d["b"], d["c"])
+    got = kda.kda_sel_scan_bwd(*args, dy, cu_seqlens=cu, **options(d, True))
+    got["y"], _ = kda.kda_sel_scan_fwd(*args, cu_seqlens=cu, **options(d, True))
+    some = slice(first, first + sum(lens))
+    for k in ("y", "dx", "ddt", "db", "dc", "dz"):
+        t = got[k].cpu()[0]
+        assert (t[some] != 0).any() == (sum(lens) > 0), k
+        t[some] = 0
+        assert not t.any(), k
+
+
+@pytest.mark.gpu
 def test_offsets_out_of_order_stay_inside():
     """Offsets that fall or leave the range: nothing behind the tensors is touched."""
     D, N, rows = 64, 16, 300
@@ -419,7 +437,7 @@ class Fake:
         self.ptr = {k: (1 << 40) + (i << 30) for i, k in enumerate(
             "cu x dt A b c skip z dt_bias S0 dy dS_T y S_T ws dx ddt dA db dc dskip dz ddt_bias dS0 slots ntok".split())}
         self.ptr["cu"] = None
-        self.ws = 1 << 29
+        self.ws, self.rest = 1 << 29, 1
         self.nslot = 4
         for k, v in over.items():
             if k in self.v:
@@ -438,7 +456,7 @@ class Fake:
     IN = ("cu", "x", "dt", "A", "b", "c", "skip", "z", "dt_bias", "S0")
 
     def fwd(self, lib):
-        return lib.kda_sel_scan_fwd(*self.sizes(), *self.p(*self.IN, "y", "S_T", "ws"), self.ws, None)
+        return lib.kda_sel_scan_fwd(*self.sizes(), *self.p("cu"), self.rest, *self.p(*self.IN[1:], "y", "S_T", "ws"), self.ws, None)
 
     def bwd(self, lib):
         return lib.kda_sel_scan_bwd(*self.sizes(), *self.p(*self.IN, "dy", "dS_T", "dx", "ddt", "dA", "db", "dc", "dskip", "dz", "ddt_bias", "dS0", "ws"),
@@ -472,6 +490,7 @@ def test_refusals_of_all(lib, over, status):
 
 def test_refusals_of_each(lib):
     at = Fake().ptr
+    assert Fake(rest=2).fwd(lib) == SHAPE and Fake(rest=-1).fwd(lib) == SHAPE
     assert Fake(y=None).fwd(lib) == NULL and Fake(dA=None).bwd(lib) == NULL and Fake(y=None).step(lib) == NULL
     assert Fake(y=at["x"]).fwd(lib) == ALIAS and Fake(S_T=at["x"]).fwd(lib) == ALIAS and Fake(y=at["S_T"]).fwd(lib) == ALIAS
     assert Fake(S_T=at["S0"] + 16).fwd(lib) == ALIAS

@@ -293,14 +293,14 @@ AT = {k: (1 << 40) + (i << 30) for i, k in enumerate("cu x w bias S0 dy dS_T y S
 
 
 def call(lib, which, **over):
-    v = dict(dtype=0, act=1, n=2, T=64, D=64, W=4, nslot=4, bytes=1 << 29)
+    v = dict(dtype=0, act=1, rest=1, n=2, T=64, D=64, W=4, nslot=4, bytes=1 << 29)
     v.update(AT)
     v["cu"] = None
     v.update(over)
     p = lambda *names: [None if v[n] is None else ctypes.c_void_p(v[n]) for n in names]   # noqa: E731
     head = [v[k] for k in ("dtype", "act", "n", "T", "D", "W")]
     if which == "fwd":
-        return lib.kda_short_conv_fwd(*head, *p("cu", "x", "w", "bias", "S0", "y", "S_T"), None)
+        return lib.kda_short_conv_fwd(*head, *p("cu"), v["rest"], *p("x", "w", "bias", "S0", "y", "S_T"), None)
     if which == "bwd":
         return lib.kda_short_conv_bwd(*head, *p("cu", "x", "w", "bias", "S0", "dy", "dS_T", "dx", "dw", "dbias", "dS0", "ws"), v["bytes"], None)
     return lib.kda_short_conv_step(*head, v["nslot"], *p("x", "w", "bias", "S0", "slots", "ntok", "y"), None)
@@ -316,6 +316,7 @@ def test_refusals_of_all(lib, over, status):
 
 
 def test_refusals_of_each(lib):
+    assert call(lib, "fwd", rest=2) == SHAPE
     assert call(lib, "fwd", y=None) == NULL and call(lib, "bwd", dw=None) == NULL and call(lib, "step", S0=None) == NULL
     assert call(lib, "bwd", bias=None) == NULL
     assert call(lib, "fwd", y=AT["x"]) == ALIAS and call(lib, "fwd", S_T=AT["S0"] + 16) == ALIAS and call(lib, "fwd", S_T=AT["x"]) == ALIAS
