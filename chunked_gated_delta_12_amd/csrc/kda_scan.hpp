@@ -99,34 +99,39 @@ __device__ __forceinline__ bool place_of(const Seqs& s, int64_t slot, Place& p) 
     return k >= 0 && k < p.pieces;
 }
 
-// e^-|v|, exactly 0 from 104 on, without a branch: NaN is not above 104 and stays.  The product's
-// rounding is put back; log2(e)'s own leaves 1.3e-8 |v| of the result.
-__device__ __forceinline__ float exp_minus(float v) {
+// e^-|v|, without a branch; NaN stays.  In fp32 storage exactly 0 from 104 on, and the product's rounding is
+// put back; log2(e)'s own leaves 1.3e-8 |v| of the result.  In bf16 storage that rounding stays: at most 2^-24 |v| of the
+// result, where a step's or gate's input was rounded by 2^-9 |v|, for five instructions of a token's hundred or so.
+template <typename E> __device__ __forceinline__ float exp_minus(float v);
+template <> __device__ __forceinline__ float exp_minus<float>(float v) {
     float a = __builtin_fabsf(v);
     a = a > 104.0f ? 104.0f : a;
     const float t = a * -LOG2E, e = __builtin_amdgcn_exp2f(t);
     return __builtin_fmaf(e, __builtin_fmaf(a, -LOG2E, -t) * 0.6931471805599453f, e);
 }
+template <> __device__ __forceinline__ float exp_minus<bf16>(float v) { return __builtin_amdgcn_exp2f(__builtin_fabsf(v) * -LOG2E); }
 
-// softplus(v) = max(v, 0) + log(1 + e^-|v|), with log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3: a relative
+// softplus(v) = max(v, 0) + log(1 + e^-|v|), with log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3: from e, a relative
 // error of a few 2^-24 for every v, also where e is small and a logarithm of the rounded 1 + e would
-// lose it.  atanh(s) / s is interpolated in s^2 on [0, 1/9] at Chebyshev's points, off by at most 4e-9.
+// lose it.  atanh(s) / s is interpolated in s^2 on [0, 1/9] at Chebyshev's points, off by at most 4e-9 (here twice that).
 __device__ __forceinline__ float softplus_of(float v, float e) {   // e = e^-|v|
     const float s = e * __builtin_amdgcn_rcpf(2.0f + e), q = s * s;
-    float p = 1.4078889183e-01f;
-    p = __builtin_fmaf(p, q, 1.3982578873e-01f);
-    p = __builtin_fmaf(p, q, 2.0012297615e-01f);
-    p = __builtin_fmaf(p, q, 3.3333160821e-01f);
-    p = __builtin_fmaf(p, q, 1.0f);
+    float p = 2 * 1.4078889183e-01f;
+    p = __builtin_fmaf(p, q, 2 * 1.3982578873e-01f);
+    p = __builtin_fmaf(p, q, 2 * 2.0012297615e-01f);
+    p = __builtin_fmaf(p, q, 2 * 3.3333160821e-01f);
+    p = __builtin_fmaf(p, q, 2.0f);
     float m;
     asm("v_max_f32 %0, 0, %1" : "=v"(m) : "v"(v));   // the compiler's is two instructions; NaN comes through p
-    return __builtin_fmaf(2.0f * s, p, m);
+    return __builtin_fmaf(s, p, m);
 }
 
-__device__ __forceinline__ float softplus(float v) { return softplus_of(v, exp_minus(v)); }
+template <typename E>
+__device__ __forceinline__ float softplus(float v) { return softplus_of(v, exp_minus<E>(v)); }
 // softplus(v) and its slope sigmoid(v), from one exponential.
+template <typename E>
 __device__ __forceinline__ float softplus(float v, float& slope) {
-    const float e = exp_minus(v), i = __builtin_amdgcn_rcpf(1.0f + e);
+    const float e = exp_minus<E>(v), i = __builtin_amdgcn_rcpf(1.0f + e);
     slope = v < 0.0f ? e * i : i;
     return softplus_of(v, e);
 }
@@ -135,7 +140,7 @@ __device__ __forceinline__ float softplus(float v, float& slope) {
 // reciprocal, whose error of a few 2^-24 |v| is far below a result's rounding.  Exactly 0 and 1 in the tails.
 template <typename E> __device__ __forceinline__ float sigmoid(float v);
 template <> __device__ __forceinline__ float sigmoid<float>(float v) {
-    const float e = exp_minus(v), d = 1.0f + e, r = __builtin_amdgcn_rcpf(d);
+    const float e = exp_minus<float>(v), d = 1.0f + e, r = __builtin_amdgcn_rcpf(d);
     const float i = __builtin_fmaf(r, __builtin_fmaf(-d, r, 1.0f), r);   // one step: 1 / (1 + e)
     return v < 0.0f ? e * i : i;
 }

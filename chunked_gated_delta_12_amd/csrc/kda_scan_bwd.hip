@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(BLOCK) scan_bwd_map(BwdArgs a) {
             }
             const float xv = value<E>(nx[g]), raw = value<E>(nt[g]) + bias, dyv = BACK ? value<E>(nd[g]) : 0.0f, zv = BACK ? value<E>(nz[g]) : 0.0f;
             fetch(g);
-            float d = SOFTPLUS ? softplus(raw) : raw;
+            float d = SOFTPLUS ? softplus<E>(raw) : raw;
             d = 4 * g < left ? d : 0.0f;   // a step of nothing behind the last token: x and dy are zero there
             const float u = d * xv, v = dyv * (gated ? zv * sigmoid<E>(zv) : 1.0f);
             sum += d;
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(NS =
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g) {
                 float slope;
-                dv[g] = softplus(dv[g], slope);
+                dv[g] = softplus<E>(dv[g], slope);
                 aside[0][g][me] = slope;
             }
         } else {

@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(BLOCK) scan_step(StepArgs a) {
         const float xv = (float)xr, zv = a.z ? (float)zr : 0.0f;
         float d = (float)dr + bias;
         if (t0 + 4 < n) fetch(t0 + 4);
-        if (a.softplus) d = softplus(d);
+        if (a.softplus) d = softplus<E>(d);
         const float u = d * xv;
         float yj[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         each_of_quad([&](auto J) {
