@@ -21,9 +21,11 @@
 // halved at each exchange.  The gradients' registers are the other bound: 16 tokens' three sums over states, decays and states
 // are 80 a lane, so the per-state values wait in LDS and the loop over states holds one (as one unrolled
 // piece of code the compiler spills), b and c are read four tokens at a time, and bf16 at 16 states fits 168 registers, three
-// wavefronts a SIMD; with two, 1,022 us where it takes 900.
-// Measured, 8 x 4,096 tokens by 2,048 channels, 16 states, bf16, every part: 1,220 us (maps 317, gradients 900 and sums 38 under the profiler;
-// 0.94 GB in and out, and 0.8 GB through the workspace); four packed sequences of 4,096 tokens by 512 channels in fp32 78 us.
+// wavefronts a SIMD; with two, 1,022 us where it took 900.  The sums over channels on the fp32 matrix instructions (a product with one
+// column a token) came to 1,435 us of a call of 1,225 for dc alone, 1,626 for both: their 32 cycles each add to the vector
+// instructions' time.
+// Measured, 8 x 4,096 tokens by 2,048 channels, 16 states, bf16, every part: 1,202 us (maps 306, gradients 870 and sums 32 under the profiler;
+// 0.94 GB in and out, and 0.8 GB through the workspace); four packed sequences of 4,096 tokens by 512 channels in fp32 71 us.
 #include "kda_rows.hpp"
 #include "kda_scan.hpp"
 

@@ -7,8 +7,8 @@
 // are converted once a workgroup, a lane's own tokens are asked for a tile ahead through buffer resources that
 // take no vector address, and each as soon as its predecessor is used, which keeps a wavefront below 100 registers (16
 // states: five wavefronts a SIMD).  Counters: 90% of the vector issue slots taken, 65% of those the six and five.
-// Measured, bf16, 16 states, gate, skip and softplus: 65,536 tokens by 2,048 channels 893 us (43% in the maps; 1.2
-// TB/s, 2.4e12 states a second), 32 x 4,096 by 4,096 uncut 2.0 ms (4.3e12); ten packed prompts of 1 to 8,192 tokens 241 us.
+// Measured, bf16, 16 states, gate, skip and softplus: 65,536 tokens by 2,048 channels 863 to 879 us (43% in the maps; 1.2
+// TB/s, 2.4e12 states a second), 32 x 4,096 by 4,096 uncut 2.0 ms (4.3e12); ten packed prompts of 1 to 8,192 tokens 230 us.
 // Before: addresses in vector registers, operands exchanged by instructions of their own, a whole tile's tokens held
 // while the next ones came: 1,376, 413.
 //
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(BLOCK) scan_walk(FwdArgs a) {
 // Tokens a piece.  A cut call forms every state twice, but 256 workgroups are one wavefront a SIMD, whose
 // instructions wait for each other.  Measured, sequences of 4,096 tokens by 2,048 channels of 16 states: at 256
 // workgroups whole 544 us, cut 514; at 512 whole 697, cut 907.  Pieces are as many as give 2,048 workgroups, eight a
-// compute unit (65,536 tokens: 512 workgroups 1,259 us, 1,024 951, 2,048 896, 4,096 916), of 64 tokens at the least
+// compute unit (65,536 tokens, before the step's exponential was shortened: 512 workgroups 1,259 us, 1,024 951, 2,048 896, 4,096 916), of 64 tokens at the least
 // (2 x 1,000 tokens by 256 channels of 32 states: 32 tokens 29.7 us, 64 30.9, 128 43.8; the backward pass of four
 // sequences by 512 channels, which has the same rule: 90.7, 81.8, 107.7) and at most 256 a sequence, each of which puts its start
 // together from all before it.
