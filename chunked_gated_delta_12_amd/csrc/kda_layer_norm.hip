@@ -6,17 +6,27 @@
 //     dy = dx = dr + rho (t - mean(t) - u mean(t u)),   dw = sum dh u,   db = sum dh   (over rows)
 // Everything is formed in fp32 and rounded once; the squares are of r less its mean, so a row far
 // from zero keeps its digits; the backward pass rebuilds r from the inputs.  Both are bound by HBM: a row stays in
-// registers, each operand is read once and each result written once.  Rows lie on the lanes as
-// those of the block norm (kda_norm.hip), whose measurements chose that.
+// registers, each operand is read once and each result written once, and the next row is asked for before
+// this one's sums meet.
 // Measured, bf16, all parts: forwards 65,536 rows of 2,048 channels 212 us (1.07 GB, 5.1 TB/s, a large copy's rate), backwards
-// 16,384 rows of 2,048 76 us (336 MB, 4.4 TB/s), of 2,056, nearly half of the lanes idle, 116, 4,096 of 8,192 97; 7
-// rows of 1,000 in fp32 11 us, the call's host time.
+// 16,384 rows of 2,048 76 us (336 MB, 4.4 TB/s), of 2,056 116, 4,096 of 8,192 97 (one workgroup a compute unit, whose three sums a
+// row nothing overlaps; with the next bf16 row asked for ahead, no change); 7 rows of 1,000 in fp32 11 us, the call's host time.
 #include "kda_launch.hpp"
 #include "kda_rows.hpp"
 
 namespace kda {
 
 namespace {
+
+// Lanes a row: a power of two within two wavefronts; beyond, whole wavefronts, up to eight any number, then an even one.
+// Beside powers of two throughout, bf16, all parts, 2^25 values forwards and backwards: 1,536 channels 49 and 91 us, now 47 and 78;
+// 2,560 50 and 102, now 47 and 93; 5,120 67 and 122, now 52 and 106; 6,144 61 and 110, now 47 and 101.
+int ln_lanes(int D) {
+    if (D <= 1024) return lanes_of(D);
+    const int waves = (D + 511) / 512;
+    return 64 * (waves <= 8 ? waves : (waves + 1) / 2 * 2);
+}
+constexpr int ln_block(int L) { return L > 128 ? L : 256; }
 
 struct LnArgs {
     int64_t rows;
@@ -54,9 +64,9 @@ __device__ __forceinline__ float centred(V8& v, bool on, float D, float eps, flo
 }
 
 template <typename E, int L>
-__global__ void __launch_bounds__(block_of(L)) ln_fwd_kernel(LnArgs a) {
+__global__ void __launch_bounds__(ln_block(L)) ln_fwd_kernel(LnArgs a) {
     __shared__ float lds[64];
-    constexpr int G = block_of(L) / L;   // rows at a time
+    constexpr int G = ln_block(L) / L;   // rows at a time
     const int lane = threadIdx.x % L, grp = threadIdx.x / L;
     const bool on = lane < a.D / 8;
     int turn = 0;
@@ -96,10 +106,10 @@ __global__ void __launch_bounds__(block_of(L)) ln_fwd_kernel(LnArgs a) {
 }
 
 template <typename E, int L>
-__global__ void __launch_bounds__(block_of(L)) ln_bwd_kernel(LnArgs a) {
+__global__ void __launch_bounds__(ln_block(L)) ln_bwd_kernel(LnArgs a) {
     __shared__ float lds[64];
-    constexpr int G = block_of(L) / L;
-    constexpr int GW = L < 64 ? block_of(L) / 64 : G;   // parts that meet in LDS: groups in one wavefront sum by lane exchange
+    constexpr int G = ln_block(L) / L;
+    constexpr int GW = L < 64 ? ln_block(L) / 64 : G;   // parts that meet in LDS: groups in one wavefront sum by lane exchange
     __shared__ float acc[GW > 1 ? GW * L * 8 : 1];
     const int lane = threadIdx.x % L, grp = threadIdx.x / L;
     const bool on = lane < a.D / 8;
@@ -174,33 +184,36 @@ __global__ void __launch_bounds__(block_of(L)) ln_bwd_kernel(LnArgs a) {
     }
 }
 
-// Workgroups of the backward pass: as many as are resident at once, each one a row of parts.
+// Workgroups of the backward pass: as many as are resident at once, each one a row of parts.  The registers leave four
+// wavefronts a SIMD, 256 compute units have four SIMDs, and a workgroup of five has two on one of them (13,107 rows of 2,560:
+// two workgroups a compute unit 93 us, three 110, 819 for all of them, which is a round and a part, 140).
 int ln_bwd_blocks(int64_t rows, int D) {
-    const int L = lanes_of(D), G = block_of(L) / L;
+    const int L = ln_lanes(D), G = ln_block(L) / L;
     const int64_t want = (rows + G - 1) / G;
-    const int64_t cap = 4 * 1024 / (block_of(L) / 64);
+    const int waves = ln_block(L) / 64;
+    const int64_t cap = 256 * (waves <= 4 ? 16 / waves : 4 / ((waves + 3) / 4));
     return (int)(want < cap ? want : cap);
 }
 
 template <typename E, int L>
 hipError_t ln_fwd_t(const LnArgs& a, hipStream_t stream) {
-    constexpr int G = block_of(L) / L;
+    constexpr int G = ln_block(L) / L;
     const int64_t want = (a.rows + G - 1) / G;
-    hipLaunchKernelGGL((ln_fwd_kernel<E, L>), dim3((unsigned)(want < 2048 ? want : 2048)), dim3(block_of(L)), 0, stream, a);
+    hipLaunchKernelGGL((ln_fwd_kernel<E, L>), dim3((unsigned)(want < 2048 ? want : 2048)), dim3(ln_block(L)), 0, stream, a);
     return hipGetLastError();
 }
 
 template <typename E, int L>
 hipError_t ln_bwd_t(const LnArgs& a, float* dw, float* db, hipStream_t stream) {
     const int nblk = ln_bwd_blocks(a.rows, a.D);
-    hipLaunchKernelGGL((ln_bwd_kernel<E, L>), dim3((unsigned)nblk), dim3(block_of(L)), 0, stream, a);
+    hipLaunchKernelGGL((ln_bwd_kernel<E, L>), dim3((unsigned)nblk), dim3(ln_block(L)), 0, stream, a);
     if (dw || db)
         launch_part_sums(PartSums{{a.part, a.part + (int64_t)nblk * a.D, nullptr}, {dw, db, nullptr}, {a.D, a.D, 0}, nblk}, stream);
     return hipGetLastError();
 }
 
 #define KDA_LN_SIZES(CALL)       \
-    switch (lanes_of(D)) {       \
+    switch (ln_lanes(D)) {       \
         case 1: CALL(1);         \
         case 2: CALL(2);         \
         case 4: CALL(4);         \
@@ -209,8 +222,15 @@ hipError_t ln_bwd_t(const LnArgs& a, float* dw, float* db, hipStream_t stream) {
         case 32: CALL(32);       \
         case 64: CALL(64);       \
         case 128: CALL(128);     \
+        case 192: CALL(192);     \
         case 256: CALL(256);     \
+        case 320: CALL(320);     \
+        case 384: CALL(384);     \
+        case 448: CALL(448);     \
         case 512: CALL(512);     \
+        case 640: CALL(640);     \
+        case 768: CALL(768);     \
+        case 896: CALL(896);     \
         case 1024: CALL(1024);   \
     }
 

@@ -466,7 +466,8 @@ int kda_block_norm_bwd_workspace_size(long long rows, int D, size_t* bytes);
  *   dtype        storage of x, dt, b, c, z and y; all arithmetic, A and the states are fp32
  *   T            at most 2^30;  D at most 2^20, D / G a multiple of 8;  N 8, 16, 32 or 64
  *   x, dt, z     [.., D]     dtype; z NULL: no gate
- *   A            [D, N]      fp32, used as given (negative in a model that forgets); finite
+ *   A            [D, N]      fp32, used as given (negative in a model that forgets); finite.  Where states
+ *                grow, exp(A sum delta) has to stay within fp32 over every part of a sequence
  *   b, c         [.., G, N]  dtype
  *   skip, dt_bias  [D]       fp32, or NULL for zero
  *   S0           [nseq, D, N]  fp32, or NULL for zero

@@ -98,7 +98,9 @@ def both(a, g, eps, dtype, **kw):
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("rows,D,parts", [(1, 8, "xwb"), (3, 16, "w"), (7, 24, "b"), (130, 64, "xwb"), (65, 136, "x"), (33, 264, "xw"), (17, 520, "xwb"),
-                                          (9, 1000, "wb"), (5, 2056, "xwb"), (3, 4104, "xb"), (4, 8192, "xwb"), (3000, 32, "xwb")])
+                                          (9, 1000, "wb"), (5, 2056, "xwb"), (3, 4104, "xb"), (4, 8192, "xwb"), (3000, 32, "xwb"), (1500, 1032, "xwb"), (5, 1536, "xw"),
+                                          (900, 2560, "xwb"), (4, 2568, "xb"), (3, 3584, "wb"), (4, 4096, "xwb"), (450, 5120, "xwb"), (3, 5128, "xwb"),
+                                          (2, 6152, "xwb"), (3, 7168, "xwb"), (2, 7176, "x")])
 def test_fwd_and_bwd(rows, D, parts, dtype):
     print(f"layer norm rows={rows} D={D} {parts} {dtype}", flush=True)
     a, g = inputs(rows, D, dtype, 3, parts)
