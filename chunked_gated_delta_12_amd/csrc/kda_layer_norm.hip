@@ -10,7 +10,7 @@
 // this one's sums meet.
 // Measured, bf16, all parts: forwards 65,536 rows of 2,048 channels 212 us (1.07 GB, 5.1 TB/s, a large copy's rate), backwards
 // 16,384 rows of 2,048 76 us (336 MB, 4.4 TB/s), of 2,056 116, 4,096 of 8,192 97 (one workgroup a compute unit, whose three sums a
-// row nothing overlaps; with the next bf16 row asked for ahead, no change); 7 rows of 1,000 in fp32 11 us, the call's host time.
+// row little overlaps); 7 rows of 1,000 in fp32 11 us, the call's host time.
 #include "kda_launch.hpp"
 #include "kda_rows.hpp"
 
@@ -128,8 +128,8 @@ __global__ void __launch_bounds__(ln_block(L)) ln_bwd_kernel(LnArgs a) {
             if (a.dr) ld_raw((const E*)a.dr + at, rd);
         }
     };
-    // at 1,024 lanes a row the registers do not hold a second row
-    constexpr bool AHEAD = L < 1024;
+    // from 896 lanes a row on the registers do not hold a second row in fp32
+    constexpr bool AHEAD = L < 896 || sizeof(E) == 2;
     if (AHEAD) fetch((int64_t)blockIdx.x * G + grp);
     for (int64_t base = (int64_t)blockIdx.x * G; base < a.rows; base += (int64_t)gridDim.x * G) {
         const int64_t row = base + grp;
