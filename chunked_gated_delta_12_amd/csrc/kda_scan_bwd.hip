@@ -316,10 +316,12 @@ __global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(NS =
                 aside[1][g][me] = vy[g] * (sg * (1.0f + zv * (1.0f - sg)));
                 vy[g] *= zv * sg;
             }
-        const int left = n - CH * k - q;
+        // a step of nothing behind the last token, where x and dy are zero, and of lanes without a channel, which read zeros: their
+        // bias alone could make states of any size, and zero times infinity would reach the sums over channels
+        const int left = real ? n - CH * k - q : 0;
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
-            if (4 * g >= left) dv[g] = aside[0][g][me] = 0.0f;   // a step of nothing behind the last token: x and dy are zero there
+            if (4 * g >= left) dv[g] = aside[0][g][me] = 0.0f;
             uv[g] *= dv[g];
         }
 #pragma unroll
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(NS =
                     e[t] = __builtin_amdgcn_exp2f(token<t>(dv) * A2i);
                     h = __builtin_fmaf(e[t], h, token<t>(uv) * bv[j]);
                     sy[t] = __builtin_fmaf(cv[j], h, sy[t]);
-                    v[t] = token<t>(vy) * h;   // zero of lanes without a channel: they read nothing
+                    v[t] = token<t>(vy) * h;   // zero of lanes without a channel: no dy, and the last channel's state kept
                 });
                 asm volatile("" : : "v"(v[t0]), "v"(v[t0 + 1]), "v"(v[t0 + 2]), "v"(v[t0 + 3]), "v"(sy[t0 + 3]) : "memory");
             });
