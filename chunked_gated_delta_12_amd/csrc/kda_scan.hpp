@@ -99,17 +99,15 @@ __device__ __forceinline__ bool place_of(const Seqs& s, int64_t slot, Place& p) 
     return k >= 0 && k < p.pieces;
 }
 
-// e^-|v|, without a branch; NaN stays.  In fp32 storage exactly 0 from 104 on, and the product's rounding is
-// put back; log2(e)'s own leaves 1.3e-8 |v| of the result.  In bf16 storage that rounding stays: at most 2^-24 |v| of the
-// result, where a step's or gate's input was rounded by 2^-9 |v|, for five instructions of a token's hundred or so.
-template <typename E> __device__ __forceinline__ float exp_minus(float v);
-template <> __device__ __forceinline__ float exp_minus<float>(float v) {
-    float a = __builtin_fabsf(v);
-    a = a > 104.0f ? 104.0f : a;
-    const float t = a * -LOG2E, e = __builtin_amdgcn_exp2f(t);
-    return __builtin_fmaf(e, __builtin_fmaf(a, -LOG2E, -t) * 0.6931471805599453f, e);
+// e^-|v|, without a branch: the hardware's power of two of the rounded product t = -|v| log2(e), and what that rounding left,
+// -|v| - t ln 2, put back (of ln 2's own rounding 2.8e-9 |v| of the result stays).  0 below 2^-126; NaN stays; the hold to
+// [-1, 1] is for infinities, whose difference is none.  In bf16 storage too: a step size goes on to states and gradients that are
+// fp32, and without the correction up to 1.2 x 2^-24 |v| of it would be lost, v being dt + bias, for three instructions of a
+// token's hundred or so.
+__device__ __forceinline__ float exp_minus(float v) {
+    const float a = __builtin_fabsf(v), t = a * -LOG2E, e = __builtin_amdgcn_exp2f(t);
+    return __builtin_fmaf(e, __builtin_amdgcn_fmed3f(__builtin_fmaf(t, -0.6931471805599453f, -a), -1.0f, 1.0f), e);
 }
-template <> __device__ __forceinline__ float exp_minus<bf16>(float v) { return __builtin_amdgcn_exp2f(__builtin_fabsf(v) * -LOG2E); }
 
 // softplus(v) = max(v, 0) + log(1 + e^-|v|), with log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3: from e, a relative
 // error of a few 2^-24 for every v, also where e is small and a logarithm of the rounded 1 + e would
@@ -126,25 +124,25 @@ __device__ __forceinline__ float softplus_of(float v, float e) {   // e = e^-|v|
     return __builtin_fmaf(s, p, m);
 }
 
-template <typename E>
-__device__ __forceinline__ float softplus(float v) { return softplus_of(v, exp_minus<E>(v)); }
+__device__ __forceinline__ float softplus(float v) { return softplus_of(v, exp_minus(v)); }
 // softplus(v) and its slope sigmoid(v), from one exponential.
-template <typename E>
 __device__ __forceinline__ float softplus(float v, float& slope) {
-    const float e = exp_minus<E>(v), i = __builtin_amdgcn_rcpf(1.0f + e);
+    const float e = exp_minus(v), i = __builtin_amdgcn_rcpf(1.0f + e);
     slope = v < 0.0f ? e * i : i;
     return softplus_of(v, e);
 }
 
-// sigmoid(v): in fp32 storage to a few ulp; in bf16 storage from the hardware exponential and
-// reciprocal, whose error of a few 2^-24 |v| is far below a result's rounding.  Exactly 0 and 1 in the tails.
-template <typename E> __device__ __forceinline__ float sigmoid(float v);
-template <> __device__ __forceinline__ float sigmoid<float>(float v) {
-    const float e = exp_minus<float>(v), d = 1.0f + e, r = __builtin_amdgcn_rcpf(d);
+// sigmoid(v) to a few ulp; exactly 0 and 1 in the tails.
+__device__ __forceinline__ float sigmoid(float v) {
+    const float e = exp_minus(v), d = 1.0f + e, r = __builtin_amdgcn_rcpf(d);
     const float i = __builtin_fmaf(r, __builtin_fmaf(-d, r, 1.0f), r);   // one step: 1 / (1 + e)
     return v < 0.0f ? e * i : i;
 }
-template <> __device__ __forceinline__ float sigmoid<bf16>(float v) { return out_sigmoid(v); }
+// The gate of an output that is stored in E: in bf16 from the hardware exponential and reciprocal, whose error of a few 2^-24 |v| is
+// far below that rounding.  The backward pass takes sigmoid, since dA, dskip, ddt_bias and dS0 are fp32.
+template <typename E> __device__ __forceinline__ float gate_sigmoid(float v);
+template <> __device__ __forceinline__ float gate_sigmoid<float>(float v) { return sigmoid(v); }
+template <> __device__ __forceinline__ float gate_sigmoid<bf16>(float v) { return out_sigmoid(v); }
 
 // ---------------------------------------------------------------- quads
 template <int CTRL>

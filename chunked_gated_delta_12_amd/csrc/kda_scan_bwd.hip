@@ -139,9 +139,9 @@ __global__ void __launch_bounds__(BLOCK) scan_bwd_map(BwdArgs a) {
             }
             const float xv = value<E>(nx[g]), raw = value<E>(nt[g]) + bias, dyv = BACK ? value<E>(nd[g]) : 0.0f, zv = BACK ? value<E>(nz[g]) : 0.0f;
             fetch(g);
-            float d = SOFTPLUS ? softplus<E>(raw) : raw;
+            float d = SOFTPLUS ? softplus(raw) : raw;
             d = 4 * g < left ? d : 0.0f;   // a step of nothing behind the last token: x and dy are zero there
-            const float u = d * xv, v = dyv * (gated ? zv * sigmoid<E>(zv) : 1.0f);
+            const float u = d * xv, v = dyv * (gated ? zv * sigmoid(zv) : 1.0f);
             sum += d;
             each_of_quad([&](auto J) {
                 constexpr int j = decltype(J)::value;
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(NS =
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g) {
                 float slope;
-                dv[g] = softplus<E>(dv[g], slope);
+                dv[g] = softplus(dv[g], slope);
                 aside[0][g][me] = slope;
             }
         } else {
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(NS =
         if (gated)
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g) {
-                const float zv = value<E>(nz[g]), sg = sigmoid<E>(zv);
+                const float zv = value<E>(nz[g]), sg = sigmoid(zv);
                 aside[1][g][me] = vy[g] * (sg * (1.0f + zv * (1.0f - sg)));
                 vy[g] *= zv * sg;
             }

@@ -114,9 +114,9 @@ __global__ void __launch_bounds__(BLOCK) scan_walk(FwdArgs a) {
             nx[g] = ld_one<E>(rx, own[g]);
             nt[g] = ld_one<E>(rt, own[g]);
             if (GATED) nz[g] = ld_one<E>(rz, own[g]);
-            float d = SOFTPLUS ? softplus<E>(raw) : raw;
+            float d = SOFTPLUS ? softplus(raw) : raw;
             d = 4 * g < left ? d : 0.0f;   // a step of nothing behind the last token: x is zero there
-            const float u = d * xv, gate = GATED ? zv * sigmoid<E>(zv) : 1.0f;
+            const float u = d * xv, gate = GATED ? zv * gate_sigmoid<E>(zv) : 1.0f;
             if (MAP) sum += d;
             float yj[4];
             each_of_quad([&](auto J) {

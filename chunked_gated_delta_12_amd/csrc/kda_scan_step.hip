@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(BLOCK) scan_step(StepArgs a) {
         const float xv = (float)xr, zv = a.z ? (float)zr : 0.0f;
         float d = (float)dr + bias;
         if (t0 + 4 < n) fetch(t0 + 4);
-        if (a.softplus) d = softplus<E>(d);
+        if (a.softplus) d = softplus(d);
         const float u = d * xv;
         float yj[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         each_of_quad([&](auto J) {
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(BLOCK) scan_step(StepArgs a) {
         });
         float yv = quad_sums(yj, q);
         if (a.skip) yv = __builtin_fmaf(skip, xv, yv);
-        if (a.z) yv *= zv * sigmoid<E>(zv);
+        if (a.z) yv *= zv * gate_sigmoid<E>(zv);
         if (t0 + q < n && real) ((E*)a.y)[(row + t0 + q) * a.D + ch] = from_f<E>(yv);
     }
     if (real) st_states<NS>(Sp, h);
