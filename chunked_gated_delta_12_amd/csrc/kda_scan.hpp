@@ -307,6 +307,18 @@ struct Rows {
 // Workgroups of 64 channels: none straddles two groups of channels.
 __host__ __device__ __forceinline__ int blocks_of(int D, int G) { return G * ((D / G + BLOCK_CH - 1) / BLOCK_CH); }
 
+// Tokens a piece where sequences are cut: as many pieces of all rows as make 2,048 workgroups, of two tiles at the least, and at most
+// 256 a sequence of T tokens, each of which puts its start together from all before it; whole tiles, no more than T has.
+inline int cut_piece(int nseq, int T, int D, int G, bool packed) {
+    const int64_t blocks = blocks_of(D, G), rows = packed ? T : (int64_t)nseq * T;
+    const int64_t most = 2048 / blocks > 1 ? 2048 / blocks : 1, whole = ((int64_t)T + TILE - 1) / TILE * TILE;
+    int64_t len = rows / most;
+    if (len < 2 * TILE) len = 2 * TILE;
+    if (len < ((int64_t)T + 255) / 256) len = ((int64_t)T + 255) / 256;
+    len = (len + TILE - 1) / TILE * TILE;
+    return (int)(len < whole ? len : whole);
+}
+
 // Slots of the pieces of all sequences.
 inline int64_t slots_of(int nseq, int T, int piece, bool packed) {
     return packed ? (int64_t)T / piece + nseq : (int64_t)nseq * (((int64_t)T + piece - 1) / piece);

@@ -474,19 +474,8 @@ scan_bwd_sums(PartSums params, int64_t nparams, Seqs s, int64_t rows, int G, int
     }
 }
 
-// Tokens a piece: the forward's rule, but always by workgroups, since the maps run in any case (8 x 4,096 tokens by
+// Tokens a piece: cut_piece, always by workgroups, since the maps run in any case (8 x 4,096 tokens by
 // 2,048 channels: 256 workgroups 2,857 us, 512 1,499, 1,024 1,351, 2,048 1,272, 4,096 1,261).
-static int bwd_piece(int nseq, int T, int D, int G, bool packed) {
-    const int64_t blocks = blocks_of(D, G), rows = packed ? T : (int64_t)nseq * T;
-    const int64_t whole = ((int64_t)T + TILE - 1) / TILE * TILE;
-    const int64_t pieces = 2048 / blocks > 1 ? 2048 / blocks : 1;
-    int64_t len = rows / pieces;
-    if (len < 2 * TILE) len = 2 * TILE;
-    if (len < T / 256) len = T / 256;
-    len = (len + TILE - 1) / TILE * TILE;
-    return (int)(len < whole ? len : whole);
-}
-
 struct BwdPlan {
     int piece;
     int64_t rows, slots, chunks;
@@ -494,7 +483,7 @@ struct BwdPlan {
 };
 static BwdPlan plan_of(int nseq, int T, int D, int N, int G, bool packed) {
     BwdPlan p;
-    p.piece = bwd_piece(nseq, T, D, G, packed);
+    p.piece = cut_piece(nseq, T, D, G, packed);
     p.rows = packed ? T : (int64_t)nseq * T;
     p.slots = slots_of(nseq, T, p.piece, packed);
     p.chunks = slots_of(nseq, T, CH, packed);
@@ -537,7 +526,7 @@ static hipError_t bwd_t(const BwdArgs& a, const BwdPlan& p, void* db, void* dc, 
 }  // namespace scan
 
 int64_t scan_bwd_workgroups(int nseq, int T, int D, int G, bool packed) {
-    return scan::slots_of(nseq, T, scan::bwd_piece(nseq, T, D, G, packed), packed) * scan::blocks_of(D, G);
+    return scan::slots_of(nseq, T, scan::cut_piece(nseq, T, D, G, packed), packed) * scan::blocks_of(D, G);
 }
 
 size_t scan_bwd_workspace_bytes(int nseq, int T, int D, int N, int G, bool packed) {

@@ -161,18 +161,10 @@ __global__ void __launch_bounds__(BLOCK) scan_walk(FwdArgs a) {
 // workgroups whole 544 us, cut 514; at 512 whole 697, cut 907.  Pieces are as many as give 2,048 workgroups, eight a
 // compute unit (65,536 tokens, before the step's exponential was shortened: 512 workgroups 1,259 us, 1,024 951, 2,048 896, 4,096 916), of 64 tokens at the least
 // (2 x 1,000 tokens by 256 channels of 32 states: 32 tokens 29.7 us, 64 30.9, 128 43.8; the backward pass of four
-// sequences by 512 channels, which has the same rule: 90.7, 81.8, 107.7) and at most 256 a sequence, each of which puts its start
-// together from all before it.
+// sequences by 512 channels, which has the same rule: 90.7, 81.8, 107.7).
 static int fwd_piece(int nseq, int T, int D, int G, bool packed) {
-    const int64_t blocks = blocks_of(D, G), rows = packed ? T : (int64_t)nseq * T;
-    const int64_t whole = ((int64_t)T + TILE - 1) / TILE * TILE;
-    if (!packed && nseq * blocks >= 512) return (int)whole;
-    const int64_t pieces = 2048 / blocks > 1 ? 2048 / blocks : 1;
-    int64_t len = rows / pieces;
-    if (len < 2 * TILE) len = 2 * TILE;
-    if (len < T / 256) len = T / 256;
-    len = (len + TILE - 1) / TILE * TILE;
-    return (int)(len < whole ? len : whole);
+    if (!packed && (int64_t)nseq * blocks_of(D, G) >= 512) return (int)(((int64_t)T + TILE - 1) / TILE * TILE);
+    return cut_piece(nseq, T, D, G, packed);
 }
 
 template <typename E, int NS, bool SOFTPLUS>
