@@ -132,11 +132,12 @@ __device__ __forceinline__ float softplus(float v, float& slope) {
     return softplus_of(v, e);
 }
 
-// sigmoid(v) to a few ulp; exactly 0 and 1 in the tails.
+// sigmoid(v) = 1 / (1 + e^-v) to a few ulp, the exponential as above; the power of two is held finite, so below e^-87 comes
+// e^-87 or 0.
 __device__ __forceinline__ float sigmoid(float v) {
-    const float e = exp_minus(v), d = 1.0f + e, r = __builtin_amdgcn_rcpf(d);
-    const float i = __builtin_fmaf(r, __builtin_fmaf(-d, r, 1.0f), r);   // one step: 1 / (1 + e)
-    return v < 0.0f ? e * i : i;
+    const float t = __builtin_fminf(v * -LOG2E, 126.0f), e = __builtin_amdgcn_exp2f(t);
+    const float rest = __builtin_amdgcn_fmed3f(__builtin_fmaf(t, -0.6931471805599453f, -v), -1.0f, 1.0f);
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_fmaf(e, rest, e));
 }
 // The gate of an output that is stored in E: in bf16 from the hardware exponential and reciprocal, whose error of a few 2^-24 |v| is
 // far below that rounding.  The backward pass takes sigmoid, since dA, dskip, ddt_bias and dS0 are fp32.
