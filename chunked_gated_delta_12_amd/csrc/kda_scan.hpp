@@ -16,7 +16,9 @@
 // device: a piece's map is (sum of delta, end state from nothing), its decay being
 // exp(A sum delta) whatever its length.  The pieces of sequence n start at slot
 // first(n) = its first row / piece + n (n * ceil(T / piece) for sequences of T tokens each),
-// which leaves room for each sequence's last, part piece.
+// which leaves room for each sequence's last, part piece.  A slot is a place in a launch alone: of maps a sequence
+// has one less than pieces, floor((length - 1) / piece), which is no more than the multiples of a piece that it spans, so the first
+// row / piece is their place in the workspace, and sequences that are not cut take none of it.
 #pragma once
 
 #include <type_traits>
@@ -39,7 +41,7 @@ struct Seqs {
 // What a slot has: the sequence, its rows [row0, row0 + len), the piece's number and how many there are.
 struct Place {
     int seq, k, pieces, len;
-    int64_t row0, first;
+    int64_t row0, map0;   // map0: the place of the sequence's first map
 };
 
 // A value that all lanes share, in a scalar register: what was loaded may have come through vector ones.
@@ -72,7 +74,7 @@ __device__ __forceinline__ bool place_of(const Seqs& s, int64_t slot, Place& p) 
         p.pieces = pieces;
         p.len = s.T;
         p.row0 = (int64_t)p.seq * s.T;
-        p.first = (int64_t)p.seq * pieces;
+        p.map0 = (int64_t)p.seq * (pieces - 1);
         return true;
     }
     // The last sequence whose first slot is not behind this one: 64 candidates at a time, so that 4,096 sequences take
@@ -92,9 +94,9 @@ __device__ __forceinline__ bool place_of(const Seqs& s, int64_t slot, Place& p) 
     p.seq = lo;
     p.row0 = r0;
     p.len = r1 - r0;
-    p.first = r0 / s.piece + (int64_t)lo;
+    p.map0 = r0 / s.piece;
     p.pieces = p.len > s.piece ? (p.len - 1) / s.piece + 1 : 1;   // a sequence without tokens has one, empty
-    const int64_t k = slot - p.first;
+    const int64_t k = slot - p.map0 - lo;
     p.k = (int)k;
     return k >= 0 && k < p.pieces;
 }
@@ -242,17 +244,17 @@ __device__ __forceinline__ void st_states(float* p, const float* x) {
     }
 }
 
-// v <- exp(A2 sum_j) v + local_j along `count` pieces from j0 on in steps of `by`, the loads of eight at a time in
-// flight: a chain of dependent loads takes half a microsecond a piece.
+// v <- exp(A2 sum_j) v + local_j along `count` pieces, the first where local and sums point, the others in steps of `by`, the loads of
+// eight at a time in flight: a chain of dependent loads takes half a microsecond a piece.
 template <int NS>
-__device__ __forceinline__ void along_pieces(float (&v)[NS], const float (&A2)[NS], const float* local, const float* sums, int64_t j0, int by,
-                                             int count, int64_t states, int D) {
+__device__ __forceinline__ void along_pieces(float (&v)[NS], const float (&A2)[NS], const float* local, const float* sums, int by, int count,
+                                             int64_t states, int D) {
     constexpr int AT_ONCE = NS <= 4 ? 8 : NS == 8 ? 4 : 2;
     for (int k = 0; k < count; k += AT_ONCE) {
         float l[AT_ONCE][NS], s[AT_ONCE];
 #pragma unroll
         for (int u = 0; u < AT_ONCE; ++u) {
-            const int64_t j = j0 + (int64_t)by * (k + u < count ? k + u : count - 1);
+            const int64_t j = (int64_t)by * (k + u < count ? k + u : count - 1);
             ld_states<NS>(local + j * states, l[u]);
             s[u] = sums[j * D];
         }
@@ -323,6 +325,11 @@ inline int cut_piece(int nseq, int T, int D, int G, bool packed) {
 // Slots of the pieces of all sequences.
 inline int64_t slots_of(int nseq, int T, int piece, bool packed) {
     return packed ? (int64_t)T / piece + nseq : (int64_t)nseq * (((int64_t)T + piece - 1) / piece);
+}
+
+// Maps of all sequences.
+inline int64_t maps_of(int nseq, int T, int piece, bool packed) {
+    return packed ? (int64_t)T / piece : (int64_t)nseq * (((int64_t)T + piece - 1) / piece - 1);
 }
 
 }  // namespace scan

@@ -43,17 +43,18 @@ struct BwdArgs {
     const float *A, *skip, *bias, *S0, *dS_T;
     void *dx, *ddt, *dz;
     float* dS0;
-    // workspace.  Of each piece: end state [slot][D][N], gradient before it [slot][D][N], sum of delta [slot][D].  Of each
-    // 16 tokens of a sequence: state before them [chunk][D][N], sum of delta before them within the piece [chunk][D].
+    // workspace.  Of each piece with one behind it: end state [map][D][N]; of each with one before it: gradient before it [map][D][N],
+    // sum of delta [map][D].  Of each 16 tokens of a piece but its first: state before them [chunk][D][N], sum of delta
+    // before them within the piece [chunk][D]; chunk 0 is zeros, which is what a piece's first 16 tokens have.
     float *local, *grad, *sums, *start, *before;
-    // parts: dA [slot][D][N], dskip and dbias [slot][D], db and dc [workgroup of channels][row][2][N]
+    // parts: dA [part][D][N], dskip and dbias [part][D], db and dc [workgroup of channels][row][2][N]
     float *pA, *pskip, *pbias, *pbc;
-    int64_t rows;
+    int64_t rows, slots, parts;
 };
 
-// The chunks of sequence n start at its first row / 16 + n.
+// The chunk before a sequence's second 16 tokens, by the rule of its maps' places.
 __device__ __forceinline__ int64_t first_chunk(const Seqs& s, const Place& p) {
-    return s.cu ? p.row0 / CH + p.seq : (int64_t)p.seq * ((s.T + CH - 1) / CH);
+    return s.cu ? p.row0 / CH : (int64_t)p.seq * ((s.T + CH - 1) / CH - 1);
 }
 
 // BACK: sequences may be cut, and the gradient before a piece is asked for (the first piece's goes unused).
@@ -64,13 +65,19 @@ __global__ void __launch_bounds__(BLOCK) scan_bwd_map(BwdArgs a) {
     const int per = (a.D / a.G + BLOCK_CH - 1) / BLOCK_CH, nblk = a.G * per;
     const int blk = (int)(blockIdx.x % (unsigned)nblk);
     const int64_t slot = blockIdx.x / (unsigned)nblk;
-    Place pl;
-    if (!place_of(a.seqs, slot, pl)) return;
     const int grp = blk / per, Dg = a.D / a.G;
     const int lane = threadIdx.x & 63, q = lane & 3;
     const int in_group = (blk % per) * BLOCK_CH + (int)(threadIdx.x >> 6) * WAVE_CH + (lane >> 2);
     const bool real = in_group < Dg;
     const int ch = grp * Dg + (real ? in_group : Dg - 1);
+    const int64_t at_state = (int64_t)ch * N + q * NS, states = (int64_t)a.D * N;
+    if (slot == 0 && real) {
+        const float zero[NS] = {};
+        st_states<NS>(a.start + at_state, zero);
+        if (q == 0) a.before[ch] = 0.0f;
+    }
+    Place pl;
+    if (!place_of(a.seqs, slot, pl)) return;
     const int t_first = pl.k * a.seqs.piece;
     const int n = uniform(pl.len - t_first < a.seqs.piece ? pl.len - t_first : a.seqs.piece);
     const int64_t row = uniform64(pl.row0 + t_first);
@@ -80,7 +87,6 @@ __global__ void __launch_bounds__(BLOCK) scan_bwd_map(BwdArgs a) {
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g) own[g] = real ? ((uint32_t)(4 * g + q) * (uint32_t)a.D + ch) * (uint32_t)sizeof(E) : NOWHERE;
     const float bias = a.bias ? a.bias[ch] : 0.0f;
-    const int64_t at_state = (int64_t)ch * N + q * NS, states = (int64_t)a.D * N;
     float* start = a.start + (first_chunk(a.seqs, pl) + t_first / CH) * states + at_state;
     float* before = a.before + (first_chunk(a.seqs, pl) + t_first / CH) * a.D + ch;
 
@@ -132,7 +138,7 @@ __global__ void __launch_bounds__(BLOCK) scan_bwd_map(BwdArgs a) {
                 if (t0 + 4 * g >= n) break;
                 const int chunk = (t0 + 4 * g) / CH;
                 const float s = quad_sum(sum);
-                if (real) {
+                if (real && chunk > 0) {
                     st_states<NS>(start + chunk * states, h);
                     if (q == 0) before[(int64_t)chunk * a.D] = s;
                 }
@@ -169,9 +175,12 @@ __global__ void __launch_bounds__(BLOCK) scan_bwd_map(BwdArgs a) {
     }
     sum = quad_sum(sum);
     if (BACK && real && pl.pieces > 1) {   // what the other pieces of the sequence ask for
-        if (pl.k < pl.pieces - 1) st_states<NS>(a.local + slot * states + at_state, h);
-        if (pl.k > 0) st_states<NS>(a.grad + slot * states + at_state, m);
-        if (q == 0) a.sums[slot * a.D + ch] = sum;
+        const int64_t map = pl.map0 + pl.k;
+        if (pl.k < pl.pieces - 1) st_states<NS>(a.local + map * states + at_state, h);
+        if (pl.k > 0) {
+            st_states<NS>(a.grad + (map - 1) * states + at_state, m);
+            if (q == 0) a.sums[(map - 1) * a.D + ch] = sum;
+        }
     }
 }
 
@@ -206,8 +215,28 @@ __device__ __forceinline__ float channel_sums(float (&v)[CH], int lane) {
 // Token T of 16's value, which lane T % 4 of the quad holds in v[T / 4].
 template <int T>
 __device__ __forceinline__ float token(const float* v) { return quad_lane<T % 4>(v[T / 4]); }
-template <typename E, int NS>
-__global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(NS == 4 && sizeof(E) == 2 ? 3 : NS <= 8 ? 2 : 1))) scan_bwd_grad(BwdArgs a) {
+
+// Which channel and states thread `me` of the workgroup of channels blk has.
+struct Mine {
+    int q, ch;
+    bool real;
+    int64_t at_state;
+};
+template <int NS>
+__device__ __forceinline__ Mine mine_of(const BwdArgs& a, int blk, int me) {
+    const int Dg = a.D / a.G, per = (Dg + BLOCK_CH - 1) / BLOCK_CH, in_group = blk % per * BLOCK_CH + (me >> 2);
+    Mine m;
+    m.q = me & 3;
+    m.real = in_group < Dg;
+    m.ch = blk / per * Dg + (m.real ? in_group : Dg - 1);
+    m.at_state = (int64_t)m.ch * 4 * NS + m.q * NS;
+    return m;
+}
+
+// MANY: a workgroup has several slots.  Where it has one, as in every call but one of very many short sequences, the loop would cost:
+// 8 x 4,096 tokens by 2,048 channels 1,232 us without, 1,252 with it; 2,048 x 16 tokens by 1,024 channels 607 and 660.
+template <typename E, int NS, bool MANY>
+__global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(NS <= 4 && sizeof(E) == 2 ? 3 : NS <= 8 ? 2 : 1))) scan_bwd_grad(BwdArgs a) {
     constexpr int N = 4 * NS, GROUPS = CH / 4, WAVES = BLOCK / 64;
     __shared__ float bc[2][N * BPAD];
     __shared__ float part[WAVES][CH][2][N];
@@ -216,219 +245,235 @@ __global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(NS =
     // what the outputs need of a lane's own tokens beside, while the registers are the states'
     __shared__ float aside[3][GROUPS][BLOCK];
     __shared__ float chan[4][BLOCK];   // a channel's bias and skip, and its parts of their gradients
-    const int me = threadIdx.x;
-    const int per = (a.D / a.G + BLOCK_CH - 1) / BLOCK_CH, nblk = a.G * per;
+    const int nblk = blocks_of(a.D, a.G);
     const int blk = (int)(blockIdx.x % (unsigned)nblk);
-    const int64_t slot = blockIdx.x / (unsigned)nblk;
-    const int grp = blk / per, Dg = a.D / a.G;
-    const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, q = lane & 3;
-    const int in_group = (blk % per) * BLOCK_CH + wave * WAVE_CH + (lane >> 2);
-    const bool real = in_group < Dg;
-    const int ch = grp * Dg + (real ? in_group : Dg - 1);
-    const int64_t at_state = (int64_t)ch * N + q * NS, states = (int64_t)a.D * N;
-    Place pl;
-    if (!place_of(a.seqs, slot, pl)) {   // its parts are read all the same
-        if (real) {
-            const float zero[NS] = {};
-            st_states<NS>(a.pA + slot * states + at_state, zero);
-            if (q == 0) a.pskip[slot * a.D + ch] = a.pbias[slot * a.D + ch] = 0.0f;
-        }
-        return;
-    }
-    const int t_first = pl.k * a.seqs.piece;
-    const int n = uniform(pl.len - t_first < a.seqs.piece ? pl.len - t_first : a.seqs.piece);
-    const int64_t row = uniform64(pl.row0 + t_first);
+    const int64_t part0 = blockIdx.x / (unsigned)nblk;
+    const int grp = blk / (nblk / a.G);
+    const int64_t states = (int64_t)a.D * N, ld = (int64_t)a.G * N;
     const bool gated = a.z != nullptr;
-    const uint32_t own = real ? ((uint32_t)q * (uint32_t)a.D + ch) * (uint32_t)sizeof(E) : NOWHERE, four = 4 * (uint32_t)a.D * (uint32_t)sizeof(E);
-    const int64_t ld = (int64_t)a.G * N;
-    chan[0][me] = a.bias ? a.bias[ch] : 0.0f;
-    chan[1][me] = a.skip ? a.skip[ch] : 0.0f;
-    chan[2][me] = chan[3][me] = 0.0f;
-    const int64_t chunk0 = first_chunk(a.seqs, pl) + t_first / CH;
-
-    float A2[NS], mu[NS], h0[NS];
-    ld_states<NS>(a.A + at_state, A2);
+    int me = threadIdx.x;
+    {
+        const Mine m = mine_of<NS>(a, blk, me);
+        float A2[NS];
+        ld_states<NS>(a.A + m.at_state, A2);
 #pragma unroll
-    for (int i = 0; i < NS; ++i) A2[i] *= LOG2E, mu[i] = h0[i] = 0.0f;
-    if (a.dS_T) ld_states<NS>(a.dS_T + (int64_t)pl.seq * states + at_state, mu);
-    // what the pieces behind make of it, and the state that the pieces before leave
-    along_pieces<NS>(mu, A2, a.grad + at_state, a.sums + ch, pl.first + pl.pieces - 1, -1, pl.pieces - 1 - pl.k, states, a.D);
-    if (pl.k > 0) {
-        ld_states<NS>(a.local + pl.first * states + at_state, h0);
-        along_pieces<NS>(h0, A2, a.local + at_state, a.sums + ch, pl.first + 1, 1, pl.k - 1, states, a.D);
+        for (int i = 0; i < NS; ++i) sA[i][me] = A2[i] * LOG2E, sdA[i][me] = 0.0f;
+        chan[0][me] = a.bias ? a.bias[m.ch] : 0.0f;
+        chan[1][me] = a.skip ? a.skip[m.ch] : 0.0f;
+        chan[2][me] = chan[3][me] = 0.0f;
     }
+    int64_t slot = part0;
+    do {
+        // hides the thread's number: what follows from it would stay in registers from before the loop to behind it, and in bf16
+        // up to 16 states there are none to spare
+        asm volatile("" : "+v"(me));
+        const Mine m = mine_of<NS>(a, blk, me);
+        const int q = m.q, ch = m.ch;
+        const bool real = m.real;
+        const int64_t at_state = m.at_state;
+        const int wave = uniform(me >> 6), lane = me & 63;
+        const uint32_t own = real ? ((uint32_t)q * (uint32_t)a.D + ch) * (uint32_t)sizeof(E) : NOWHERE, four = 4 * (uint32_t)a.D * (uint32_t)sizeof(E);
+        Place pl;
+        if (!place_of(a.seqs, slot, pl)) continue;
+        const int t_first = pl.k * a.seqs.piece;
+        const int n = uniform(pl.len - t_first < a.seqs.piece ? pl.len - t_first : a.seqs.piece);
+        const int64_t row = uniform64(pl.row0 + t_first);
+        const int64_t chunk0 = first_chunk(a.seqs, pl) + t_first / CH;
+        {
+            float A2[NS], mu[NS], h0[NS];
 #pragma unroll
-    for (int i = 0; i < NS; ++i) sA[i][me] = A2[i], smu[i][me] = mu[i], sh0[i][me] = h0[i], sdA[i][me] = 0.0f;
+            for (int i = 0; i < NS; ++i) A2[i] = sA[i][me], mu[i] = h0[i] = 0.0f;
+            if (a.dS_T) ld_states<NS>(a.dS_T + (int64_t)pl.seq * states + at_state, mu);
+            // what the pieces behind make of it, and the state that the pieces before leave
+            const int64_t last = pl.map0 + pl.pieces - 2;
+            along_pieces<NS>(mu, A2, a.grad + last * states + at_state, a.sums + last * a.D + ch, -1, pl.pieces - 1 - pl.k, states, a.D);
+            if (pl.k > 0) {
+                ld_states<NS>(a.local + pl.map0 * states + at_state, h0);
+                along_pieces<NS>(h0, A2, a.local + (pl.map0 + 1) * states + at_state, a.sums + pl.map0 * a.D + ch, 1, pl.k - 1, states, a.D);
+            }
+#pragma unroll
+            for (int i = 0; i < NS; ++i) smu[i][me] = mu[i], sh0[i][me] = h0[i];
+        }
 
-    // a chunk's operands are asked for one chunk ahead
-    Rows<E, N, CH> next;
-    uint32_t nx[GROUPS], nt[GROUPS], nz[GROUPS], nd[GROUPS];
-    float nh[NS], ns = 0.0f;
-    auto fetch = [&](int chunk) {
-        const int tokens = n - CH * chunk < CH ? n - CH * chunk : CH;
-        const int64_t from = row + CH * chunk, at = from * ld + grp * N;
-        next.fetch((const E*)a.b + at, (const E*)a.c + at, ld, tokens);
-        const Rsrc rx = rows_rsrc<E>(a.x, from, a.D, tokens), rt = rows_rsrc<E>(a.dt, from, a.D, tokens),
-                   rd = rows_rsrc<E>(a.dy, from, a.D, tokens);
-#pragma unroll
-        for (int g = 0; g < GROUPS; ++g) {
-            nx[g] = ld_one<E>(rx, own + g * four);
-            nt[g] = ld_one<E>(rt, own + g * four);
-            nd[g] = ld_one<E>(rd, own + g * four);
-        }
-        if (gated) {
-            const Rsrc rz = rows_rsrc<E>(a.z, from, a.D, tokens);
-#pragma unroll
-            for (int g = 0; g < GROUPS; ++g) nz[g] = ld_one<E>(rz, own + g * four);
-        }
-        ld_states<NS>(a.start + (chunk0 + chunk) * states + (uint32_t)at_state, nh);
-        ns = a.before[(chunk0 + chunk) * a.D + (uint32_t)ch];
-    };
-    const int chunks = (n + CH - 1) / CH;
-    if (chunks > 0) fetch(chunks - 1);
-    for (int k = chunks - 1; k >= 0; --k) {
-        float dv[GROUPS], uv[GROUPS], vy[GROUPS];
-        next.each([&](bool of_c, int t, int n0, f32x4 x) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) bc[of_c ? 1 : 0][(n0 + j) * BPAD + t] = x[j];
-        });
-#pragma unroll
-        for (int g = 0; g < GROUPS; ++g) {
-            dv[g] = value<E>(nt[g]) + chan[0][me];
-            uv[g] = aside[2][g][me] = value<E>(nx[g]);
-            vy[g] = value<E>(nd[g]);
-        }
-        if (a.softplus) {
+        // a chunk's operands are asked for one chunk ahead
+        Rows<E, N, CH> next;
+        uint32_t nx[GROUPS], nt[GROUPS], nz[GROUPS], nd[GROUPS];
+        float nh[NS], ns = 0.0f;
+        auto fetch = [&](int chunk) {
+            const int tokens = n - CH * chunk < CH ? n - CH * chunk : CH;
+            const int64_t from = row + CH * chunk, at = from * ld + grp * N;
+            next.fetch((const E*)a.b + at, (const E*)a.c + at, ld, tokens);
+            const Rsrc rx = rows_rsrc<E>(a.x, from, a.D, tokens), rt = rows_rsrc<E>(a.dt, from, a.D, tokens),
+                       rd = rows_rsrc<E>(a.dy, from, a.D, tokens);
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g) {
-                float slope;
-                dv[g] = softplus(dv[g], slope);
-                aside[0][g][me] = slope;
+                nx[g] = ld_one<E>(rx, own + g * four);
+                nt[g] = ld_one<E>(rt, own + g * four);
+                nd[g] = ld_one<E>(rd, own + g * four);
             }
-        } else {
+            if (gated) {
+                const Rsrc rz = rows_rsrc<E>(a.z, from, a.D, tokens);
 #pragma unroll
-            for (int g = 0; g < GROUPS; ++g) aside[0][g][me] = 1.0f;
-        }
-        if (gated)
+                for (int g = 0; g < GROUPS; ++g) nz[g] = ld_one<E>(rz, own + g * four);
+            }
+            const float* from_S0 = a.S0 + (int64_t)pl.seq * states;
+            const int64_t at_chunk = chunk > 0 ? chunk0 + chunk : 0;
+            ld_states<NS>((chunk == 0 && pl.k == 0 && a.S0 ? from_S0 : a.start + at_chunk * states) + (uint32_t)at_state, nh);
+            ns = a.before[at_chunk * a.D + (uint32_t)ch];
+        };
+        const int chunks = (n + CH - 1) / CH;
+        if (chunks > 0) fetch(chunks - 1);
+        for (int k = chunks - 1; k >= 0; --k) {
+            float dv[GROUPS], uv[GROUPS], vy[GROUPS];
+            next.each([&](bool of_c, int t, int n0, f32x4 x) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) bc[of_c ? 1 : 0][(n0 + j) * BPAD + t] = x[j];
+            });
 #pragma unroll
             for (int g = 0; g < GROUPS; ++g) {
-                const float zv = value<E>(nz[g]), sg = sigmoid(zv);
-                aside[1][g][me] = vy[g] * (sg * (1.0f + zv * (1.0f - sg)));
-                vy[g] *= zv * sg;
+                dv[g] = value<E>(nt[g]) + chan[0][me];
+                uv[g] = aside[2][g][me] = value<E>(nx[g]);
+                vy[g] = value<E>(nd[g]);
             }
-        // a step of nothing behind the last token, where x and dy are zero, and of lanes without a channel, which read zeros: their
-        // bias alone could make states of any size, and zero times infinity would reach the sums over channels
-        const int left = real ? n - CH * k - q : 0;
+            if (a.softplus) {
 #pragma unroll
-        for (int g = 0; g < GROUPS; ++g) {
-            if (4 * g >= left) dv[g] = aside[0][g][me] = 0.0f;
-            uv[g] *= dv[g];
-        }
+                for (int g = 0; g < GROUPS; ++g) {
+                    float slope;
+                    dv[g] = softplus(dv[g], slope);
+                    aside[0][g][me] = slope;
+                }
+            } else {
 #pragma unroll
-        for (int i = 0; i < NS; ++i)
-            sh[i][me] = pl.k > 0 ? __builtin_fmaf(__builtin_amdgcn_exp2f(ns * sA[i][me]), sh0[i][me], nh[i]) : nh[i];
-        lds_barrier();
-        if (k > 0) fetch(k - 1);
+                for (int g = 0; g < GROUPS; ++g) aside[0][g][me] = 1.0f;
+            }
+            if (gated)
+#pragma unroll
+                for (int g = 0; g < GROUPS; ++g) {
+                    const float zv = value<E>(nz[g]), sg = sigmoid(zv);
+                    aside[1][g][me] = vy[g] * (sg * (1.0f + zv * (1.0f - sg)));
+                    vy[g] *= zv * sg;
+                }
+            // a step of nothing behind the last token, where x and dy are zero, and of lanes without a channel, which read zeros: their
+            // bias alone could make states of any size, and zero times infinity would reach the sums over channels
+            const int left = real ? n - CH * k - q : 0;
+#pragma unroll
+            for (int g = 0; g < GROUPS; ++g) {
+                if (4 * g >= left) dv[g] = aside[0][g][me] = 0.0f;
+                uv[g] *= dv[g];
+            }
+#pragma unroll
+            for (int i = 0; i < NS; ++i)
+                sh[i][me] = pl.k > 0 ? __builtin_fmaf(__builtin_amdgcn_exp2f(ns * sA[i][me]), sh0[i][me], nh[i]) : nh[i];
+            lds_barrier();
+            if (k > 0) fetch(k - 1);
 
-        float s1[CH], s2[CH], sy[CH];
+            float s1[CH], s2[CH], sy[CH];
 #pragma unroll
-        for (int t = 0; t < CH; ++t) s1[t] = s2[t] = sy[t] = 0.0f;
+            for (int t = 0; t < CH; ++t) s1[t] = s2[t] = sy[t] = 0.0f;
 #pragma unroll 1
-        for (int i = 0; i < NS; ++i) {
-            // Operands are handed round the quad as modifiers of multiplications, which have to follow one another closely for
-            // that; the empty statements keep the compiler from drawing the tokens together.
+            for (int i = 0; i < NS; ++i) {
+                // Operands are handed round the quad as modifiers of multiplications, which have to follow one another closely for
+                // that; the empty statements keep the compiler from drawing the tokens together.
 #pragma unroll
-            for (int g = 0; g < GROUPS; ++g) asm volatile("" : "+v"(dv[g]), "+v"(uv[g]), "+v"(vy[g]));
-            float e[CH], hp[CH], v[CH];
-            const float *bi = bc[0] + (q * NS + i) * BPAD, *ci = bc[1] + (q * NS + i) * BPAD;
-            float h = sh[i][me];
-            const float A2i = sA[i][me], Ai = A2i * (1.0f / LOG2E);
-            each_of_quad([&](auto Gr) {
-                constexpr int t0 = 4 * decltype(Gr)::value;
-                float bv[4], cv[4];
-                ld_states<4>(bi + t0, bv);
-                ld_states<4>(ci + t0, cv);
-                each_of_quad([&](auto J) {
-                    constexpr int j = decltype(J)::value, t = t0 + j;
-                    hp[t] = h;
-                    e[t] = __builtin_amdgcn_exp2f(token<t>(dv) * A2i);
-                    h = __builtin_fmaf(e[t], h, token<t>(uv) * bv[j]);
-                    sy[t] = __builtin_fmaf(cv[j], h, sy[t]);
-                    v[t] = token<t>(vy) * h;   // zero of lanes without a channel: no dy, and the last channel's state kept
+                for (int g = 0; g < GROUPS; ++g) asm volatile("" : "+v"(dv[g]), "+v"(uv[g]), "+v"(vy[g]));
+                float e[CH], hp[CH], v[CH];
+                const float *bi = bc[0] + (q * NS + i) * BPAD, *ci = bc[1] + (q * NS + i) * BPAD;
+                float h = sh[i][me];
+                const float A2i = sA[i][me], Ai = A2i * (1.0f / LOG2E);
+                each_of_quad([&](auto Gr) {
+                    constexpr int t0 = 4 * decltype(Gr)::value;
+                    float bv[4], cv[4];
+                    ld_states<4>(bi + t0, bv);
+                    ld_states<4>(ci + t0, cv);
+                    each_of_quad([&](auto J) {
+                        constexpr int j = decltype(J)::value, t = t0 + j;
+                        hp[t] = h;
+                        e[t] = __builtin_amdgcn_exp2f(token<t>(dv) * A2i);
+                        h = __builtin_fmaf(e[t], h, token<t>(uv) * bv[j]);
+                        sy[t] = __builtin_fmaf(cv[j], h, sy[t]);
+                        v[t] = token<t>(vy) * h;   // zero of lanes without a channel: no dy, and the last channel's state kept
+                    });
+                    asm volatile("" : : "v"(v[t0]), "v"(v[t0 + 1]), "v"(v[t0 + 2]), "v"(v[t0 + 3]), "v"(sy[t0 + 3]) : "memory");
                 });
-                asm volatile("" : : "v"(v[t0]), "v"(v[t0 + 1]), "v"(v[t0 + 2]), "v"(v[t0 + 3]), "v"(sy[t0 + 3]) : "memory");
-            });
-            const int t_mine = lane >> 2;
-            part[wave][t_mine][1][q * NS + i] = channel_sums(v, lane);
+                const int t_mine = lane >> 2;
+                part[wave][t_mine][1][q * NS + i] = channel_sums(v, lane);
 #pragma unroll
-            for (int g = 0; g < GROUPS; ++g) asm volatile("" : "+v"(dv[g]), "+v"(uv[g]), "+v"(vy[g]) : : "memory");
-            float m = smu[i][me], s = 0.0f;
-            each_of_quad([&](auto Gr) {
-                constexpr int t0 = CH - 4 - 4 * decltype(Gr)::value;
-                float bv[4], cv[4];
-                ld_states<4>(bi + t0, bv);
-                ld_states<4>(ci + t0, cv);
-                float w[4];
-                each_of_quad([&](auto J) {
-                    constexpr int j = 3 - decltype(J)::value, t = t0 + j;
-                    const float lam = token<t>(vy) * cv[j] + m;
-                    v[t] = token<t>(uv) * lam;
-                    m = e[t] * lam;
-                    w[j] = m * hp[t];   // lam a_t h_t-1
-                    s1[t] = __builtin_fmaf(lam, bv[j], s1[t]);
-                    s2[t] = __builtin_fmaf(Ai, w[j], s2[t]);
+                for (int g = 0; g < GROUPS; ++g) asm volatile("" : "+v"(dv[g]), "+v"(uv[g]), "+v"(vy[g]) : : "memory");
+                float m = smu[i][me], s = 0.0f;
+                each_of_quad([&](auto Gr) {
+                    constexpr int t0 = CH - 4 - 4 * decltype(Gr)::value;
+                    float bv[4], cv[4];
+                    ld_states<4>(bi + t0, bv);
+                    ld_states<4>(ci + t0, cv);
+                    float w[4];
+                    each_of_quad([&](auto J) {
+                        constexpr int j = 3 - decltype(J)::value, t = t0 + j;
+                        const float lam = token<t>(vy) * cv[j] + m;
+                        v[t] = token<t>(uv) * lam;
+                        m = e[t] * lam;
+                        w[j] = m * hp[t];   // lam a_t h_t-1
+                        s1[t] = __builtin_fmaf(lam, bv[j], s1[t]);
+                        s2[t] = __builtin_fmaf(Ai, w[j], s2[t]);
+                    });
+                    quad_fma(s, dv[t0 / 4], w);
+                    asm volatile("" : : "v"(v[t0]), "v"(v[t0 + 1]), "v"(v[t0 + 2]), "v"(v[t0 + 3]), "v"(s) : "memory");
                 });
-                quad_fma(s, dv[t0 / 4], w);
-                asm volatile("" : : "v"(v[t0]), "v"(v[t0 + 1]), "v"(v[t0 + 2]), "v"(v[t0 + 3]), "v"(s) : "memory");
-            });
-            smu[i][me] = m;
-            sdA[i][me] += s;
-            part[wave][t_mine][0][q * NS + i] = channel_sums(v, lane);
-        }
-        const int64_t from = row + CH * k;
-        const int tokens = n - CH * k < CH ? n - CH * k : CH;
-        const Rsrc wx = rows_rsrc<E>(a.dx, from, a.D, tokens), wt = rows_rsrc<E>(a.ddt, from, a.D, tokens);
-        const float skip = chan[1][me];
-        float dskip = chan[3][me], dbias = chan[2][me];
+                smu[i][me] = m;
+                sdA[i][me] += s;
+                part[wave][t_mine][0][q * NS + i] = channel_sums(v, lane);
+            }
+            const int64_t from = row + CH * k;
+            const int tokens = n - CH * k < CH ? n - CH * k : CH;
+            const Rsrc wx = rows_rsrc<E>(a.dx, from, a.D, tokens), wt = rows_rsrc<E>(a.ddt, from, a.D, tokens);
+            const float skip = chan[1][me];
+            float dskip = chan[3][me], dbias = chan[2][me];
 #pragma unroll
-        for (int g = 0; g < GROUPS; ++g) {
-            const float lb = quad_sums(s1 + 4 * g, q), lw = quad_sums(s2 + 4 * g, q);
-            const float xv = aside[2][g][me], ddt = __builtin_fmaf(xv, lb, lw) * aside[0][g][me];
-            st_one<E>(wx, own + g * four, __builtin_fmaf(skip, vy[g], dv[g] * lb));
-            st_one<E>(wt, own + g * four, ddt);
-            dskip = __builtin_fmaf(vy[g], xv, dskip);
-            dbias += ddt;   // zero where there is no token
-        }
-        if (gated) {
-            const Rsrc wz = rows_rsrc<E>(a.dz, from, a.D, tokens);
+            for (int g = 0; g < GROUPS; ++g) {
+                const float lb = quad_sums(s1 + 4 * g, q), lw = quad_sums(s2 + 4 * g, q);
+                const float xv = aside[2][g][me], ddt = __builtin_fmaf(xv, lb, lw) * aside[0][g][me];
+                st_one<E>(wx, own + g * four, __builtin_fmaf(skip, vy[g], dv[g] * lb));
+                st_one<E>(wt, own + g * four, ddt);
+                dskip = __builtin_fmaf(vy[g], xv, dskip);
+                dbias += ddt;   // zero where there is no token
+            }
+            if (gated) {
+                const Rsrc wz = rows_rsrc<E>(a.dz, from, a.D, tokens);
 #pragma unroll
-            for (int g = 0; g < GROUPS; ++g)
-                st_one<E>(wz, own + g * four, aside[1][g][me] * __builtin_fmaf(skip, aside[2][g][me], quad_sums(sy + 4 * g, q)));
-        }
-        chan[3][me] = dskip;
-        chan[2][me] = dbias;
-        lds_barrier();
-        // the workgroup's part of db and dc
-        float* to = a.pbc + ((int64_t)blk * a.rows + row + CH * k) * 2 * N;
-        for (int i = threadIdx.x; i < CH * 2 * N; i += BLOCK) {
-            if (CH * k + i / (2 * N) >= n) break;
-            float s = 0.0f;
+                for (int g = 0; g < GROUPS; ++g)
+                    st_one<E>(wz, own + g * four, aside[1][g][me] * __builtin_fmaf(skip, aside[2][g][me], quad_sums(sy + 4 * g, q)));
+            }
+            chan[3][me] = dskip;
+            chan[2][me] = dbias;
+            lds_barrier();
+            // the workgroup's part of db and dc
+            float* to = a.pbc + ((int64_t)blk * a.rows + row + CH * k) * 2 * N;
+            for (int i = me; i < CH * 2 * N; i += BLOCK) {
+                if (CH * k + i / (2 * N) >= n) break;
+                float s = 0.0f;
 #pragma unroll
-            for (int w = 0; w < WAVES; ++w) s += (&part[w][0][0][0])[i];
-            to[i] = s;
+                for (int w = 0; w < WAVES; ++w) s += (&part[w][0][0][0])[i];
+                to[i] = s;
+            }
         }
-    }
+        if (pl.k == 0 && a.dS0 && real) {
+            float mu[NS];
+#pragma unroll
+            for (int i = 0; i < NS; ++i) mu[i] = smu[i][me];
+            st_states<NS>(a.dS0 + (int64_t)pl.seq * states + at_state, mu);
+        }
+    } while (MANY && (slot += a.parts) < a.slots);
+    asm volatile("" : "+v"(me));
+    const Mine m = mine_of<NS>(a, blk, me);
     const float dskip = quad_sum(chan[3][me]), dbias = quad_sum(chan[2][me]);
     float dA[NS];
 #pragma unroll
-    for (int i = 0; i < NS; ++i) dA[i] = sdA[i][me], mu[i] = smu[i][me];
-    if (real) {
-        st_states<NS>(a.pA + slot * states + at_state, dA);
-        if (q == 0) {
-            a.pskip[slot * a.D + ch] = dskip;
-            a.pbias[slot * a.D + ch] = dbias;
+    for (int i = 0; i < NS; ++i) dA[i] = sdA[i][me];
+    if (m.real) {
+        st_states<NS>(a.pA + part0 * states + m.at_state, dA);
+        if (m.q == 0) {
+            a.pskip[part0 * a.D + m.ch] = dskip;
+            a.pbias[part0 * a.D + m.ch] = dbias;
         }
-        if (pl.k == 0 && a.dS0) st_states<NS>(a.dS0 + (int64_t)pl.seq * states + at_state, mu);
     }
 }
 
@@ -478,7 +523,7 @@ scan_bwd_sums(PartSums params, int64_t nparams, Seqs s, int64_t rows, int G, int
 // 2,048 channels: 256 workgroups 2,857 us, 512 1,499, 1,024 1,351, 2,048 1,272, 4,096 1,261).
 struct BwdPlan {
     int piece;
-    int64_t rows, slots, chunks;
+    int64_t rows, slots, parts;
     int64_t local, grad, sums, start, before, pA, pskip, pbias, pbc, floats;
 };
 static BwdPlan plan_of(int nseq, int T, int D, int N, int G, bool packed) {
@@ -486,7 +531,11 @@ static BwdPlan plan_of(int nseq, int T, int D, int N, int G, bool packed) {
     p.piece = cut_piece(nseq, T, D, G, packed);
     p.rows = packed ? T : (int64_t)nseq * T;
     p.slots = slots_of(nseq, T, p.piece, packed);
-    p.chunks = slots_of(nseq, T, CH, packed);
+    const int64_t maps = maps_of(nseq, T, p.piece, packed), chunks = maps_of(nseq, T, CH, packed);
+    // Of dA, dskip and ddt_bias a workgroup has the part of one slot, unless there are more than four times the slots that the rows
+    // make pieces (and more than fill the device): many short sequences, whose parts would be most of the workspace.
+    const int64_t fill = 2048 / blocks_of(D, G), four = 4 * (p.rows / p.piece), most = fill > four ? fill : four;
+    p.parts = p.slots < most ? p.slots : most > 1 ? most : 1;
     int64_t at = 0;
     auto take = [&](int64_t n) {
         const int64_t r = at;
@@ -494,15 +543,15 @@ static BwdPlan plan_of(int nseq, int T, int D, int N, int G, bool packed) {
         return r;
     };
     const int64_t states = (int64_t)D * N;
-    p.local = take(p.slots * states);
-    p.grad = take(p.slots * states);
-    p.pA = take(p.slots * states);
-    p.start = take(p.chunks * states);
+    p.local = take(maps * states);
+    p.grad = take(maps * states);
+    p.pA = take(p.parts * states);
+    p.start = take((1 + chunks) * states);
     p.pbc = take((int64_t)blocks_of(D, G) * p.rows * 2 * N);
-    p.sums = take(p.slots * D);
-    p.pskip = take(p.slots * D);
-    p.pbias = take(p.slots * D);
-    p.before = take(p.chunks * D);
+    p.sums = take(maps * D);
+    p.pskip = take(p.parts * D);
+    p.pbias = take(p.parts * D);
+    p.before = take((1 + chunks) * D);
     p.floats = at;
     return p;
 }
@@ -515,8 +564,9 @@ static hipError_t bwd_t(const BwdArgs& a, const BwdPlan& p, void* db, void* dc, 
     auto map = p.piece < a.seqs.T ? (a.softplus ? scan_bwd_map<E, NS, true, true> : scan_bwd_map<E, NS, false, true>)
                                   : (a.softplus ? scan_bwd_map<E, NS, true, false> : scan_bwd_map<E, NS, false, false>);
     hipLaunchKernelGGL(map, dim3(grid), dim3(BLOCK), 0, stream, a);
-    hipLaunchKernelGGL((scan_bwd_grad<E, NS>), dim3(grid), dim3(BLOCK), 0, stream, a);
-    const PartSums params{{a.pA, a.pskip, a.pbias}, {dA, dskip, dbias}, {(int64_t)a.D * N, a.D, a.D}, p.slots};
+    auto grad = p.parts < p.slots ? scan_bwd_grad<E, NS, true> : scan_bwd_grad<E, NS, false>;
+    hipLaunchKernelGGL(grad, dim3((unsigned)(p.parts * blocks)), dim3(BLOCK), 0, stream, a);
+    const PartSums params{{a.pA, a.pskip, a.pbias}, {dA, dskip, dbias}, {(int64_t)a.D * N, a.D, a.D}, p.parts};
     const int64_t nparams = part_sums_blocks(params), want = (p.rows * 2 * a.G * N + 1023) / 1024;
     hipLaunchKernelGGL(scan_bwd_sums<E>, dim3((unsigned)(nparams + (want < 2048 ? want : 2048) + (a.seqs.cu ? REST_BLOCKS : 0))), dim3(1024), 0, stream, params, nparams, a.seqs,
                        p.rows, a.G, N, blocks / a.G, a.pbc, (E*)db, (E*)dc, (E*)a.dx, (E*)a.ddt, (E*)a.dz, a.D);
@@ -539,7 +589,7 @@ hipError_t launch_scan_bwd(const ScanCall& c, const void* dy, const float* dS_T,
     float* w = (float*)workspace;
     const scan::BwdArgs a{{c.nseq, c.T, p.piece, c.cu}, c.D, c.G, c.softplus, c.x, c.dt, c.b, c.c, c.z, dy, c.A, c.skip, c.bias, c.S0, dS_T,
                           dx, ddt, dz, dS0, w + p.local, w + p.grad, w + p.sums, w + p.start, w + p.before, w + p.pA, w + p.pskip,
-                          w + p.pbias, w + p.pbc, p.rows};
+                          w + p.pbias, w + p.pbc, p.rows, p.slots, p.parts};
 #define KDA_SB(N)                                                                                          \
     return c.f32 ? scan::bwd_t<float, N / 4>(a, p, db, dc, dA, dskip, dbias, stream)                       \
                  : scan::bwd_t<bf16, N / 4>(a, p, db, dc, dA, dskip, dbias, stream)

@@ -27,8 +27,11 @@ struct FwdArgs {
     const float *A, *skip, *bias, *S0;
     void* y;
     unsigned walks;   // workgroups with a piece; those behind them clear y's rows of no sequence
-    float *S_T, *local, *sums;   // maps: end state from nothing [slot][D][N], sum of delta [slot][D]
+    float *S_T, *local, *keep, *sums;   // maps: end state from nothing [map][D][N], sum of delta [map][D]; S0 of cut sequences [..][D][N]
 };
+
+// Places for the S0 of cut sequences: one a sequence, or by its first row, whichever is fewer (kept_of).
+__device__ __forceinline__ bool kept_by_row(const Seqs& s) { return s.cu && s.nseq > s.T / s.piece; }
 
 template <typename E, int NS, bool SOFTPLUS, bool MAP, bool GATED>
 __global__ void __launch_bounds__(BLOCK) scan_walk(FwdArgs a) {
@@ -85,14 +88,14 @@ __global__ void __launch_bounds__(BLOCK) scan_walk(FwdArgs a) {
     for (int i = 0; i < NS; ++i) A2[i] *= LOG2E, h[i] = 0.0f;
     float* local = a.local + at_state;
     if (pl.k == 0) {
-        // the last piece has no map: its place keeps S0, which S_T may overwrite during the walk
-        const float* from = !MAP && pl.pieces > 1 ? local + (pl.first + pl.pieces - 1) * states
-                                                  : a.S0 + (int64_t)pl.seq * states + at_state;
+        // S_T may overwrite S0 during the walk, so the maps keep a copy for the first piece
+        float* kept = a.keep + (kept_by_row(a.seqs) ? pl.map0 : pl.seq) * states + at_state;
+        const float* from = !MAP && pl.pieces > 1 ? kept : a.S0 + (int64_t)pl.seq * states + at_state;
         if (a.S0) ld_states<NS>(from, h);
-        if (MAP && a.S0 && real) st_states<NS>(local + (pl.first + pl.pieces - 1) * states, h);
+        if (MAP && a.S0 && real) st_states<NS>(kept, h);
     } else if (!MAP) {
-        ld_states<NS>(local + pl.first * states, h);   // the first piece's map starts from S0
-        along_pieces<NS>(h, A2, local, a.sums + ch, pl.first + 1, 1, pl.k - 1, states, a.D);
+        ld_states<NS>(local + pl.map0 * states, h);   // the first piece's map starts from S0
+        along_pieces<NS>(h, A2, local + (pl.map0 + 1) * states, a.sums + (pl.map0 + 1) * a.D + ch, 1, pl.k - 1, states, a.D);
     }
     float sum = 0.0f;
     for (int t0 = 0, buf = 0; t0 < n; t0 += TILE, buf ^= 1) {
@@ -148,8 +151,8 @@ __global__ void __launch_bounds__(BLOCK) scan_walk(FwdArgs a) {
     if (MAP) {
         sum = quad_sum(sum);
         if (real) {
-            st_states<NS>(local + slot * states, h);
-            if (q == 0) a.sums[slot * a.D + ch] = sum;
+            st_states<NS>(local + (pl.map0 + pl.k) * states, h);
+            if (q == 0) a.sums[(pl.map0 + pl.k) * a.D + ch] = sum;
         }
     } else if (a.S_T && pl.k == pl.pieces - 1 && real) {
         st_states<NS>(a.S_T + (int64_t)pl.seq * states + at_state, h);
@@ -166,6 +169,8 @@ static int fwd_piece(int nseq, int T, int D, int G, bool packed) {
     if (!packed && (int64_t)nseq * blocks_of(D, G) >= 512) return (int)(((int64_t)T + TILE - 1) / TILE * TILE);
     return cut_piece(nseq, T, D, G, packed);
 }
+
+static int64_t kept_of(int nseq, int T, int piece, bool packed) { return packed && nseq > T / piece ? T / piece : nseq; }
 
 template <typename E, int NS, bool SOFTPLUS>
 static hipError_t fwd_t(const FwdArgs& a, bool cut, bool zero_rest, hipStream_t stream) {
@@ -185,16 +190,18 @@ int64_t scan_fwd_workgroups(int nseq, int T, int D, int G, bool packed) {
 size_t scan_fwd_workspace_bytes(int nseq, int T, int D, int N, int G, bool packed) {
     const int piece = scan::fwd_piece(nseq, T, D, G, packed);
     if (piece >= T) return 0;
-    return (size_t)scan::slots_of(nseq, T, piece, packed) * D * (N + 1) * sizeof(float);
+    return (size_t)(scan::maps_of(nseq, T, piece, packed) + scan::kept_of(nseq, T, piece, packed)) * D * (N + 1) * sizeof(float);
 }
 
 hipError_t launch_scan_fwd(const ScanCall& c, bool zero_rest, void* y, float* S_T, void* workspace, hipStream_t stream) {
     const bool packed = c.cu != nullptr;
     const int piece = scan::fwd_piece(c.nseq, c.T, c.D, c.G, packed);
     const int64_t slots = scan::slots_of(c.nseq, c.T, piece, packed);
+    const int64_t maps = scan::maps_of(c.nseq, c.T, piece, packed), kept = scan::kept_of(c.nseq, c.T, piece, packed), states = (int64_t)c.D * c.N;
     float* local = (float*)workspace;
     const scan::FwdArgs a{{c.nseq, c.T, piece, c.cu}, c.D, c.G, c.x, c.dt, c.b, c.c, c.z, c.A, c.skip, c.bias, c.S0,
-                          y, (unsigned)(slots * scan::blocks_of(c.D, c.G)), S_T, local, local ? local + slots * c.D * c.N : nullptr};
+                          y, (unsigned)(slots * scan::blocks_of(c.D, c.G)), S_T, local, local ? local + maps * states : nullptr,
+                          local ? local + (maps + kept) * states : nullptr};
     const bool cut = piece < c.T;
 #define KDA_SF(N)                                                                                                          \
     return c.f32 ? c.softplus ? scan::fwd_t<float, N / 4, true>(a, cut, zero_rest && packed, stream) : scan::fwd_t<float, N / 4, false>(a, cut, zero_rest && packed, stream) \
