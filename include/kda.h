@@ -465,6 +465,7 @@ int kda_block_norm_bwd_workspace_size(long long rows, int D, size_t* bytes);
  *
  *   dtype        storage of x, dt, b, c, z and y; all arithmetic, A and the states are fp32
  *   T            at most 2^30;  D at most 2^20, D / G a multiple of 8;  N 8, 16, 32 or 64
+ *   nseq         fewer than 2^24 workgroups a call, for which (nseq + 2048) G ceil(D / G / 64) < 2^24 is enough
  *   x, dt, z     [.., D]     dtype; z NULL: no gate
  *   A            [D, N]      fp32, used as given (negative in a model that forgets); finite.  Where states
  *                grow, exp(A sum delta) has to stay within fp32 over every part of a sequence

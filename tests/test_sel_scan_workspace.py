@@ -47,6 +47,14 @@ def test_dense_workspace(nseq, T):
     assert size <= nseq * T * (D * (N + 1) / 4 + 8 * N * 16) + 24 * D * (N + 2) * max(1, nseq * T / 32) + (N + 2) / 2 * mib + 256
 
 
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("T,D,G", [(1, 1024, 1), (300, 64, 8), (1 << 22, 1024, 1), (70, 1 << 20, 1), (9000, 200, 5)])
+def test_sequences_that_are_enough_for_the_header(T, D, G, packed):
+    nseq = ((1 << 24) - 1) // (G * -(-D // G // 64)) - 2048
+    for size in (kda.kda_sel_scan_fwd_workspace_size, kda.kda_sel_scan_bwd_workspace_size):
+        assert nseq < 1 or size(nseq, T, D, 16, G, packed) >= 0
+
+
 def poisoned(nbytes):
     return torch.full((nbytes,), 255, dtype=torch.uint8, device=DEV)   # as fp32 NaN
 
