@@ -9,8 +9,8 @@
 // a run of rows, whose last W inputs stay in registers; a run reads W - 1 rows of its neighbour's.
 // Measured, bf16, 4 taps, silu: forwards 65,536 rows of 6,144 channels 316 us (1.61 GB, 5.1 TB/s, a large copy's rate);
 // backwards 32,768 rows of 2,048 channels in six packed sequences 99 us (403 MB, 4.1 TB/s; 5 us of it the sums'
-// launch), where the taps, their sums, the inputs and the waiting gradients are 200 registers and a SIMD
-// has two wavefronts.  Four channels a lane (119), two (114 to 120), rows without branches in the middle of
+// launch), where the taps, their sums, the inputs and the waiting gradients are 242 registers and a SIMD
+// has two wavefronts; in fp32 266, one wavefront, and 215 us (805 MB, 3.7 TB/s).  Four channels a lane (119), two (114 to 120), rows without branches in the middle of
 // a run (114 beside 110) and other lengths of runs gained nothing there.
 #include "kda_launch.hpp"
 #include "kda_rows.hpp"

@@ -8,8 +8,8 @@
 // from zero keeps its digits; the backward pass rebuilds r from the inputs.  Both are bound by HBM: a row stays in
 // registers, each operand is read once and each result written once, and the next row is asked for before
 // this one's sums meet.
-// Measured, bf16, all parts: forwards 65,536 rows of 2,048 channels 212 us (1.07 GB, 5.1 TB/s, a large copy's rate), backwards
-// 16,384 rows of 2,048 76 us (336 MB, 4.4 TB/s), of 2,056 116, 4,096 of 8,192 97 (one workgroup a compute unit, whose three sums a
+// Measured, bf16, all parts: forwards 65,536 rows of 2,048 channels 212 to 217 us (1.07 GB, 5 TB/s, a large copy's rate), backwards
+// 16,384 rows of 2,048 75 us (336 MB, 4.5 TB/s), of 2,056 100, 4,096 of 8,192 93 (one workgroup a compute unit, whose three sums a
 // row little overlaps); 7 rows of 1,000 in fp32 11 us, the call's host time.
 #include "kda_launch.hpp"
 #include "kda_rows.hpp"

@@ -54,7 +54,9 @@ __device__ __forceinline__ void st8(bf16* p, const V8& v) {
 
 // sigmoid(z): in fp32 storage from the library exponential and a true division
 // (a unit or two in the last place); in bf16 storage from the hardware exponential and reciprocal,
-// whose error of a few 2^-23 |z| is far below the result's rounding.
+// whose error of a few 2^-23 |z| is far below the rounding of what is stored in bf16.  Weights' gradients are fp32: there it is a
+// term's, of sums over all rows whose own roundings are as large (convolution, 32,768 rows by 2,048 channels, against 64 bits: dw off by
+// 1.83e-7 and dbias by 1.86e-7 of their root mean square; with a sigmoid of a few 2^-24 1.84e-7 and 1.84e-7, in 2% more time).
 template <typename E> __device__ __forceinline__ float sigmoid(float z);
 template <> __device__ __forceinline__ float sigmoid<float>(float z) { return 1.0f / (1.0f + expf(-z)); }
 template <> __device__ __forceinline__ float sigmoid<bf16>(float z) { return out_sigmoid(z); }

@@ -11,7 +11,7 @@
 // and ddt = ddelta softplus'(dt + bias), dz = dy (sum_n c h + skip x) silu'(z).
 //
 // Three launches.  Maps: every piece forwards from nothing, leaving the state before each 16
-// tokens, the piece's end state, and its part of the state's gradient before it (which needs the running product of
+// tokens but the first, the piece's end state, and its part of the state's gradient before it (which needs the running product of
 // the decays only, so it is formed in the same sweep).  Gradients: every piece backwards, 16 tokens at a time; a
 // state's 16 decays and states stay in registers between the sweep forwards and the one back.  Sums: what
 // several workgroups have parts of, always in the same order.
@@ -24,8 +24,9 @@
 // wavefronts a SIMD; with two, 1,022 us where it took 900.  The sums over channels on the fp32 matrix instructions (a product with one
 // column a token) came to 1,435 us of a call of 1,225 for dc alone, 1,626 for both: their 32 cycles each add to the vector
 // instructions' time.
-// Measured, 8 x 4,096 tokens by 2,048 channels, 16 states, bf16, every part: 1,202 us (maps 306, gradients 870 and sums 32 under the profiler;
-// 0.94 GB in and out, and 0.8 GB through the workspace); four packed sequences of 4,096 tokens by 512 channels in fp32 71 us.
+// Measured, 8 x 4,096 tokens by 2,048 channels, 16 states, bf16, every part: 1,228 us (maps 324, gradients 890 and sums 32 under the profiler;
+// 0.94 GB in and out, and 0.8 GB through the workspace); four packed sequences of 4,096 tokens by 512 channels in fp32 70 us.  At 64 states
+// a workgroup's LDS, 141,312 bytes, leaves one a compute unit, one wavefront a SIMD, where the registers (201 and 205) would hold two.
 #include "kda_rows.hpp"
 #include "kda_scan.hpp"
 

@@ -3,12 +3,12 @@
 //
 // What bounds it: vector instructions.  A token, channel and state takes two products, an exponential (two
 // instructions' time), two fused products for y and the state: six of them forwards, five in a map, against
-// a quarter of a byte of HBM.  So operands that a quad shares are handed round inside the products (kda_scan.hpp), b and c
+// half a byte of HBM in the walk and a quarter in a map (16 states, bf16).  So operands that a quad shares are handed round inside the products (kda_scan.hpp), b and c
 // are converted once a workgroup, a lane's own tokens are asked for a tile ahead through buffer resources that
 // take no vector address, and each as soon as its predecessor is used, which keeps a wavefront below 100 registers (16
 // states: five wavefronts a SIMD).  Counters: 90% of the vector issue slots taken, 65% of those the six and five.
-// Measured, bf16, 16 states, gate, skip and softplus: 65,536 tokens by 2,048 channels 863 to 879 us (43% in the maps; 1.2
-// TB/s, 2.4e12 states a second), 32 x 4,096 by 4,096 uncut 2.0 ms (4.3e12); ten packed prompts of 1 to 8,192 tokens 230 us.
+// Measured, bf16, 16 states, gate, skip and softplus: 65,536 tokens by 2,048 channels 886 us (43% in the maps; 1.2
+// TB/s, 2.4e12 states a second), 32 x 4,096 by 4,096 uncut 1.97 ms (4.4e12); ten packed prompts of 1 to 8,192 tokens 237 us.
 // Before: addresses in vector registers, operands exchanged by instructions of their own, a whole tile's tokens held
 // while the next ones came: 1,376, 413.
 //
@@ -160,9 +160,10 @@ __global__ void __launch_bounds__(BLOCK) scan_walk(FwdArgs a) {
 }
 
 // Tokens a piece.  A cut call forms every state twice, but 256 workgroups are one wavefront a SIMD, whose
-// instructions wait for each other.  Measured, sequences of 4,096 tokens by 2,048 channels of 16 states: at 256
-// workgroups whole 544 us, cut 514; at 512 whole 697, cut 907.  Pieces are as many as give 2,048 workgroups, eight a
-// compute unit (65,536 tokens, before the step's exponential was shortened: 512 workgroups 1,259 us, 1,024 951, 2,048 896, 4,096 916), of 64 tokens at the least
+// instructions wait for each other.  Measured, sequences of 4,096 tokens by 2,048 channels of 16 states, when the call below took 896: at 256
+// workgroups whole 544 us, cut 514; at 512 whole 697, cut 907 (now 600 and 829).  A packed call's lengths are not known here, so it is
+// cut however many sequences it has.  Pieces are as many as give 2,048 workgroups, eight a
+// compute unit (65,536 tokens, in the course of the work: 512 workgroups 1,259 us, 1,024 951, 2,048 896, 4,096 916), of 64 tokens at the least
 // (2 x 1,000 tokens by 256 channels of 32 states: 32 tokens 29.7 us, 64 30.9, 128 43.8; the backward pass of four
 // sequences by 512 channels, which has the same rule: 90.7, 81.8, 107.7).
 static int fwd_piece(int nseq, int T, int D, int G, bool packed) {

@@ -4,8 +4,8 @@
 // A call reads and writes each state once, whatever the number of tokens: an HBM stream of
 // 8 D N bytes a request.  Four lanes a channel, so that a wavefront's states are one run of
 // 16 N floats, and four tokens at a time, as in the walk over whole sequences.
-// Measured, 2,048 channels of 16 states, bf16: 256 requests 18.5 us (71 MB, 3.8 TB/s; the states of 34 MB are partly in
-// the last-level cache), one request 12.4 us, its call's host time; 4,096 requests of 256 channels 53 us, half of it the search for duplicates.
+// Measured, 2,048 channels of 16 states, bf16: 256 requests 17.5 us (71 MB, 4.1 TB/s; the states of 34 MB are partly in
+// the last-level cache), one request 10.5 us, its call's host time; 4,096 requests of 256 channels 50 us, half of it the search for duplicates.
 #include "kda_scan.hpp"
 
 namespace kda {
