@@ -492,8 +492,8 @@ int kda_sel_scan_fwd(int dtype, int nseq, int T, int D, int N, int G, int softpl
  *   dA           [D, N] fp32, written;  dskip, ddt_bias  [D] fp32, written, or NULL to skip
  *   dS0          as S0, fp32, written; or NULL to skip
  *   workspace    kda_sel_scan_bwd_workspace_size bytes: about D N / 4 + 8 N B a token, B = G ceil(D / G / 64); 24 D N
- *                a piece of sequences, which has at least 64 tokens (32 where none is longer); and (N + 2) / 2
- *                MiB at most.  However many sequences the rows are
+ *                a piece of sequences, which has at least 64 tokens (32 where none is longer; one piece at
+ *                least); and (N + 2) / 2 MiB at most.  However many sequences the rows are
  *   No output may overlap anything.  Sums over rows and channels are in a fixed order.
  * Returns a kda_status.
  * ------------------------------------------------------------------------- */

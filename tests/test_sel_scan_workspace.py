@@ -23,7 +23,7 @@ def test_at_most_256_pieces_a_sequence(T):
     assert rest == 0 and 2 <= pieces <= 256
 
 
-SIZES = [(4096, 2048, 16, 1), (1 << 20, 256, 64, 2), (100, 64, 8, 1), (65536, 1024, 16, 128), (777, 4096, 32, 1)]
+SIZES = [(4096, 2048, 16, 1), (1 << 20, 256, 64, 2), (100, 64, 8, 1), (65536, 1024, 16, 128), (777, 4096, 32, 1), (3, 1 << 20, 64, 1)]
 
 
 @pytest.mark.parametrize("T,D,N,G", SIZES)
@@ -37,7 +37,7 @@ def test_packed_workspace_is_the_rows_not_the_sequences(T, D, N, G):
             continue
         assert kda.kda_sel_scan_fwd_workspace_size(n, T, D, N, G, True) <= 2 * one
         size = kda.kda_sel_scan_bwd_workspace_size(n, T, D, N, G, True)
-        assert size <= T * (D * (N + 1) / 4 + 8 * N * B) + 24 * D * (N + 2) * (T / 64) + (N + 2) / 2 * mib + 256, n
+        assert size <= T * (D * (N + 1) / 4 + 8 * N * B) + 24 * D * (N + 2) * max(1, T / 64) + (N + 2) / 2 * mib + 256, n
 
 
 @pytest.mark.parametrize("nseq,T", [(1, 4096), (4096, 1), (1000, 33), (64, 4096)])
