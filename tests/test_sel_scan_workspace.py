@@ -32,7 +32,7 @@ def test_packed_workspace_is_the_rows_not_the_sequences(T, D, N, G):
     floats a state beside the N."""
     one, mib = kda.kda_sel_scan_fwd_workspace_size(1, T, D, N, G, True), 1 << 20
     B = G * -(-D // G // 64)
-    for n in (1, 10, T // 16, T, 2 * T):
+    for n in (1, 10, max(1, T // 16), T, 2 * T):
         if n * B >= 1 << 23:
             continue
         assert kda.kda_sel_scan_fwd_workspace_size(n, T, D, N, G, True) <= 2 * one
