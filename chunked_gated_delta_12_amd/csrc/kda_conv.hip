@@ -35,11 +35,10 @@ struct Span {
     int n;
     int64_t lo, hi;
 };
-__device__ __forceinline__ int conv_held(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
 __device__ __forceinline__ Span span_at(const ConvArgs& a, int n) {
     if (!a.cu) return Span{n, (int64_t)n * a.T, (int64_t)(n + 1) * a.T};
-    const int lo = conv_held(a.cu[n], 0, a.T);
-    return Span{n, lo, conv_held(a.cu[n + 1], lo, a.T)};
+    const int lo = held(a.cu[n], 0, a.T);
+    return Span{n, lo, held(a.cu[n + 1], lo, a.T)};
 }
 // The last sequence that starts at or before the row, or the first.
 __device__ __forceinline__ Span span_of(const ConvArgs& a, int64_t row) {

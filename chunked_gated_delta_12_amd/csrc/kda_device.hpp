@@ -118,6 +118,9 @@ __device__ __forceinline__ void store_pair(E* p, float a, float b) {
 }
 
 // ---------------------------------------------------------------- rows and slots
+// An offset within [lo, hi].
+__device__ __forceinline__ int held(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
+
 // Whether a row before row r that has tokens (ntok NULL: every one) names the same slot; the answer is the
 // wavefront's.  256 rows at a time: the search is every wavefront's own and grows with the rows before it.
 __device__ __forceinline__ bool earlier_row(const int* __restrict__ slots, const int* __restrict__ ntok, int r, int slot, int lane) {

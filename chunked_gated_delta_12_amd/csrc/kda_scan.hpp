@@ -51,8 +51,6 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
     return (int64_t)(((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32) | (uint32_t)uniform((int)v));
 }
 
-__device__ __forceinline__ int held(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
-
 // Zeros in the rows of no sequence, those before the first and behind the last, of a tensor of D values a row: workgroup blk of
 // the REST_BLOCKS that a launch has for that behind its others.
 constexpr int REST_BLOCKS = 64;
